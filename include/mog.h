@@ -477,6 +477,164 @@ int mog_build_from_partition(const mog_kv *kv, const int32_t *lengths_dev,
  */
 int mog_check_bounded_wait(int32_t limit, int32_t arrive, int32_t *scratch_dev, void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * Caches of 8-bit rows, differential heads, and the pages of a shared cache.  None of
+ * these has a counterpart in the papers: they are the other half of a decode step, the
+ * writing and sharing of the cache that the attentions above read.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * A KV cache of bf16 or e4m3 rows in device memory, contiguous or paged (mog_kv's layouts).
+ *  type MOG_CACHE_BF16 : rows as mog_kv; k_scale, v_scale NULL.
+ *  type MOG_CACHE_E4M3 : one byte per element (fp8 e4m3), and one fp32 scale >= 0 per row
+ *    of K and of V: the row of position n stands for scale * code.  Scales of (b, h, n) at
+ *    b*scale_b + h*scale_h + n*scale_n floats (pages: page, h, row in page).
+ *  stride_b, stride_h, stride_n are in elements, multiples of 16 bytes, stride_n >= d;
+ *  base pointers 16-byte aligned.
+ *  Contiguous: block_table NULL, positions [0, n_cap).  Paged: page_rows a power of two
+ *  >= 16, n_pages pages in the pool; a block-table entry outside [0, n_pages) holds no
+ *  rows: they are left out of an attention and not written by a store.
+ */
+#define MOG_CACHE_BF16 0
+#define MOG_CACHE_E4M3 1
+typedef struct mog_cache {
+    int32_t type;
+    int32_t n_cap;
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t stride_b, stride_h, stride_n;
+    int64_t scale_b, scale_h, scale_n;
+    const int32_t *block_table; /* NULL: contiguous */
+    int32_t page_rows, pages_per_seq, n_pages;
+} mog_cache;
+
+/* Element type of an output: fp32, or bf16 rounded once from fp32. */
+#define MOG_OUT_F32 0
+#define MOG_OUT_BF16 1
+
+/*
+ * dense_decode over an e4m3 cache: for every query head softmax(tau q.K^T) V over keys
+ * [0, N_b), K and V the rows' values scale * code, tau = 1/sqrt(d).  A sequence without
+ * rows gives zeros.
+ *  c           : MOG_CACHE_E4M3
+ *  lengths_dev : int32[batch] on the device, clamped to [0, n_max]; n_max <= the cache's
+ *                positions
+ *  q_dev       : bf16 [batch][h_q][d];  out_dev: out_type [batch][h_q][d]
+ *  scratch_dev : at least dense_decode8_scratch_bytes() bytes, 16-byte aligned; no initial
+ *                contents needed, not shared by calls that overlap on the GPU
+ * d must be 128, h_q / h_kv <= 16.
+ */
+int dense_decode8_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t n_max,
+                                size_t *bytes);
+int dense_decode8(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                  int32_t h_kv, int32_t h_q, int32_t d, const void *q_dev, void *out_dev,
+                  int32_t out_type, void *scratch_dev, size_t scratch_bytes, void *stream);
+
+/*
+ * Differential decode attention, one new token per sequence.  A head's query row and a key
+ * row are two halves of d/2, q = [q1 | q2], k = [k1 | k2]; its value row has d elements:
+ *   a   = softmax(tau q1.K1^T) V - lambda softmax(tau q2.K2^T) V,   tau = 1/sqrt(d/2)
+ *   lambda = exp(l_q1 . l_k1) - exp(l_q2 . l_k2) + lambda_init
+ *   out = (1 - lambda_init) * a / sqrt(mean(a^2) + eps) * gamma
+ * over keys [0, N_b); a sequence without rows gives zeros.
+ *  lam         : device f32 [lam_heads][4][d/2], the vectors l_q1, l_k1, l_q2, l_k2, with
+ *                lam_heads 1 (shared by the heads) or h_q; 16-byte aligned
+ *  gamma       : device f32 [d], 16-byte aligned, or NULL for ones;  eps > 0
+ * Caches of both types; the other arguments as dense_decode8.  h_q / h_kv <= 8.
+ */
+typedef struct mog_diff_params {
+    const float *lam;
+    const float *gamma;
+    int32_t lam_heads;
+    float lambda_init;
+    float eps;
+} mog_diff_params;
+int mog_diff_decode_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t n_max,
+                                  size_t *bytes);
+int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                    int32_t h_kv, int32_t h_q, int32_t d, const void *q_dev,
+                    const mog_diff_params *params, void *out_dev, int32_t out_type,
+                    void *scratch_dev, size_t scratch_bytes, void *stream);
+
+/*
+ * Write new keys and values into a cache: token t < count[b] of sequence b goes to position
+ * pos[b] + t.  Positions outside the cache, or in no page, are left out.
+ *  pos_dev, count_dev   : int32[batch] on the device; count NULL: t_max for every sequence
+ *                         (counts are clamped to [0, t_max])
+ *  k_new_dev, v_new_dev : bf16, element (b, t, h, j) at b*new_b + t*new_t + h*new_h + j;
+ *                         strides multiples of 8, 16-byte aligned
+ * An e4m3 row's scale is the least power of two 2^e, e >= -126, with
+ * amax <= 448 * 2^e, amax the row's largest finite magnitude (scale 1 if that is 0); its
+ * codes are x / 2^e (exact) rounded to nearest even, infinities saturated, NaN kept.  Rows
+ * must not be stored twice by one call (pages shared by two sequences that both write).
+ */
+int mog_kv_store(const mog_cache *c, int32_t batch, int32_t h_kv, int32_t d, int32_t t_max,
+                 const int32_t *pos_dev, const int32_t *count_dev, const void *k_new_dev,
+                 const void *v_new_dev, int64_t new_b, int64_t new_t, int64_t new_h, void *stream);
+
+/*
+ * The pages of a paged cache shared by sequences.  All state is in device memory and owned
+ * by the caller; the calls are enqueued on `stream` and do not wait for it, so they may be
+ * captured.  Calls on one mog_pages must not overlap on the GPU.
+ *  block_table : int32 [batch][pages_per_seq]: row b holds ceil(lengths[b]/page_rows)
+ *                pages, -1 behind them
+ *  refs        : int32 [n_pages]: how many block-table entries hold a page
+ *  pools       : host array of the n_pools page pools that the table addresses (K and V,
+ *                and their scales, of every layer); page p of a pool is the page_bytes bytes
+ *                at base + p*page_stride, all multiples of 16.  Read during the call only.
+ *  work        : mog_pages_work_bytes() bytes, 4-byte aligned, all zero before the first
+ *                call and used by nothing else after it
+ * page_rows a power of two >= 16, batch <= 4096, pages_per_seq * page_rows < 2^31.
+ */
+typedef struct mog_page_pool {
+    void *base;
+    int64_t page_stride, page_bytes;
+} mog_page_pool;
+typedef struct mog_pages {
+    int32_t n_pages, page_rows, batch, pages_per_seq;
+    int32_t *block_table, *lengths, *refs;
+    void *work;
+    size_t work_bytes;
+    const mog_page_pool *pools;
+    int32_t n_pools;
+} mog_pages;
+int mog_pages_work_bytes(int32_t n_pages, int32_t batch, size_t *bytes);
+
+/*
+ * Fork, reorder and free: sequence b becomes another holder of the pages that sequence
+ * src_dev[b] held before the call, with its length; src[b] = b keeps b as it is, -1 frees
+ * it.  All sources are read before any sequence changes.  A page that no sequence holds any
+ * more is free; page contents stay.
+ */
+int mog_pages_assign(const mog_pages *p, const int32_t *src_dev, void *stream);
+
+/*
+ * Room for n_new_dev[b] >= 0 more tokens of every sequence: lengths grow by it, and pages are
+ * taken from the free ones, lowest first, in the order of the sequences.  A sequence that
+ * grows behind a partly filled page which it shares gets a copy of that page (in every
+ * pool) in its place; the last of its holders keeps the page itself.  pos_dev[b] receives
+ * the old length and granted_dev[b] n_new[b], the position and count that mog_kv_store
+ * takes.  If the pool has too few free pages, or a sequence would outgrow the table or
+ * has a bad length or page, nothing changes and every granted[b] is 0.
+ */
+int mog_pages_grow(const mog_pages *p, const int32_t *n_new_dev, int32_t *pos_dev, int32_t *granted_dev,
+                   void *stream);
+
+/*
+ * Move the pages in use to the front of the pools: with n_live pages held, the live pages
+ * behind the first n_live move, in ascending order, to the free places among them, and the
+ * block table and refs follow.  Afterwards pages [n_live, n_pages) are free.  A mog_handle
+ * built over the old table is no longer valid.
+ */
+int mog_pages_compact(const mog_pages *p, void *stream);
+
+/*
+ * Synchronise `stream`, then read and clear the status that the calls above left: MOG_OK,
+ * MOG_ERR_CAPACITY (a mog_pages_grow found no room) or MOG_ERR_DEVICE_CHECK (an index,
+ * length or page out of range, which the call left out).
+ */
+int mog_pages_status(const mog_pages *p, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

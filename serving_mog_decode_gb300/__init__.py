@@ -77,6 +77,111 @@ class PagedKV:
                   self.page_rows, self.block_table.shape[1])
 
 
+class Cache(C.Structure):
+    _fields_ = [("type", C.c_int32), ("n_cap", C.c_int32), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("stride_b", C.c_int64),
+                ("stride_h", C.c_int64), ("stride_n", C.c_int64), ("scale_b", C.c_int64),
+                ("scale_h", C.c_int64), ("scale_n", C.c_int64), ("block_table", C.c_void_p),
+                ("page_rows", C.c_int32), ("pages_per_seq", C.c_int32), ("n_pages", C.c_int32)]
+
+
+class DiffParams(C.Structure):
+    _fields_ = [("lam", C.c_void_p), ("gamma", C.c_void_p), ("lam_heads", C.c_int32),
+                ("lambda_init", C.c_float), ("eps", C.c_float)]
+
+
+class PagePoolDesc(C.Structure):
+    _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("page_bytes", C.c_int64)]
+
+
+class Pages(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("page_rows", C.c_int32), ("batch", C.c_int32),
+                ("pages_per_seq", C.c_int32), ("block_table", C.c_void_p), ("lengths", C.c_void_p),
+                ("refs", C.c_void_p), ("work", C.c_void_p), ("work_bytes", C.c_size_t),
+                ("pools", C.POINTER(PagePoolDesc)), ("n_pools", C.c_int32)]
+
+
+def _check_rows8(K, V, k_scale, v_scale):
+    torch = _torch()
+    for t in (K, V):
+        if t.dtype != torch.float8_e4m3fn or t.dim() != 4 or t.stride(3) != 1 or not t.is_cuda:
+            raise ValueError("K and V must be CUDA float8_e4m3fn tensors with 4 dims, last contiguous")
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or t.shape != K.shape[:3] or t.device != K.device:
+            raise ValueError("the scales must be float32 tensors of K's first three dims on its device")
+    if K.shape != V.shape or K.stride() != V.stride() or V.device != K.device:
+        raise ValueError("K and V must share shape, strides and device")
+    if k_scale.stride() != v_scale.stride():
+        raise ValueError("the scales must share strides")
+    if K.shape[3] != 128:
+        raise ValueError("the last dim of K and V must be 128")
+
+
+class KV8:
+    """A contiguous e4m3 KV cache: codes K, V float8_e4m3fn [B, H_kv, n_cap, 128] and a scale
+    per row, k_scale, v_scale float32 [B, H_kv, n_cap] (value = scale * code).  Pass it as K
+    (with V=None) to dense_decode, diff_decode and kv_store.  The tensors are fixed once it
+    is made."""
+
+    def __init__(self, K, V, k_scale, v_scale):
+        _check_rows8(K, V, k_scale, v_scale)
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self.batch, self.h_kv, self.device = K.shape[0], K.shape[1], K.device
+        self.positions = K.shape[2]
+        self.cache = Cache(1, K.shape[2], K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                           *K.stride()[:3], *k_scale.stride(), None, 0, 0, 0)
+
+
+class PagedKV8:
+    """A paged e4m3 KV cache: page pools K, V float8_e4m3fn [pages, H_kv, page_rows, 128]
+    (heads_first) or [pages, page_rows, H_kv, 128], a scale per row, k_scale, v_scale float32
+    of the pools' first three dims, and an int32 block table [B, pages_per_seq] on the device.
+    Pass it as K (with V=None) to dense_decode, diff_decode and kv_store.  The tensors are
+    fixed once it is made; the block table's entries may change between calls."""
+
+    def __init__(self, K, V, k_scale, v_scale, block_table, page_rows, heads_first=True):
+        _check_rows8(K, V, k_scale, v_scale)
+        _check_table(block_table, K)
+        if K.shape[2 if heads_first else 1] != page_rows:
+            raise ValueError("page_rows must be the pools' rows per page")
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self.block_table, self.page_rows, self.heads_first = block_table, page_rows, heads_first
+        self.batch, self.h_kv = block_table.shape[0], K.shape[1 if heads_first else 2]
+        self.positions, self.device = block_table.shape[1] * page_rows, K.device
+        h, n = (1, 2) if heads_first else (2, 1)
+        ks, ss = K.stride(), k_scale.stride()
+        self.cache = Cache(1, 0, K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ks[0], ks[h],
+                           ks[n], ss[0], ss[h], ss[n], block_table.data_ptr(), page_rows, block_table.shape[1],
+                           K.shape[0])
+
+
+def _check_table(block_table, K):
+    torch = _torch()
+    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous()
+            or block_table.device != K.device):
+        raise ValueError("block_table must be a contiguous int32 tensor [B, pages_per_seq] on the pools' device")
+
+
+def _cache(K, V):
+    """(mog_cache, batch, KV heads, positions, device) of a KV8, a PagedKV8, a PagedKV or two
+    bf16 tensors [B, H_kv, n_cap, 128]."""
+    if isinstance(K, (KV8, PagedKV8)):
+        return K.cache, K.batch, K.h_kv, K.positions, K.device
+    if isinstance(K, PagedKV):
+        kv, t = K.struct(), K.block_table
+        _check_table(t, K.K)
+        if K.V.device != K.device or K.K.shape[3] != 128 or K.K.shape[2 if K.heads_first else 1] != K.page_rows:
+            raise ValueError("page pools must share a device and hold page_rows rows of 128")
+        c = Cache(0, 0, kv.k, kv.v, None, None, kv.stride_b, kv.stride_h, kv.stride_n, 0, 0, 0, kv.block_table,
+                  kv.page_rows, kv.pages_per_seq, K.K.shape[0])
+        return c, t.shape[0], K.h_kv, t.shape[1] * K.page_rows, K.device
+    kv = _kv(K, V)
+    if V.device != K.device or K.shape[3] != 128:
+        raise ValueError("K and V must share a device and have rows of 128")
+    c = Cache(0, K.shape[2], kv.k, kv.v, None, None, kv.stride_b, kv.stride_h, kv.stride_n)
+    return c, K.shape[0], K.shape[1], K.shape[2], K.device
+
+
 class Layout(C.Structure):
     _fields_ = ([(n, C.c_int32) for n in ("units", "c_max", "l_max", "n_cap", "d", "group",
                                            "top_c", "top_s")] +
@@ -125,6 +230,16 @@ _SIGS = {
                                     C.c_size_t, _P, _P]),
     "mog_kmeans_assign_segments": (C.c_int, [_P, C.c_int64, _P, _P, C.c_int32, _P, C.c_int32,
                                              C.c_int32, _P, _P]),
+    "dense_decode8_scratch_bytes": (C.c_int, [C.c_int32] * 5 + [_P]),
+    "dense_decode8": (C.c_int, [_P, _P] + [C.c_int32] * 5 + [_P, _P, C.c_int32, _P, C.c_size_t, _P]),
+    "mog_diff_decode_scratch_bytes": (C.c_int, [C.c_int32] * 5 + [_P]),
+    "mog_diff_decode": (C.c_int, [_P, _P] + [C.c_int32] * 5 + [_P, _P, _P, C.c_int32, _P, C.c_size_t, _P]),
+    "mog_kv_store": (C.c_int, [_P] + [C.c_int32] * 4 + [_P] * 4 + [C.c_int64] * 3 + [_P]),
+    "mog_pages_work_bytes": (C.c_int, [C.c_int32, C.c_int32, _P]),
+    "mog_pages_assign": (C.c_int, [_P, _P, _P]),
+    "mog_pages_grow": (C.c_int, [_P, _P, _P, _P, _P]),
+    "mog_pages_compact": (C.c_int, [_P, _P]),
+    "mog_pages_status": (C.c_int, [_P, _P]),
     "mog_check_bounded_wait": (C.c_int, [C.c_int32, C.c_int32, _P, _P]),
 }
 
@@ -176,6 +291,8 @@ def _kv(K, V):
     if isinstance(K, PagedKV):
         return K.struct()
     torch = _torch()
+    if isinstance(K, (KV8, PagedKV8)) or V is None:
+        raise ValueError("this call takes bf16 K and V tensors, or a PagedKV as K")
     for t in (K, V):
         if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1 or not t.is_cuda:
             raise ValueError("K and V must be CUDA bf16 tensors [B, H_kv, n_cap, d], last dim contiguous")
@@ -416,7 +533,10 @@ def _check_q_out(K, q, out):
 
 
 def dense_decode(K, V, lengths_dev, n_max, q, out=None, scratch=None, stream=None):
-    """Full-scan exact attention.  q: bf16 [B, H_q, d] -> out f32 [B, H_q, d]."""
+    """Full-scan exact attention.  q: bf16 [B, H_q, d] -> out f32 [B, H_q, d].  Over an e4m3
+    cache (K a KV8 or PagedKV8; dense_decode8) `out` may also be bf16."""
+    if isinstance(K, (KV8, PagedKV8)):
+        return _cache_decode("dense_decode8", K, V, lengths_dev, n_max, q, None, out, scratch, stream)
     torch = _torch()
     B, H_kv = (q.shape[0], K.h_kv) if isinstance(K, PagedKV) else (K.shape[0], K.shape[1])
     H_q = q.shape[1]
@@ -443,6 +563,213 @@ def dense_decode_noalloc(K, V, lengths_dev, n_max, q, out, stream=None):
                                       128, _ptr(q), _ptr(out), _stream(stream)),
            "dense_decode_noalloc")
     return out
+
+
+def _cache_decode(entry, K, V, lengths_dev, n_max, q, diff, out, scratch, stream):
+    torch = _torch()
+    c, B, H_kv, positions, dev = _cache(K, V)
+    if (q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != B or q.shape[2] != 128
+            or not q.is_contiguous() or q.device != dev):
+        raise ValueError("q must be a contiguous bf16 tensor [B, H_q, 128] on the cache's device")
+    _check_counts(lengths_dev, B, dev, "lengths_dev")
+    if not 1 <= n_max <= positions:
+        raise ValueError(f"n_max must be between 1 and the cache's {positions} positions")
+    H_q = q.shape[1]
+    need = C.c_size_t(0)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        elif (out.dtype not in (torch.float32, torch.bfloat16) or out.shape != q.shape
+              or not out.is_contiguous() or out.device != dev):
+            raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape on q's device")
+        if scratch is None:
+            _check(getattr(lib(), entry + "_scratch_bytes")(B, H_kv, H_q, 128, n_max, C.byref(need)), entry)
+            scratch = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        elif scratch.device != dev or not scratch.is_contiguous():
+            raise ValueError("scratch must be a contiguous tensor on the cache's device")
+        args = [C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr()]
+        args += [C.byref(diff)] if diff is not None else []
+        _check(getattr(lib(), entry)(*args, out.data_ptr(), int(out.dtype == torch.bfloat16), scratch.data_ptr(),
+                                     scratch.numel() * scratch.element_size(), s), entry)
+    return out
+
+
+class _on:
+    """The device `dev` made current, and work and allocations on `stream` (its current stream
+    if None), for the length of a call; gives the cudaStream_t."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
+        self.cms = []
+
+    def __enter__(self):
+        torch = _torch()
+        if self.dev.index != torch.cuda.current_device():
+            self.cms.append(torch.cuda.device(self.dev))
+        if self.stream is not None:
+            self.cms.append(torch.cuda.stream(self.stream))
+        for cm in self.cms:
+            cm.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        for cm in reversed(self.cms):
+            cm.__exit__(*exc)
+
+
+def _strides(t):
+    """Strides of a tensor's leading dims, 0 where there is only one entry."""
+    return [st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride())]
+
+
+def _check_counts(t, B, dev, name):
+    if t.dtype != _torch().int32 or t.shape != (B,) or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{B}] on the cache's device")
+
+
+def diff_decode(K, V, lengths_dev, n_max, q, lam, lambda_init, gamma=None, eps=1e-5, out=None, scratch=None,
+                stream=None):
+    """Differential decode attention (mog_diff_decode): a head is two halves of 64, q bf16
+    [B, H_q, 128] = [q1 | q2] over keys [k1 | k2] and values of 128; the second softmax map is
+    subtracted lambda times and the result normalised.  K, V: bf16 tensors, or K a PagedKV, KV8
+    or PagedKV8.  lam: float32 [4, 64] or [H_q, 4, 64], the vectors l_q1, l_k1, l_q2, l_k2 of
+    lambda = exp(l_q1.l_k1) - exp(l_q2.l_k2) + lambda_init; gamma: float32 [128] norm weights
+    or None.  -> out f32 (or bf16 if given so) [B, H_q, 128]."""
+    torch = _torch()
+    shared = lam.dim() == 2
+    if (lam.dtype != torch.float32 or lam.shape[-2:] != (4, 64) or lam.dim() not in (2, 3) or not lam.is_contiguous()
+            or (not shared and lam.shape[0] != q.shape[1]) or lam.device != q.device):
+        raise ValueError("lam must be a contiguous float32 tensor [4, 64] or [H_q, 4, 64] on q's device")
+    if gamma is not None and (gamma.dtype != torch.float32 or gamma.shape != (128,) or not gamma.is_contiguous()
+                              or gamma.device != q.device):
+        raise ValueError("gamma must be a contiguous float32 tensor [128] on q's device")
+    d = DiffParams(lam.data_ptr(), None if gamma is None else gamma.data_ptr(), 1 if shared else lam.shape[0],
+                   lambda_init, eps)
+    return _cache_decode("mog_diff_decode", K, V, lengths_dev, n_max, q, d, out, scratch, stream)
+
+
+def diff_scratch_bytes(batch, h_kv, h_q, n_max, d=128) -> int:
+    v = C.c_size_t(0)
+    _check(lib().mog_diff_decode_scratch_bytes(batch, h_kv, h_q, d, n_max, C.byref(v)),
+           "mog_diff_decode_scratch_bytes")
+    return v.value
+
+
+def dense8_scratch_bytes(batch, h_kv, h_q, n_max, d=128) -> int:
+    v = C.c_size_t(0)
+    _check(lib().dense_decode8_scratch_bytes(batch, h_kv, h_q, d, n_max, C.byref(v)), "dense_decode8_scratch_bytes")
+    return v.value
+
+
+def kv_store(K, V, pos, count, k_new, v_new, stream=None):
+    """Write new rows into a cache (mog_kv_store): k_new, v_new bf16 [B, T, H_kv, 128] (any
+    strides of whole 16-byte chunks, alike for both, last dim contiguous), token t < count[b] of
+    sequence b to position pos[b] + t; pos, count int32 [B] on the device, count None for T
+    each.  K, V: bf16 tensors [B, H_kv, n_cap, 128], or K a PagedKV, KV8 or PagedKV8 (rounded
+    to e4m3 with a power-of-two scale per row)."""
+    torch = _torch()
+    c, B, H_kv, _, dev = _cache(K, V)
+    for t in (k_new, v_new):
+        if (t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[0] != B or t.shape[2:] != (H_kv, 128)
+                or t.stride(3) != 1 or t.device != dev):
+            raise ValueError(f"k_new and v_new must be bf16 tensors [{B}, T, {H_kv}, 128] on the cache's device")
+    if k_new.shape != v_new.shape or _strides(k_new) != _strides(v_new):
+        raise ValueError("k_new and v_new must share shape and strides")
+    _check_counts(pos, B, dev, "pos")
+    if count is not None:
+        _check_counts(count, B, dev, "count")
+    T = k_new.shape[1]
+    if T == 0:
+        return
+    with _on(dev, stream) as s:
+        _check(lib().mog_kv_store(C.byref(c), B, H_kv, 128, T, pos.data_ptr(),
+                                  None if count is None else count.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                  *_strides(k_new), s), "mog_kv_store")
+
+
+class PagePool:
+    """Sequences that share the pages of one or more paged caches (mog_pages): a block table
+    [batch, pages_per_seq], the sequences' lengths and the pages' holders, all on the device.
+
+    K, V: page pools [pages, H_kv, page_rows, 128] (heads_first) or [pages, page_rows, H_kv, 128],
+    one tensor each or a list with one per layer, bf16, or float8_e4m3fn with k_scale, v_scale.  A page's
+    elements must be contiguous.  block_table, lengths, refs: existing state, int32, used as it
+    is; by default every sequence is empty.  No method waits for the GPU but status()."""
+
+    def __init__(self, K, V, batch, pages_per_seq, heads_first=True, k_scale=None, v_scale=None, block_table=None,
+                 lengths=None, refs=None):
+        torch = _torch()
+        lists = [list(x) if isinstance(x, (list, tuple)) else [x] for x in (K, V)]
+        self.K, self.V = lists
+        if k_scale is not None or v_scale is not None:
+            lists += [list(x) if isinstance(x, (list, tuple)) else [x] for x in (k_scale, v_scale)]
+        self.k_scale, self.v_scale = lists[2:] if len(lists) == 4 else (None, None)
+        if len({len(x) for x in lists}) != 1 or not self.K:
+            raise ValueError("K, V and their scales must have one tensor per layer each")
+        first = self.K[0]
+        self.device, n_pages = first.device, first.shape[0]
+        self.heads_first, self.page_rows = heads_first, first.shape[2 if heads_first else 1]
+        pools = [t for x in lists for t in x]
+        for t in pools:
+            if not t.is_cuda or t.device != self.device or t.shape[:3] != first.shape[:3] or not t[0].is_contiguous():
+                raise ValueError("page pools must share a CUDA device and their first three dims, a page contiguous")
+        for name, t, shape in (("block_table", block_table, (batch, pages_per_seq)), ("lengths", lengths, (batch,)),
+                               ("refs", refs, (n_pages,))):
+            if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()
+                                  or t.device != self.device):
+                raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on the pools' device")
+
+        def state(t, shape, fill):
+            return t if t is not None else torch.full(shape, fill, dtype=torch.int32, device=self.device)
+
+        self.block_table = state(block_table, (batch, pages_per_seq), -1)
+        self.lengths, self.refs = state(lengths, (batch,), 0), state(refs, (n_pages,), 0)
+        need = C.c_size_t(0)
+        _check(lib().mog_pages_work_bytes(n_pages, batch, C.byref(need)), "mog_pages_work_bytes")
+        self.work = torch.zeros(need.value // 4, dtype=torch.int32, device=self.device)
+        self._descs = (PagePoolDesc * len(pools))(*[
+            PagePoolDesc(t.data_ptr(), max(t.stride(0), t[0].numel()) * t.element_size(),
+                         t[0].numel() * t.element_size()) for t in pools])
+        self._s = Pages(n_pages, self.page_rows, batch, pages_per_seq, self.block_table.data_ptr(),
+                        self.lengths.data_ptr(), self.refs.data_ptr(), self.work.data_ptr(), need.value, self._descs,
+                        len(pools))
+        self.batch = batch
+
+    def cache(self, layer=0):
+        """The paged cache of a layer (PagedKV or PagedKV8), for the calls that take one."""
+        if self.k_scale is None:
+            return PagedKV(self.K[layer], self.V[layer], self.block_table, self.page_rows, self.heads_first)
+        return PagedKV8(self.K[layer], self.V[layer], self.k_scale[layer], self.v_scale[layer], self.block_table,
+                        self.page_rows, self.heads_first)
+
+    def assign(self, src, stream=None):
+        """Fork, reorder and free (mog_pages_assign): sequence b takes the pages and length that
+        src[b] had (b: as it is; -1: none).  src: int32 [batch] on the device."""
+        _check_counts(src, self.batch, self.device, "src")
+        with _on(self.device, stream) as s:
+            _check(lib().mog_pages_assign(C.byref(self._s), src.data_ptr(), s), "mog_pages_assign")
+
+    def grow(self, n_new, stream=None):
+        """Room for n_new[b] more tokens of every sequence (mog_pages_grow); a shared last page
+        becomes private.  -> (pos, granted) int32 [batch]: where kv_store puts the new rows, and
+        how many (0 everywhere if there was no room: see status())."""
+        _check_counts(n_new, self.batch, self.device, "n_new")
+        with _on(self.device, stream) as s:
+            both = _torch().empty((2, self.batch), dtype=_torch().int32, device=self.device)
+            _check(lib().mog_pages_grow(C.byref(self._s), n_new.data_ptr(), both.data_ptr(),
+                                        both.data_ptr() + 4 * self.batch, s), "mog_pages_grow")
+        return both[0], both[1]
+
+    def compact(self, stream=None):
+        """Move the pages in use to the front of the pools (mog_pages_compact)."""
+        with _on(self.device, stream) as s:
+            _check(lib().mog_pages_compact(C.byref(self._s), s), "mog_pages_compact")
+
+    def status(self, stream=None) -> int:
+        """Wait for the stream, then read and clear the status of the calls so far: MOG_OK,
+        MOG_ERR_CAPACITY (8) or MOG_ERR_DEVICE_CHECK (5)."""
+        with _on(self.device, stream) as s:
+            return lib().mog_pages_status(C.byref(self._s), s)
 
 
 def kmeans_assign(x, cent, stream=None, with_recheck=False):

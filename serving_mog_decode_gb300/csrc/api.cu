@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <set>
@@ -885,4 +886,171 @@ extern "C" int mog_check_bounded_wait(int32_t limit, int32_t arrive, int32_t *sc
     CK(cudaStreamSynchronize(s));
     if (st & (1 << ST_TIMEOUT)) return MOG_ERR_TIMEOUT;
     return st ? MOG_ERR_DEVICE_CHECK : MOG_OK;
+}
+
+// ------------------------------------------------- caches of 8-bit rows, differential heads
+
+// Layout of a mog_cache; n positions of it are used.
+static int check_cache(const mog_cache *c, int64_t n) {
+    if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return MOG_ERR_INVALID_ARG;
+    if (c->type != MOG_CACHE_BF16 && c->type != MOG_CACHE_E4M3) return MOG_ERR_INVALID_ARG;
+    const bool e4 = c->type == MOG_CACHE_E4M3;
+    if (e4 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale)) return MOG_ERR_INVALID_ARG;
+    if (e4 && (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3)) return MOG_ERR_INVALID_ARG;
+    const int64_t m = e4 ? 15 : 7;
+    if (c->stride_n < MOG_D || ((c->stride_b | c->stride_h | c->stride_n) & m)) return MOG_ERR_SHAPE;
+    if (c->stride_b < 0 || c->stride_h < 0) return MOG_ERR_SHAPE;
+    if (c->block_table) {
+        if (c->page_rows < 16 || log2_exact(c->page_rows) < 0 || c->pages_per_seq <= 0 || c->n_pages <= 0)
+            return MOG_ERR_SHAPE;
+        if ((int64_t)c->pages_per_seq * c->page_rows < n) return MOG_ERR_SHAPE;
+    } else if (c->n_cap < n) {
+        return MOG_ERR_SHAPE;
+    }
+    return MOG_OK;
+}
+
+static int cache_scratch(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t n_max, int max_g, int maps,
+                         size_t *bytes) {
+    if (!bytes || batch <= 0 || h_kv <= 0 || h_q <= 0 || n_max <= 0) return MOG_ERR_INVALID_ARG;
+    if (d != MOG_D || h_q % h_kv != 0 || h_q / h_kv > max_g) return MOG_ERR_SHAPE;
+    // the kernels count tiles and heads in 32 bits
+    if ((int64_t)batch * h_q > INT32_MAX / 2 || (int64_t)batch * h_kv * ceil_div64(n_max, 64) > INT32_MAX / 2)
+        return MOG_ERR_SHAPE;
+    const int units = batch * h_kv;
+    *bytes = ((size_t)units + cache_splits(units, n_max)) * maps * (h_q / h_kv) * (MOG_D + 4) * sizeof(float);
+    return MOG_OK;
+}
+
+static int cache_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch, int32_t h_kv,
+                        int32_t h_q, const void *q_dev, const mog_diff_params *diff, void *out_dev,
+                        int32_t out_type, void *scratch_dev, size_t need, size_t scratch_bytes, void *stream,
+                        const char *where) {
+    const int st = check_cache(c, n_max);
+    if (st != MOG_OK) return st;
+    if (!lengths_dev || !q_dev || !out_dev || !scratch_dev) return MOG_ERR_INVALID_ARG;
+    if (out_type != MOG_OUT_F32 && out_type != MOG_OUT_BF16) return MOG_ERR_INVALID_ARG;
+    if (!aligned16(q_dev) || !aligned16(out_dev) || !aligned16(scratch_dev)) return MOG_ERR_INVALID_ARG;
+    if (scratch_bytes < need) return MOG_ERR_ARENA_TOO_SMALL;
+    const cudaError_t e = launch_cache_decode(c, lengths_dev, n_max, batch, h_kv, h_q / h_kv, q_dev, diff, out_type,
+                                              out_dev, static_cast<float *>(scratch_dev),
+                                              static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOG_OK : cuda_fail(e, where);
+}
+
+extern "C" int dense_decode8_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t n_max,
+                                           size_t *bytes) {
+    return cache_scratch(batch, h_kv, h_q, d, n_max, MOG_MAX_G, 1, bytes);
+}
+
+extern "C" int dense_decode8(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                             int32_t h_kv, int32_t h_q, int32_t d, const void *q_dev, void *out_dev,
+                             int32_t out_type, void *scratch_dev, size_t scratch_bytes, void *stream) {
+    size_t need = 0;
+    const int st = dense_decode8_scratch_bytes(batch, h_kv, h_q, d, n_max, &need);
+    if (st != MOG_OK) return st;
+    if (!c || c->type != MOG_CACHE_E4M3) return MOG_ERR_INVALID_ARG;
+    return cache_decode(c, lengths_dev, n_max, batch, h_kv, h_q, q_dev, nullptr, out_dev, out_type, scratch_dev, need,
+                        scratch_bytes, stream, "dense_decode8 launch");
+}
+
+extern "C" int mog_diff_decode_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t n_max,
+                                             size_t *bytes) {
+    return cache_scratch(batch, h_kv, h_q, d, n_max, MOG_MAX_G / 2, 2, bytes);
+}
+
+extern "C" int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                               int32_t h_kv, int32_t h_q, int32_t d, const void *q_dev,
+                               const mog_diff_params *params, void *out_dev, int32_t out_type, void *scratch_dev,
+                               size_t scratch_bytes, void *stream) {
+    size_t need = 0;
+    const int st = mog_diff_decode_scratch_bytes(batch, h_kv, h_q, d, n_max, &need);
+    if (st != MOG_OK) return st;
+    if (!params || !params->lam || !aligned16(params->lam) || !aligned16(params->gamma)) return MOG_ERR_INVALID_ARG;
+    if (params->lam_heads != 1 && params->lam_heads != h_q) return MOG_ERR_SHAPE;
+    if (!(params->eps > 0.f) || !std::isfinite(params->eps) || !std::isfinite(params->lambda_init))
+        return MOG_ERR_INVALID_ARG;
+    return cache_decode(c, lengths_dev, n_max, batch, h_kv, h_q, q_dev, params, out_dev, out_type, scratch_dev, need,
+                        scratch_bytes, stream, "mog_diff_decode launch");
+}
+
+extern "C" int mog_kv_store(const mog_cache *c, int32_t batch, int32_t h_kv, int32_t d, int32_t t_max,
+                            const int32_t *pos_dev, const int32_t *count_dev, const void *k_new_dev,
+                            const void *v_new_dev, int64_t new_b, int64_t new_t, int64_t new_h, void *stream) {
+    if (batch <= 0 || h_kv <= 0 || t_max <= 0) return MOG_ERR_INVALID_ARG;
+    if (d != MOG_D || batch > 65535) return MOG_ERR_SHAPE;
+    const int st = check_cache(c, 1);
+    if (st != MOG_OK) return st;
+    if (!pos_dev || !k_new_dev || !v_new_dev) return MOG_ERR_INVALID_ARG;
+    if (!aligned16(k_new_dev) || !aligned16(v_new_dev)) return MOG_ERR_INVALID_ARG;
+    if ((new_b | new_t | new_h) & 7) return MOG_ERR_SHAPE;
+    CK(launch_kv_store(c, batch, h_kv, t_max, pos_dev, count_dev, k_new_dev, v_new_dev, new_b, new_t, new_h,
+                       static_cast<cudaStream_t>(stream)));
+    return MOG_OK;
+}
+
+// ------------------------------------------------------------------------ shared pages
+
+extern "C" int mog_pages_work_bytes(int32_t n_pages, int32_t batch, size_t *bytes) {
+    if (!bytes || n_pages <= 0 || batch <= 0) return MOG_ERR_INVALID_ARG;
+    if (batch > 4096) return MOG_ERR_SHAPE;
+    *bytes = 4 * pages_work_ints(n_pages, batch);
+    return MOG_OK;
+}
+
+static int check_pages(const mog_pages *p) {
+    if (!p) return MOG_ERR_INVALID_ARG;
+    size_t need = 0;
+    const int st = mog_pages_work_bytes(p->n_pages, p->batch, &need);
+    if (st != MOG_OK) return st;
+    if (p->page_rows < 16 || log2_exact(p->page_rows) < 0 || p->pages_per_seq <= 0) return MOG_ERR_SHAPE;
+    if ((int64_t)p->pages_per_seq * p->page_rows > INT32_MAX || (int64_t)p->batch * p->pages_per_seq > INT32_MAX)
+        return MOG_ERR_SHAPE;
+    if (!p->block_table || !p->lengths || !p->refs || !p->work) return MOG_ERR_INVALID_ARG;
+    if (((uintptr_t)p->block_table | (uintptr_t)p->lengths | (uintptr_t)p->refs | (uintptr_t)p->work) & 3)
+        return MOG_ERR_INVALID_ARG;
+    if (p->work_bytes < need) return MOG_ERR_ARENA_TOO_SMALL;
+    if (p->n_pools < 0 || (p->n_pools > 0 && !p->pools)) return MOG_ERR_INVALID_ARG;
+    for (int i = 0; i < p->n_pools; ++i) {
+        const mog_page_pool &l = p->pools[i];
+        if (!l.base || !aligned16(l.base)) return MOG_ERR_INVALID_ARG;
+        if (l.page_bytes <= 0 || l.page_stride < l.page_bytes || ((l.page_bytes | l.page_stride) & 15)) return MOG_ERR_SHAPE;
+    }
+    return MOG_OK;
+}
+
+extern "C" int mog_pages_assign(const mog_pages *p, const int32_t *src_dev, void *stream) {
+    const int st = check_pages(p);
+    if (st != MOG_OK) return st;
+    if (!src_dev) return MOG_ERR_INVALID_ARG;
+    CK(launch_pages_assign(p, src_dev, static_cast<cudaStream_t>(stream)));
+    return MOG_OK;
+}
+
+extern "C" int mog_pages_grow(const mog_pages *p, const int32_t *n_new_dev, int32_t *pos_dev, int32_t *granted_dev,
+                              void *stream) {
+    const int st = check_pages(p);
+    if (st != MOG_OK) return st;
+    if (!n_new_dev || !pos_dev || !granted_dev) return MOG_ERR_INVALID_ARG;
+    CK(launch_pages_grow(p, n_new_dev, pos_dev, granted_dev, static_cast<cudaStream_t>(stream)));
+    return MOG_OK;
+}
+
+extern "C" int mog_pages_compact(const mog_pages *p, void *stream) {
+    const int st = check_pages(p);
+    if (st != MOG_OK) return st;
+    CK(launch_pages_compact(p, static_cast<cudaStream_t>(stream)));
+    return MOG_OK;
+}
+
+extern "C" int mog_pages_status(const mog_pages *p, void *stream) {
+    const int st = check_pages(p);
+    if (st != MOG_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int bits = 0;
+    CK(cudaMemcpyAsync(&bits, p->work, sizeof bits, cudaMemcpyDeviceToHost, s));
+    CK(cudaMemsetAsync(p->work, 0, sizeof bits, s));
+    CK(cudaStreamSynchronize(s));
+    if (bits & PAGES_BAD_INDEX) return MOG_ERR_DEVICE_CHECK;
+    return bits ? MOG_ERR_CAPACITY : MOG_OK;
 }

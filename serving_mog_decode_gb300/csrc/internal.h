@@ -144,6 +144,19 @@ cudaError_t launch_fm_resid(const Dev &dv, const uint16_t *q, int SW, cudaStream
 cudaError_t launch_dense(const mog_kv *kv, const int32_t *lengths, int n_max, int batch, int h_kv,
                          int G, const void *q, float *out, float *scratch, int splits,
                          cudaStream_t s);
+constexpr int MOG_MAX_POOLS = 64;  // page pools of one copy launch (further pools: further launches)
+int cache_splits(int units, int n_max);
+cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
+                                const void *q, const mog_diff_params *diff, int out_type, void *out, float *scratch,
+                                cudaStream_t s);
+cudaError_t launch_kv_store(const mog_cache *c, int batch, int h_kv, int t_max, const int32_t *pos,
+                            const int32_t *count, const void *kn, const void *vn, int64_t nb, int64_t nt,
+                            int64_t nh, cudaStream_t s);
+enum { PAGES_FULL = 1, PAGES_BAD_INDEX = 2 };  // status bits of a pages work buffer
+size_t pages_work_ints(int n_pages, int batch);
+cudaError_t launch_pages_assign(const mog_pages *p, const int32_t *src, cudaStream_t s);
+cudaError_t launch_pages_grow(const mog_pages *p, const int32_t *n_new, int32_t *pos, int32_t *granted, cudaStream_t s);
+cudaError_t launch_pages_compact(const mog_pages *p, cudaStream_t s);
 int log2_exact(int x);  // log2 of a power of two, -1 otherwise
 int dense_splits(int units, int n_max);
 cudaError_t dense_static_scratch(float **ptr, size_t *bytes);
