@@ -12,6 +12,7 @@ Sources: "Iceberg Attention: Sublinear Long-Context Decoding with Mixture-of-Gau
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -168,13 +169,15 @@ def _cache(K, V):
     if isinstance(K, (KV8, PagedKV8)):
         return K.cache, K.batch, K.h_kv, K.positions, K.device
     if isinstance(K, PagedKV):
-        kv, t = K.struct(), K.block_table
-        _check_table(t, K.K)
-        if K.V.device != K.device or K.K.shape[3] != 128 or K.K.shape[2 if K.heads_first else 1] != K.page_rows:
+        k, v, t, rows = K.K, K.V, K.block_table, K.page_rows
+        _check_table(t, k)
+        shape, st = k.shape, k.stride()
+        h, n = (1, 2) if K.heads_first else (2, 1)
+        if v.device != k.device or shape[3] != 128 or shape[n] != rows:
             raise ValueError("page pools must share a device and hold page_rows rows of 128")
-        c = Cache(0, 0, kv.k, kv.v, None, None, kv.stride_b, kv.stride_h, kv.stride_n, 0, 0, 0, kv.block_table,
-                  kv.page_rows, kv.pages_per_seq, K.K.shape[0])
-        return c, t.shape[0], K.h_kv, t.shape[1] * K.page_rows, K.device
+        per = t.shape[1]
+        return Cache(0, 0, k.data_ptr(), v.data_ptr(), None, None, st[0], st[h], st[n], 0, 0, 0, t.data_ptr(), rows,
+                     per, shape[0]), t.shape[0], shape[h], per * rows, k.device
     kv = _kv(K, V)
     if V.device != K.device or K.shape[3] != 128:
         raise ValueError("K and V must share a device and have rows of 128")
@@ -565,66 +568,81 @@ def dense_decode_noalloc(K, V, lengths_dev, n_max, q, out, stream=None):
     return out
 
 
-def _cache_decode(entry, K, V, lengths_dev, n_max, q, diff, out, scratch, stream):
-    torch = _torch()
-    c, B, H_kv, positions, dev = _cache(K, V)
-    if (q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != B or q.shape[2] != 128
-            or not q.is_contiguous() or q.device != dev):
-        raise ValueError("q must be a contiguous bf16 tensor [B, H_q, 128] on the cache's device")
-    _check_counts(lengths_dev, B, dev, "lengths_dev")
-    if not 1 <= n_max <= positions:
-        raise ValueError(f"n_max must be between 1 and the cache's {positions} positions")
-    H_q = q.shape[1]
-    need = C.c_size_t(0)
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=dev)
-        elif (out.dtype not in (torch.float32, torch.bfloat16) or out.shape != q.shape
-              or not out.is_contiguous() or out.device != dev):
-            raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape on q's device")
-        if scratch is None:
-            _check(getattr(lib(), entry + "_scratch_bytes")(B, H_kv, H_q, 128, n_max, C.byref(need)), entry)
-            scratch = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        elif scratch.device != dev or not scratch.is_contiguous():
-            raise ValueError("scratch must be a contiguous tensor on the cache's device")
-        args = [C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr()]
-        args += [C.byref(diff)] if diff is not None else []
-        _check(getattr(lib(), entry)(*args, out.data_ptr(), int(out.dtype == torch.bfloat16), scratch.data_ptr(),
-                                     scratch.numel() * scratch.element_size(), s), entry)
-    return out
-
-
-class _on:
-    """The device `dev` made current, and work and allocations on `stream` (its current stream
-    if None), for the length of a call; gives the cudaStream_t."""
+class _there:
+    """The device `dev` made current, and work and allocations on `stream` (dev's current
+    stream if None)."""
 
     def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
-        self.cms = []
+        torch = _torch()
+        self.cms = [torch.cuda.device(dev)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
-        torch = _torch()
-        if self.dev.index != torch.cuda.current_device():
-            self.cms.append(torch.cuda.device(self.dev))
-        if self.stream is not None:
-            self.cms.append(torch.cuda.stream(self.stream))
         for cm in self.cms:
             cm.__enter__()
-        return torch.cuda.current_stream(self.dev).cuda_stream
 
     def __exit__(self, *exc):
         for cm in reversed(self.cms):
             cm.__exit__(*exc)
 
 
-def _strides(t):
-    """Strides of a tensor's leading dims, 0 where there is only one entry."""
-    return [st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride())]
+def _here(dev, stream):
+    """The cudaStream_t for work on `dev` if that is the current device and no stream is asked
+    for; None if _there has to be entered first."""
+    c = _torch()._C  # (torch.cuda's wrappers of these two cost 2 us a call)
+    if stream is not None or dev.index != c._cuda_getDevice():
+        return None
+    return c._cuda_getCurrentRawStream(dev.index)
 
 
 def _check_counts(t, B, dev, name):
-    if t.dtype != _torch().int32 or t.shape != (B,) or not t.is_contiguous() or t.device != dev:
+    if t.dtype is not _torch().int32 or t.shape != (B,) or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name} must be a contiguous int32 tensor [{B}] on the cache's device")
+
+
+@functools.lru_cache(maxsize=512)
+def _scratch_bytes(entry, B, H_kv, H_q, n_max, dev_index) -> int:
+    need = C.c_size_t(0)
+    _check(getattr(lib(), entry + "_scratch_bytes")(B, H_kv, H_q, 128, n_max, C.byref(need)), entry)
+    return need.value
+
+
+def _cache_decode(entry, K, V, lengths_dev, n_max, q, diff, out, scratch, stream):
+    torch = _torch()
+    c, B, H_kv, positions, dev = _cache(K, V)
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return _cache_decode(entry, K, V, lengths_dev, n_max, q, diff, out, scratch, None)
+    shape = q.shape
+    if (q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[0] != B or shape[2] != 128
+            or not q.is_contiguous() or q.device != dev):
+        raise ValueError("q must be a contiguous bf16 tensor [B, H_q, 128] on the cache's device")
+    _check_counts(lengths_dev, B, dev, "lengths_dev")
+    if not 1 <= n_max <= positions:
+        raise ValueError(f"n_max must be between 1 and the cache's {positions} positions")
+    H_q = shape[1]
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
+    elif (out.dtype not in (torch.float32, torch.bfloat16) or out.shape != shape or not out.is_contiguous()
+          or out.device != dev):
+        raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape on q's device")
+    if scratch is None:
+        nbytes = _scratch_bytes(entry, B, H_kv, H_q, n_max, dev.index)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif scratch.device != dev or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous tensor on the cache's device")
+    else:
+        nbytes = scratch.numel() * scratch.element_size()
+    bf = out.dtype is torch.bfloat16
+    if diff is None:
+        rc = lib().dense_decode8(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
+                                 out.data_ptr(), bf, scratch.data_ptr(), nbytes, s)
+    else:
+        rc = lib().mog_diff_decode(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
+                                   C.byref(diff), out.data_ptr(), bf, scratch.data_ptr(), nbytes, s)
+    if rc:
+        _check(rc, entry)
+    return out
 
 
 def diff_decode(K, V, lengths_dev, n_max, q, lam, lambda_init, gamma=None, eps=1e-5, out=None, scratch=None,
@@ -648,17 +666,16 @@ def diff_decode(K, V, lengths_dev, n_max, q, lam, lambda_init, gamma=None, eps=1
     return _cache_decode("mog_diff_decode", K, V, lengths_dev, n_max, q, d, out, scratch, stream)
 
 
-def diff_scratch_bytes(batch, h_kv, h_q, n_max, d=128) -> int:
-    v = C.c_size_t(0)
-    _check(lib().mog_diff_decode_scratch_bytes(batch, h_kv, h_q, d, n_max, C.byref(v)),
-           "mog_diff_decode_scratch_bytes")
-    return v.value
+def diff_scratch_bytes(batch, h_kv, h_q, n_max) -> int:
+    """Bytes of diff_decode's scratch on the current device."""
+    return _scratch_bytes("mog_diff_decode", batch, h_kv, h_q, n_max, _torch().cuda.current_device()
+                          if _torch().cuda.is_available() else -1)
 
 
-def dense8_scratch_bytes(batch, h_kv, h_q, n_max, d=128) -> int:
-    v = C.c_size_t(0)
-    _check(lib().dense_decode8_scratch_bytes(batch, h_kv, h_q, d, n_max, C.byref(v)), "dense_decode8_scratch_bytes")
-    return v.value
+def dense8_scratch_bytes(batch, h_kv, h_q, n_max) -> int:
+    """Bytes of dense_decode's scratch over an e4m3 cache, on the current device."""
+    return _scratch_bytes("dense_decode8", batch, h_kv, h_q, n_max, _torch().cuda.current_device()
+                          if _torch().cuda.is_available() else -1)
 
 
 def kv_store(K, V, pos, count, k_new, v_new, stream=None):
@@ -669,22 +686,29 @@ def kv_store(K, V, pos, count, k_new, v_new, stream=None):
     to e4m3 with a power-of-two scale per row)."""
     torch = _torch()
     c, B, H_kv, _, dev = _cache(K, V)
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return kv_store(K, V, pos, count, k_new, v_new)
+    shape, sk, sv = k_new.shape, k_new.stride(), v_new.stride()
     for t in (k_new, v_new):
-        if (t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[0] != B or t.shape[2:] != (H_kv, 128)
-                or t.stride(3) != 1 or t.device != dev):
+        if (t.dtype is not torch.bfloat16 or len(shape) != 4 or t.shape != shape or shape[0] != B or shape[2] != H_kv
+                or shape[3] != 128 or t.device != dev):
             raise ValueError(f"k_new and v_new must be bf16 tensors [{B}, T, {H_kv}, 128] on the cache's device")
-    if k_new.shape != v_new.shape or _strides(k_new) != _strides(v_new):
-        raise ValueError("k_new and v_new must share shape and strides")
+    T = shape[1]
+    if 1 in shape:  # a dim of one entry has no stride that counts
+        sk, sv = ([x if n > 1 else 0 for n, x in zip(shape, st)] for st in (sk, sv))
+    if sk[3] != 1 or sk[:3] != sv[:3] or sv[3] != 1:
+        raise ValueError("k_new and v_new must share strides, the last dim contiguous")
     _check_counts(pos, B, dev, "pos")
     if count is not None:
         _check_counts(count, B, dev, "count")
-    T = k_new.shape[1]
     if T == 0:
         return
-    with _on(dev, stream) as s:
-        _check(lib().mog_kv_store(C.byref(c), B, H_kv, 128, T, pos.data_ptr(),
-                                  None if count is None else count.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                                  *_strides(k_new), s), "mog_kv_store")
+    rc = lib().mog_kv_store(C.byref(c), B, H_kv, 128, T, pos.data_ptr(), None if count is None else count.data_ptr(),
+                            k_new.data_ptr(), v_new.data_ptr(), sk[0], sk[1], sk[2], s)
+    if rc:
+        _check(rc, "mog_kv_store")
 
 
 class PagePool:
@@ -742,34 +766,46 @@ class PagePool:
         return PagedKV8(self.K[layer], self.V[layer], self.k_scale[layer], self.v_scale[layer], self.block_table,
                         self.page_rows, self.heads_first)
 
+    def _call(self, fn, stream, *args):
+        s = _here(self.device, stream)
+        if s is None:
+            with _there(self.device, stream):
+                return self._call(fn, None, *args)
+        rc = getattr(lib(), fn)(C.byref(self._s), *args, s)
+        if rc:
+            _check(rc, fn)
+
     def assign(self, src, stream=None):
         """Fork, reorder and free (mog_pages_assign): sequence b takes the pages and length that
         src[b] had (b: as it is; -1: none).  src: int32 [batch] on the device."""
         _check_counts(src, self.batch, self.device, "src")
-        with _on(self.device, stream) as s:
-            _check(lib().mog_pages_assign(C.byref(self._s), src.data_ptr(), s), "mog_pages_assign")
+        self._call("mog_pages_assign", stream, src.data_ptr())
 
     def grow(self, n_new, stream=None):
         """Room for n_new[b] more tokens of every sequence (mog_pages_grow); a shared last page
         becomes private.  -> (pos, granted) int32 [batch]: where kv_store puts the new rows, and
         how many (0 everywhere if there was no room: see status())."""
         _check_counts(n_new, self.batch, self.device, "n_new")
-        with _on(self.device, stream) as s:
-            both = _torch().empty((2, self.batch), dtype=_torch().int32, device=self.device)
-            _check(lib().mog_pages_grow(C.byref(self._s), n_new.data_ptr(), both.data_ptr(),
-                                        both.data_ptr() + 4 * self.batch, s), "mog_pages_grow")
-        return both[0], both[1]
+        if stream is not None:
+            with _there(self.device, stream):
+                return self.grow(n_new)
+        both = n_new.new_empty((2, self.batch))
+        at = both.data_ptr()
+        self._call("mog_pages_grow", None, n_new.data_ptr(), at, at + 4 * self.batch)
+        return both.unbind(0)
 
     def compact(self, stream=None):
         """Move the pages in use to the front of the pools (mog_pages_compact)."""
-        with _on(self.device, stream) as s:
-            _check(lib().mog_pages_compact(C.byref(self._s), s), "mog_pages_compact")
+        self._call("mog_pages_compact", stream)
 
     def status(self, stream=None) -> int:
         """Wait for the stream, then read and clear the status of the calls so far: MOG_OK,
         MOG_ERR_CAPACITY (8) or MOG_ERR_DEVICE_CHECK (5)."""
-        with _on(self.device, stream) as s:
-            return lib().mog_pages_status(C.byref(self._s), s)
+        s = _here(self.device, stream)
+        if s is None:
+            with _there(self.device, stream):
+                return self.status()
+        return lib().mog_pages_status(C.byref(self._s), s)
 
 
 def kmeans_assign(x, cent, stream=None, with_recheck=False):

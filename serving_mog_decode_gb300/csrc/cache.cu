@@ -33,20 +33,24 @@
 
 namespace mog {
 
-constexpr int CT_ROWS = 64;
-constexpr int CT_THREADS = 128;
+constexpr int CT_WARPS = 4;
+constexpr int CT_THREADS = 32 * CT_WARPS;
 constexpr float W_SCALE = 16384.f;  // 2^14: scale of fp16 weights
 
-template <bool E4M3, int NB>
+// A tile is copied by the whole CTA, 2 KB of neighbouring rows per instruction, and each
+// warp consumes BLK blocks of 16 of its rows.  Stages are aligned to 128 bytes: 16 bytes off,
+// the copies of the same kernel were 5% slower (1M e4m3 tokens, 8 heads: 329 against 316 us).
+template <bool E4M3>
 struct Tile {
+    static constexpr int BLK = E4M3 ? 2 : 1;              // blocks of 16 rows per warp
+    static constexpr int WROWS = 16 * BLK;                // rows per warp
+    static constexpr int ROWS = CT_WARPS * WROWS;
     static constexpr int ROW = E4M3 ? MOG_D : 2 * MOG_D;  // bytes
-    static constexpr int KV = CT_ROWS * ROW;              // bytes of the K or V tile
-    static constexpr int AUX = 2 * KV;                    // row masks, then K and V scales
-    static constexpr int RAW = AUX + CT_ROWS * 4 * (E4M3 ? 3 : 1);
-    static constexpr int XCH = 2 * 32 * 36 * 4 * NB;  // two warps' states (the exchange at a unit's end)
-    static constexpr int STAGE = RAW > XCH ? RAW : XCH;
-    // e4m3: 16.75 KB a stage, four of them and three CTAs per SM; bf16: 32.3 KB, two
-    static constexpr int STAGES = E4M3 ? 4 : 2;
+    static constexpr int KV = ROWS * ROW;                 // bytes of the K or V tile: 16 KB
+    static constexpr int AUX = 2 * KV;                    // K scales, V scales
+    static constexpr int MASK = AUX + (E4M3 ? 2 * ROWS * 4 : 0);  // bit per row
+    static constexpr int STAGE = MASK + 128;              // rows stay aligned to 128 bytes
+    static constexpr int STAGES = 2;  // 3 CTAs per SM: 96 KB in flight while 96 KB are consumed
     static constexpr int SMEM = STAGES * STAGE;
 };
 
@@ -71,25 +75,28 @@ struct DiffArgs {
     float lambda_init, eps;
 };
 
+template <int ROWS>
 __device__ __forceinline__ int seq_tiles(const CacheArgs &a, int b) {
     const int n = min(max(a.lengths[b], 0), a.n_max);
-    return (n + CT_ROWS - 1) / CT_ROWS;
+    return (int)(((unsigned)n + ROWS - 1) / ROWS);
 }
 
 // Tiles of the whole batch, times h_kv: called by a full warp.
+template <int ROWS>
 __device__ __forceinline__ int total_tiles(const CacheArgs &a) {
     int s = 0;
-    for (int b = threadIdx.x & 31; b < a.batch; b += 32) s += seq_tiles(a, b);
+    for (int b = threadIdx.x & 31; b < a.batch; b += 32) s += seq_tiles<ROWS>(a, b);
     return warp_isum(s) * a.h_kv;
 }
 
 // Sequence holding tile `t` of the list and the list position of its first tile (called by
 // a full warp; t < total).
+template <int ROWS>
 __device__ __forceinline__ void find_seq(const CacheArgs &a, int t, int &b, int &first) {
     const int lane = threadIdx.x & 31;
     int base = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const int mine = b0 + lane < a.batch ? seq_tiles(a, b0 + lane) * a.h_kv : 0;
+        const int mine = b0 + lane < a.batch ? seq_tiles<ROWS>(a, b0 + lane) * a.h_kv : 0;
         int end = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -110,11 +117,12 @@ __device__ __forceinline__ void find_seq(const CacheArgs &a, int t, int &b, int 
 }
 
 // A place in the tile list.
+template <int ROWS>
 struct Cursor {
     int b, h, t, nt, n;  // sequence, head, tile, tiles of the sequence, its length
     __device__ __forceinline__ void seek(const CacheArgs &a, int tile) {
         int first;
-        find_seq(a, tile, b, first);
+        find_seq<ROWS>(a, tile, b, first);
         load(a);
         const int r = tile - first;
         h = nt > 0 ? r / nt : 0;
@@ -122,7 +130,7 @@ struct Cursor {
     }
     __device__ __forceinline__ void load(const CacheArgs &a) {
         n = b < a.batch ? min(max(a.lengths[b], 0), a.n_max) : 0;
-        nt = (n + CT_ROWS - 1) / CT_ROWS;
+        nt = (int)(((unsigned)n + ROWS - 1) / ROWS);
     }
     __device__ __forceinline__ bool last() const { return t + 1 == nt; }
     __device__ __forceinline__ void next(const CacheArgs &a) {
@@ -141,56 +149,65 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int src
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes));
 }
 
-// Shared-memory position of a 16-byte chunk of a 128-byte e4m3 row, conflict-free for the
-// readers: K is read by rows r, r+1 and chunks t (t < 4), V by rows 0, 2, 4, 6 (+1, +8) and
-// two neighbouring chunks.
-__device__ __forceinline__ uint32_t swz8_k(int row, int ch) {
-    return (uint32_t)(row * MOG_D + ((ch ^ ((row & 1) << 2)) << 4));
+// Shared-memory position of a 16-byte chunk of a row, conflict-free for the readers.  e4m3
+// (128-byte rows): K is read at rows r, r+1 and chunks t (t < 4), V at rows 0, 2, 4, 6 (+1,
+// +8) and two neighbouring chunks.  bf16 (256-byte rows): ldmatrix.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t swz_k(int row, int ch) {
+    return E4M3 ? (uint32_t)(row * MOG_D + ((ch ^ ((row & 1) << 2)) << 4)) : swz(row, ch);
 }
-__device__ __forceinline__ uint32_t swz8_v(int row, int ch) {
-    return (uint32_t)(row * MOG_D + ((ch ^ (row & 6)) << 4));
+template <bool E4M3>
+__device__ __forceinline__ uint32_t swz_v(int row, int ch) {
+    return E4M3 ? (uint32_t)(row * MOG_D + ((ch ^ (row & 6)) << 4)) : swz(row, ch);
 }
 
-// Pages of the four 16-row groups of a tile, loaded one tile ahead of their use (unchecked:
-// a check here would wait for the load).
-template <bool PAGED>
-__device__ __forceinline__ void tile_pages(const CacheArgs &a, const Cursor &c, int (&pg)[4]) {
+// Page of the tile's 16-row group `lane`, loaded one tile ahead of its use (unchecked: a
+// check here would wait for the load).
+template <bool E4M3, bool PAGED>
+__device__ __forceinline__ void tile_page(const CacheArgs &a, const Cursor<Tile<E4M3>::ROWS> &c, int &pg) {
     if constexpr (PAGED) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = c.t * CT_ROWS + 16 * i;
-            pg[i] = row < c.n ? __ldg(a.bt + (int64_t)c.b * a.pps + (row >> a.pshift)) : -1;
-        }
+        using T = Tile<E4M3>;
+        const int lane = threadIdx.x & 31, row = c.t * T::ROWS + 16 * lane;
+        pg = -1;
+        if (lane < T::ROWS / 16 && row < c.n) pg = __ldg(a.bt + (int64_t)c.b * a.pps + (row >> a.pshift));
     }
 }
 
-// Start the copies of one tile.  Rows behind the sequence's end or in no page are zero and
+// Start the copies of a tile.  Rows behind the sequence's end or in no page are zero and
 // masked; they are never read.
-template <bool E4M3, int NB, bool PAGED>
-__device__ __forceinline__ void issue(const CacheArgs &a, const Cursor &c, const int (&pg)[4], uint8_t *stage) {
-    using T = Tile<E4M3, NB>;
-    constexpr int CH = T::ROW / 16;             // chunks per row
-    constexpr int STEP = CT_THREADS / CH;       // rows per pass
-    const uint32_t sk = smem_u32(stage), sv = sk + T::KV;
-    uint32_t *mask = reinterpret_cast<uint32_t *>(stage + T::AUX);
-    const int ch = threadIdx.x % CH, r0 = threadIdx.x / CH;
+template <bool E4M3, bool PAGED>
+__device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<Tile<E4M3>::ROWS> &c, int pg, uint32_t stage) {
+    using T = Tile<E4M3>;
+    constexpr int CH = T::ROW / 16;        // chunks per row
+    constexpr int RP = CT_THREADS / CH;    // rows per instruction: 16 or 8
+    const int tid = threadIdx.x, lane = tid & 31, ch = tid % CH, r0 = tid / CH;
+    const int first = c.t * T::ROWS, left = c.n - first;  // rows of the sequence from here on
     const int pmask = (1 << a.pshift) - 1;
+    const int64_t head = c.h * a.sh + r0 * a.sn + ch * 16 + (PAGED ? 0 : c.b * a.sb);
 #pragma unroll
-    for (int i = 0; i < CT_ROWS / STEP; ++i) {
-        const int r = r0 + STEP * i, pos = c.t * CT_ROWS + r;
-        const int page = PAGED ? pg[(STEP * i) / 16] : c.b;
-        const bool ok = pos < c.n && (!PAGED || (unsigned)page < (unsigned)a.n_pages);
-        const int64_t slab = ok ? page : 0, row = ok ? (PAGED ? (pos & pmask) : pos) : 0;
-        const int64_t off = slab * a.sb + c.h * a.sh + row * a.sn + ch * 16;
+    for (int i = 0; i < T::ROWS / RP; ++i) {
+        const int r = r0 + RP * i;
+        const int page = PAGED ? __shfl_sync(0xffffffffu, pg, RP * i / 16) : 0;
+        const bool ok = r < left && (!PAGED || (unsigned)page < (unsigned)a.n_pages);
+        int64_t off = head + (int64_t)(PAGED ? (first + RP * i) & pmask : first + RP * i) * a.sn;
+        if (PAGED) off += page * a.sb;
+        off = ok ? off : 0;
         const int bytes = ok ? 16 : 0;
-        cp_async16(sk + (E4M3 ? swz8_k(r, ch) : swz(r, ch)), a.K + off, bytes);
-        cp_async16(sv + (E4M3 ? swz8_v(r, ch) : swz(r, ch)), a.V + off, bytes);
-        if (ch == 0) mask[r] = ok;
-        if (E4M3 && ch < 2) {
-            const int64_t so = slab * a.ssb + c.h * a.ssh + row * a.ssn;
-            cp_async4(smem_u32(mask + (1 + ch) * CT_ROWS + r), (ch ? a.vs : a.ks) + so, ok ? 4 : 0);
-        }
+        cp_async16(stage + swz_k<E4M3>(r, ch), a.K + off, bytes);
+        cp_async16(stage + T::KV + swz_v<E4M3>(r, ch), a.V + off, bytes);
     }
+    // thread r: row r's scales and whether it is there
+    if (tid >= T::ROWS) return;
+    const int page = PAGED ? __shfl_sync(0xffffffffu, pg, tid / 16) : c.b;
+    const bool ok = tid < left && (!PAGED || (unsigned)page < (unsigned)a.n_pages);
+    if (E4M3) {
+        const int64_t row = PAGED ? (first + tid) & pmask : first + tid;
+        const int64_t so = ok ? page * a.ssb + c.h * a.ssh + row * a.ssn : 0;
+        cp_async4(stage + T::AUX + 4 * tid, a.ks + so, ok ? 4 : 0);
+        cp_async4(stage + T::AUX + 4 * (T::ROWS + tid), a.vs + so, ok ? 4 : 0);
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + T::MASK + 4 * (tid >> 5)), "r"(mask) : "memory");
 }
 
 // Column -> (map, head) of a differential block layout, (0, column) otherwise.
@@ -320,64 +337,98 @@ __device__ __forceinline__ uint32_t part16(float &x, float &y) {
     return h;
 }
 
-// This warp's 16 rows of a tile.
-template <bool E4M3, int NB, bool DIFF, int PARTS>
-__device__ __forceinline__ void compute(State<NB> &st, const QF<NB> &qf, const uint8_t *stage) {
-    using T = Tile<E4M3, NB>;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, mat = lane >> 3, r8 = lane & 7;
-    const int rb = (threadIdx.x >> 5) * 16;
-    const uint32_t sk = smem_u32(stage), sv = sk + T::KV;
-    const uint32_t *mask = reinterpret_cast<const uint32_t *>(stage + T::AUX);
-    const float *sc = reinterpret_cast<const float *>(mask + CT_ROWS);
-    const int rA = rb + g, rB = rA + 8;
+__device__ __forceinline__ float lds4(uint32_t addr) {
+    float r;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr));
+    return r;
+}
 
-    // logits: rows rA (0, 1) and rB (2, 3) of columns 2t, 2t+1.  The two maps of a
+// This warp's rows of a tile.
+//
+// The products of one tile start from zero on the tensor cores, which truncate their sums,
+// and join the running sum rounded to nearest (the same fused multiply-add that rescales
+// it): summing a 1M-token sequence on the tensor cores alone drifted by 1.1e-5.
+template <bool E4M3, int NB, bool DIFF, int PARTS>
+__device__ __forceinline__ void compute(State<NB> &st, const QF<NB> &qf, uint32_t stage) {
+    using T = Tile<E4M3>;
+    constexpr int BLK = T::BLK;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, mat = lane >> 3, r8 = lane & 7;
+    const int wr = (threadIdx.x >> 5) * T::WROWS;  // this warp's first row (a multiple of 16)
+    const uint32_t sk = stage + wr * T::ROW, sv = sk + T::KV, sc = stage + T::AUX + 4 * wr;
+    constexpr uint32_t ALL = (uint32_t)((1ull << T::WROWS) - 1);
+    const uint32_t rows = (__float_as_uint(lds4(stage + T::MASK + 4 * (wr / 32))) >> (wr % 32)) & ALL;
+    if (rows == 0) return;
+
+    // logits: rows g (0, 1) and g+8 (2, 3) of columns 2t, 2t+1.  The two maps of a
     // differential block accumulate apart (half j of the dimensions is map j).
-    float s[NB][4], s2[4];
+    float s[BLK][NB][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int blk = 0; blk < BLK; ++blk) {
+        float s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) s[nb][e] = 0.f;
-        s2[e] = 0.f;
-    }
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        uint4 wa, wb;
-        if (E4M3) {
-            wa = lds16(sk + swz8_k(rA, t + 4 * j));
-            wb = lds16(sk + swz8_k(rB, t + 4 * j));
-        }
+            for (int e = 0; e < 4; ++e) s[blk][nb][e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int ks = 4 * j + w;
-            uint32_t a[4];
+        for (int j = 0; j < 2; ++j) {
+            uint4 wa, wb;
             if (E4M3) {
-                widen(word(wa, w), a[0], a[2]);
-                widen(word(wb, w), a[1], a[3]);
-            } else {
-                ldsm_x4(sk + swz(rb + (mat & 1) * 8 + r8, 2 * ks + (mat >> 1)), a[0], a[1], a[2], a[3]);
+                wa = lds16(sk + swz_k<E4M3>(16 * blk + g, t + 4 * j));
+                wb = lds16(sk + swz_k<E4M3>(16 * blk + g + 8, t + 4 * j));
             }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int ks = 4 * j + w;
+                uint32_t a[4];
+                if (E4M3) {
+                    widen(word(wa, w), a[0], a[2]);
+                    widen(word(wb, w), a[1], a[3]);
+                } else {
+                    ldsm_x4(sk + swz_k<E4M3>((mat & 1) * 8 + r8, 2 * ks + (mat >> 1)), a[0], a[1], a[2], a[3]);
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    if (DIFF && NB == 2 && nb != j) continue;
+                    if (DIFF && NB == 1 && j == 1) mma_t<E4M3>(s2, a, qf.b[nb][ks][0], qf.b[nb][ks][1]);
+                    else mma_t<E4M3>(s[blk][nb], a, qf.b[nb][ks][0], qf.b[nb][ks][1]);
+                }
+            }
+        }
+        if (DIFF && NB == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[blk][0][e] = t >= 2 ? s2[e] : s[blk][0][e];
+        }
+    }
+
+    // log2-domain logits
+#pragma unroll
+    for (int blk = 0; blk < BLK; ++blk) {
+        float kA = 1.f, kB = 1.f;
+        if (E4M3) kA = lds4(sc + 4 * (16 * blk + g)), kB = lds4(sc + 4 * (16 * blk + g + 8));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            s[blk][nb][0] *= kA * qf.f[nb][0];
+            s[blk][nb][1] *= kA * qf.f[nb][1];
+            s[blk][nb][2] *= kB * qf.f[nb][0];
+            s[blk][nb][3] *= kB * qf.f[nb][1];
+        }
+    }
+    if (rows != ALL) {  // the sequence's end, or a page that is none
+#pragma unroll
+        for (int blk = 0; blk < BLK; ++blk) {
+            const bool okA = (rows >> (16 * blk + g)) & 1u, okB = (rows >> (16 * blk + g + 8)) & 1u;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                if (DIFF && NB == 2 && nb != j) continue;
-                if (DIFF && NB == 1 && j == 1) mma_t<E4M3>(s2, a, qf.b[nb][ks][0], qf.b[nb][ks][1]);
-                else mma_t<E4M3>(s[nb], a, qf.b[nb][ks][0], qf.b[nb][ks][1]);
+                if (!okA) s[blk][nb][0] = s[blk][nb][1] = -INFINITY;
+                if (!okB) s[blk][nb][2] = s[blk][nb][3] = -INFINITY;
             }
         }
     }
-    if (DIFF && NB == 1 && t >= 2) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[0][e] = s2[e];
-    }
-
-    const bool okA = mask[rA] != 0, okB = mask[rB] != 0;
-    float kA = 1.f, kB = 1.f, vA = 1.f, vB = 1.f;
+    float inv = 0.f;
     if (E4M3) {
-        kA = sc[rA], kB = sc[rB];
-        vA = sc[CT_ROWS + rA], vB = sc[CT_ROWS + rB];
-        const float vt = fmaxf(fabsf(vA), fabsf(vB));
-        if (__any_sync(0xffffffffu, vt > st.vr)) {  // a larger value scale: new unit
-            const float vr = pow2f(min(max((__float_as_int(warp_max(vt)) >> 23) - 126, -100), 127));
+        const float mine = fabsf(lds4(sc + 4 * (T::ROWS + lane)));
+        if (__any_sync(0xffffffffu, mine > st.vr)) {  // a larger value scale: new unit
+            const float vr = pow2f(min(max((__float_as_int(warp_max(mine)) >> 23) - 126, -100), 127));
             const float f = st.vr / vr;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -387,153 +438,180 @@ __device__ __forceinline__ void compute(State<NB> &st, const QF<NB> &qf, const u
                     for (int e = 0; e < 4; ++e) st.o[nb][i][e] *= f;
             st.vr = vr;
         }
-        // a row's weight factor; a batch of rows whose scales are all 0 has no unit yet
-        const float inv = st.vr > 0.f ? W_SCALE / st.vr : 0.f;
-        vA *= inv, vB *= inv;
+        inv = st.vr > 0.f ? W_SCALE / st.vr : 0.f;  // (rows whose scales are all 0 have no unit yet)
     }
-    uint32_t pb[NB][PARTS][2];
+    uint32_t pb[BLK][NB][PARTS][2];
+    float al[NB][2];
+    float vA[BLK], vB[BLK];
+    if (E4M3) {
+#pragma unroll
+        for (int blk = 0; blk < BLK; ++blk) {
+            vA[blk] = lds4(sc + 4 * (T::ROWS + 16 * blk + g)) * inv;
+            vB[blk] = lds4(sc + 4 * (T::ROWS + 16 * blk + g + 8)) * inv;
+        }
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        const float f0 = qf.f[nb][0], f1 = qf.f[nb][1];
-        const float s0 = okA ? s[nb][0] * (kA * f0) : -INFINITY, s1 = okA ? s[nb][1] * (kA * f1) : -INFINITY;
-        const float s2_ = okB ? s[nb][2] * (kB * f0) : -INFINITY, s3 = okB ? s[nb][3] * (kB * f1) : -INFINITY;
-        float mx0 = fmaxf(s0, s2_), mx1 = fmaxf(s1, s3);
+        float sh[2];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(s[0][nb][e], s[0][nb][e + 2]);
+            if (BLK == 2) mx = fmaxf(mx, fmaxf(s[BLK - 1][nb][e], s[BLK - 1][nb][e + 2]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // the shift: 0 until a row has been seen, so that no infinities are subtracted
+            const float mn = fmaxf(st.m[nb][e], mx);
+            sh[e] = mn == -INFINITY ? 0.f : mn;
+            al[nb][e] = ex2(st.m[nb][e] - sh[e]);
+            st.m[nb][e] = mn;
+            st.l[nb][e] *= al[nb][e];
         }
-        // the shift: 0 until a row has been seen, so that no infinities are subtracted
-        const float mn0 = fmaxf(st.m[nb][0], mx0), mn1 = fmaxf(st.m[nb][1], mx1);
-        const float sh0 = mn0 == -INFINITY ? 0.f : mn0, sh1 = mn1 == -INFINITY ? 0.f : mn1;
-        const float al0 = ex2(st.m[nb][0] - sh0), al1 = ex2(st.m[nb][1] - sh1);
-        st.m[nb][0] = mn0;
-        st.m[nb][1] = mn1;
-        float p0 = ex2(s0 - sh0), p1 = ex2(s1 - sh1), p2 = ex2(s2_ - sh0), p3 = ex2(s3 - sh1);
-        st.l[nb][0] = st.l[nb][0] * al0 + (p0 + p2);
-        st.l[nb][1] = st.l[nb][1] * al1 + (p1 + p3);
-        if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                st.o[nb][i][0] *= al0;
-                st.o[nb][i][1] *= al1;
-                st.o[nb][i][2] *= al0;
-                st.o[nb][i][3] *= al1;
+        for (int blk = 0; blk < BLK; ++blk) {
+            float p0 = ex2(s[blk][nb][0] - sh[0]), p1 = ex2(s[blk][nb][1] - sh[1]);
+            float p2 = ex2(s[blk][nb][2] - sh[0]), p3 = ex2(s[blk][nb][3] - sh[1]);
+            st.l[nb][0] += p0 + p2;
+            st.l[nb][1] += p1 + p3;
+            if (E4M3) p0 *= vA[blk], p1 *= vA[blk], p2 *= vB[blk], p3 *= vB[blk];
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                pb[blk][nb][i][0] = movmatrix_t(part16<E4M3>(p0, p1));
+                pb[blk][nb][i][1] = movmatrix_t(part16<E4M3>(p2, p3));
             }
-        }
-        if (E4M3) p0 *= vA, p1 *= vA, p2 *= vB, p3 *= vB;
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i) {
-            pb[nb][i][0] = movmatrix_t(part16<E4M3>(p0, p1));
-            pb[nb][i][1] = movmatrix_t(part16<E4M3>(p2, p3));
         }
     }
 
-    // O^T += V^T P^T
+    // O^T = O^T diag(al) + V^T P^T, 16 dimensions at a time; lowest parts first
     if (E4M3) {
-        // rows 2t, 2t+1, 2t+8, 2t+9, dimensions 16g .. 16g+15: word w holds dimensions
-        // 16g + 4w .. +3, of tiles 2w (+0: row g of the fragment, +1: row g+8) and 2w+1
-        const uint4 x0 = lds16(sv + swz8_v(rb + 2 * t, g)), y0 = lds16(sv + swz8_v(rb + 2 * t + 1, g));
-        const uint4 x1 = lds16(sv + swz8_v(rb + 2 * t + 8, g)), y1 = lds16(sv + swz8_v(rb + 2 * t + 9, g));
+        // rows 2t, 2t+1, 2t+8, 2t+9 of a block, dimensions 16g .. 16g+15: word w holds
+        // dimensions 16g + 4w .. +3, of tiles 2w (+0: row g of the fragment, +1: row g+8), 2w+1
+        uint4 x[BLK][4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int blk = 0; blk < BLK; ++blk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[blk][i] = lds16(sv + swz_v<E4M3>(16 * blk + 2 * t + (i & 1) + 8 * (i >> 1), g));
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const uint32_t sel = hf ? 0x7362u : 0x5140u;
-                uint32_t a[4];
-                widen(__byte_perm(word(x0, w), word(y0, w), sel), a[0], a[1]);
-                widen(__byte_perm(word(x1, w), word(y1, w), sel), a[2], a[3]);
+                float d[NB][4] = {};
+#pragma unroll
+                for (int blk = 0; blk < BLK; ++blk) {
+                    uint32_t a[4];
+                    widen(__byte_perm(word(x[blk][0], w), word(x[blk][1], w), sel), a[0], a[1]);
+                    widen(__byte_perm(word(x[blk][2], w), word(x[blk][3], w), sel), a[2], a[3]);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int i = PARTS - 1; i >= 0; --i) mma_f16(d[nb], a, pb[blk][nb][i][0], pb[blk][nb][i][1]);
+                }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) mma_f16(st.o[nb][2 * w + hf], a, pb[nb][i][0], pb[nb][i][1]);
+                    for (int e = 0; e < 4; ++e)
+                        st.o[nb][2 * w + hf][e] = fmaf(st.o[nb][2 * w + hf][e], al[nb][e & 1], d[nb][e]);
             }
-        }
     } else {
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             uint32_t a[4];
-            ldsm_x4_t(sv + swz(rb + (mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0], a[1], a[2], a[3]);
+            ldsm_x4_t(sv + swz_v<E4M3>((mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb) {
+                float d[4] = {};
 #pragma unroll
-                for (int i = 0; i < PARTS; ++i) mma_bf16(st.o[nb][mt], a, pb[nb][i][0], pb[nb][i][1]);
+                for (int i = PARTS - 1; i >= 0; --i) mma_bf16(d, a, pb[0][nb][i][0], pb[0][nb][i][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st.o[nb][mt][e] = fmaf(st.o[nb][mt][e], al[nb][e & 1], d[e]);
+            }
         }
-    }
-}
-
-// Fold the state that another warp left in shared memory (word i of lane l at i*32 + l).
-template <int NB>
-__device__ __forceinline__ void state_put(const State<NB> &st, float *x) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        float *p = x + nb * 36 * 32 + lane;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) p[i * 32] = st.o[nb][i >> 2][i & 3];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            p[(32 + e) * 32] = st.m[nb][e];
-            p[(34 + e) * 32] = st.l[nb][e];
-        }
-    }
-}
-template <int NB>
-__device__ __forceinline__ void state_fold(State<NB> &st, const float *x) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const float *p = x + nb * 36 * 32 + lane;
-        float mine[2], his[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float m2 = p[(32 + e) * 32], mn = fmaxf(st.m[nb][e], m2);
-            const float sh = mn == -INFINITY ? 0.f : mn;
-            mine[e] = ex2(st.m[nb][e] - sh);
-            his[e] = ex2(m2 - sh);
-            st.m[nb][e] = mn;
-            st.l[nb][e] = st.l[nb][e] * mine[e] + p[(34 + e) * 32] * his[e];
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            st.o[nb][i >> 2][i & 3] = st.o[nb][i >> 2][i & 3] * mine[i & 1] + p[i * 32] * his[i & 1];
     }
 }
 
 // A unit's end: the four warps' states become one partial in `dst` ([columns][PART_W]).
-// `x` is a stage that nothing reads or fills any more.  Called by the whole CTA.
-template <bool E4M3, int NB, bool DIFF>
-__device__ __forceinline__ void flush(State<NB> &st, float *x, const CacheArgs &a, float *dst) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    constexpr int SW = 36 * 32 * NB;
-    if (E4M3) {  // to the values' own unit
-        const float u = st.vr / W_SCALE;
+// Accumulators pass through the stage that has just been consumed (word i of lane l at
+// i*32 + l), maxima and sums through `ex`.  Called by the whole CTA.
+template <int NB>
+struct Exchange {
+    float m[CT_WARPS][NB * 8], l[CT_WARPS][NB * 8];
+};
+template <int NB>
+__device__ __forceinline__ void state_put(const State<NB> &st, float *x, Exchange<NB> &ex) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[(nb * 32 + i) * 32 + lane] = st.o[nb][i >> 2][i & 3];
+        if (lane < 4) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                ex.m[w][nb * 8 + 2 * lane + e] = st.m[nb][e];
+                ex.l[w][nb * 8 + 2 * lane + e] = st.l[nb][e];
+            }
+        }
+    }
+}
+template <int NB>
+__device__ __forceinline__ void state_fold(State<NB> &st, const float *x, const Exchange<NB> &ex, int from) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        float mine[2], his[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float m2 = ex.m[from][nb * 8 + 2 * t + e], mn = fmaxf(st.m[nb][e], m2);
+            const float sh = mn == -INFINITY ? 0.f : mn;
+            mine[e] = ex2(st.m[nb][e] - sh);
+            his[e] = ex2(m2 - sh);
+            st.m[nb][e] = mn;
+            st.l[nb][e] = st.l[nb][e] * mine[e] + ex.l[from][nb * 8 + 2 * t + e] * his[e];
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            st.o[nb][i >> 2][i & 3] = st.o[nb][i >> 2][i & 3] * mine[i & 1] + x[(nb * 32 + i) * 32 + lane] * his[i & 1];
+    }
+}
+
+template <bool E4M3, int NB, bool DIFF>
+__device__ __forceinline__ void flush(State<NB> &st, float *x, Exchange<NB> &ex, const CacheArgs &a, float *dst) {
+    using T = Tile<E4M3>;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int SW = 32 * 32 * NB;  // words of a warp's accumulators
+    static_assert(T::AUX >= 2 * SW * 4, "two states fit in a stage");
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        if (E4M3) {  // to the values' own unit
+            const float u = st.vr / W_SCALE;
 #pragma unroll
             for (int i = 0; i < 32; ++i) st.o[nb][i >> 2][i & 3] *= u;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) st.l[nb][e] += __shfl_xor_sync(0xffffffffu, st.l[nb][e], o);
     }
     __syncthreads();  // every warp has read its rows of the stage
-    if (w >= 2) state_put(st, x + (w - 2) * SW);
+    if (w >= 2) state_put(st, x + (w - 2) * SW, ex);
     __syncthreads();
-    if (w < 2) state_fold(st, x + w * SW);
-    __syncthreads();
-    if (w == 1) state_put(st, x);
+    if (w < 2) state_fold(st, x + w * SW, ex, w + 2);
+    if (w == 1) {
+        __syncwarp();
+        state_put(st, x + SW, ex);
+    }
     __syncthreads();
     if (w == 0) {
-        state_fold(st, x);
+        state_fold(st, x + SW, ex, 1);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float l = st.l[nb][e];
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
                 int map, head;
                 column<DIFF, NB>(nb, 2 * t + e, map, head);
                 if (head >= a.G) continue;
                 float *r = dst + (int64_t)(map * a.G + head) * PART_W;
-                if (g == 0) *reinterpret_cast<float2 *>(r) = make_float2(st.m[nb][e], l);
+                if (g == 0) *reinterpret_cast<float2 *>(r) = make_float2(st.m[nb][e], st.l[nb][e]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float lo = st.o[nb][i][e], hi = st.o[nb][i][e + 2];
@@ -551,50 +629,52 @@ __device__ __forceinline__ void flush(State<NB> &st, float *x, const CacheArgs &
 template <bool E4M3, int NB, bool PAGED, bool DIFF, int PARTS>
 __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
     extern __shared__ __align__(128) uint8_t csm[];
-    using T = Tile<E4M3, NB>;
+    __shared__ Exchange<NB> ex;
+    using T = Tile<E4M3>;
     pdl_trigger();
-    const int total = total_tiles(a);
+    const int total = total_tiles<T::ROWS>(a);
     const int chunk = (total + gridDim.x - 1) / gridDim.x;
     const int t0 = min((int64_t)blockIdx.x * chunk, (int64_t)total), cnt = min(chunk, total - t0);
     if (cnt <= 0) return;
-    Cursor ci, cc;
+    const uint32_t stages = smem_u32(csm);
+    Cursor<T::ROWS> ci, cc;  // the next tile to copy, the next to compute
     ci.seek(a, t0);
     cc = ci;
-    int pg[4];
-    tile_pages<PAGED>(a, ci, pg);
+    int pg = 0;
+    tile_page<E4M3, PAGED>(a, ci, pg);
     int ahead = 0;  // tiles whose copies have started
-    auto feed = [&]() {
+    auto feed = [&](uint32_t stage) {
         if (ahead < cnt) {
-            issue<E4M3, NB, PAGED>(a, ci, pg, csm + (ahead % T::STAGES) * T::STAGE);
-            ++ahead;
-            if (ahead < cnt) {
+            issue<E4M3, PAGED>(a, ci, pg, stage);
+            if (++ahead < cnt) {
                 ci.next(a);
-                tile_pages<PAGED>(a, ci, pg);
+                tile_page<E4M3, PAGED>(a, ci, pg);
             }
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int s = 0; s < T::STAGES - 1; ++s) feed();
+    for (int s = 0; s < T::STAGES - 1; ++s) feed(stages + s * T::STAGE);
     const int G2 = DIFF ? 2 * a.G : a.G;
     int unit = cc.b * a.h_kv + cc.h;
     QF<NB> qf;
     load_q<E4M3, NB, DIFF>(qf, a, unit);
     State<NB> st;
     st.init();
+    int slot = 0;
     for (int i = 0; i < cnt; ++i) {
         cp_async_wait<T::STAGES - 2>();
-        __syncthreads();
-        feed();
-        uint8_t *stage = csm + (i % T::STAGES) * T::STAGE;
-        compute<E4M3, NB, DIFF, PARTS>(st, qf, stage);
+        __syncthreads();  // the tile is there, and the stage before it has been consumed
+        feed(stages + (slot == 0 ? T::STAGES - 1 : slot - 1) * T::STAGE);
+        compute<E4M3, NB, DIFF, PARTS>(st, qf, stages + slot * T::STAGE);
         const bool end = cc.last();
         if (end || i == cnt - 1) {
-            flush<E4M3, NB, DIFF>(st, reinterpret_cast<float *>(stage), a,
+            flush<E4M3, NB, DIFF>(st, reinterpret_cast<float *>(csm + slot * T::STAGE), ex, a,
                                   a.part + ((int64_t)blockIdx.x + unit) * G2 * PART_W);
             if (i == cnt - 1) break;
             st.init();
         }
+        slot = slot + 1 == T::STAGES ? 0 : slot + 1;
         cc.next(a);
         if (end) {
             unit = cc.b * a.h_kv + cc.h;
@@ -608,7 +688,7 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
 // then the warps are folded and normalised; for a differential head both maps, their
 // difference, the root-mean-square norm and its weights.
 constexpr int CM_WARPS = 8;
-template <bool DIFF, bool BF16OUT>
+template <int ROWS, bool DIFF, bool BF16OUT>
 __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, DiffArgs d, void *out, int splits) {
     constexpr int M = DIFF ? 2 : 1;
     __shared__ float4 s_acc[M][CM_WARPS][32];
@@ -619,12 +699,12 @@ __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, Diff
     // the unit's tiles in the list, and with them the CTAs that hold its partials
     int before = 0, all = 0;
     for (int i = lane; i < a.batch; i += 32) {
-        const int nt = seq_tiles(a, i);
+        const int nt = seq_tiles<ROWS>(a, i);
         all += nt;
         if (i < b) before += nt;
     }
     before = warp_isum(before), all = warp_isum(all);
-    const int nt = seq_tiles(a, b), chunk = (all * a.h_kv + splits - 1) / splits;
+    const int nt = seq_tiles<ROWS>(a, b), chunk = (all * a.h_kv + splits - 1) / splits;
     const int first = before * a.h_kv + h * nt;
     const int c0 = nt ? first / chunk : 0, c1 = nt ? (first + nt - 1) / chunk + 1 : 0;
     float weight = 0.f;
@@ -708,16 +788,17 @@ __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, Diff
 
 int cache_splits(int units, int n_max) {
     // one wave of three CTAs per SM, and no more CTAs than tiles
-    const int64_t tiles = units * ceil_div64(n_max, CT_ROWS), slots = 3LL * num_sms();
+    // (tiles of 64 rows: the smaller kind)
+    const int64_t tiles = units * ceil_div64(n_max, Tile<false>::ROWS), slots = 3LL * num_sms();
     return (int)(tiles < slots ? tiles : slots);
 }
 
 template <bool E4M3, int NB, bool PAGED, bool DIFF, int PARTS>
 static cudaError_t launch_split(const CacheArgs &a, int splits, cudaStream_t s) {
     const auto fn = k_cache_split<E4M3, NB, PAGED, DIFF, PARTS>;
-    cudaError_t e = ensure_smem((const void *)fn, Tile<E4M3, NB>::SMEM);
+    cudaError_t e = ensure_smem((const void *)fn, Tile<E4M3>::SMEM);
     if (e != cudaSuccess) return e;
-    fn<<<splits, CT_THREADS, Tile<E4M3, NB>::SMEM, s>>>(a);
+    fn<<<splits, CT_THREADS, Tile<E4M3>::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 template <bool E4M3, bool DIFF, int PARTS>
@@ -725,6 +806,15 @@ static cudaError_t pick_split(const CacheArgs &a, int splits, cudaStream_t s) {
     const bool one = (DIFF ? 2 : 1) * a.G <= 8;
     if (a.bt) return one ? launch_split<E4M3, 1, true, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, 2, true, DIFF, PARTS>(a, splits, s);
     return one ? launch_split<E4M3, 1, false, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, 2, false, DIFF, PARTS>(a, splits, s);
+}
+
+template <int ROWS>
+static cudaError_t launch_merge(const cudaLaunchConfig_t &cfg, bool diff, bool bf_out, const CacheArgs &a,
+                                const DiffArgs &d, void *out, int splits) {
+    if (diff) return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, true, true>, a, d, out, splits)
+                            : cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, true, false>, a, d, out, splits);
+    return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, false, true>, a, d, out, splits)
+                  : cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, false, false>, a, d, out, splits);
 }
 
 cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
@@ -757,10 +847,8 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (diff) return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<true, true>, a, d, out, splits)
-                            : cudaLaunchKernelEx(&cfg, k_cache_merge<true, false>, a, d, out, splits);
-    return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<false, true>, a, d, out, splits)
-                  : cudaLaunchKernelEx(&cfg, k_cache_merge<false, false>, a, d, out, splits);
+    if (e4) return launch_merge<Tile<true>::ROWS>(cfg, diff, bf_out, a, d, out, splits);
+    return launch_merge<Tile<false>::ROWS>(cfg, diff, bf_out, a, d, out, splits);
 }
 
 // ------------------------------------------------------------------------------------
