@@ -12,10 +12,12 @@
 // (max, sum, acc per head) in slot c + unit, which no other pair (c, unit) shares, because
 // along the list either c or the unit grows by one.
 //
-// Work of one warp: 16 rows of each tile; rows in the M dimension of m16n8k16, the heads of
-// a KV head in N.  A differential head is two columns (its two maps): columns 0..3 and
-// 4..7 of one block for up to 4 heads, blocks 0 and 1 for up to 8, so both maps share each
-// value row that is read.
+// One warp takes 16 rows (bf16) or 32 (e4m3) of each tile.  Up to 8 columns (query heads, or
+// the two maps of up to 4 differential heads) sit in N of m16n8k16 with the rows in M
+// ("narrow"); up to 16 columns sit in M with the rows in N ("wide").  Either way a value
+// row is read once for all of them, and no column of the product is padding at its limit.
+// The wide form needs no transposition between the two products (its weights leave the first
+// one in the layout that the second takes) and a maximum over 4 lanes instead of 8.
 //
 // e4m3 rows are read by 16-byte loads in the order the fragments want (dimensions are
 // permuted alike in K and q, and back in the output), then widened in registers to fp16,
@@ -210,92 +212,110 @@ __device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<Tile<E4M3
     if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + T::MASK + 4 * (tid >> 5)), "r"(mask) : "memory");
 }
 
-// Column -> (map, head) of a differential block layout, (0, column) otherwise.
-template <bool DIFF, int NB>
-__device__ __forceinline__ void column(int nb, int c, int &map, int &head) {
-    map = DIFF ? (NB == 1 ? c >> 2 : nb) : 0;
-    head = DIFF ? (NB == 1 ? c & 3 : c) : nb * 8 + c;
+// Column -> (map, head).  Narrow: 4 + 4 columns of two maps; wide: 8 + 8.
+template <bool DIFF, bool WIDE>
+__device__ __forceinline__ void column(int c, int &map, int &head) {
+    map = DIFF ? (WIDE ? c >> 3 : c >> 2) : 0;
+    head = DIFF ? (WIDE ? c & 7 : c & 3) : c;
 }
 
-template <int NB>
+// Running state of a warp.  A lane holds two columns: 2t, 2t+1 (narrow) or g, g+8 (wide),
+// with g = lane / 4, t = lane % 4; o[i][e] belongs to the lane's column e & 1 (narrow) or
+// e >> 1 (wide).
+template <bool WIDE>
 struct State {
-    float o[NB][8][4];  // [block][16 dimensions][...] of O^T
-    float m[NB][2], l[NB][2];
+    static constexpr int NT = WIDE ? 16 : 8;
+    float o[NT][4];
+    float m[2], l[2];  // maximum (log2 domain); this lane's share of the sum
     float vr;  // e4m3: power of two >= every v_scale seen (0: none yet); o is in units of vr / W_SCALE
     __device__ __forceinline__ void init() {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nb][t][e] = 0.f;
-            m[nb][0] = m[nb][1] = -INFINITY;
-            l[nb][0] = l[nb][1] = 0.f;
-        }
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
         vr = 0.f;
     }
+    static __device__ __forceinline__ int col(int e) { return WIDE ? e >> 1 : e & 1; }
 };
 
-// q of a unit as B fragments, and the factor that turns an accumulator of column (2t, 2t+1)
-// into a log2-domain logit.
-template <int NB>
+// q of a unit: B fragments in registers (narrow), or A fragments in shared memory (wide: 32
+// registers otherwise).  f: the factor that turns an accumulator of the lane's column into a
+// log2-domain logit.
 struct QF {
-    uint32_t b[NB][8][2];
-    float f[NB][2];
+    uint32_t b[8][2];
+    float f[2];
 };
+typedef uint4 QShared[8][32];
 
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-template <bool E4M3, int NB, bool DIFF>
-__device__ __forceinline__ void load_q(QF<NB> &qf, const CacheArgs &a, int unit) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+// One column's fragment pieces: this lane's dimensions of each of the 8 steps.
+template <bool E4M3, bool DIFF, bool WIDE>
+__device__ __forceinline__ float load_column(uint32_t (&w)[8][2], const CacheArgs &a, int unit, int c) {
+    const int t = threadIdx.x & 3;
+    int map, head;
+    column<DIFF, WIDE>(c, map, head);
+    const bool have = head < a.G;
+    const uint16_t *row = a.q + ((int64_t)unit * a.G + (have ? head : 0)) * MOG_D;
+    if (!E4M3) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        int map, head;
-        column<DIFF, NB>(nb, g, map, head);
-        const bool have = head < a.G;
-        const uint16_t *row = a.q + ((int64_t)unit * a.G + (have ? head : 0)) * MOG_D;
-        if (!E4M3) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const bool use = have && (!DIFF || (ks >> 2) == map);
-                const uint32_t *p = reinterpret_cast<const uint32_t *>(row + ks * 16 + 2 * t);
-                qf.b[nb][ks][0] = use ? p[0] : 0u;
-                qf.b[nb][ks][1] = use ? p[4] : 0u;
-            }
-            qf.f[nb][0] = qf.f[nb][1] = a.scale2;
-        } else {
-            // this lane's dimensions: 16(t + 4j) .. +15, word w of chunk j in step 4j + w
-            uint32_t raw[2][8];
-            float amax = 0.f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const bool use = have && (!DIFF || j == map);
-                const uint4 *p = reinterpret_cast<const uint4 *>(row + 16 * (t + 4 * j));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 v = use ? p[i] : make_uint4(0, 0, 0, 0);
-                    raw[j][4 * i] = v.x, raw[j][4 * i + 1] = v.y, raw[j][4 * i + 2] = v.z, raw[j][4 * i + 3] = v.w;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf_lo(raw[j][i])), fabsf(bf_hi(raw[j][i]))));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // largest magnitude to [2^14, 2^15); below 2^-100 a head's logits are 0 to fp32
-            const int e = max((__float_as_int(amax) >> 23) - 127, -100);
-            const float up = pow2f(14 - e), back = pow2f(max(e - 14, -126)) * a.scale2;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t w = raw[ks >> 2][2 * (ks & 3) + i];
-                    const __half2 h = __floats2half2_rn(bf_lo(w) * up, bf_hi(w) * up);
-                    qf.b[nb][ks][i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-            qf.f[nb][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-            qf.f[nb][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        for (int ks = 0; ks < 8; ++ks) {
+            const bool use = have && (!DIFF || (ks >> 2) == map);
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(row + ks * 16 + 2 * t);
+            w[ks][0] = use ? p[0] : 0u;
+            w[ks][1] = use ? p[4] : 0u;
         }
+        return a.scale2;
+    }
+    // dimensions 16(t + 4j) .. +15, word k of chunk j in step 4j + k
+    uint32_t raw[2][8];
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const bool use = have && (!DIFF || j == map);
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + 16 * (t + 4 * j));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = use ? p[i] : make_uint4(0, 0, 0, 0);
+            raw[j][4 * i] = v.x, raw[j][4 * i + 1] = v.y, raw[j][4 * i + 2] = v.z, raw[j][4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf_lo(raw[j][i])), fabsf(bf_hi(raw[j][i]))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // largest magnitude to [2^14, 2^15); below 2^-100 a head's logits are 0 to fp32
+    const int e = max((__float_as_int(amax) >> 23) - 127, -100);
+    const float up = pow2f(14 - e);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t r = raw[ks >> 2][2 * (ks & 3) + i];
+            const __half2 h = __floats2half2_rn(bf_lo(r) * up, bf_hi(r) * up);
+            w[ks][i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    return pow2f(e - 14) * a.scale2;
+}
+
+// (wide: the caller puts a CTA barrier between the last reads of qs, this, and the next reads)
+template <bool E4M3, bool DIFF, bool WIDE>
+__device__ __forceinline__ void load_q(QF &qf, QShared &qs, const CacheArgs &a, int unit) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const float f = load_column<E4M3, DIFF, WIDE>(qf.b, a, unit, g);
+    if (!WIDE) {
+        qf.f[0] = __shfl_sync(0xffffffffu, f, 8 * t);
+        qf.f[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+        return;
+    }
+    uint32_t w[8][2];
+    qf.f[0] = f;
+    qf.f[1] = load_column<E4M3, DIFF, WIDE>(w, a, unit, g + 8);
+    if (threadIdx.x < 32) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) qs[ks][lane] = make_uint4(qf.b[ks][0], w[ks][0], qf.b[ks][1], w[ks][1]);
     }
 }
 
@@ -343,13 +363,32 @@ __device__ __forceinline__ float lds4(uint32_t addr) {
     return r;
 }
 
+__device__ __forceinline__ float2 lds8(uint32_t addr) {
+    float2 r;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr));
+    return r;
+}
+
+// 16 rows by 16 dimensions of K: {rows g | rows g+8} x {dimension pairs 0 | 1} of step ks, as
+// the operand with rows in M; its halves (0, 2) and (1, 3) are the two with 8 rows in N.
+template <bool E4M3>
+__device__ __forceinline__ void k_frag(uint32_t (&a)[4], uint32_t sk, int ks, const uint4 &wa, const uint4 &wb) {
+    if (E4M3) {
+        widen(word(wa, ks & 3), a[0], a[2]);
+        widen(word(wb, ks & 3), a[1], a[3]);
+    } else {
+        const int lane = threadIdx.x & 31, mat = lane >> 3, r8 = lane & 7;
+        ldsm_x4(sk + swz_k<E4M3>((mat & 1) * 8 + r8, 2 * ks + (mat >> 1)), a[0], a[1], a[2], a[3]);
+    }
+}
+
 // This warp's rows of a tile.
 //
 // The products of one tile start from zero on the tensor cores, which truncate their sums,
 // and join the running sum rounded to nearest (the same fused multiply-add that rescales
 // it): summing a 1M-token sequence on the tensor cores alone drifted by 1.1e-5.
-template <bool E4M3, int NB, bool DIFF, int PARTS>
-__device__ __forceinline__ void compute(State<NB> &st, const QF<NB> &qf, uint32_t stage) {
+template <bool E4M3, bool WIDE, bool DIFF, int PARTS>
+__device__ __forceinline__ void compute(State<WIDE> &st, const QF &qf, const QShared &qs, uint32_t stage) {
     using T = Tile<E4M3>;
     constexpr int BLK = T::BLK;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, mat = lane >> 3, r8 = lane & 7;
@@ -359,70 +398,75 @@ __device__ __forceinline__ void compute(State<NB> &st, const QF<NB> &qf, uint32_
     const uint32_t rows = (__float_as_uint(lds4(stage + T::MASK + 4 * (wr / 32))) >> (wr % 32)) & ALL;
     if (rows == 0) return;
 
-    // logits: rows g (0, 1) and g+8 (2, 3) of columns 2t, 2t+1.  The two maps of a
-    // differential block accumulate apart (half j of the dimensions is map j).
-    float s[BLK][NB][4];
-#pragma unroll
-    for (int blk = 0; blk < BLK; ++blk) {
-        float s2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[blk][nb][e] = 0.f;
+    // Logits s[blk][i]: narrow: rows g (i = 0, 1) and g+8 (2, 3) of columns 2t, 2t+1 (even and
+    // odd i); wide: columns g (i = 0, 1, 4, 5) and g+8 of rows 2t, 2t+1 (0..3), 2t+8, 2t+9.
+    // The two maps of a differential head accumulate apart (half j of the dimensions is map
+    // j), so that a row's infinity in one does not meet the zeros of the other.
+    constexpr int NS = WIDE ? 8 : 4;
+    float s[BLK][NS];
+    {
+        float d[BLK][2][NS] = {};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            uint4 wa, wb;
+            uint4 wa[BLK], wb[BLK];
             if (E4M3) {
-                wa = lds16(sk + swz_k<E4M3>(16 * blk + g, t + 4 * j));
-                wb = lds16(sk + swz_k<E4M3>(16 * blk + g + 8, t + 4 * j));
+#pragma unroll
+                for (int blk = 0; blk < BLK; ++blk) {
+                    wa[blk] = lds16(sk + swz_k<E4M3>(16 * blk + g, t + 4 * j));
+                    wb[blk] = lds16(sk + swz_k<E4M3>(16 * blk + g + 8, t + 4 * j));
+                }
             }
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const int ks = 4 * j + w;
-                uint32_t a[4];
-                if (E4M3) {
-                    widen(word(wa, w), a[0], a[2]);
-                    widen(word(wb, w), a[1], a[3]);
-                } else {
-                    ldsm_x4(sk + swz_k<E4M3>((mat & 1) * 8 + r8, 2 * ks + (mat >> 1)), a[0], a[1], a[2], a[3]);
-                }
+                const int ks = 4 * j + w, acc = DIFF ? j : 0;
+                uint4 qw;
+                if (WIDE) qw = qs[ks][lane];
+                const uint32_t qa[4] = {qw.x, qw.y, qw.z, qw.w};
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    if (DIFF && NB == 2 && nb != j) continue;
-                    if (DIFF && NB == 1 && j == 1) mma_t<E4M3>(s2, a, qf.b[nb][ks][0], qf.b[nb][ks][1]);
-                    else mma_t<E4M3>(s[blk][nb], a, qf.b[nb][ks][0], qf.b[nb][ks][1]);
+                for (int blk = 0; blk < BLK; ++blk) {
+                    uint32_t a[4];
+                    k_frag<E4M3>(a, sk, ks, wa[blk], wb[blk]);
+                    float (&dd)[NS] = d[blk][acc];
+                    if (WIDE) {
+                        mma_t<E4M3>(reinterpret_cast<float (&)[4]>(dd[0]), qa, a[0], a[2]);
+                        mma_t<E4M3>(reinterpret_cast<float (&)[4]>(dd[NS - 4]), qa, a[1], a[3]);
+                    } else {
+                        mma_t<E4M3>(reinterpret_cast<float (&)[4]>(dd[0]), a, qf.b[ks][0], qf.b[ks][1]);
+                    }
                 }
             }
         }
-        if (DIFF && NB == 1) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[blk][0][e] = t >= 2 ? s2[e] : s[blk][0][e];
-        }
+        for (int blk = 0; blk < BLK; ++blk)
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                s[blk][i] = !DIFF ? d[blk][0][i] : WIDE ? d[blk][(i >> 1) & 1][i] : t >= 2 ? d[blk][1][i] : d[blk][0][i];
     }
 
-    // log2-domain logits
+    // log2-domain logits; row of s[blk][i]: rowof(i)
+    auto rowof = [&](int i) { return WIDE ? 2 * t + (i & 1) + 8 * (i >> 2) : g + 8 * (i >> 1); };
+    auto colof = [](int i) { return WIDE ? (i >> 1) & 1 : i & 1; };
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
-        float kA = 1.f, kB = 1.f;
-        if (E4M3) kA = lds4(sc + 4 * (16 * blk + g)), kB = lds4(sc + 4 * (16 * blk + g + 8));
+        float k[4];  // scales of this lane's rows of the block (narrow: two of them)
+        if (E4M3 && WIDE) {
+            const float2 x = lds8(sc + 4 * (16 * blk + 2 * t)), y = lds8(sc + 4 * (16 * blk + 2 * t + 8));
+            k[0] = x.x, k[1] = x.y, k[2] = y.x, k[3] = y.y;
+        } else if (E4M3) {
+            k[0] = lds4(sc + 4 * (16 * blk + g)), k[1] = lds4(sc + 4 * (16 * blk + g + 8));
+        }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            s[blk][nb][0] *= kA * qf.f[nb][0];
-            s[blk][nb][1] *= kA * qf.f[nb][1];
-            s[blk][nb][2] *= kB * qf.f[nb][0];
-            s[blk][nb][3] *= kB * qf.f[nb][1];
+        for (int i = 0; i < NS; ++i) {
+            const float kk = E4M3 ? k[WIDE ? (i & 1) + 2 * (i >> 2) : i >> 1] : 1.f;
+            s[blk][i] *= kk * qf.f[colof(i)];
         }
     }
     if (rows != ALL) {  // the sequence's end, or a page that is none
 #pragma unroll
-        for (int blk = 0; blk < BLK; ++blk) {
-            const bool okA = (rows >> (16 * blk + g)) & 1u, okB = (rows >> (16 * blk + g + 8)) & 1u;
+        for (int blk = 0; blk < BLK; ++blk)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                if (!okA) s[blk][nb][0] = s[blk][nb][1] = -INFINITY;
-                if (!okB) s[blk][nb][2] = s[blk][nb][3] = -INFINITY;
-            }
-        }
+            for (int i = 0; i < NS; ++i)
+                if (!((rows >> (16 * blk + rowof(i))) & 1u)) s[blk][i] = -INFINITY;
     }
     float inv = 0.f;
     if (E4M3) {
@@ -431,101 +475,115 @@ __device__ __forceinline__ void compute(State<NB> &st, const QF<NB> &qf, uint32_
             const float vr = pow2f(min(max((__float_as_int(warp_max(mine)) >> 23) - 126, -100), 127));
             const float f = st.vr / vr;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int i = 0; i < State<WIDE>::NT; ++i)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st.o[nb][i][e] *= f;
+                for (int e = 0; e < 4; ++e) st.o[i][e] *= f;
             st.vr = vr;
         }
         inv = st.vr > 0.f ? W_SCALE / st.vr : 0.f;  // (rows whose scales are all 0 have no unit yet)
     }
-    uint32_t pb[BLK][NB][PARTS][2];
-    float al[NB][2];
-    float vA[BLK], vB[BLK];
-    if (E4M3) {
+
+    // maxima, rescale factors, weights
+    float al[2], sh[2];
 #pragma unroll
-        for (int blk = 0; blk < BLK; ++blk) {
-            vA[blk] = lds4(sc + 4 * (T::ROWS + 16 * blk + g)) * inv;
-            vB[blk] = lds4(sc + 4 * (T::ROWS + 16 * blk + g + 8)) * inv;
-        }
+    for (int c = 0; c < 2; ++c) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int blk = 0; blk < BLK; ++blk)
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                if (colof(i) == c) mx = fmaxf(mx, s[blk][i]);
+#pragma unroll
+        for (int o = WIDE ? 1 : 4; o < (WIDE ? 4 : 32); o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // the shift: 0 until a row has been seen, so that no infinities are subtracted
+        const float mn = fmaxf(st.m[c], mx);
+        sh[c] = mn == -INFINITY ? 0.f : mn;
+        al[c] = ex2(st.m[c] - sh[c]);
+        st.m[c] = mn;
+        st.l[c] *= al[c];
     }
+    uint32_t pf[BLK][PARTS][NS / 2];  // weights as the second product's operand
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        float sh[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(s[0][nb][e], s[0][nb][e + 2]);
-            if (BLK == 2) mx = fmaxf(mx, fmaxf(s[BLK - 1][nb][e], s[BLK - 1][nb][e + 2]));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // the shift: 0 until a row has been seen, so that no infinities are subtracted
-            const float mn = fmaxf(st.m[nb][e], mx);
-            sh[e] = mn == -INFINITY ? 0.f : mn;
-            al[nb][e] = ex2(st.m[nb][e] - sh[e]);
-            st.m[nb][e] = mn;
-            st.l[nb][e] *= al[nb][e];
+    for (int blk = 0; blk < BLK; ++blk) {
+        float v[4];
+        if (E4M3 && WIDE) {
+            const float2 x = lds8(sc + 4 * (T::ROWS + 16 * blk + 2 * t)), y = lds8(sc + 4 * (T::ROWS + 16 * blk + 2 * t + 8));
+            v[0] = x.x * inv, v[1] = x.y * inv, v[2] = y.x * inv, v[3] = y.y * inv;
+        } else if (E4M3) {
+            v[0] = lds4(sc + 4 * (T::ROWS + 16 * blk + g)) * inv, v[1] = lds4(sc + 4 * (T::ROWS + 16 * blk + g + 8)) * inv;
         }
 #pragma unroll
-        for (int blk = 0; blk < BLK; ++blk) {
-            float p0 = ex2(s[blk][nb][0] - sh[0]), p1 = ex2(s[blk][nb][1] - sh[1]);
-            float p2 = ex2(s[blk][nb][2] - sh[0]), p3 = ex2(s[blk][nb][3] - sh[1]);
-            st.l[nb][0] += p0 + p2;
-            st.l[nb][1] += p1 + p3;
-            if (E4M3) p0 *= vA[blk], p1 *= vA[blk], p2 *= vB[blk], p3 *= vB[blk];
+        for (int i = 0; i < NS; i += 2) {
+            float x = ex2(s[blk][i] - sh[colof(i)]), y = ex2(s[blk][i + 1] - sh[colof(i + 1)]);
+            st.l[colof(i)] += x;
+            st.l[colof(i + 1)] += y;
+            if (E4M3) {
+                x *= v[WIDE ? 2 * (i >> 2) : i >> 1];
+                y *= v[WIDE ? 1 + 2 * (i >> 2) : i >> 1];
+            }
 #pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
-                pb[blk][nb][i][0] = movmatrix_t(part16<E4M3>(p0, p1));
-                pb[blk][nb][i][1] = movmatrix_t(part16<E4M3>(p2, p3));
+            for (int k = 0; k < PARTS; ++k) {
+                const uint32_t h = part16<E4M3>(x, y);
+                pf[blk][k][i / 2] = WIDE ? h : movmatrix_t(h);
             }
         }
     }
 
-    // O^T = O^T diag(al) + V^T P^T, 16 dimensions at a time; lowest parts first
+    // O = O diag(al) + P V, 16 dimensions at a time, lowest parts first.  a: V fragment with
+    // {dimension set 0 | 1} x {rows 2t, 2t+1 | 2t+8, 2t+9}
+    auto add = [&](int mt, const uint32_t (&a)[BLK][4], int b0, int b1) {  // of blocks b0 .. b1-1
+        float d[WIDE ? 2 : 1][4] = {};
+#pragma unroll
+        for (int blk = b0; blk < b1; ++blk)
+#pragma unroll
+            for (int k = PARTS - 1; k >= 0; --k) {
+                if (WIDE) {
+                    const uint32_t p[4] = {pf[blk][k][0], pf[blk][k][1], pf[blk][k][NS / 2 - 2], pf[blk][k][NS / 2 - 1]};
+                    mma_t<E4M3>(d[0], p, a[blk][0], a[blk][2]);
+                    mma_t<E4M3>(d[WIDE ? 1 : 0], p, a[blk][1], a[blk][3]);
+                } else {
+                    mma_t<E4M3>(d[0], a[blk], pf[blk][k][0], pf[blk][k][1]);
+                }
+            }
+#pragma unroll
+        for (int k = 0; k < (WIDE ? 2 : 1); ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float &o = st.o[WIDE ? 2 * mt + k : mt][e];
+                o = b0 == 0 ? fmaf(o, al[State<WIDE>::col(e)], d[k][e]) : o + d[k][e];
+            }
+    };
     if (E4M3) {
         // rows 2t, 2t+1, 2t+8, 2t+9 of a block, dimensions 16g .. 16g+15: word w holds
-        // dimensions 16g + 4w .. +3, of tiles 2w (+0: row g of the fragment, +1: row g+8), 2w+1
-        uint4 x[BLK][4];
+        // dimensions 16g + 4w .. +3, the sets 0 and 1 of mt = 2w, then of 2w + 1
+        // (wide: block after block, whose 16 words and 64 accumulators fit beside each other)
+        constexpr int STEP = WIDE ? 1 : BLK;
 #pragma unroll
-        for (int blk = 0; blk < BLK; ++blk)
+        for (int b0 = 0; b0 < BLK; b0 += STEP) {
+            uint4 x[BLK][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[blk][i] = lds16(sv + swz_v<E4M3>(16 * blk + 2 * t + (i & 1) + 8 * (i >> 1), g));
+            for (int blk = b0; blk < b0 + STEP; ++blk)
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+                for (int i = 0; i < 4; ++i)
+                    x[blk][i] = lds16(sv + swz_v<E4M3>(16 * blk + 2 * t + (i & 1) + 8 * (i >> 1), g));
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t sel = hf ? 0x7362u : 0x5140u;
-                float d[NB][4] = {};
+            for (int mt = 0; mt < 8; ++mt) {
+                const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
+                uint32_t a[BLK][4];
 #pragma unroll
-                for (int blk = 0; blk < BLK; ++blk) {
-                    uint32_t a[4];
-                    widen(__byte_perm(word(x[blk][0], w), word(x[blk][1], w), sel), a[0], a[1]);
-                    widen(__byte_perm(word(x[blk][2], w), word(x[blk][3], w), sel), a[2], a[3]);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int i = PARTS - 1; i >= 0; --i) mma_f16(d[nb], a, pb[blk][nb][i][0], pb[blk][nb][i][1]);
+                for (int blk = b0; blk < b0 + STEP; ++blk) {
+                    widen(__byte_perm(word(x[blk][0], mt >> 1), word(x[blk][1], mt >> 1), sel), a[blk][0], a[blk][1]);
+                    widen(__byte_perm(word(x[blk][2], mt >> 1), word(x[blk][3], mt >> 1), sel), a[blk][2], a[blk][3]);
                 }
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        st.o[nb][2 * w + hf][e] = fmaf(st.o[nb][2 * w + hf][e], al[nb][e & 1], d[nb][e]);
+                add(mt, a, b0, b0 + STEP);
             }
+        }
     } else {
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-            uint32_t a[4];
-            ldsm_x4_t(sv + swz_v<E4M3>((mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0], a[1], a[2], a[3]);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float d[4] = {};
-#pragma unroll
-                for (int i = PARTS - 1; i >= 0; --i) mma_bf16(d, a, pb[0][nb][i][0], pb[0][nb][i][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st.o[nb][mt][e] = fmaf(st.o[nb][mt][e], al[nb][e & 1], d[e]);
-            }
+            uint32_t a[BLK][4];
+            ldsm_x4_t(sv + swz_v<E4M3>((mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0][0], a[0][1], a[0][2], a[0][3]);
+            add(mt, a, 0, 1);
         }
     }
 }
@@ -533,65 +591,65 @@ __device__ __forceinline__ void compute(State<NB> &st, const QF<NB> &qf, uint32_
 // A unit's end: the four warps' states become one partial in `dst` ([columns][PART_W]).
 // Accumulators pass through the stage that has just been consumed (word i of lane l at
 // i*32 + l), maxima and sums through `ex`.  Called by the whole CTA.
-template <int NB>
 struct Exchange {
-    float m[CT_WARPS][NB * 8], l[CT_WARPS][NB * 8];
+    float m[CT_WARPS][16], l[CT_WARPS][16];
 };
-template <int NB>
-__device__ __forceinline__ void state_put(const State<NB> &st, float *x, Exchange<NB> &ex) {
+template <bool WIDE>
+__device__ __forceinline__ int lane_column(int c) {  // the lane's column c (0, 1) among all
+    const int lane = threadIdx.x & 31;
+    return WIDE ? (lane >> 2) + 8 * c : 2 * (lane & 3) + c;
+}
+template <bool WIDE>
+__device__ __forceinline__ void state_put(const State<WIDE> &st, float *x, Exchange &ex) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int i = 0; i < State<WIDE>::NT * 4; ++i) x[i * 32 + lane] = st.o[i >> 2][i & 3];
+    if (WIDE ? (lane & 3) == 0 : lane < 4) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[(nb * 32 + i) * 32 + lane] = st.o[nb][i >> 2][i & 3];
-        if (lane < 4) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ex.m[w][nb * 8 + 2 * lane + e] = st.m[nb][e];
-                ex.l[w][nb * 8 + 2 * lane + e] = st.l[nb][e];
-            }
+        for (int c = 0; c < 2; ++c) {
+            ex.m[w][lane_column<WIDE>(c)] = st.m[c];
+            ex.l[w][lane_column<WIDE>(c)] = st.l[c];
         }
     }
 }
-template <int NB>
-__device__ __forceinline__ void state_fold(State<NB> &st, const float *x, const Exchange<NB> &ex, int from) {
-    const int lane = threadIdx.x & 31, t = lane & 3;
+template <bool WIDE>
+__device__ __forceinline__ void state_fold(State<WIDE> &st, const float *x, const Exchange &ex, int from) {
+    const int lane = threadIdx.x & 31;
+    float mine[2], his[2];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        float mine[2], his[2];
+    for (int c = 0; c < 2; ++c) {
+        const float m2 = ex.m[from][lane_column<WIDE>(c)], mn = fmaxf(st.m[c], m2);
+        const float sh = mn == -INFINITY ? 0.f : mn;
+        mine[c] = ex2(st.m[c] - sh);
+        his[c] = ex2(m2 - sh);
+        st.m[c] = mn;
+        st.l[c] = st.l[c] * mine[c] + ex.l[from][lane_column<WIDE>(c)] * his[c];
+    }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float m2 = ex.m[from][nb * 8 + 2 * t + e], mn = fmaxf(st.m[nb][e], m2);
-            const float sh = mn == -INFINITY ? 0.f : mn;
-            mine[e] = ex2(st.m[nb][e] - sh);
-            his[e] = ex2(m2 - sh);
-            st.m[nb][e] = mn;
-            st.l[nb][e] = st.l[nb][e] * mine[e] + ex.l[from][nb * 8 + 2 * t + e] * his[e];
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            st.o[nb][i >> 2][i & 3] = st.o[nb][i >> 2][i & 3] * mine[i & 1] + x[(nb * 32 + i) * 32 + lane] * his[i & 1];
+    for (int i = 0; i < State<WIDE>::NT * 4; ++i) {
+        const int c = State<WIDE>::col(i & 3);
+        st.o[i >> 2][i & 3] = st.o[i >> 2][i & 3] * mine[c] + x[i * 32 + lane] * his[c];
     }
 }
 
-template <bool E4M3, int NB, bool DIFF>
-__device__ __forceinline__ void flush(State<NB> &st, float *x, Exchange<NB> &ex, const CacheArgs &a, float *dst) {
+template <bool E4M3, bool WIDE, bool DIFF>
+__device__ __forceinline__ void flush(State<WIDE> &st, float *x, Exchange &ex, const CacheArgs &a, float *dst) {
     using T = Tile<E4M3>;
+    using S = State<WIDE>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    constexpr int SW = 32 * 32 * NB;  // words of a warp's accumulators
+    constexpr int SW = S::NT * 4 * 32;  // words of a warp's accumulators
     static_assert(T::AUX >= 2 * SW * 4, "two states fit in a stage");
+    if (E4M3) {  // to the values' own unit
+        const float u = st.vr / W_SCALE;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        if (E4M3) {  // to the values' own unit
-            const float u = st.vr / W_SCALE;
+        for (int i = 0; i < S::NT; ++i)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) st.o[nb][i >> 2][i & 3] *= u;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) st.l[nb][e] += __shfl_xor_sync(0xffffffffu, st.l[nb][e], o);
+            for (int e = 0; e < 4; ++e) st.o[i][e] *= u;
     }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int o = WIDE ? 1 : 4; o < (WIDE ? 4 : 32); o <<= 1) st.l[c] += __shfl_xor_sync(0xffffffffu, st.l[c], o);
     __syncthreads();  // every warp has read its rows of the stage
     if (w >= 2) state_put(st, x + (w - 2) * SW, ex);
     __syncthreads();
@@ -601,35 +659,50 @@ __device__ __forceinline__ void flush(State<NB> &st, float *x, Exchange<NB> &ex,
         state_put(st, x + SW, ex);
     }
     __syncthreads();
-    if (w == 0) {
-        state_fold(st, x + SW, ex, 1);
+    if (w != 0) return;
+    state_fold(st, x + SW, ex, 1);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+    for (int c = 0; c < 2; ++c) {
+        int map, head;
+        column<DIFF, WIDE>(lane_column<WIDE>(c), map, head);
+        if (head >= a.G) continue;
+        float *r = dst + (int64_t)(map * a.G + head) * PART_W;
+        if ((WIDE ? t : g) == 0) *reinterpret_cast<float2 *>(r) = make_float2(st.m[c], st.l[c]);
+        r += PART_ACC;
+        if (WIDE) {
+            // o[2 mt + k][2c + e]: e4m3: dimension 16(2t + e) + 2 mt + k; bf16: 16 mt + 8 k + 2t + e
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                int map, head;
-                column<DIFF, NB>(nb, 2 * t + e, map, head);
-                if (head >= a.G) continue;
-                float *r = dst + (int64_t)(map * a.G + head) * PART_W;
-                if (g == 0) *reinterpret_cast<float2 *>(r) = make_float2(st.m[nb][e], st.l[nb][e]);
+            for (int i = 0; i < S::NT; i += E4M3 ? 4 : 1) {
+                if (E4M3) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float lo = st.o[nb][i][e], hi = st.o[nb][i][e + 2];
-                    if (E4M3) {
-                        *reinterpret_cast<float2 *>(r + PART_ACC + 16 * g + 2 * i) = make_float2(lo, hi);
-                    } else {
-                        r[PART_ACC + 16 * i + g] = lo;
-                        r[PART_ACC + 16 * i + g + 8] = hi;
-                    }
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float4 *>(r + 16 * (2 * t + e) + i) =
+                            make_float4(st.o[i][2 * c + e], st.o[(i + 1) % S::NT][2 * c + e],
+                                        st.o[(i + 2) % S::NT][2 * c + e], st.o[(i + 3) % S::NT][2 * c + e]);
+                } else {
+                    *reinterpret_cast<float2 *>(r + 8 * i + 2 * t) = make_float2(st.o[i][2 * c], st.o[i][2 * c + 1]);
                 }
             }
+        } else {
+            // o[mt][c + 2 k]: e4m3: dimension 16 g + 2 mt + k; bf16: 16 mt + 8 k + g
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (E4M3) {
+                    *reinterpret_cast<float2 *>(r + 16 * g + 2 * i) = make_float2(st.o[i][c], st.o[i][c + 2]);
+                } else {
+                    r[16 * i + g] = st.o[i][c];
+                    r[16 * i + g + 8] = st.o[i][c + 2];
+                }
+            }
+        }
     }
 }
 
-template <bool E4M3, int NB, bool PAGED, bool DIFF, int PARTS>
+template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
 __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
     extern __shared__ __align__(128) uint8_t csm[];
-    __shared__ Exchange<NB> ex;
+    __shared__ Exchange ex;
+    __shared__ QShared qs;  // (wide)
     using T = Tile<E4M3>;
     pdl_trigger();
     const int total = total_tiles<T::ROWS>(a);
@@ -657,19 +730,19 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
     for (int s = 0; s < T::STAGES - 1; ++s) feed(stages + s * T::STAGE);
     const int G2 = DIFF ? 2 * a.G : a.G;
     int unit = cc.b * a.h_kv + cc.h;
-    QF<NB> qf;
-    load_q<E4M3, NB, DIFF>(qf, a, unit);
-    State<NB> st;
+    QF qf;
+    load_q<E4M3, DIFF, WIDE>(qf, qs, a, unit);
+    State<WIDE> st;
     st.init();
     int slot = 0;
     for (int i = 0; i < cnt; ++i) {
         cp_async_wait<T::STAGES - 2>();
         __syncthreads();  // the tile is there, and the stage before it has been consumed
         feed(stages + (slot == 0 ? T::STAGES - 1 : slot - 1) * T::STAGE);
-        compute<E4M3, NB, DIFF, PARTS>(st, qf, stages + slot * T::STAGE);
+        compute<E4M3, WIDE, DIFF, PARTS>(st, qf, qs, stages + slot * T::STAGE);
         const bool end = cc.last();
         if (end || i == cnt - 1) {
-            flush<E4M3, NB, DIFF>(st, reinterpret_cast<float *>(csm + slot * T::STAGE), ex, a,
+            flush<E4M3, WIDE, DIFF>(st, reinterpret_cast<float *>(csm + slot * T::STAGE), ex, a,
                                   a.part + ((int64_t)blockIdx.x + unit) * G2 * PART_W);
             if (i == cnt - 1) break;
             st.init();
@@ -678,7 +751,7 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
         cc.next(a);
         if (end) {
             unit = cc.b * a.h_kv + cc.h;
-            load_q<E4M3, NB, DIFF>(qf, a, unit);
+            load_q<E4M3, DIFF, WIDE>(qf, qs, a, unit);
         }
     }
     cp_async_wait<0>();
@@ -793,9 +866,9 @@ int cache_splits(int units, int n_max) {
     return (int)(tiles < slots ? tiles : slots);
 }
 
-template <bool E4M3, int NB, bool PAGED, bool DIFF, int PARTS>
+template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
 static cudaError_t launch_split(const CacheArgs &a, int splits, cudaStream_t s) {
-    const auto fn = k_cache_split<E4M3, NB, PAGED, DIFF, PARTS>;
+    const auto fn = k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS>;
     cudaError_t e = ensure_smem((const void *)fn, Tile<E4M3>::SMEM);
     if (e != cudaSuccess) return e;
     fn<<<splits, CT_THREADS, Tile<E4M3>::SMEM, s>>>(a);
@@ -803,9 +876,9 @@ static cudaError_t launch_split(const CacheArgs &a, int splits, cudaStream_t s) 
 }
 template <bool E4M3, bool DIFF, int PARTS>
 static cudaError_t pick_split(const CacheArgs &a, int splits, cudaStream_t s) {
-    const bool one = (DIFF ? 2 : 1) * a.G <= 8;
-    if (a.bt) return one ? launch_split<E4M3, 1, true, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, 2, true, DIFF, PARTS>(a, splits, s);
-    return one ? launch_split<E4M3, 1, false, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, 2, false, DIFF, PARTS>(a, splits, s);
+    const bool wide = (DIFF ? 2 : 1) * a.G > 8;
+    if (a.bt) return wide ? launch_split<E4M3, true, true, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, false, true, DIFF, PARTS>(a, splits, s);
+    return wide ? launch_split<E4M3, true, false, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, false, false, DIFF, PARTS>(a, splits, s);
 }
 
 template <int ROWS>
