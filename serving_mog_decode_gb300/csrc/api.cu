@@ -978,7 +978,8 @@ extern "C" int mog_kv_store(const mog_cache *c, int32_t batch, int32_t h_kv, int
                             const int32_t *pos_dev, const int32_t *count_dev, const void *k_new_dev,
                             const void *v_new_dev, int64_t new_b, int64_t new_t, int64_t new_h, void *stream) {
     if (batch <= 0 || h_kv <= 0 || t_max <= 0) return MOG_ERR_INVALID_ARG;
-    if (d != MOG_D || batch > 65535) return MOG_ERR_SHAPE;
+    // a sequence's rows are counted in 31 bits, with the grid's step to spare
+    if (d != MOG_D || batch > 65535 || (int64_t)t_max * 2 * h_kv > (1 << 30)) return MOG_ERR_SHAPE;
     const int st = check_cache(c, 1);
     if (st != MOG_OK) return st;
     if (!pos_dev || !k_new_dev || !v_new_dev) return MOG_ERR_INVALID_ARG;

@@ -42,9 +42,10 @@ constexpr float W_SCALE = 16384.f;  // 2^14: scale of fp16 weights
 // A tile is copied by the whole CTA, 2 KB of neighbouring rows per instruction, and each
 // warp consumes BLK blocks of 16 of its rows.  Stages are aligned to 128 bytes: 16 bytes off,
 // the copies of the same kernel were 5% slower (1M e4m3 tokens, 8 heads: 329 against 316 us).
-template <bool E4M3>
+template <bool E4M3_, bool WIDE_>
 struct Tile {
-    static constexpr int BLK = E4M3 ? 2 : 1;              // blocks of 16 rows per warp
+    static constexpr bool E4M3 = E4M3_, WIDE = WIDE_;
+    static constexpr int BLK = E4M3 && !WIDE ? 2 : 1;     // blocks of 16 rows per warp
     static constexpr int WROWS = 16 * BLK;                // rows per warp
     static constexpr int ROWS = CT_WARPS * WROWS;
     static constexpr int ROW = E4M3 ? MOG_D : 2 * MOG_D;  // bytes
@@ -52,7 +53,7 @@ struct Tile {
     static constexpr int AUX = 2 * KV;                    // K scales, V scales
     static constexpr int MASK = AUX + (E4M3 ? 2 * ROWS * 4 : 0);  // bit per row
     static constexpr int STAGE = MASK + 128;              // rows stay aligned to 128 bytes
-    static constexpr int STAGES = 2;  // 3 CTAs per SM: 96 KB in flight while 96 KB are consumed
+    static constexpr int STAGES = 2;  // one in flight: 96 KB per SM with 3 CTAs of 32 KB stages
     static constexpr int SMEM = STAGES * STAGE;
 };
 
@@ -165,10 +166,9 @@ __device__ __forceinline__ uint32_t swz_v(int row, int ch) {
 
 // Page of the tile's 16-row group `lane`, loaded one tile ahead of its use (unchecked: a
 // check here would wait for the load).
-template <bool E4M3, bool PAGED>
-__device__ __forceinline__ void tile_page(const CacheArgs &a, const Cursor<Tile<E4M3>::ROWS> &c, int &pg) {
+template <class T, bool PAGED>
+__device__ __forceinline__ void tile_page(const CacheArgs &a, const Cursor<T::ROWS> &c, int &pg) {
     if constexpr (PAGED) {
-        using T = Tile<E4M3>;
         const int lane = threadIdx.x & 31, row = c.t * T::ROWS + 16 * lane;
         pg = -1;
         if (lane < T::ROWS / 16 && row < c.n) pg = __ldg(a.bt + (int64_t)c.b * a.pps + (row >> a.pshift));
@@ -177,9 +177,9 @@ __device__ __forceinline__ void tile_page(const CacheArgs &a, const Cursor<Tile<
 
 // Start the copies of a tile.  Rows behind the sequence's end or in no page are zero and
 // masked; they are never read.
-template <bool E4M3, bool PAGED>
-__device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<Tile<E4M3>::ROWS> &c, int pg, uint32_t stage) {
-    using T = Tile<E4M3>;
+template <class T, bool PAGED>
+__device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<T::ROWS> &c, int pg, uint32_t stage) {
+    constexpr bool E4M3 = T::E4M3;
     constexpr int CH = T::ROW / 16;        // chunks per row
     constexpr int RP = CT_THREADS / CH;    // rows per instruction: 16 or 8
     const int tid = threadIdx.x, lane = tid & 31, ch = tid % CH, r0 = tid / CH;
@@ -387,9 +387,9 @@ __device__ __forceinline__ void k_frag(uint32_t (&a)[4], uint32_t sk, int ks, co
 // The products of one tile start from zero on the tensor cores, which truncate their sums,
 // and join the running sum rounded to nearest (the same fused multiply-add that rescales
 // it): summing a 1M-token sequence on the tensor cores alone drifted by 1.1e-5.
-template <bool E4M3, bool WIDE, bool DIFF, int PARTS>
-__device__ __forceinline__ void compute(State<WIDE> &st, const QF &qf, const QShared &qs, uint32_t stage) {
-    using T = Tile<E4M3>;
+template <class T, bool DIFF, int PARTS>
+__device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const QShared &qs, uint32_t stage) {
+    constexpr bool E4M3 = T::E4M3, WIDE = T::WIDE;
     constexpr int BLK = T::BLK;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, mat = lane >> 3, r8 = lane & 7;
     const int wr = (threadIdx.x >> 5) * T::WROWS;  // this warp's first row (a multiple of 16)
@@ -632,9 +632,9 @@ __device__ __forceinline__ void state_fold(State<WIDE> &st, const float *x, cons
     }
 }
 
-template <bool E4M3, bool WIDE, bool DIFF>
-__device__ __forceinline__ void flush(State<WIDE> &st, float *x, Exchange &ex, const CacheArgs &a, float *dst) {
-    using T = Tile<E4M3>;
+template <class T, bool DIFF>
+__device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex, const CacheArgs &a, float *dst) {
+    constexpr bool E4M3 = T::E4M3, WIDE = T::WIDE;
     using S = State<WIDE>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     constexpr int SW = S::NT * 4 * 32;  // words of a warp's accumulators
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
     extern __shared__ __align__(128) uint8_t csm[];
     __shared__ Exchange ex;
     __shared__ QShared qs;  // (wide)
-    using T = Tile<E4M3>;
+    using T = Tile<E4M3, WIDE>;
     pdl_trigger();
     const int total = total_tiles<T::ROWS>(a);
     const int chunk = (total + gridDim.x - 1) / gridDim.x;
@@ -714,14 +714,14 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
     ci.seek(a, t0);
     cc = ci;
     int pg = 0;
-    tile_page<E4M3, PAGED>(a, ci, pg);
+    tile_page<T, PAGED>(a, ci, pg);
     int ahead = 0;  // tiles whose copies have started
     auto feed = [&](uint32_t stage) {
         if (ahead < cnt) {
-            issue<E4M3, PAGED>(a, ci, pg, stage);
+            issue<T, PAGED>(a, ci, pg, stage);
             if (++ahead < cnt) {
                 ci.next(a);
-                tile_page<E4M3, PAGED>(a, ci, pg);
+                tile_page<T, PAGED>(a, ci, pg);
             }
         }
         cp_async_commit();
@@ -739,10 +739,10 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
         cp_async_wait<T::STAGES - 2>();
         __syncthreads();  // the tile is there, and the stage before it has been consumed
         feed(stages + (slot == 0 ? T::STAGES - 1 : slot - 1) * T::STAGE);
-        compute<E4M3, WIDE, DIFF, PARTS>(st, qf, qs, stages + slot * T::STAGE);
+        compute<T, DIFF, PARTS>(st, qf, qs, stages + slot * T::STAGE);
         const bool end = cc.last();
         if (end || i == cnt - 1) {
-            flush<E4M3, WIDE, DIFF>(st, reinterpret_cast<float *>(csm + slot * T::STAGE), ex, a,
+            flush<T, DIFF>(st, reinterpret_cast<float *>(csm + slot * T::STAGE), ex, a,
                                   a.part + ((int64_t)blockIdx.x + unit) * G2 * PART_W);
             if (i == cnt - 1) break;
             st.init();
@@ -861,22 +861,21 @@ __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, Diff
 
 int cache_splits(int units, int n_max) {
     // one wave of three CTAs per SM, and no more CTAs than tiles
-    // (tiles of 64 rows: the smaller kind)
-    const int64_t tiles = units * ceil_div64(n_max, Tile<false>::ROWS), slots = 3LL * num_sms();
+    // (tiles of 64 rows, the smaller kind)
+    const int64_t tiles = units * ceil_div64(n_max, 64), slots = 3LL * num_sms();
     return (int)(tiles < slots ? tiles : slots);
 }
 
 template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
 static cudaError_t launch_split(const CacheArgs &a, int splits, cudaStream_t s) {
     const auto fn = k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS>;
-    cudaError_t e = ensure_smem((const void *)fn, Tile<E4M3>::SMEM);
+    cudaError_t e = ensure_smem((const void *)fn, Tile<E4M3, WIDE>::SMEM);
     if (e != cudaSuccess) return e;
-    fn<<<splits, CT_THREADS, Tile<E4M3>::SMEM, s>>>(a);
+    fn<<<splits, CT_THREADS, Tile<E4M3, WIDE>::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 template <bool E4M3, bool DIFF, int PARTS>
-static cudaError_t pick_split(const CacheArgs &a, int splits, cudaStream_t s) {
-    const bool wide = (DIFF ? 2 : 1) * a.G > 8;
+static cudaError_t pick_split(const CacheArgs &a, bool wide, int splits, cudaStream_t s) {
     if (a.bt) return wide ? launch_split<E4M3, true, true, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, false, true, DIFF, PARTS>(a, splits, s);
     return wide ? launch_split<E4M3, true, false, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, false, false, DIFF, PARTS>(a, splits, s);
 }
@@ -903,12 +902,14 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
     DiffArgs d{};
     if (diff) d = DiffArgs{diff->lam, diff->lam_heads > 1 ? 4 * (MOG_D / 2) : 0, diff->gamma, diff->lambda_init, diff->eps};
     const int splits = cache_splits(batch * h_kv, n_max);
+    const bool wide = (diff ? 2 : 1) * G > 8;
+    static_assert(Tile<true, true>::ROWS == 64 && Tile<false, false>::ROWS == 64 && Tile<false, true>::ROWS == 64, "merge");
     cudaError_t e;
     if (diff) {
-        if (e4) e = bf_out ? pick_split<true, true, 1>(a, splits, s) : pick_split<true, true, 2>(a, splits, s);
-        else e = bf_out ? pick_split<false, true, 2>(a, splits, s) : pick_split<false, true, 3>(a, splits, s);
+        if (e4) e = bf_out ? pick_split<true, true, 1>(a, wide, splits, s) : pick_split<true, true, 2>(a, wide, splits, s);
+        else e = bf_out ? pick_split<false, true, 2>(a, wide, splits, s) : pick_split<false, true, 3>(a, wide, splits, s);
     } else {
-        e = bf_out ? pick_split<true, false, 1>(a, splits, s) : pick_split<true, false, 2>(a, splits, s);
+        e = bf_out ? pick_split<true, false, 1>(a, wide, splits, s) : pick_split<true, false, 2>(a, wide, splits, s);
     }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -920,13 +921,16 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (e4) return launch_merge<Tile<true>::ROWS>(cfg, diff, bf_out, a, d, out, splits);
-    return launch_merge<Tile<false>::ROWS>(cfg, diff, bf_out, a, d, out, splits);
+    if (e4 && !wide) return launch_merge<Tile<true, false>::ROWS>(cfg, diff, bf_out, a, d, out, splits);
+    return launch_merge<64>(cfg, diff, bf_out, a, d, out, splits);
 }
 
 // ------------------------------------------------------------------------------------
-// mog_kv_store: rows of new keys and values to their positions.  One half-warp per row:
-// its 128 elements are one 16-byte load a lane, the largest finite magnitude four shuffles.
+// mog_kv_store: rows of new keys and values to their positions.  A row is 8 lanes' work, 16
+// elements a lane: with 16 lanes a row the kernel was bound by the instructions of its
+// addresses and of the elements' conversion, 45 us for 24K tokens of 8 heads in 16-row pages
+// (100 MB read, 50 MB written: 22 us).  Elements stay packed in pairs: their magnitudes' maximum and
+// their scaling are bf16x2 instructions, exact both.
 // A row's e4m3 scale is the least power of two 2^e (e >= -126) with amax <= 448*2^e, so
 // that dividing by it is exact and the only rounding is the one to e4m3.
 // ------------------------------------------------------------------------------------
@@ -942,65 +946,101 @@ struct StoreArgs {
     int t_max, h_kv;
 };
 
-constexpr int SR_THREADS = 256;
+// Rows of a group of lanes in flight together: page numbers are loaded for all of them, then
+// elements, before any of them is rounded.
+constexpr int SR_THREADS = 256, SR_ROWS = 2, SR_LANES = 8;
+
+__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {  // (a NaN half gives way)
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {  // bf16 pair -> two codes
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(bf_hi(w)), "f"(bf_lo(w)));
+    return c;
+}
 
 template <bool E4M3>
 __global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs a) {
-    const int b = blockIdx.y;
+    const int b = blockIdx.y, lane = threadIdx.x % SR_LANES;
     const int count = a.count ? min(max(a.count[b], 0), a.t_max) : a.t_max;
+    const int per = 2 * a.h_kv, rows = count * per;  // head fastest, then key or value, then token
     const int64_t start = a.pos[b];
-    const int64_t rows = (int64_t)count * 2 * a.h_kv;  // head fastest, then key or value, then token
-    const int lane = threadIdx.x & 15;
-    const int64_t step = (int64_t)gridDim.x * (SR_THREADS / 16);
-    // (whole half-warps enter or leave: the shuffles below stay inside one)
-    const unsigned half = 0xffffu << (threadIdx.x & 16);
-    for (int64_t i = blockIdx.x * (int64_t)(SR_THREADS / 16) + threadIdx.x / 16; i < rows; i += step) {
-        const int t = (int)(i / (2 * a.h_kv)), r = (int)(i - (int64_t)t * 2 * a.h_kv);
-        const bool val = r >= a.h_kv;
-        const int h = val ? r - a.h_kv : r;
-        const int64_t pos = start + t;
-        if (pos < 0 || pos >= a.n_cap) continue;
-        int64_t slab = b, row = pos;
-        if (a.bt) {
-            slab = a.bt[(int64_t)b * a.pps + (pos >> a.pshift)];
-            if (slab < 0 || slab >= a.n_pages) continue;
-            row = pos & ((1 << a.pshift) - 1);
-        }
-        const uint4 x = ldg_nc16((val ? a.vn : a.kn) + b * a.nb + t * a.nt + h * a.nh + lane * 8);
-        uint8_t *dst = (val ? a.V : a.K) + slab * a.sb + h * a.sh + row * a.sn;
-        if (!E4M3) {
-            *reinterpret_cast<uint4 *>(dst + lane * 16) = x;
-            continue;
-        }
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        float amax = 0.f;
+    const int step = gridDim.x * (SR_THREADS / SR_LANES), dt = step / per, dr = step - dt * per;
+    int i = blockIdx.x * (SR_THREADS / SR_LANES) + threadIdx.x / SR_LANES;
+    int t = i / per, r = i - t * per;
+    // (whole groups enter or leave: the shuffles below stay inside one)
+    const unsigned group = 0xffu << (threadIdx.x & 24);
+    while (i < rows) {
+        int64_t slab[SR_ROWS], pos[SR_ROWS];
+        const uint16_t *src[SR_ROWS];
+        int head[SR_ROWS];  // >= h_kv: a value row
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float u = fabsf(bf_lo(w[k])), v = fabsf(bf_hi(w[k]));
-            amax = fmaxf(amax, u < INFINITY ? u : 0.f);
-            amax = fmaxf(amax, v < INFINITY ? v : 0.f);
+        for (int u = 0; u < SR_ROWS; ++u) {
+            pos[u] = start + t;
+            head[u] = r;
+            const bool ok = i < rows && pos[u] >= 0 && pos[u] < a.n_cap;
+            slab[u] = !ok ? -1 : a.bt ? a.bt[(int64_t)b * a.pps + (pos[u] >> a.pshift)] : b;
+            const int h = r >= a.h_kv ? r - a.h_kv : r;
+            src[u] = (r >= a.h_kv ? a.vn : a.kn) + b * a.nb + t * a.nt + h * a.nh + lane * 8;
+            i = i < rows ? i + step : i;  // (stays below 2^31)
+            t += dt;
+            r += dr;
+            if (r >= per) r -= per, ++t;
+        }
+        uint4 x[SR_ROWS][2];  // elements 8*lane .. and 64 + 8*lane ..
+#pragma unroll
+        for (int u = 0; u < SR_ROWS; ++u) {
+            if (a.bt && slab[u] >= a.n_pages) slab[u] = -1;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) x[u][k] = slab[u] >= 0 ? ldg_nc16(src[u] + 64 * k) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, o));
-        // amax = m * 2^E, 1 <= m < 2: 448 = 1.75 * 2^8
-        const int bits = __float_as_int(amax), E = (bits >> 23) - 127;
-        int e = E - 8 + ((bits & 0x7fffff) > 0x600000);
-        e = amax > 0.f ? max(e, -126) : 0;
-        const float inv = pow2f(-e);
-        uint32_t c[2];
+        for (int u = 0; u < SR_ROWS; ++u) {
+            if (slab[u] < 0) continue;
+            const bool val = head[u] >= a.h_kv;
+            const int64_t h = val ? head[u] - a.h_kv : head[u];
+            const int64_t row = a.bt ? pos[u] & ((1 << a.pshift) - 1) : pos[u];
+            uint8_t *dst = (val ? a.V : a.K) + slab[u] * a.sb + h * a.sh + row * a.sn;
+            if (!E4M3) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t u = 0;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                uint16_t p;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(bf_hi(w[2 * k + m]) * inv), "f"(bf_lo(w[2 * k + m]) * inv));
-                u |= (uint32_t)p << (16 * m);
+                for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4 *>(dst + 128 * k + lane * 16) = x[u][k];
+                continue;
             }
-            c[k] = u;
+            const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = bf2_max(m, w[k] & 0x7fff7fffu);
+            float amax = fmaxf(bf_lo(m), bf_hi(m));
+            if (amax == INFINITY) {  // the largest finite magnitude instead
+                amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float p = fabsf(bf_lo(w[k])), q = fabsf(bf_hi(w[k]));
+                    amax = fmaxf(amax, fmaxf(p < INFINITY ? p : 0.f, q < INFINITY ? q : 0.f));
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < SR_LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
+            // amax = m * 2^E, 1 <= m < 2: 448 = 1.75 * 2^8
+            const int bits = __float_as_int(amax), E = (bits >> 23) - 127;
+            int e = E - 8 + ((bits & 0x7fffff) > 0x600000);
+            e = amax > 0.f ? max(e, -126) : 0;
+            const uint32_t inv = (uint32_t)(127 - e) << 7, inv2 = inv | inv << 16;  // 2^-e twice, -126 <= -e <= 126
+            // (a product below bf16's normal range rounds, but e4m3 has only 0 there)
+            uint32_t c[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = e4m3_pair(bf2_mul(w[2 * k], inv2)) | e4m3_pair(bf2_mul(w[2 * k + 1], inv2)) << 16;
+            *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(c[0], c[1]);
+            *reinterpret_cast<uint2 *>(dst + 64 + lane * 8) = make_uint2(c[2], c[3]);
+            if (lane == 0) (val ? a.vs : a.ks)[slab[u] * a.ssb + h * a.ssh + row * a.ssn] = pow2f(e);
         }
-        *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(c[0], c[1]);
-        if (lane == 0) (val ? a.vs : a.ks)[slab * a.ssb + h * a.ssh + row * a.ssn] = pow2f(e);
     }
 }
 
@@ -1015,7 +1055,8 @@ cudaError_t launch_kv_store(const mog_cache *c, int batch, int h_kv, int t_max, 
                 c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
                 (int)(cap < INT32_MAX ? cap : INT32_MAX), pos, count, static_cast<const uint16_t *>(kn),
                 static_cast<const uint16_t *>(vn), nb, nt, nh, t_max, h_kv};
-    const int64_t rows = (int64_t)t_max * 2 * h_kv, per = SR_THREADS / 16;
+    const int64_t rows = (int64_t)t_max * 2 * h_kv, per = SR_THREADS / SR_LANES;
+    // up to 16 CTAs per SM; fewer rows: one per group of lanes
     const int64_t most = ceil_div64(16LL * num_sms(), batch);
     const int64_t want = ceil_div64(rows, per);
     const dim3 grid((unsigned)(want < most ? want : most), batch);
