@@ -521,7 +521,8 @@ typedef struct mog_cache {
  *                positions
  *  q_dev       : bf16 [batch][h_q][d];  out_dev: out_type [batch][h_q][d]
  *  scratch_dev : at least dense_decode8_scratch_bytes() bytes, 16-byte aligned; no initial
- *                contents needed, not shared by calls that overlap on the GPU
+ *                contents needed, not shared by calls that overlap on the GPU.  Short
+ *                caches need none (0 bytes; scratch_dev may then be NULL)
  * d must be 128, h_q / h_kv <= 16.
  */
 int dense_decode8_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t n_max,

@@ -628,18 +628,20 @@ def _cache_decode(entry, K, V, lengths_dev, n_max, q, diff, out, scratch, stream
         raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape on q's device")
     if scratch is None:
         nbytes = _scratch_bytes(entry, B, H_kv, H_q, n_max, dev.index)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if nbytes:
+            scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif scratch.device != dev or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous tensor on the cache's device")
     else:
         nbytes = scratch.numel() * scratch.element_size()
     bf = out.dtype is torch.bfloat16
+    at = None if scratch is None else scratch.data_ptr()
     if diff is None:
         rc = lib().dense_decode8(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
-                                 out.data_ptr(), bf, scratch.data_ptr(), nbytes, s)
+                                 out.data_ptr(), bf, at, nbytes, s)
     else:
         rc = lib().mog_diff_decode(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
-                                   C.byref(diff), out.data_ptr(), bf, scratch.data_ptr(), nbytes, s)
+                                   C.byref(diff), out.data_ptr(), bf, at, nbytes, s)
     if rc:
         _check(rc, entry)
     return out
@@ -789,10 +791,10 @@ class PagePool:
         if stream is not None:
             with _there(self.device, stream):
                 return self.grow(n_new)
-        both = n_new.new_empty((2, self.batch))
-        at = both.data_ptr()
-        self._call("mog_pages_grow", None, n_new.data_ptr(), at, at + 4 * self.batch)
-        return both.unbind(0)
+        torch = _torch()
+        pos, granted = torch.empty_like(n_new), torch.empty_like(n_new)
+        self._call("mog_pages_grow", None, n_new.data_ptr(), pos.data_ptr(), granted.data_ptr())
+        return pos, granted
 
     def compact(self, stream=None):
         """Move the pages in use to the front of the pools (mog_pages_compact)."""

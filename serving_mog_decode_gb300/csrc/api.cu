@@ -918,7 +918,7 @@ static int cache_scratch(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, in
     if ((int64_t)batch * h_q > INT32_MAX / 2 || (int64_t)batch * h_kv * ceil_div64(n_max, 64) > INT32_MAX / 2)
         return MOG_ERR_SHAPE;
     const int units = batch * h_kv;
-    *bytes = ((size_t)units + cache_splits(units, n_max)) * maps * (h_q / h_kv) * (MOG_D + 4) * sizeof(float);
+    *bytes = cache_cluster(units, n_max) ? 0 : ((size_t)units + cache_splits(units, n_max)) * maps * (h_q / h_kv) * (MOG_D + 4) * sizeof(float);
     return MOG_OK;
 }
 
@@ -928,7 +928,7 @@ static int cache_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t 
                         const char *where) {
     const int st = check_cache(c, n_max);
     if (st != MOG_OK) return st;
-    if (!lengths_dev || !q_dev || !out_dev || !scratch_dev) return MOG_ERR_INVALID_ARG;
+    if (!lengths_dev || !q_dev || !out_dev || (need && !scratch_dev)) return MOG_ERR_INVALID_ARG;
     if (out_type != MOG_OUT_F32 && out_type != MOG_OUT_BF16) return MOG_ERR_INVALID_ARG;
     if (!aligned16(q_dev) || !aligned16(out_dev) || !aligned16(scratch_dev)) return MOG_ERR_INVALID_ARG;
     if (scratch_bytes < need) return MOG_ERR_ARENA_TOO_SMALL;

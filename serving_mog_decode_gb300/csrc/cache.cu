@@ -54,7 +54,11 @@ struct Tile {
     static constexpr int MASK = AUX + (E4M3 ? 2 * ROWS * 4 : 0);  // bit per row
     static constexpr int STAGE = MASK + 128;              // rows stay aligned to 128 bytes
     static constexpr int STAGES = 2;  // one in flight: 96 KB per SM with 3 CTAs of 32 KB stages
-    static constexpr int SMEM = STAGES * STAGE;
+    static constexpr int COLS = WIDE ? 16 : 8;
+    static constexpr int XCH = 2 * COLS * MOG_D * 4;      // two warps' accumulators, in a consumed stage
+    // a cluster's CTA leaves its partial behind that in stage 0, or behind the stages
+    static constexpr int PART = STAGE >= XCH + COLS * PART_W * 4 ? XCH : STAGES * STAGE;
+    static constexpr int SMEM = STAGES * STAGE + (PART == XCH ? 0 : COLS * PART_W * 4);
 };
 
 struct CacheArgs {
@@ -69,6 +73,7 @@ struct CacheArgs {
     const uint16_t *q;
     float *part;
     float scale2;
+    int cs;  // CTAs of a cluster that works on one unit; 0: the tile list is split
 };
 
 struct DiffArgs {
@@ -470,7 +475,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
     }
     float inv = 0.f;
     if (E4M3) {
-        const float mine = fabsf(lds4(sc + 4 * (T::ROWS + lane)));
+        const float mine = fabsf(lds4(sc + 4 * (T::ROWS + lane % T::WROWS)));
         if (__any_sync(0xffffffffu, mine > st.vr)) {  // a larger value scale: new unit
             const float vr = pow2f(min(max((__float_as_int(warp_max(mine)) >> 23) - 126, -100), 127));
             const float f = st.vr / vr;
@@ -638,7 +643,7 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
     using S = State<WIDE>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     constexpr int SW = S::NT * 4 * 32;  // words of a warp's accumulators
-    static_assert(T::AUX >= 2 * SW * 4, "two states fit in a stage");
+    static_assert(T::XCH == 2 * SW * 4 && T::AUX >= T::XCH, "two states fit in a stage");
     if (E4M3) {  // to the values' own unit
         const float u = st.vr / W_SCALE;
 #pragma unroll
@@ -698,20 +703,134 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
     }
 }
 
+// Weight of a differential head's second map (called by a full warp).
+template <bool DIFF>
+__device__ __forceinline__ float map_weight(const DiffArgs &d, int head) {
+    if (!DIFF) return 0.f;
+    const float *L = d.lam + d.lam_stride * head + 2 * (threadIdx.x & 31);
+    const float2 x0 = *reinterpret_cast<const float2 *>(L), x1 = *reinterpret_cast<const float2 *>(L + 64);
+    const float2 x2 = *reinterpret_cast<const float2 *>(L + 128), x3 = *reinterpret_cast<const float2 *>(L + 192);
+    const float e1 = warp_sum(x0.x * x1.x + x0.y * x1.y), e2 = warp_sum(x2.x * x3.x + x2.y * x3.y);
+    return expf(e1) - expf(e2) + d.lambda_init;
+}
+
+// Running fold of partials: maximum, sum, four dimensions of a lane.
+struct Fold {
+    float m, l;
+    float4 acc;
+    __device__ __forceinline__ void init() { m = -INFINITY, l = 0.f, acc = make_float4(0.f, 0.f, 0.f, 0.f); }
+    template <int U>
+    __device__ __forceinline__ void add(const float2 (&ml)[U], const float4 (&v)[U]) {
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < U; ++i) mn = fmaxf(mn, ml[i].x);
+        const float sh = mn == -INFINITY ? 0.f : mn, f = exp2f(m - sh);
+        m = mn;
+        l *= f;
+        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const float fi = exp2f(ml[i].x - sh);
+            l += fi * ml[i].y;
+            acc.x += fi * v[i].x, acc.y += fi * v[i].y, acc.z += fi * v[i].z, acc.w += fi * v[i].w;
+        }
+    }
+};
+
+// A head's output from the folds of its map (both maps: their difference, the root-mean-square
+// norm and its weights), four dimensions a lane of a full warp, as row `row` of out.
+template <bool DIFF, bool BF16OUT>
+__device__ __forceinline__ void finish(const Fold (&f)[DIFF ? 2 : 1], float weight, const DiffArgs &d, void *out,
+                                       int64_t row) {
+    const int lane = threadIdx.x & 31;
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < (DIFF ? 2 : 1); ++k) {
+        // nothing seen: zeros (a sum that is NaN stays NaN)
+        const float x = (f[k].l == 0.f ? 0.f : 1.f / f[k].l) * (k ? -weight : 1.f);
+        r.x += x * f[k].acc.x, r.y += x * f[k].acc.y, r.z += x * f[k].acc.z, r.w += x * f[k].acc.w;
+    }
+    if (DIFF) {
+        const float ss = warp_sum(r.x * r.x + r.y * r.y + r.z * r.z + r.w * r.w);
+        const float x = (1.f - d.lambda_init) / sqrtf(ss * (1.f / MOG_D) + d.eps);
+        const float4 gm = d.gamma ? reinterpret_cast<const float4 *>(d.gamma)[lane] : make_float4(1.f, 1.f, 1.f, 1.f);
+        r.x *= x * gm.x, r.y *= x * gm.y, r.z *= x * gm.z, r.w *= x * gm.w;
+    }
+    const int64_t o = row * MOG_D + 4 * lane;
+    if (BF16OUT) {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + o) = make_uint2(cvt_bf2(r.x, r.y), cvt_bf2(r.z, r.w));
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + o) = r;
+    }
+}
+
+// A cluster's end: every CTA has its partial at T::PART; CTA r of the cluster takes heads r,
+// r + cs, ..., a warp each, and folds them over the cluster's shared memory.
+template <class T, bool DIFF, bool BF16OUT>
+__device__ __forceinline__ void cluster_end(const CacheArgs &a, const DiffArgs &d, void *out, uint32_t smem, int unit) {
+    constexpr int M = DIFF ? 2 : 1, U = 8;
+    const int rank = blockIdx.x % a.cs, w = threadIdx.x >> 5, lane = threadIdx.x & 31, h = unit % a.h_kv;
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int head = rank + a.cs * w; head < a.G; head += a.cs * CT_WARPS) {
+        Fold f[M];
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+            f[k].init();
+            const uint32_t at = smem + T::PART + (k * a.G + head) * PART_W * 4;
+            for (int c0 = 0; c0 < a.cs; c0 += U) {
+                float2 ml[U];
+                float4 v[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    ml[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c0 + i >= a.cs) continue;
+                    uint32_t p;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(at), "r"(c0 + i));
+                    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(ml[i].x), "=f"(ml[i].y) : "r"(p));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(v[i].x), "=f"(v[i].y), "=f"(v[i].z), "=f"(v[i].w) : "r"(p + 4 * PART_ACC + 16 * lane));
+                }
+                f[k].add(ml, v);
+            }
+        }
+        finish<DIFF, BF16OUT>(f, map_weight<DIFF>(d, h * a.G + head), d, out, (int64_t)unit * a.G + head);
+    }
+    // nobody leaves while its partial is read
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
-__global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
+__global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
     extern __shared__ __align__(128) uint8_t csm[];
     __shared__ Exchange ex;
     __shared__ QShared qs;  // (wide)
     using T = Tile<E4M3, WIDE>;
-    pdl_trigger();
-    const int total = total_tiles<T::ROWS>(a);
-    const int chunk = (total + gridDim.x - 1) / gridDim.x;
-    const int t0 = min((int64_t)blockIdx.x * chunk, (int64_t)total), cnt = min(chunk, total - t0);
-    if (cnt <= 0) return;
+    constexpr bool BF16OUT = PARTS == (E4M3 ? 1 : 2);  // (the parts go by the output's type)
     const uint32_t stages = smem_u32(csm);
+    const int G2 = DIFF ? 2 * a.G : a.G;
     Cursor<T::ROWS> ci, cc;  // the next tile to copy, the next to compute
-    ci.seek(a, t0);
+    int cnt;
+    if (a.cs == 0) {
+        pdl_trigger();
+        const int total = total_tiles<T::ROWS>(a);
+        const int chunk = (total + gridDim.x - 1) / gridDim.x;
+        const int t0 = min((int64_t)blockIdx.x * chunk, (int64_t)total);
+        cnt = min(chunk, total - t0);
+        if (cnt <= 0) return;
+        ci.seek(a, t0);
+    } else {  // an equal share of one unit's tiles
+        const int u = blockIdx.x / a.cs, rank = blockIdx.x - u * a.cs;
+        ci.b = u / a.h_kv, ci.h = u - ci.b * a.h_kv;
+        ci.load(a);
+        ci.t = (int)((int64_t)ci.nt * rank / a.cs);
+        cnt = (int)((int64_t)ci.nt * (rank + 1) / a.cs) - ci.t;
+        if (cnt == 0) {  // an empty partial
+            for (int i = threadIdx.x; i < G2 * PART_W; i += CT_THREADS)
+                reinterpret_cast<float *>(csm + T::PART)[i] = i % PART_W == 0 ? -INFINITY : 0.f;
+            cluster_end<T, DIFF, BF16OUT>(a, d, out, stages, u);
+            return;
+        }
+    }
     cc = ci;
     int pg = 0;
     tile_page<T, PAGED>(a, ci, pg);
@@ -728,7 +847,6 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
     };
 #pragma unroll
     for (int s = 0; s < T::STAGES - 1; ++s) feed(stages + s * T::STAGE);
-    const int G2 = DIFF ? 2 * a.G : a.G;
     int unit = cc.b * a.h_kv + cc.h;
     QF qf;
     load_q<E4M3, DIFF, WIDE>(qf, qs, a, unit);
@@ -742,8 +860,9 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
         compute<T, DIFF, PARTS>(st, qf, qs, stages + slot * T::STAGE);
         const bool end = cc.last();
         if (end || i == cnt - 1) {
-            flush<T, DIFF>(st, reinterpret_cast<float *>(csm + slot * T::STAGE), ex, a,
-                                  a.part + ((int64_t)blockIdx.x + unit) * G2 * PART_W);
+            float *dst = a.cs ? reinterpret_cast<float *>(csm + T::PART)
+                              : a.part + ((int64_t)blockIdx.x + unit) * G2 * PART_W;
+            flush<T, DIFF>(st, reinterpret_cast<float *>(csm + slot * T::STAGE), ex, a, dst);
             if (i == cnt - 1) break;
             st.init();
         }
@@ -755,17 +874,16 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a) {
         }
     }
     cp_async_wait<0>();
+    if (a.cs) cluster_end<T, DIFF, BF16OUT>(a, d, out, stages, unit);
 }
 
-// One CTA per (unit, head): warp w folds partials w, w + 8, ... (each lane four dimensions),
-// then the warps are folded and normalised; for a differential head both maps, their
-// difference, the root-mean-square norm and its weights.
+// One CTA per (unit, head): warp w folds partials w, w + 8, ..., then the warps are folded.
 constexpr int CM_WARPS = 8;
 template <int ROWS, bool DIFF, bool BF16OUT>
 __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, DiffArgs d, void *out, int splits) {
     constexpr int M = DIFF ? 2 : 1;
     __shared__ float4 s_acc[M][CM_WARPS][32];
-    __shared__ float s_m[M][CM_WARPS], s_l[M][CM_WARPS];
+    __shared__ float2 s_ml[M][CM_WARPS];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.x / a.G, head = blockIdx.x % a.G;
     const int b = unit / a.h_kv, h = unit % a.h_kv;
@@ -780,21 +898,14 @@ __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, Diff
     const int nt = seq_tiles<ROWS>(a, b), chunk = (all * a.h_kv + splits - 1) / splits;
     const int first = before * a.h_kv + h * nt;
     const int c0 = nt ? first / chunk : 0, c1 = nt ? (first + nt - 1) / chunk + 1 : 0;
-    float weight = 0.f;
-    if (DIFF) {
-        const float *L = d.lam + d.lam_stride * (h * a.G + head) + 2 * lane;
-        const float2 x0 = *reinterpret_cast<const float2 *>(L), x1 = *reinterpret_cast<const float2 *>(L + 64);
-        const float2 x2 = *reinterpret_cast<const float2 *>(L + 128), x3 = *reinterpret_cast<const float2 *>(L + 192);
-        const float e1 = warp_sum(x0.x * x1.x + x0.y * x1.y), e2 = warp_sum(x2.x * x3.x + x2.y * x3.y);
-        weight = expf(e1) - expf(e2) + d.lambda_init;
-    }
+    const float weight = map_weight<DIFF>(d, h * a.G + head);
     pdl_wait();
     const int64_t step = (int64_t)M * a.G * PART_W;  // floats of a slot
 #pragma unroll
     for (int k = 0; k < M; ++k) {
         const float *p = a.part + (int64_t)unit * step + (int64_t)(k * a.G + head) * PART_W;
-        float m = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        Fold f;
+        f.init();
         constexpr int U = 4;
         for (int c = c0 + w; c < c1; c += CM_WARPS * U) {
             float2 ml[U];
@@ -806,78 +917,66 @@ __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, Diff
                 ml[i] = ok ? __ldcg(reinterpret_cast<const float2 *>(r)) : make_float2(-INFINITY, 0.f);
                 v[i] = ok ? __ldcg(reinterpret_cast<const float4 *>(r + PART_ACC) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            float mn = m;
-#pragma unroll
-            for (int i = 0; i < U; ++i) mn = fmaxf(mn, ml[i].x);
-            const float sh = mn == -INFINITY ? 0.f : mn, f = exp2f(m - sh);
-            m = mn;
-            l *= f;
-            acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const float fi = exp2f(ml[i].x - sh);
-                l += fi * ml[i].y;
-                acc.x += fi * v[i].x, acc.y += fi * v[i].y, acc.z += fi * v[i].z, acc.w += fi * v[i].w;
-            }
+            f.add(ml, v);
         }
-        s_acc[k][w][lane] = acc;
-        if (lane == 0) s_m[k][w] = m, s_l[k][w] = l;
+        s_acc[k][w][lane] = f.acc;
+        if (lane == 0) s_ml[k][w] = make_float2(f.m, f.l);
     }
     __syncthreads();
     if (w != 0) return;
-    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    Fold f[M];
 #pragma unroll
     for (int k = 0; k < M; ++k) {
-        float m = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 ml[CM_WARPS];
+        float4 v[CM_WARPS];
 #pragma unroll
-        for (int i = 0; i < CM_WARPS; ++i) m = fmaxf(m, s_m[k][i]);
-        const float sh = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < CM_WARPS; ++i) {
-            const float fi = exp2f(s_m[k][i] - sh);
-            const float4 v = s_acc[k][i][lane];
-            l += fi * s_l[k][i];
-            acc.x += fi * v.x, acc.y += fi * v.y, acc.z += fi * v.z, acc.w += fi * v.w;
-        }
-        // nothing seen: zeros (a sum that is NaN stays NaN)
-        const float f = (l == 0.f ? 0.f : 1.f / l) * (k ? -weight : 1.f);
-        r.x += f * acc.x, r.y += f * acc.y, r.z += f * acc.z, r.w += f * acc.w;
+        for (int i = 0; i < CM_WARPS; ++i) ml[i] = s_ml[k][i], v[i] = s_acc[k][i][lane];
+        f[k].init();
+        f[k].add(ml, v);
     }
-    if (DIFF) {
-        const float ss = warp_sum(r.x * r.x + r.y * r.y + r.z * r.z + r.w * r.w);
-        const float f = (1.f - d.lambda_init) / sqrtf(ss * (1.f / MOG_D) + d.eps);
-        const float4 gm = d.gamma ? reinterpret_cast<const float4 *>(d.gamma)[lane] : make_float4(1.f, 1.f, 1.f, 1.f);
-        r.x *= f * gm.x, r.y *= f * gm.y, r.z *= f * gm.z, r.w *= f * gm.w;
-    }
-    const int64_t o = (int64_t)blockIdx.x * MOG_D + 4 * lane;
-    if (BF16OUT) {
-        const uint2 v = make_uint2(cvt_bf2(r.x, r.y), cvt_bf2(r.z, r.w));
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + o) = v;
-    } else {
-        *reinterpret_cast<float4 *>(static_cast<float *>(out) + o) = r;
-    }
+    finish<DIFF, BF16OUT>(f, weight, d, out, blockIdx.x);
 }
 
 int cache_splits(int units, int n_max) {
-    // one wave of three CTAs per SM, and no more CTAs than tiles
-    // (tiles of 64 rows, the smaller kind)
+    // one wave of three CTAs per SM, and no more CTAs than tiles (of 64 rows, the smaller kind)
     const int64_t tiles = units * ceil_div64(n_max, 64), slots = 3LL * num_sms();
     return (int)(tiles < slots ? tiles : slots);
 }
 
+// CTAs of a cluster per unit, or 0 for the split form with its second kernel.
+constexpr int CLUSTER_MAX = 8, CLUSTER_TILES = 4;
+int cache_cluster(int units, int n_max) {
+    const int64_t tiles = ceil_div64(n_max, 64);
+    int cs = 1;
+    while (cs < CLUSTER_MAX && cs < tiles && (int64_t)units * cs < 3LL * num_sms()) cs *= 2;
+    return tiles <= (int64_t)cs * CLUSTER_TILES ? cs : 0;
+}
+
 template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
-static cudaError_t launch_split(const CacheArgs &a, int splits, cudaStream_t s) {
+static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out, int splits, cudaStream_t s) {
+    using T = Tile<E4M3, WIDE>;
     const auto fn = k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS>;
-    cudaError_t e = ensure_smem((const void *)fn, Tile<E4M3, WIDE>::SMEM);
+    const cudaError_t e = ensure_smem((const void *)fn, T::SMEM);
     if (e != cudaSuccess) return e;
-    fn<<<splits, CT_THREADS, Tile<E4M3, WIDE>::SMEM, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.cs ? a.cs * a.batch * a.h_kv : splits);
+    cfg.blockDim = dim3(CT_THREADS);
+    cfg.dynamicSmemBytes = T::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = a.cs;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.cs > 1;
+    return cudaLaunchKernelEx(&cfg, fn, a, d, out);
 }
 template <bool E4M3, bool DIFF, int PARTS>
-static cudaError_t pick_split(const CacheArgs &a, bool wide, int splits, cudaStream_t s) {
-    if (a.bt) return wide ? launch_split<E4M3, true, true, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, false, true, DIFF, PARTS>(a, splits, s);
-    return wide ? launch_split<E4M3, true, false, DIFF, PARTS>(a, splits, s) : launch_split<E4M3, false, false, DIFF, PARTS>(a, splits, s);
+static cudaError_t pick_split(const CacheArgs &a, const DiffArgs &d, void *out, bool wide, int splits, cudaStream_t s) {
+    if (a.bt) return wide ? launch_split<E4M3, true, true, DIFF, PARTS>(a, d, out, splits, s)
+                          : launch_split<E4M3, false, true, DIFF, PARTS>(a, d, out, splits, s);
+    return wide ? launch_split<E4M3, true, false, DIFF, PARTS>(a, d, out, splits, s)
+                : launch_split<E4M3, false, false, DIFF, PARTS>(a, d, out, splits, s);
 }
 
 template <int ROWS>
@@ -898,20 +997,22 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
                 c->stride_b * es, c->stride_h * es, c->stride_n * es, c->scale_b, c->scale_h, c->scale_n,
                 c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
                 lengths, n_max, batch, h_kv, G, static_cast<const uint16_t *>(q), scratch,
-                (float)(LOG2E / sqrt(diff ? MOG_D / 2.0 : (double)MOG_D))};
+                (float)(LOG2E / sqrt(diff ? MOG_D / 2.0 : (double)MOG_D)), cache_cluster(batch * h_kv, n_max)};
     DiffArgs d{};
     if (diff) d = DiffArgs{diff->lam, diff->lam_heads > 1 ? 4 * (MOG_D / 2) : 0, diff->gamma, diff->lambda_init, diff->eps};
     const int splits = cache_splits(batch * h_kv, n_max);
     const bool wide = (diff ? 2 : 1) * G > 8;
     static_assert(Tile<true, true>::ROWS == 64 && Tile<false, false>::ROWS == 64 && Tile<false, true>::ROWS == 64, "merge");
+    // (tiles of 128 rows: as many CTAs as tiles do)
+    while (e4 && !wide && a.cs > 1 && a.cs / 2 >= ceil_div64(n_max, Tile<true, false>::ROWS)) a.cs /= 2;
     cudaError_t e;
     if (diff) {
-        if (e4) e = bf_out ? pick_split<true, true, 1>(a, wide, splits, s) : pick_split<true, true, 2>(a, wide, splits, s);
-        else e = bf_out ? pick_split<false, true, 2>(a, wide, splits, s) : pick_split<false, true, 3>(a, wide, splits, s);
+        if (e4) e = bf_out ? pick_split<true, true, 1>(a, d, out, wide, splits, s) : pick_split<true, true, 2>(a, d, out, wide, splits, s);
+        else e = bf_out ? pick_split<false, true, 2>(a, d, out, wide, splits, s) : pick_split<false, true, 3>(a, d, out, wide, splits, s);
     } else {
-        e = bf_out ? pick_split<true, false, 1>(a, wide, splits, s) : pick_split<true, false, 2>(a, wide, splits, s);
+        e = bf_out ? pick_split<true, false, 1>(a, d, out, wide, splits, s) : pick_split<true, false, 2>(a, d, out, wide, splits, s);
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.cs) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(batch * h_kv * G);
     cfg.blockDim = dim3(CM_WARPS * 32);

@@ -146,6 +146,7 @@ cudaError_t launch_dense(const mog_kv *kv, const int32_t *lengths, int n_max, in
                          cudaStream_t s);
 constexpr int MOG_MAX_POOLS = 64;  // page pools of one copy launch (further pools: further launches)
 int cache_splits(int units, int n_max);
+int cache_cluster(int units, int n_max);  // > 0: one launch that needs no scratch
 cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
                                 const void *q, const mog_diff_params *diff, int out_type, void *out, float *scratch,
                                 cudaStream_t s);

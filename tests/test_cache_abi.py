@@ -21,8 +21,8 @@ def lib():
 
 
 def cache(**kw):
-    base = dict(type=1, n_cap=256, k=P.value, v=P.value, k_scale=P.value, v_scale=P.value, stride_b=8 * 256 * 128,
-                stride_h=256 * 128, stride_n=128, scale_b=8 * 256, scale_h=256, scale_n=1)
+    base = dict(type=1, n_cap=1 << 20, k=P.value, v=P.value, k_scale=P.value, v_scale=P.value, stride_b=8 << 27,
+                stride_h=1 << 27, stride_n=128, scale_b=8 << 20, scale_h=1 << 20, scale_n=1)
     base.update(kw)
     return mog.Cache(**base)
 
@@ -30,22 +30,22 @@ def cache(**kw):
 BAD_CACHES = [
     (dict(k=None), ARG), (dict(v=None), ARG), (dict(k=ODD.value), ARG), (dict(type=2), ARG), (dict(type=-1), ARG),
     (dict(k_scale=None), ARG), (dict(v_scale=P.value + 2), ARG), (dict(stride_n=64), SHAPE), (dict(stride_n=136), SHAPE),
-    (dict(stride_h=256 * 128 + 8), SHAPE), (dict(stride_b=-16), SHAPE), (dict(n_cap=255), SHAPE),
-    (dict(block_table=P.value, page_rows=8, pages_per_seq=64, n_pages=64), SHAPE),
-    (dict(block_table=P.value, page_rows=24, pages_per_seq=64, n_pages=64), SHAPE),
+    (dict(stride_h=(1 << 27) + 8), SHAPE), (dict(stride_b=-16), SHAPE), (dict(n_cap=(1 << 20) - 1), SHAPE),
+    (dict(block_table=P.value, page_rows=8, pages_per_seq=1 << 18, n_pages=64), SHAPE),
+    (dict(block_table=P.value, page_rows=24, pages_per_seq=1 << 18, n_pages=64), SHAPE),
     (dict(block_table=P.value, page_rows=16, pages_per_seq=0, n_pages=64), SHAPE),
-    (dict(block_table=P.value, page_rows=16, pages_per_seq=15, n_pages=64), SHAPE),
-    (dict(block_table=P.value, page_rows=16, pages_per_seq=16, n_pages=0), SHAPE),
+    (dict(block_table=P.value, page_rows=16, pages_per_seq=(1 << 16) - 1, n_pages=64), SHAPE),
+    (dict(block_table=P.value, page_rows=16, pages_per_seq=1 << 16, n_pages=0), SHAPE),
 ]
 
 
-def dense8(lib, c, n_max=256, batch=2, h_kv=8, h_q=32, d=128, q=P, out=P, out_type=0, scratch=P, nbytes=1 << 40,
+def dense8(lib, c, n_max=1 << 20, batch=2, h_kv=8, h_q=32, d=128, q=P, out=P, out_type=0, scratch=P, nbytes=1 << 40,
            lengths=P):
     return lib.dense_decode8(C.byref(c) if c else None, lengths, n_max, batch, h_kv, h_q, d, q, out, out_type, scratch,
                              nbytes, None)
 
 
-def diff(lib, c, n_max=256, batch=2, h_kv=8, h_q=32, d=128, q=P, out=P, out_type=0, scratch=P, nbytes=1 << 40,
+def diff(lib, c, n_max=1 << 20, batch=2, h_kv=8, h_q=32, d=128, q=P, out=P, out_type=0, scratch=P, nbytes=1 << 40,
          lengths=P, prm=None, **kw):
     base = dict(lam=P.value, gamma=P.value, lam_heads=1, lambda_init=0.5, eps=1e-5)
     base.update(kw)
@@ -62,7 +62,7 @@ def test_decode_refusals(lib, call):
     most = 16 if call is dense8 else 8
     for kw, why in [(dict(n_max=0), ARG), (dict(batch=0), ARG), (dict(h_kv=0), ARG), (dict(h_q=0), ARG),
                     (dict(d=64), SHAPE), (dict(h_q=33), SHAPE), (dict(h_kv=1, h_q=most + 1), SHAPE),
-                    (dict(n_max=257), SHAPE), (dict(batch=1 << 28), SHAPE), (dict(q=None), ARG), (dict(q=ODD), ARG),
+                    (dict(n_max=(1 << 20) + 1), SHAPE), (dict(batch=1 << 28), SHAPE), (dict(q=None), ARG), (dict(q=ODD), ARG),
                     (dict(out=None), ARG), (dict(out=ODD), ARG), (dict(out_type=2), ARG), (dict(scratch=None), ARG),
                     (dict(scratch=ODD), ARG), (dict(lengths=None), ARG), (dict(nbytes=16), SMALL)]:
         assert call(lib, cache(), **kw) == why, kw
@@ -75,12 +75,13 @@ def test_diff_parameter_refusals(lib):
                     (dict(lam_heads=8), SHAPE), (dict(lam_heads=0), SHAPE), (dict(eps=0.0), ARG),
                     (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG), (dict(lambda_init=float("inf")), ARG)]:
         assert diff(lib, cache(), **kw) == why, kw
-    assert lib.mog_diff_decode(C.byref(cache()), P, 256, 2, 8, 32, 128, P, None, P, 0, P, 1 << 40, None) == ARG
+    assert lib.mog_diff_decode(C.byref(cache()), P, 1 << 20, 2, 8, 32, 128, P, None, P, 0, P, 1 << 40, None) == ARG
 
 
 def test_scratch_grows_with_the_heads_and_maps(lib):
-    a, b = mog.dense8_scratch_bytes(2, 8, 8, 4096), mog.dense8_scratch_bytes(2, 8, 16, 4096)
-    assert b == 2 * a and mog.diff_scratch_bytes(2, 8, 8, 4096) == 2 * a
+    a, b = mog.dense8_scratch_bytes(2, 8, 8, 1 << 20), mog.dense8_scratch_bytes(2, 8, 16, 1 << 20)
+    assert a > 0 and b == 2 * a and mog.diff_scratch_bytes(2, 8, 8, 1 << 20) == 2 * a
+    assert mog.dense8_scratch_bytes(1, 1, 1, 64) == 0  # short: one launch without scratch
     with pytest.raises(mog.MogError, match="SHAPE"):
         mog.diff_scratch_bytes(1, 1, 9, 4096)
 
@@ -90,7 +91,7 @@ def test_store_refusals(lib):
         return lib.mog_kv_store(C.byref(c) if c else None, batch, h_kv, d, t, pos, None, k, v, sb, st, sh, None)
 
     for kw, why in BAD_CACHES:
-        if "n_cap" not in kw and kw.get("pages_per_seq") != 15:  # (a store may have fewer positions)
+        if "n_cap" not in kw and kw.get("pages_per_seq") != (1 << 16) - 1:  # (a store may have fewer positions)
             assert store(cache(**kw)) == why, kw
     for kw, why in [(dict(batch=0), ARG), (dict(h_kv=0), ARG), (dict(t=0), ARG), (dict(d=256), SHAPE),
                     (dict(batch=65536), SHAPE), (dict(pos=None), ARG), (dict(k=None), ARG), (dict(v=ODD), ARG),

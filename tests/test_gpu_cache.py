@@ -168,22 +168,25 @@ LAYOUTS = [(0, True), (16, True), (64, False), (128, True)]
 
 # ---------------------------------------------------------------------------- dense8
 
+@pytest.mark.parametrize("slack", [0, 3000])  # one launch, clusters; two launches, the tile list split
 @pytest.mark.parametrize("out_type", OUTS)
 @pytest.mark.parametrize("page,hf", LAYOUTS)
 @pytest.mark.parametrize("lens,H,G", [((1,), 1, 1), ((0, 1, 63, 64, 65), 2, 4), ((1000,), 3, 5), ((3001, 17), 2, 8),
                                       ((130, 0, 777), 1, 16), ((500,), 2, 9)])
-def test_dense8(lens, H, G, page, hf, out_type):
-    m = Made(1, lens, H, page, heads_first=hf)
+def test_dense8(lens, H, G, page, hf, out_type, slack):
+    m = Made(1, lens, H, page, heads_first=hf, slack=slack)
+    assert (mog.dense8_scratch_bytes(m.B, H, H * G, m.n_max) == 0) == (m.n_max < 2000)
     q = queries(2, m.B, H * G)
     out = torch.full(q.shape, float("nan"), dtype=out_type, device=DEV)
     mog.dense_decode(*m.cache, m.lengths, m.n_max, q, out=out)
     check_dense8(m, q, out, G)
 
 
-def test_dense8_many_sequences_and_long_ones():
+@pytest.mark.parametrize("slack", [5, 3000])
+def test_dense8_many_sequences_and_long_ones(slack):
     g = torch.Generator().manual_seed(3)
     lens = tuple(int(x) for x in torch.randint(0, 300, (70,), generator=g))
-    m = Made(4, lens, 2, 16, slack=5)
+    m = Made(4, lens, 2, 16, slack=slack)
     q = queries(5, m.B, 4)
     check_dense8(m, q, mog.dense_decode(*m.cache, m.lengths, m.n_max, q), 2)
     m = Made(6, (70001, 33), 1, 64)
@@ -191,8 +194,9 @@ def test_dense8_many_sequences_and_long_ones():
     check_dense8(m, q, mog.dense_decode(*m.cache, m.lengths, m.n_max, q), 4)
 
 
-def test_dense8_scales_far_apart_and_zero():
-    m = Made(8, (777, 300), 2, 16, spread=40)
+@pytest.mark.parametrize("slack", [0, 3000])
+def test_dense8_scales_far_apart_and_zero(slack):
+    m = Made(8, (777, 300), 2, 16, spread=40, slack=slack)
     q = queries(9, 2, 4)
     check_dense8(m, q, mog.dense_decode(*m.cache, m.lengths, m.n_max, q), 2)
     # all value scales zero: zeros, not NaN
@@ -250,6 +254,7 @@ def test_dense8_is_deterministic_and_follows_lengths_in_a_graph():
     m = Made(18, (4000, 1200), 2, 64)
     q = queries(19, 2, 8)
     scratch = torch.empty(mog.dense8_scratch_bytes(2, 2, 8, m.n_max), dtype=torch.uint8, device=DEV)
+    assert scratch.numel() > 0
     out = torch.empty(q.shape, dtype=torch.float32, device=DEV)
     call = lambda o: mog.dense_decode(*m.cache, m.lengths, m.n_max, q, out=o, scratch=scratch)  # noqa: E731
     first = call(torch.empty_like(out)).clone()
@@ -302,13 +307,14 @@ def weights(seed, heads=None):
     return lam, 1 + 0.2 * randn(g, D)
 
 
+@pytest.mark.parametrize("slack", [0, 3000])
 @pytest.mark.parametrize("out_type", OUTS)
 @pytest.mark.parametrize("e4m3", [True, False])
 @pytest.mark.parametrize("page,hf", LAYOUTS)
 @pytest.mark.parametrize("lens,H,G", [((1,), 1, 1), ((0, 1, 63, 64, 65), 2, 4), ((1000,), 3, 3), ((2001, 17), 2, 8),
                                       ((300, 0, 77), 1, 5)])
-def test_diff(lens, H, G, page, hf, e4m3, out_type):
-    m = Made(31, lens, H, page, e4m3=e4m3, heads_first=hf)
+def test_diff(lens, H, G, page, hf, e4m3, out_type, slack):
+    m = Made(31, lens, H, page, e4m3=e4m3, heads_first=hf, slack=slack)
     q = queries(32, m.B, H * G)
     lam, gamma = weights(33)
     out = torch.full(q.shape, float("nan"), dtype=out_type, device=DEV)
@@ -325,12 +331,13 @@ def test_diff_weights_per_head_and_no_gamma(e4m3):
     check_diff(m, q, out, 3, lam, 0.2, None, 1e-6, e4m3)
 
 
+@pytest.mark.parametrize("slack", [0, 3000])
 @pytest.mark.parametrize("e4m3", [True, False])
-def test_diff_many_sequences_and_long_ones(e4m3):
+def test_diff_many_sequences_and_long_ones(e4m3, slack):
     g = torch.Generator().manual_seed(37)
     lens = tuple(int(x) for x in torch.randint(0, 200, (40,), generator=g))
     lam, gamma = weights(38)
-    m = Made(39, lens, 2, 16, e4m3=e4m3)
+    m = Made(39, lens, 2, 16, e4m3=e4m3, slack=slack)
     q = queries(40, m.B, 4)
     check_diff(m, q, mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma), 2, lam, 0.5, gamma, 1e-5, e4m3)
     m = Made(41, (50001,), 1, 64, e4m3=e4m3)
@@ -379,9 +386,10 @@ def test_diff_bf16_pages_that_do_not_exist_are_left_out():
     check_diff(m, q, out, 2, lam, 0.5, gamma, 1e-5, False, lens=(int(keep.sum()),))
 
 
+@pytest.mark.parametrize("slack", [0, 3000])
 @pytest.mark.parametrize("e4m3", [True, False])
-def test_diff_in_a_graph(e4m3):
-    m = Made(52, (3000, 100), 2, 16, e4m3=e4m3)
+def test_diff_in_a_graph(e4m3, slack):
+    m = Made(52, (2000, 100), 2, 16, e4m3=e4m3, slack=slack)
     q = queries(53, 2, 4)
     lam, gamma = weights(54)
     mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma)
@@ -389,7 +397,7 @@ def test_diff_in_a_graph(e4m3):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out = mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma)
-    for lens in ((3000, 100), (5, 0), (2999, 65)):
+    for lens in ((2000, 100), (5, 0), (1999, 65)):
         m.lengths.copy_(torch.tensor(lens, dtype=torch.int32))
         graph.replay()
         torch.cuda.synchronize()
@@ -531,8 +539,10 @@ def test_python_refusals():
             mog.dense_decode(c, None, **{**ok, **kw})
         with pytest.raises(ValueError):
             mog.diff_decode(c, None, **{**ok, **kw}, lam=lam, lambda_init=0.5)
+    long = Made(64, (64,), 2, 16, slack=4000)
     with pytest.raises(mog.MogError, match="ARENA"):
-        mog.dense_decode(c, None, **ok, scratch=torch.empty(64, dtype=torch.uint8, device=DEV))
+        mog.dense_decode(long.cache[0], None, long.lengths, long.n_max, q,
+                         scratch=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(mog.MogError, match="SHAPE"):
         mog.diff_decode(c, None, m.lengths, 64, queries(67, 1, 18), lam, 0.5)
     for w in (lam.double(), lam[:3], lam[:, :32].contiguous(), lam[None].expand(3, -1, -1).contiguous()):
