@@ -1,5 +1,7 @@
 // cache.cu -- decode attentions over a mog_cache: the fold of the split form's partials and
 // the launches; and the store that writes a cache.
+#include <algorithm>
+
 #include "cache.cuh"
 
 namespace mog {
@@ -104,11 +106,11 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
                 (float)(LOG2E / sqrt(diff ? MOG_D / 2.0 : (double)MOG_D)), cache_cluster(batch * h_kv, n_max)};
     DiffArgs d{};
     if (diff) d = DiffArgs{diff->lam, diff->lam_heads > 1 ? 4 * (MOG_D / 2) : 0, diff->gamma, diff->lambda_init, diff->eps};
-    const int splits = cache_splits(batch * h_kv, n_max);
     const bool wide = (diff ? 2 : 1) * G > 8;
-    static_assert(Tile<true, true>::ROWS == 64 && Tile<false, false>::ROWS == 64 && Tile<false, true>::ROWS == 64, "merge");
-    // (tiles of 128 rows: as many CTAs as tiles do)
-    while (e4 && !wide && a.cs > 1 && a.cs / 2 >= ceil_div64(n_max, Tile<true, false>::ROWS)) a.cs /= 2;
+    const int per_sm = !e4 ? 3 : wide ? Tile<true, true>::PER_SM : Tile<true, false>::PER_SM;
+    const int rows = !e4 ? 64 : wide ? Tile<true, true>::ROWS : Tile<true, false>::ROWS;
+    const int splits = std::min(cache_splits(batch * h_kv, n_max), per_sm * num_sms());
+    while (a.cs > 1 && a.cs / 2 >= ceil_div64(n_max, rows)) a.cs /= 2;  // as many CTAs as tiles do
     const cudaError_t e = e4 ? launch_split8(a, d, out, diff != nullptr, bf_out, wide, splits, s)
                           : bf_out ? pick_split<false, true, 2>(a, d, out, wide, splits, s)
                                    : pick_split<false, true, 3>(a, d, out, wide, splits, s);
@@ -122,8 +124,8 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (e4 && !wide) return launch_merge<Tile<true, false>::ROWS>(cfg, diff, bf_out, a, d, out, splits);
-    return launch_merge<64>(cfg, diff, bf_out, a, d, out, splits);
+    return rows == 128 ? launch_merge<128>(cfg, diff, bf_out, a, d, out, splits)
+                       : launch_merge<64>(cfg, diff, bf_out, a, d, out, splits);
 }
 
 // ------------------------------------------------------------------------------------

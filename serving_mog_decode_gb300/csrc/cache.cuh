@@ -24,7 +24,7 @@
 // permuted alike in K and q, and back in the output), then widened in registers to fp16,
 // which holds every e4m3 value exactly.  q enters as fp16 scaled by a power of two of its
 // own, so that its elements down to 2^-29 of the largest are exact.  Weights enter the P.V
-// product as fp16 (scaled p * v_scale / running power of two >= v_scale): high part alone
+// product as fp16 (2^14 * p * v_scale / running power of two >= v_scale): high part alone
 // (2^-12 relative) when the output is rounded to bf16, high + low parts (2^-22) when it
 // stays fp32.  bf16 rows go through ldmatrix; their weights are bf16 high + low parts for
 // a bf16 output (2^-17) and three parts (2^-24) for an fp32 one.  All sums are fp32.
@@ -40,6 +40,7 @@ namespace mog {
 
 constexpr int CT_WARPS = 4;
 constexpr int CT_THREADS = 32 * CT_WARPS;
+constexpr float W_SCALE = 16384.f;  // 2^14: scale of fp16 weights
 
 // A tile is copied by the whole CTA, 2 KB of neighbouring rows per instruction, and each
 // warp consumes BLK blocks of 16 of its rows.  Stages are aligned to 128 bytes: 16 bytes off,
@@ -47,28 +48,24 @@ constexpr int CT_THREADS = 32 * CT_WARPS;
 template <bool E4M3_, bool WIDE_>
 struct Tile {
     static constexpr bool E4M3 = E4M3_, WIDE = WIDE_;
-    static constexpr int BLK = E4M3 && !WIDE ? 2 : 1;     // blocks of 16 rows per warp
+    static constexpr int BLK = E4M3 ? 2 : 1;              // blocks of 16 rows per warp
     static constexpr int WROWS = 16 * BLK;                // rows per warp
     static constexpr int ROWS = CT_WARPS * WROWS;
+    // Three CTAs per SM, but two of the wide e4m3 form: it is bound by the latencies of its
+    // longer chains, which 255 registers (32 rows a warp in flight, no spills) hide better than
+    // a third CTA (16 heads, 512K: 202 us against 231 with three CTAs and 16 rows a warp).
+    static constexpr int PER_SM = E4M3 && WIDE ? 2 : 3;
     static constexpr int ROW = E4M3 ? MOG_D : 2 * MOG_D;  // bytes
     static constexpr int KV = ROWS * ROW;                 // bytes of the K or V tile: 16 KB
     static constexpr int AUX = 2 * KV;                    // K scales, V scales
     static constexpr int MASK = AUX + (E4M3 ? 2 * ROWS * 4 : 0);  // bit per row
     static constexpr int STAGE = MASK + 128;              // rows stay aligned to 128 bytes
-    static constexpr int STAGES = 2;  // one in flight: 96 KB per SM with 3 CTAs of 32 KB stages
+    static constexpr int STAGES = E4M3 && WIDE ? 3 : 2;   // 32 KB each: 96 KB or more in flight per SM
     static constexpr int COLS = WIDE ? 16 : 8;
-    // The wide e4m3 form accumulates on the tensor cores over BANK_TILES tiles and then adds
-    // to fp32 sums in shared memory, which the other forms do in registers for every tile:
-    // there its 64 accumulators' rescaling is a tenth of the instructions that bind it.
-    // Its maxima may lag the true ones by 2^LAG, so that it rarely has to rescale at all.
-    static constexpr bool BANK = E4M3 && WIDE;
-    static constexpr int BANK_TILES = 16, LAG = 8;
-    static constexpr float W = BANK ? 64.f : 16384.f;     // scale of fp16 weights, 2^14 at most with the lag
     static constexpr int XCH = 2 * COLS * MOG_D * 4;      // two warps' accumulators, in a consumed stage
     // a cluster's CTA leaves its partial behind that in stage 0, or behind the stages
     static constexpr int PART = STAGE >= XCH + COLS * PART_W * 4 ? XCH : STAGES * STAGE;
-    static constexpr int SMEM_CLUSTER = STAGES * STAGE + (PART == XCH ? 0 : COLS * PART_W * 4);
-    static constexpr int SMEM = STAGES * STAGE + (BANK ? CT_THREADS * COLS * 4 * 4 : 0);
+    static constexpr int SMEM = STAGES * STAGE + (PART == XCH ? 0 : COLS * PART_W * 4);
 };
 
 struct CacheArgs {
@@ -242,7 +239,7 @@ struct State {
     static constexpr int NT = WIDE ? 16 : 8;
     float o[NT][4];
     float m[2], l[2];  // maximum (log2 domain); this lane's share of the sum
-    float vr;  // e4m3: power of two >= every v_scale seen (0: none yet); o is in units of vr / T::W
+    float vr;  // e4m3: power of two >= every v_scale seen (0: none yet); o is in units of vr / W_SCALE
     __device__ __forceinline__ void init() {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -495,7 +492,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
                 for (int e = 0; e < 4; ++e) st.o[i][e] *= f;
             st.vr = vr;
         }
-        inv = st.vr > 0.f ? T::W / st.vr : 0.f;  // (rows whose scales are all 0 have no unit yet)
+        inv = st.vr > 0.f ? W_SCALE / st.vr : 0.f;  // (rows whose scales are all 0 have no unit yet)
     }
 
     // maxima, rescale factors, weights
@@ -511,17 +508,11 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
         for (int o = WIDE ? 1 : 4; o < (WIDE ? 4 : 32); o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         // the shift: 0 until a row has been seen, so that no infinities are subtracted
-        const float mn = T::BANK ? (mx > st.m[c] + T::LAG ? mx : st.m[c]) : fmaxf(st.m[c], mx);
+        const float mn = fmaxf(st.m[c], mx);
         sh[c] = mn == -INFINITY ? 0.f : mn;
-        al[c] = T::BANK && mn == st.m[c] ? 1.f : ex2(st.m[c] - sh[c]);
+        al[c] = ex2(st.m[c] - sh[c]);
         st.m[c] = mn;
         st.l[c] *= al[c];
-    }
-    if (T::BANK && __any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < State<WIDE>::NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st.o[i][e] *= al[State<WIDE>::col(e)];
     }
     uint32_t pf[BLK][PARTS][NS / 2];  // weights as the second product's operand
 #pragma unroll
@@ -560,13 +551,12 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
             for (int k = PARTS - 1; k >= 0; --k) {
                 if (WIDE) {
                     const uint32_t p[4] = {pf[blk][k][0], pf[blk][k][1], pf[blk][k][NS / 2 - 2], pf[blk][k][NS / 2 - 1]};
-                    mma_t<E4M3>(T::BANK ? st.o[(2 * mt) % State<WIDE>::NT] : d[0], p, a[blk][0], a[blk][2]);
-                    mma_t<E4M3>(T::BANK ? st.o[(2 * mt + 1) % State<WIDE>::NT] : d[WIDE ? 1 : 0], p, a[blk][1], a[blk][3]);
+                    mma_t<E4M3>(d[0], p, a[blk][0], a[blk][2]);
+                    mma_t<E4M3>(d[WIDE ? 1 : 0], p, a[blk][1], a[blk][3]);
                 } else {
                     mma_t<E4M3>(d[0], a[blk], pf[blk][k][0], pf[blk][k][1]);
                 }
             }
-        if (T::BANK) return;
 #pragma unroll
         for (int k = 0; k < (WIDE ? 2 : 1); ++k)
 #pragma unroll
@@ -603,36 +593,6 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
             add(mt, a);
         }
     }
-}
-
-// The wide e4m3 form's fp32 sums: word i of the lane at x[i * 32], with the maxima and the
-// value unit that they were last added at.
-struct Bank {
-    float m[2], vr;
-    __device__ __forceinline__ void init() { m[0] = m[1] = -INFINITY, vr = 0.f; }
-};
-// Adds the state to the sums (fresh: there are none yet) and leaves it empty, or (TAKE) adds
-// the sums to the state.
-template <bool TAKE>
-__device__ __forceinline__ void bank_add(State<true> &st, Bank &bk, float *x) {
-    float f[2];
-    const bool fresh = bk.vr == 0.f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) f[c] = fresh ? 0.f : ex2(bk.m[c] - (st.m[c] == -INFINITY ? 0.f : st.m[c])) * (bk.vr / st.vr);
-#pragma unroll
-    for (int i = 0; i < State<true>::NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float &o = st.o[i][e];
-            const float sum = fresh ? o : fmaf(x[(4 * i + e) * 32], f[State<true>::col(e)], o);
-            if (TAKE) {
-                o = sum;
-            } else {
-                x[(4 * i + e) * 32] = sum;
-                o = 0.f;
-            }
-        }
-    bk.m[0] = st.m[0], bk.m[1] = st.m[1], bk.vr = st.vr;
 }
 
 // A unit's end: the four warps' states become one partial in `dst` ([columns][PART_W]).
@@ -687,7 +647,7 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
     constexpr int SW = S::NT * 4 * 32;  // words of a warp's accumulators
     static_assert(T::XCH == 2 * SW * 4 && T::AUX >= T::XCH, "two states fit in a stage");
     if (E4M3) {  // to the values' own unit
-        const float u = st.vr / T::W;
+        const float u = st.vr / W_SCALE;
 #pragma unroll
         for (int i = 0; i < S::NT; ++i)
 #pragma unroll
@@ -844,7 +804,7 @@ __device__ __forceinline__ void cluster_end(const CacheArgs &a, const DiffArgs &
 // CLUSTER: the form with a cluster of a.cs CTAs per unit (a kernel of its own: the two in one cost
 // the split form registers and 14% of its speed).
 template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS, bool CLUSTER>
-__global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
+__global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE>::PER_SM) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
     extern __shared__ __align__(128) uint8_t csm[];
     __shared__ Exchange ex;
     __shared__ QShared qs;  // (wide)
@@ -896,14 +856,6 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a, Diff
     load_q<E4M3, DIFF, WIDE>(qf, qs, a, unit);
     State<WIDE> st;
     st.init();
-    constexpr bool BANK = T::BANK && !CLUSTER;  // (a cluster's CTA has no more than 4 tiles)
-    Bank bk;
-    float *sums = nullptr;
-    int fill = 0;  // tiles since the last bank_add
-    if constexpr (BANK) {
-        bk.init();
-        sums = reinterpret_cast<float *>(csm + T::STAGES * T::STAGE) + (threadIdx.x >> 5) * T::COLS * 4 * 32 + (threadIdx.x & 31);
-    }
     int slot = 0;
     for (int i = 0; i < cnt; ++i) {
         cp_async_wait<T::STAGES - 2>();
@@ -911,16 +863,6 @@ __global__ void __launch_bounds__(CT_THREADS, 3) k_cache_split(CacheArgs a, Diff
         feed(stages + (slot == 0 ? T::STAGES - 1 : slot - 1) * T::STAGE);
         compute<T, DIFF, PARTS>(st, qf, qs, stages + slot * T::STAGE);
         const bool end = cc.last();
-        if constexpr (BANK) {
-            if (end || i == cnt - 1) {
-                bank_add<true>(st, bk, sums);
-                bk.init();
-                fill = 0;
-            } else if (++fill == T::BANK_TILES) {
-                if (st.vr > 0.f) bank_add<false>(st, bk, sums);
-                fill = 0;
-            }
-        }
         if (end || i == cnt - 1) {
             float *dst = CLUSTER ? reinterpret_cast<float *>(csm + T::PART)
                               : a.part + ((int64_t)blockIdx.x + unit) * G2 * PART_W;
@@ -943,13 +885,12 @@ template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
 static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out, int splits, cudaStream_t s) {
     using T = Tile<E4M3, WIDE>;
     const auto fn = a.cs ? k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS, true> : k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS, false>;
-    const int smem = a.cs ? T::SMEM_CLUSTER : T::SMEM;
-    const cudaError_t e = ensure_smem((const void *)fn, smem);
+    const cudaError_t e = ensure_smem((const void *)fn, T::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.cs ? a.cs * a.batch * a.h_kv : splits);
     cfg.blockDim = dim3(CT_THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = T::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
