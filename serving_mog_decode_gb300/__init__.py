@@ -760,6 +760,8 @@ class PagePool:
                         self.lengths.data_ptr(), self.refs.data_ptr(), self.work.data_ptr(), need.value, self._descs,
                         len(pools))
         self.batch = batch
+        self.pos, self.granted = torch.zeros_like(self.lengths), torch.zeros_like(self.lengths)
+        self._pos_ptr, self._granted_ptr = self.pos.data_ptr(), self.granted.data_ptr()
 
     def cache(self, layer=0):
         """The paged cache of a layer (PagedKV or PagedKV8), for the calls that take one."""
@@ -785,16 +787,12 @@ class PagePool:
 
     def grow(self, n_new, stream=None):
         """Room for n_new[b] more tokens of every sequence (mog_pages_grow); a shared last page
-        becomes private.  -> (pos, granted) int32 [batch]: where kv_store puts the new rows, and
-        how many (0 everywhere if there was no room: see status())."""
+        becomes private.  -> (self.pos, self.granted), int32 [batch]: where kv_store puts the new
+        rows, and how many (0 everywhere if there was no room: see status()).  They are the
+        same two tensors every time: the next grow overwrites them."""
         _check_counts(n_new, self.batch, self.device, "n_new")
-        if stream is not None:
-            with _there(self.device, stream):
-                return self.grow(n_new)
-        torch = _torch()
-        pos, granted = torch.empty_like(n_new), torch.empty_like(n_new)
-        self._call("mog_pages_grow", None, n_new.data_ptr(), pos.data_ptr(), granted.data_ptr())
-        return pos, granted
+        self._call("mog_pages_grow", stream, n_new.data_ptr(), self._pos_ptr, self._granted_ptr)
+        return self.pos, self.granted
 
     def compact(self, stream=None):
         """Move the pages in use to the front of the pools (mog_pages_compact)."""

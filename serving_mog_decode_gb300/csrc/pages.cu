@@ -42,27 +42,35 @@ struct PoolArgs {
 };
 
 // ---------------------------------------------------------------------------- assign
-// table_new[b] = table_old[src[b]].  Every CTA owns a block of table columns: it loads them
-// for all sequences into shared memory before it writes any of them, so that sequences may
-// take each other's pages in any pattern, in one launch.
-constexpr int AS_THREADS = 256;
+// table_new[b] = table_old[src[b]].  Every CTA owns eight table columns (a 32-byte sector of
+// each row): it loads them for all sequences into shared memory before it writes any of
+// them, so that sequences may take each other's pages in any pattern, in one launch.
+// 64 rows go at a time, four of them in flight per thread: 288 rows of 129 pages take 3 us (32
+// columns and an integer division per entry: 13 us).
+constexpr int AS_THREADS = 512, AS_COLS = 8, AS_STEP = AS_THREADS / AS_COLS;
 
-__global__ void __launch_bounds__(AS_THREADS) k_pages_assign(PagesArgs a, const int *src, int cols) {
-    extern __shared__ int old[];  // [batch][cols]
-    const int c0 = blockIdx.x * cols, nc = min(cols, a.pps - c0);
-    const int n = a.batch * nc;
-    for (int i = threadIdx.x; i < n; i += AS_THREADS) {
-        const int b = i / nc, c = i - b * nc;
-        old[i] = a.table[(int64_t)b * a.pps + c0 + c];
+__global__ void __launch_bounds__(AS_THREADS) k_pages_assign(PagesArgs a, const int *src) {
+    extern __shared__ int old[];  // [batch][AS_COLS], then [batch] sources
+    int *from = old + a.batch * AS_COLS;
+    const int c = threadIdx.x % AS_COLS, r = threadIdx.x / AS_COLS, col = blockIdx.x * AS_COLS + c;
+    const bool in = col < a.pps;
+#pragma unroll 4
+    for (int b = r; b < a.batch; b += AS_STEP)
+        if (in) old[b * AS_COLS + c] = a.table[(int64_t)b * a.pps + col];
+    for (int b = threadIdx.x; b < a.batch; b += AS_THREADS) {
+        const int s = src[b];
+        const bool bad = s < -1 || s >= a.batch;
+        from[b] = bad ? b : s;  // (a bad source: the sequence stays as it is)
+        if (bad && blockIdx.x == 0) atomicOr(a.work + PW_STATUS, PAGES_BAD_INDEX);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += AS_THREADS) {
-        const int b = i / nc, c = i - b * nc;
-        const int s = src[b];
-        if (s == b || s < -1 || s >= a.batch) continue;  // stays (bad indices are flagged below)
-        const int was = old[i], now = s < 0 ? -1 : old[s * nc + c];
+#pragma unroll 4
+    for (int b = r; b < a.batch; b += AS_STEP) {
+        const int s = from[b];
+        if (s == b || !in) continue;
+        const int was = old[b * AS_COLS + c], now = s < 0 ? -1 : old[s * AS_COLS + c];
         if (was == now) continue;
-        a.table[(int64_t)b * a.pps + c0 + c] = now;
+        a.table[(int64_t)b * a.pps + col] = now;
         if ((unsigned)was < (unsigned)a.n_pages) atomicAdd(a.refs + was, -1);
         if ((unsigned)now < (unsigned)a.n_pages) atomicAdd(a.refs + now, 1);
         if (was >= a.n_pages || was < -1 || now >= a.n_pages || now < -1) atomicOr(a.work + PW_STATUS, PAGES_BAD_INDEX);
@@ -72,9 +80,8 @@ __global__ void __launch_bounds__(AS_THREADS) k_pages_assign(PagesArgs a, const 
     for (int b = threadIdx.x; b < a.batch; b += AS_THREADS) old[b] = a.lengths[b];
     __syncthreads();
     for (int b = threadIdx.x; b < a.batch; b += AS_THREADS) {
-        const int s = src[b];
-        if (s < -1 || s >= a.batch) atomicOr(a.work + PW_STATUS, PAGES_BAD_INDEX);
-        else if (s != b) a.lengths[b] = s < 0 ? 0 : old[s];
+        const int s = from[b];
+        if (s != b) a.lengths[b] = s < 0 ? 0 : old[s];
     }
 }
 
@@ -362,11 +369,10 @@ static cudaError_t launch_copies(const mog_pages *p, const PagesArgs &a, int64_t
 
 cudaError_t launch_pages_assign(const mog_pages *p, const int32_t *src, cudaStream_t s) {
     const PagesArgs a = pages_args(p);
-    // as many columns as 48 KB hold, 32 at most (a 128-byte line of the table): more CTAs, less each
-    int cols = 48 * 1024 / 4 / p->batch;
-    cols = cols > 32 ? 32 : cols < 1 ? 1 : cols;
-    if (cols > p->pages_per_seq) cols = p->pages_per_seq;
-    k_pages_assign<<<(unsigned)ceil_div64(p->pages_per_seq, cols), AS_THREADS, (size_t)cols * p->batch * 4, s>>>(a, src, cols);
+    const size_t smem = (size_t)p->batch * (AS_COLS + 1) * 4;
+    const cudaError_t e = ensure_smem((const void *)k_pages_assign, smem);
+    if (e != cudaSuccess) return e;
+    k_pages_assign<<<(unsigned)ceil_div64(p->pages_per_seq, AS_COLS), AS_THREADS, smem, s>>>(a, src);
     return cudaGetLastError();
 }
 
