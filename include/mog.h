@@ -523,7 +523,7 @@ typedef struct mog_cache {
  *  scratch_dev : at least dense_decode8_scratch_bytes() bytes, 16-byte aligned; no initial
  *                contents needed, not shared by calls that overlap on the GPU.  Short
  *                caches need none (0 bytes; scratch_dev may then be NULL)
- * d must be 128, h_q / h_kv <= 16.
+ * d must be 128, h_q / h_kv <= 16, n_max <= 2^30.
  */
 int dense_decode8_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t n_max,
                                 size_t *bytes);
@@ -563,7 +563,7 @@ int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_ma
  *  pos_dev, count_dev   : int32[batch] on the device; count NULL: t_max for every sequence
  *                         (counts are clamped to [0, t_max])
  *  k_new_dev, v_new_dev : bf16, element (b, t, h, j) at b*new_b + t*new_t + h*new_h + j;
- *                         strides multiples of 8, 16-byte aligned
+ *                         strides multiples of 8, 16-byte aligned; t_max * 2 * h_kv <= 2^30
  * An e4m3 row's scale is the least power of two 2^e, e >= -126, with
  * amax <= 448 * 2^e, amax the row's largest finite magnitude (scale 1 if that is 0); its
  * codes are x / 2^e (exact) rounded to nearest even, infinities saturated, NaN kept.  Rows

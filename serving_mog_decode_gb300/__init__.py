@@ -102,6 +102,12 @@ class Pages(C.Structure):
                 ("pools", C.POINTER(PagePoolDesc)), ("n_pools", C.c_int32)]
 
 
+def _strides(t):
+    """Strides of a tensor's first three dims, 0 where there is only one entry (its stride may
+    be anything)."""
+    return [st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride())]
+
+
 def _check_rows8(K, V, k_scale, v_scale):
     torch = _torch()
     for t in (K, V):
@@ -130,7 +136,7 @@ class KV8:
         self.batch, self.h_kv, self.device = K.shape[0], K.shape[1], K.device
         self.positions = K.shape[2]
         self.cache = Cache(1, K.shape[2], K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                           *K.stride()[:3], *k_scale.stride(), None, 0, 0, 0)
+                           *_strides(K)[:2], K.stride(2), *_strides(k_scale), None, 0, 0, 0)
 
 
 class PagedKV8:
@@ -150,7 +156,7 @@ class PagedKV8:
         self.batch, self.h_kv = block_table.shape[0], K.shape[1 if heads_first else 2]
         self.positions, self.device = block_table.shape[1] * page_rows, K.device
         h, n = (1, 2) if heads_first else (2, 1)
-        ks, ss = K.stride(), k_scale.stride()
+        ks, ss = _strides(K), _strides(k_scale)
         self.cache = Cache(1, 0, K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ks[0], ks[h],
                            ks[n], ss[0], ss[h], ss[n], block_table.data_ptr(), page_rows, block_table.shape[1],
                            K.shape[0])
@@ -176,13 +182,14 @@ def _cache(K, V):
         if v.device != k.device or shape[3] != 128 or shape[n] != rows:
             raise ValueError("page pools must share a device and hold page_rows rows of 128")
         per = t.shape[1]
-        return Cache(0, 0, k.data_ptr(), v.data_ptr(), None, None, st[0], st[h], st[n], 0, 0, 0, t.data_ptr(), rows,
-                     per, shape[0]), t.shape[0], shape[h], per * rows, k.device
+        return Cache(0, 0, k.data_ptr(), v.data_ptr(), None, None, st[0] if shape[0] > 1 else 0,
+                     st[h] if shape[h] > 1 else 0, st[n], 0, 0, 0, t.data_ptr(), rows, per, shape[0]), t.shape[0], shape[h], per * rows, k.device
     kv = _kv(K, V)
     if V.device != K.device or K.shape[3] != 128:
         raise ValueError("K and V must share a device and have rows of 128")
-    c = Cache(0, K.shape[2], kv.k, kv.v, None, None, kv.stride_b, kv.stride_h, kv.stride_n)
-    return c, K.shape[0], K.shape[1], K.shape[2], K.device
+    shape, st = K.shape, K.stride()
+    c = Cache(0, shape[2], kv.k, kv.v, None, None, st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0, st[2])
+    return c, shape[0], shape[1], shape[2], K.device
 
 
 class Layout(C.Structure):
@@ -736,6 +743,10 @@ class PagePool:
         self.device, n_pages = first.device, first.shape[0]
         self.heads_first, self.page_rows = heads_first, first.shape[2 if heads_first else 1]
         pools = [t for x in lists for t in x]
+        rows = torch.float8_e4m3fn if len(lists) == 4 else torch.bfloat16
+        if any(t.dtype != rows or t.dim() != 4 or t.shape != first.shape for t in self.K + self.V) or any(
+                t.dtype != torch.float32 or t.dim() != 3 for x in lists[2:] for t in x):
+            raise ValueError("K and V must be bf16 pools of one shape, or float8_e4m3fn with float32 k_scale and v_scale")
         for t in pools:
             if not t.is_cuda or t.device != self.device or t.shape[:3] != first.shape[:3] or not t[0].is_contiguous():
                 raise ValueError("page pools must share a CUDA device and their first three dims, a page contiguous")

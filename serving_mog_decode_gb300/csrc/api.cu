@@ -914,8 +914,8 @@ static int cache_scratch(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, in
                          size_t *bytes) {
     if (!bytes || batch <= 0 || h_kv <= 0 || h_q <= 0 || n_max <= 0) return MOG_ERR_INVALID_ARG;
     if (d != MOG_D || h_q % h_kv != 0 || h_q / h_kv > max_g) return MOG_ERR_SHAPE;
-    // the kernels count tiles and heads in 32 bits
-    if ((int64_t)batch * h_q > INT32_MAX / 2 || (int64_t)batch * h_kv * ceil_div64(n_max, 64) > INT32_MAX / 2)
+    // the kernels count rows, tiles and heads in 32 bits
+    if (n_max > (1 << 30) || (int64_t)batch * h_q > INT32_MAX / 2 || (int64_t)batch * h_kv * ceil_div64(n_max, 64) > INT32_MAX / 2)
         return MOG_ERR_SHAPE;
     const int units = batch * h_kv;
     *bytes = cache_cluster(units, n_max) ? 0 : ((size_t)units + cache_splits(units, n_max)) * maps * (h_q / h_kv) * (MOG_D + 4) * sizeof(float);
@@ -1011,7 +1011,7 @@ static int check_pages(const mog_pages *p) {
     if (((uintptr_t)p->block_table | (uintptr_t)p->lengths | (uintptr_t)p->refs | (uintptr_t)p->work) & 3)
         return MOG_ERR_INVALID_ARG;
     if (p->work_bytes < need) return MOG_ERR_ARENA_TOO_SMALL;
-    if (p->n_pools < 0 || (p->n_pools > 0 && !p->pools)) return MOG_ERR_INVALID_ARG;
+    if (p->n_pools <= 0 || !p->pools) return MOG_ERR_INVALID_ARG;
     for (int i = 0; i < p->n_pools; ++i) {
         const mog_page_pool &l = p->pools[i];
         if (!l.base || !aligned16(l.base)) return MOG_ERR_INVALID_ARG;

@@ -270,6 +270,7 @@ __device__ __forceinline__ float load_column(uint32_t (&w)[8][2], const CacheArg
     int map, head;
     column<DIFF, WIDE>(c, map, head);
     const bool have = head < a.G;
+    unit = min(unit, a.batch * a.h_kv - 1);  // (lengths that change under a call must not lead out of q)
     const uint16_t *row = a.q + ((int64_t)unit * a.G + (have ? head : 0)) * MOG_D;
     if (!E4M3) {
 #pragma unroll

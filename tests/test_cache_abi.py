@@ -62,7 +62,7 @@ def test_decode_refusals(lib, call):
     most = 16 if call is dense8 else 8
     for kw, why in [(dict(n_max=0), ARG), (dict(batch=0), ARG), (dict(h_kv=0), ARG), (dict(h_q=0), ARG),
                     (dict(d=64), SHAPE), (dict(h_q=33), SHAPE), (dict(h_kv=1, h_q=most + 1), SHAPE),
-                    (dict(n_max=(1 << 20) + 1), SHAPE), (dict(batch=1 << 28), SHAPE), (dict(q=None), ARG), (dict(q=ODD), ARG),
+                    (dict(n_max=(1 << 20) + 1), SHAPE), (dict(n_max=(1 << 30) + 1), SHAPE), (dict(batch=1 << 28), SHAPE), (dict(q=None), ARG), (dict(q=ODD), ARG),
                     (dict(out=None), ARG), (dict(out=ODD), ARG), (dict(out_type=2), ARG), (dict(scratch=None), ARG),
                     (dict(scratch=ODD), ARG), (dict(lengths=None), ARG), (dict(nbytes=16), SMALL)]:
         assert call(lib, cache(), **kw) == why, kw
@@ -94,7 +94,7 @@ def test_store_refusals(lib):
         if "n_cap" not in kw and kw.get("pages_per_seq") != (1 << 16) - 1:  # (a store may have fewer positions)
             assert store(cache(**kw)) == why, kw
     for kw, why in [(dict(batch=0), ARG), (dict(h_kv=0), ARG), (dict(t=0), ARG), (dict(d=256), SHAPE),
-                    (dict(batch=65536), SHAPE), (dict(pos=None), ARG), (dict(k=None), ARG), (dict(v=ODD), ARG),
+                    (dict(batch=65536), SHAPE), (dict(t=(1 << 26) + 1), SHAPE), (dict(pos=None), ARG), (dict(k=None), ARG), (dict(v=ODD), ARG),
                     (dict(sb=4), SHAPE), (dict(st=4), SHAPE), (dict(sh=130), SHAPE)]:
         assert store(cache(), **kw) == why, kw
     assert store(None) == ARG
@@ -119,7 +119,7 @@ def test_page_refusals(lib):
     for kw, why in [(dict(n_pages=0), ARG), (dict(batch=0), ARG), (dict(batch=5000), SHAPE), (dict(page_rows=8), SHAPE),
                     (dict(page_rows=48), SHAPE), (dict(pages_per_seq=0), SHAPE), (dict(pages_per_seq=1 << 28), SHAPE),
                     (dict(block_table=None), ARG), (dict(lengths=None), ARG), (dict(refs=P.value + 2), ARG),
-                    (dict(work=None), ARG), (dict(work_bytes=need.value - 4), SMALL), (dict(n_pools=-1), ARG),
+                    (dict(work=None), ARG), (dict(work_bytes=need.value - 4), SMALL), (dict(n_pools=-1), ARG), (dict(n_pools=0), ARG),
                     (dict(pools=None), ARG), (dict(pool=(None, 4096, 4096)), ARG),
                     (dict(pool=((1 << 20) + 4, 4096, 4096)), ARG), (dict(pool=(1 << 20, 4096, 4104)), SHAPE),
                     (dict(pool=(1 << 20, 4096, 8192)), SHAPE), (dict(pool=(1 << 20, 4096, 0)), SHAPE)]:

@@ -263,6 +263,10 @@ def test_pool_refusals():
             mog.PagePool(K, bad, 2, 4)
     with pytest.raises(ValueError):
         mog.PagePool([K, K], [K], 2, 4)
+    with pytest.raises(ValueError):  # e4m3 rows without scales, scales with bf16 rows
+        mog.PagePool(K.to(torch.float8_e4m3fn), K.to(torch.float8_e4m3fn), 2, 4)
+    with pytest.raises(ValueError):
+        mog.PagePool(K, K.clone(), 2, 4, k_scale=K[..., 0].float(), v_scale=K[..., 0].float())
     with pytest.raises(ValueError):
         mog.PagePool(K, K.clone(), 2, 4, lengths=torch.zeros(3, dtype=torch.int32, device=DEV))
     with pytest.raises(mog.MogError, match="SHAPE"):
