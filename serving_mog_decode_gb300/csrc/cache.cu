@@ -72,17 +72,20 @@ int cache_splits(int units, int n_max) {
     return (int)(tiles < slots ? tiles : slots);
 }
 
-// CTAs of a cluster per unit, or 0 for the split form with its second kernel.  One launch is
-// taken while all clusters fit on the GPU together and no CTA has more than four tiles of 64
-// rows: it saves the partials' way through L2, a launch and the scratch (8 KV heads, 1000
-// tokens: 5.8 us against 6.5 for the kernels, 14 against 18 with the host's part; 2000: 7.5
-// against 7.0).  Clusters of 16 and more tiles a CTA were slower.
-constexpr int CLUSTER_MAX = 8, CLUSTER_TILES = 4;
+// CTAs of a cluster per unit, or 0 for the split form with its second kernel.  One launch saves
+// the partials' way through L2, a launch and the scratch, but has no more than 8 CTAs for a
+// KV head.  It is taken while all clusters fit on the GPU together (two CTAs per SM, three
+// stages each) and no CTA has more than 8 tiles of 64 rows, 4 if there is not a CTA for every SM.
+// Kernel times, one launch against two: 8 KV heads and G = 4 of e4m3, 1000 tokens 5.5 us against
+// 6.3, 2000 7.0 against 6.6 (12 against 18 with the host's part), 4096 9.5 against 7.8;
+// 32 KV heads, 4096 tokens 10.7 against 13.1.  Clusters of 16 were slower throughout.
+constexpr int CLUSTER_MAX = 8;
 int cache_cluster(int units, int n_max) {
-    const int64_t tiles = ceil_div64(n_max, 64), slots = 3LL * num_sms();
+    const int64_t tiles = ceil_div64(n_max, 64), sms = num_sms(), slots = CL_PER_SM * sms;
     int cs = 1;
     while (cs < CLUSTER_MAX && cs < tiles && (int64_t)units * cs * 2 <= slots) cs *= 2;
-    return tiles <= (int64_t)cs * CLUSTER_TILES && (int64_t)units * cs <= slots ? cs : 0;
+    const int64_t ctas = (int64_t)units * cs, most = ctas >= sms ? 8 : 4;
+    return ctas <= slots && tiles <= cs * most ? cs : 0;
 }
 
 template <int ROWS>

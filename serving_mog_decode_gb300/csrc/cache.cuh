@@ -39,13 +39,14 @@
 namespace mog {
 
 constexpr int CT_WARPS = 4;
+constexpr int CL_PER_SM = 2, CL_STAGES = 3;  // CTAs per SM and stages of the cluster form: short caches, latency
 constexpr int CT_THREADS = 32 * CT_WARPS;
 constexpr float W_SCALE = 16384.f;  // 2^14: scale of fp16 weights
 
 // A tile is copied by the whole CTA, 2 KB of neighbouring rows per instruction, and each
 // warp consumes BLK blocks of 16 of its rows.  Stages are aligned to 128 bytes: 16 bytes off,
 // the copies of the same kernel were 5% slower (1M e4m3 tokens, 8 heads: 329 against 316 us).
-template <bool E4M3_, bool WIDE_>
+template <bool E4M3_, bool WIDE_, bool CLUSTER = false>
 struct Tile {
     static constexpr bool E4M3 = E4M3_, WIDE = WIDE_;
     static constexpr int BLK = E4M3 ? 2 : 1;              // blocks of 16 rows per warp
@@ -54,13 +55,13 @@ struct Tile {
     // Three CTAs per SM, but two of the wide e4m3 form: it is bound by the latencies of its
     // longer chains, which 255 registers (32 rows a warp in flight, no spills) hide better than
     // a third CTA (16 heads, 512K: 202 us against 231 with three CTAs and 16 rows a warp).
-    static constexpr int PER_SM = E4M3 && WIDE ? 2 : 3;
+    static constexpr int PER_SM = CLUSTER ? CL_PER_SM : E4M3 && WIDE ? 2 : 3;
     static constexpr int ROW = E4M3 ? MOG_D : 2 * MOG_D;  // bytes
     static constexpr int KV = ROWS * ROW;                 // bytes of the K or V tile: 16 KB
     static constexpr int AUX = 2 * KV;                    // K scales, V scales
     static constexpr int MASK = AUX + (E4M3 ? 2 * ROWS * 4 : 0);  // bit per row
     static constexpr int STAGE = MASK + 128;              // rows stay aligned to 128 bytes
-    static constexpr int STAGES = E4M3 && WIDE ? 3 : 2;   // 32 KB each: 96 KB or more in flight per SM
+    static constexpr int STAGES = CLUSTER ? CL_STAGES : E4M3 && WIDE ? 3 : 2;   // 32 KB each: 96 KB or more in flight per SM
     static constexpr int COLS = WIDE ? 16 : 8;
     static constexpr int XCH = 2 * COLS * MOG_D * 4;      // two warps' accumulators, in a consumed stage
     // a cluster's CTA leaves its partial behind that in stage 0, or behind the stages
@@ -805,11 +806,11 @@ __device__ __forceinline__ void cluster_end(const CacheArgs &a, const DiffArgs &
 // CLUSTER: the form with a cluster of a.cs CTAs per unit (a kernel of its own: the two in one cost
 // the split form registers and 14% of its speed).
 template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS, bool CLUSTER>
-__global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE>::PER_SM) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
+__global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
     extern __shared__ __align__(128) uint8_t csm[];
     __shared__ Exchange ex;
     __shared__ QShared qs;  // (wide)
-    using T = Tile<E4M3, WIDE>;
+    using T = Tile<E4M3, WIDE, CLUSTER>;
     constexpr bool BF16OUT = PARTS == (E4M3 ? 1 : 2);  // (the parts go by the output's type)
     const uint32_t stages = smem_u32(csm);
     const int G2 = DIFF ? 2 * a.G : a.G;
@@ -884,14 +885,14 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE>::PER_SM) k_cache_
 
 template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
 static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out, int splits, cudaStream_t s) {
-    using T = Tile<E4M3, WIDE>;
+    const int smem = a.cs ? Tile<E4M3, WIDE, true>::SMEM : Tile<E4M3, WIDE>::SMEM;
     const auto fn = a.cs ? k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS, true> : k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS, false>;
-    const cudaError_t e = ensure_smem((const void *)fn, T::SMEM);
+    const cudaError_t e = ensure_smem((const void *)fn, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.cs ? a.cs * a.batch * a.h_kv : splits);
     cfg.blockDim = dim3(CT_THREADS);
-    cfg.dynamicSmemBytes = T::SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

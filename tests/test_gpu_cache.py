@@ -175,7 +175,7 @@ LAYOUTS = [(0, True), (16, True), (64, False), (128, True)]
                                       ((130, 0, 777), 1, 16), ((500,), 2, 9)])
 def test_dense8(lens, H, G, page, hf, out_type, slack):
     m = Made(1, lens, H, page, heads_first=hf, slack=slack)
-    assert (mog.dense8_scratch_bytes(m.B, H, H * G, m.n_max) == 0) == (m.n_max < 2000)
+    assert (mog.dense8_scratch_bytes(m.B, H, H * G, m.n_max) == 0) == (m.n_max <= 2048)
     q = queries(2, m.B, H * G)
     out = torch.full(q.shape, float("nan"), dtype=out_type, device=DEV)
     mog.dense_decode(*m.cache, m.lengths, m.n_max, q, out=out)
