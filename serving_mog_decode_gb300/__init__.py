@@ -70,6 +70,7 @@ class PagedKV:
         self.heads_first = heads_first
         self.h_kv = K.shape[1] if heads_first else K.shape[2]
         self.device = K.device
+        self._cache = None  # (made when a call first needs it)
 
     def struct(self) -> KV:
         K = self.K
@@ -169,21 +170,29 @@ def _check_table(block_table, K):
         raise ValueError("block_table must be a contiguous int32 tensor [B, pages_per_seq] on the pools' device")
 
 
+def _paged_cache(P):
+    k, v, t, rows = made = P.K, P.V, P.block_table, P.page_rows
+    _check_table(t, k)
+    shape, st = k.shape, k.stride()
+    h, n = (1, 2) if P.heads_first else (2, 1)
+    if v.device != k.device or shape[3] != 128 or shape[n] != rows:
+        raise ValueError("page pools must share a device and hold page_rows rows of 128")
+    per = t.shape[1]
+    c = Cache(0, 0, k.data_ptr(), v.data_ptr(), None, None, st[0] if shape[0] > 1 else 0, st[h] if shape[h] > 1 else 0,
+              st[n], 0, 0, 0, t.data_ptr(), rows, per, shape[0])
+    return made, (c, t.shape[0], shape[h], per * rows, k.device)
+
+
 def _cache(K, V):
     """(mog_cache, batch, KV heads, positions, device) of a KV8, a PagedKV8, a PagedKV or two
     bf16 tensors [B, H_kv, n_cap, 128]."""
     if isinstance(K, (KV8, PagedKV8)):
         return K.cache, K.batch, K.h_kv, K.positions, K.device
     if isinstance(K, PagedKV):
-        k, v, t, rows = K.K, K.V, K.block_table, K.page_rows
-        _check_table(t, k)
-        shape, st = k.shape, k.stride()
-        h, n = (1, 2) if K.heads_first else (2, 1)
-        if v.device != k.device or shape[3] != 128 or shape[n] != rows:
-            raise ValueError("page pools must share a device and hold page_rows rows of 128")
-        per = t.shape[1]
-        return Cache(0, 0, k.data_ptr(), v.data_ptr(), None, None, st[0] if shape[0] > 1 else 0,
-                     st[h] if shape[h] > 1 else 0, st[n], 0, 0, 0, t.data_ptr(), rows, per, shape[0]), t.shape[0], shape[h], per * rows, k.device
+        made = K._cache  # its mog_cache, with the attributes that it was made of
+        if made is None or any(x is not y for x, y in zip(made[0], (K.K, K.V, K.block_table, K.page_rows))):
+            made = K._cache = _paged_cache(K)
+        return made[1]
     kv = _kv(K, V)
     if V.device != K.device or K.shape[3] != 128:
         raise ValueError("K and V must share a device and have rows of 128")
@@ -633,22 +642,28 @@ def _cache_decode(entry, K, V, lengths_dev, n_max, q, diff, out, scratch, stream
     elif (out.dtype not in (torch.float32, torch.bfloat16) or out.shape != shape or not out.is_contiguous()
           or out.device != dev):
         raise ValueError("out must be a contiguous float32 or bf16 tensor of q's shape on q's device")
+    bf = out.dtype is torch.bfloat16
+    own = None  # scratch of this call: from torch's allocator, given back to the stream's pool at the end
     if scratch is None:
         nbytes = _scratch_bytes(entry, B, H_kv, H_q, n_max, dev.index)
-        if nbytes:
-            scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if nbytes:  # (without the tensor around it, whose making costs 6 us between launches)
+            own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+        at = own
     elif scratch.device != dev or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous tensor on the cache's device")
     else:
         nbytes = scratch.numel() * scratch.element_size()
-    bf = out.dtype is torch.bfloat16
-    at = None if scratch is None else scratch.data_ptr()
-    if diff is None:
-        rc = lib().dense_decode8(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
-                                 out.data_ptr(), bf, at, nbytes, s)
-    else:
-        rc = lib().mog_diff_decode(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
-                                   C.byref(diff), out.data_ptr(), bf, at, nbytes, s)
+        at = scratch.data_ptr()
+    try:
+        if diff is None:
+            rc = lib().dense_decode8(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
+                                     out.data_ptr(), bf, at, nbytes, s)
+        else:
+            rc = lib().mog_diff_decode(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, q.data_ptr(),
+                                       C.byref(diff), out.data_ptr(), bf, at, nbytes, s)
+    finally:
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     if rc:
         _check(rc, entry)
     return out
@@ -663,15 +678,15 @@ def diff_decode(K, V, lengths_dev, n_max, q, lam, lambda_init, gamma=None, eps=1
     lambda = exp(l_q1.l_k1) - exp(l_q2.l_k2) + lambda_init; gamma: float32 [128] norm weights
     or None.  -> out f32 (or bf16 if given so) [B, H_q, 128]."""
     torch = _torch()
-    shared = lam.dim() == 2
-    if (lam.dtype != torch.float32 or lam.shape[-2:] != (4, 64) or lam.dim() not in (2, 3) or not lam.is_contiguous()
-            or (not shared and lam.shape[0] != q.shape[1]) or lam.device != q.device):
+    shape, dev, shared = lam.shape, q.device, lam.dim() == 2
+    if (lam.dtype is not torch.float32 or shape != ((4, 64) if shared else (q.shape[1], 4, 64))
+            or not lam.is_contiguous() or lam.device != dev):
         raise ValueError("lam must be a contiguous float32 tensor [4, 64] or [H_q, 4, 64] on q's device")
-    if gamma is not None and (gamma.dtype != torch.float32 or gamma.shape != (128,) or not gamma.is_contiguous()
-                              or gamma.device != q.device):
+    if gamma is not None and (gamma.dtype is not torch.float32 or gamma.shape != (128,) or not gamma.is_contiguous()
+                              or gamma.device != dev):
         raise ValueError("gamma must be a contiguous float32 tensor [128] on q's device")
-    d = DiffParams(lam.data_ptr(), None if gamma is None else gamma.data_ptr(), 1 if shared else lam.shape[0],
-                   lambda_init, eps)
+    d = DiffParams(lam.data_ptr(), None if gamma is None else gamma.data_ptr(), 1 if shared else shape[0], lambda_init,
+                   eps)
     return _cache_decode("mog_diff_decode", K, V, lengths_dev, n_max, q, d, out, scratch, stream)
 
 
