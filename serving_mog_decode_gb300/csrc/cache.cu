@@ -6,8 +6,8 @@
 
 namespace mog {
 
-// One CTA per (unit, head): warp w folds partials w, w + 8, ..., then the warps are folded.
-constexpr int CM_WARPS = 8;
+// One CTA per (unit, head): warp w folds partials w, w + 16, ..., then the warps are folded.
+constexpr int CM_WARPS = 16;
 template <int ROWS, bool DIFF, bool BF16OUT>
 __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, DiffArgs d, void *out, int splits) {
     constexpr int M = DIFF ? 2 : 1;
@@ -30,26 +30,30 @@ __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, Diff
     const float weight = map_weight<DIFF>(d, h * a.G + head);
     pdl_wait();
     const int64_t step = (int64_t)M * a.G * PART_W;  // floats of a slot
+    const float *p = a.part + (int64_t)unit * step + (int64_t)head * PART_W;
+    Fold part[M];
+#pragma unroll
+    for (int k = 0; k < M; ++k) part[k].init();
+    constexpr int U = 8 / M;  // partials in flight, of every map
+    for (int c = c0 + w; c < c1; c += CM_WARPS * U) {
+        float2 ml[M][U];
+        float4 v[M][U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+                const bool ok = c + CM_WARPS * i < c1;
+                const float *r = p + (c + CM_WARPS * i) * step + (int64_t)k * a.G * PART_W;
+                ml[k][i] = ok ? __ldcg(reinterpret_cast<const float2 *>(r)) : make_float2(-INFINITY, 0.f);
+                v[k][i] = ok ? __ldcg(reinterpret_cast<const float4 *>(r + PART_ACC) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+        for (int k = 0; k < M; ++k) part[k].add(ml[k], v[k]);
+    }
 #pragma unroll
     for (int k = 0; k < M; ++k) {
-        const float *p = a.part + (int64_t)unit * step + (int64_t)(k * a.G + head) * PART_W;
-        Fold f;
-        f.init();
-        constexpr int U = 4;
-        for (int c = c0 + w; c < c1; c += CM_WARPS * U) {
-            float2 ml[U];
-            float4 v[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const bool ok = c + CM_WARPS * i < c1;
-                const float *r = p + (c + CM_WARPS * i) * step;
-                ml[i] = ok ? __ldcg(reinterpret_cast<const float2 *>(r)) : make_float2(-INFINITY, 0.f);
-                v[i] = ok ? __ldcg(reinterpret_cast<const float4 *>(r + PART_ACC) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            f.add(ml, v);
-        }
-        s_acc[k][w][lane] = f.acc;
-        if (lane == 0) s_ml[k][w] = make_float2(f.m, f.l);
+        s_acc[k][w][lane] = part[k].acc;
+        if (lane == 0) s_ml[k][w] = make_float2(part[k].m, part[k].l);
     }
     __syncthreads();
     if (w != 0) return;
