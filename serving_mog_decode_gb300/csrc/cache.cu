@@ -6,18 +6,23 @@
 
 namespace mog {
 
-// One CTA per (unit, head): warp w folds partials w, w + 16, ..., then the warps are folded.
-constexpr int CM_WARPS = 16;
-template <int ROWS, bool DIFF, bool BF16OUT>
-__global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, DiffArgs d, void *out, int splits) {
-    constexpr int M = DIFF ? 2 : 1;
-    __shared__ float4 s_acc[M][CM_WARPS][32];
-    __shared__ float2 s_ml[M][CM_WARPS];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = blockIdx.x / a.G, head = blockIdx.x % a.G;
-    const int b = unit / a.h_kv, h = unit % a.h_kv;
+// Folds the partials of the split form.  HEADS = 1: a CTA's 16 warps share one (unit, head), warp
+// w folding partials w, w + 16, ...; HEADS = 8: a warp per (unit, head), for batches of many
+// short units, which have a partial or two each (whole step, 256 sequences of 1000 e4m3 tokens, 8 KV heads,
+// G = 4: 103 us against 161; 4 sequences of 16000: 35.9 against 33.8).
+template <int ROWS, bool DIFF, bool BF16OUT, int HEADS>
+__global__ void __launch_bounds__(HEADS == 1 ? 512 : 256) k_cache_merge(CacheArgs a, DiffArgs d, void *out, int splits) {
+    constexpr int M = DIFF ? 2 : 1, W = HEADS == 1 ? 16 : 1;  // warps of a head
+    __shared__ float4 s_acc[M][W][32];
+    __shared__ float2 s_ml[M][W];
+    const int lane = threadIdx.x & 31, w = W == 1 ? 0 : threadIdx.x >> 5;
+    const int row = HEADS == 1 ? blockIdx.x : blockIdx.x * HEADS + (threadIdx.x >> 5);
+    if (row >= a.batch * a.h_kv * a.G) return;
+    const int unit = row / a.G, head = row - unit * a.G;
+    const int b = unit / a.h_kv, h = unit - b * a.h_kv;
     // the unit's tiles in the list, and with them the CTAs that hold its partials
     int before = 0, all = 0;
+#pragma unroll 4
     for (int i = lane; i < a.batch; i += 32) {
         const int nt = seq_tiles<ROWS>(a, i);
         all += nt;
@@ -31,43 +36,44 @@ __global__ void __launch_bounds__(CM_WARPS * 32) k_cache_merge(CacheArgs a, Diff
     pdl_wait();
     const int64_t step = (int64_t)M * a.G * PART_W;  // floats of a slot
     const float *p = a.part + (int64_t)unit * step + (int64_t)head * PART_W;
-    Fold part[M];
+    Fold f[M];
 #pragma unroll
-    for (int k = 0; k < M; ++k) part[k].init();
-    constexpr int U = 8 / M;  // partials in flight, of every map
-    for (int c = c0 + w; c < c1; c += CM_WARPS * U) {
+    for (int k = 0; k < M; ++k) f[k].init();
+    constexpr int U = (W == 1 ? 4 : 8) / M;  // partials in flight, of every map
+    for (int c = c0 + w; c < c1; c += W * U) {
         float2 ml[M][U];
         float4 v[M][U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
             for (int k = 0; k < M; ++k) {
-                const bool ok = c + CM_WARPS * i < c1;
-                const float *r = p + (c + CM_WARPS * i) * step + (int64_t)k * a.G * PART_W;
+                const bool ok = c + W * i < c1;
+                const float *r = p + (c + W * i) * step + (int64_t)k * a.G * PART_W;
                 ml[k][i] = ok ? __ldcg(reinterpret_cast<const float2 *>(r)) : make_float2(-INFINITY, 0.f);
                 v[k][i] = ok ? __ldcg(reinterpret_cast<const float4 *>(r + PART_ACC) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
-        for (int k = 0; k < M; ++k) part[k].add(ml[k], v[k]);
+        for (int k = 0; k < M; ++k) f[k].add(ml[k], v[k]);
     }
+    if (W > 1) {
 #pragma unroll
-    for (int k = 0; k < M; ++k) {
-        s_acc[k][w][lane] = part[k].acc;
-        if (lane == 0) s_ml[k][w] = make_float2(part[k].m, part[k].l);
+        for (int k = 0; k < M; ++k) {
+            s_acc[k][w][lane] = f[k].acc;
+            if (lane == 0) s_ml[k][w] = make_float2(f[k].m, f[k].l);
+        }
+        __syncthreads();
+        if (w != 0) return;
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+            float2 ml[W];
+            float4 v[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) ml[i] = s_ml[k][i], v[i] = s_acc[k][i][lane];
+            f[k].init();
+            f[k].add(ml, v);
+        }
     }
-    __syncthreads();
-    if (w != 0) return;
-    Fold f[M];
-#pragma unroll
-    for (int k = 0; k < M; ++k) {
-        float2 ml[CM_WARPS];
-        float4 v[CM_WARPS];
-#pragma unroll
-        for (int i = 0; i < CM_WARPS; ++i) ml[i] = s_ml[k][i], v[i] = s_acc[k][i][lane];
-        f[k].init();
-        f[k].add(ml, v);
-    }
-    finish<DIFF, BF16OUT>(f, weight, d, out, blockIdx.x);
+    finish<DIFF, BF16OUT>(f, weight, d, out, row);
 }
 
 int cache_splits(int units, int n_max) {
@@ -84,6 +90,7 @@ int cache_splits(int units, int n_max) {
 // 6.3, 2000 7.0 against 6.6 (12 against 18 with the host's part), 4096 9.5 against 7.8;
 // 32 KV heads, 4096 tokens 10.7 against 13.1.  Clusters of 16 were slower throughout.
 constexpr int CLUSTER_MAX = 8;
+
 int cache_cluster(int units, int n_max) {
     const int64_t tiles = ceil_div64(n_max, 64), sms = num_sms(), slots = CL_PER_SM * sms;
     int cs = 1;
@@ -92,13 +99,22 @@ int cache_cluster(int units, int n_max) {
     return ctas <= slots && tiles <= cs * most ? cs : 0;
 }
 
-template <int ROWS>
-static cudaError_t launch_merge(const cudaLaunchConfig_t &cfg, bool diff, bool bf_out, const CacheArgs &a,
-                                const DiffArgs &d, void *out, int splits) {
-    if (diff) return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, true, true>, a, d, out, splits)
-                            : cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, true, false>, a, d, out, splits);
-    return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, false, true>, a, d, out, splits)
-                  : cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, false, false>, a, d, out, splits);
+template <int ROWS, int HEADS>
+static cudaError_t launch_merge(cudaStream_t s, bool diff, bool bf_out, const CacheArgs &a, const DiffArgs &d, void *out,
+                                int splits) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ceil_div64((int64_t)a.batch * a.h_kv * a.G, HEADS));
+    cfg.blockDim = dim3(HEADS == 1 ? 512 : 256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (diff) return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, true, true, HEADS>, a, d, out, splits)
+                            : cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, true, false, HEADS>, a, d, out, splits);
+    return bf_out ? cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, false, true, HEADS>, a, d, out, splits)
+                  : cudaLaunchKernelEx(&cfg, k_cache_merge<ROWS, false, false, HEADS>, a, d, out, splits);
 }
 
 cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
@@ -122,17 +138,12 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
                           : bf_out ? pick_split<false, true, 2>(a, d, out, wide, splits, s)
                                    : pick_split<false, true, 3>(a, d, out, wide, splits, s);
     if (e != cudaSuccess || a.cs) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(batch * h_kv * G);
-    cfg.blockDim = dim3(CM_WARPS * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return rows == 128 ? launch_merge<128>(cfg, diff, bf_out, a, d, out, splits)
-                       : launch_merge<64>(cfg, diff, bf_out, a, d, out, splits);
+    // a unit has splits / units partials and one more: a CTA per head from about five
+    if (splits > 4 * batch * h_kv)
+        return rows == 128 ? launch_merge<128, 1>(s, diff, bf_out, a, d, out, splits)
+                           : launch_merge<64, 1>(s, diff, bf_out, a, d, out, splits);
+    return rows == 128 ? launch_merge<128, 8>(s, diff, bf_out, a, d, out, splits)
+                       : launch_merge<64, 8>(s, diff, bf_out, a, d, out, splits);
 }
 
 // ------------------------------------------------------------------------------------

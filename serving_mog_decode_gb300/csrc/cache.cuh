@@ -101,32 +101,38 @@ __device__ __forceinline__ int seq_tiles(const CacheArgs &a, int b) {
 template <int ROWS>
 __device__ __forceinline__ int total_tiles(const CacheArgs &a) {
     int s = 0;
+#pragma unroll 4
     for (int b = threadIdx.x & 31; b < a.batch; b += 32) s += seq_tiles<ROWS>(a, b);
     return warp_isum(s) * a.h_kv;
 }
 
 // Sequence holding tile `t` of the list and the list position of its first tile (called by
-// a full warp; t < total).
+// a full warp; t < total).  Lengths of 128 sequences are loaded at a time.
 template <int ROWS>
 __device__ __forceinline__ void find_seq(const CacheArgs &a, int t, int &b, int &first) {
     const int lane = threadIdx.x & 31;
     int base = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const int mine = b0 + lane < a.batch ? seq_tiles<ROWS>(a, b0 + lane) * a.h_kv : 0;
-        int end = mine;
+    for (int b0 = 0; b0 < a.batch; b0 += 128) {
+        int mine[4];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, end, o);
-            if (lane >= o) end += v;
+        for (int i = 0; i < 4; ++i) mine[i] = b0 + 32 * i + lane < a.batch ? seq_tiles<ROWS>(a, b0 + 32 * i + lane) * a.h_kv : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int end = mine[i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += v;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, base + end > t);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                b = b0 + 32 * i + l;
+                first = base + __shfl_sync(0xffffffffu, end - mine[i], l);
+                return;
+            }
+            base += __shfl_sync(0xffffffffu, end, 31);
         }
-        const unsigned in = __ballot_sync(0xffffffffu, base + end > t);
-        if (in) {
-            const int l = __ffs(in) - 1;
-            b = b0 + l;
-            first = base + __shfl_sync(0xffffffffu, end - mine, l);
-            return;
-        }
-        base += __shfl_sync(0xffffffffu, end, 31);
     }
     b = a.batch;
     first = base;
