@@ -193,12 +193,16 @@ def _cache(K, V):
         if made is None or any(x is not y for x, y in zip(made[0], (K.K, K.V, K.block_table, K.page_rows))):
             made = K._cache = _paged_cache(K)
         return made[1]
-    kv = _kv(K, V)
-    if V.device != K.device or K.shape[3] != 128:
-        raise ValueError("K and V must share a device and have rows of 128")
-    shape, st = K.shape, K.stride()
-    c = Cache(0, shape[2], kv.k, kv.v, None, None, st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0, st[2])
-    return c, shape[0], shape[1], shape[2], K.device
+    torch = _torch()
+    if V is None:
+        raise ValueError("this call takes K and V tensors, or a PagedKV, KV8 or PagedKV8 as K")
+    shape, st, dev = K.shape, K.stride(), K.device
+    if (K.dtype is not torch.bfloat16 or V.dtype is not torch.bfloat16 or len(shape) != 4 or shape[3] != 128
+            or st[3] != 1 or V.shape != shape or V.stride() != st or dev.type != "cuda" or V.device != dev):
+        raise ValueError("K and V must be CUDA bf16 tensors [B, H_kv, n_cap, 128] of one shape, strides and device, "
+                         "last dim contiguous")
+    B, H, n = shape[:3]
+    return Cache(0, n, K.data_ptr(), V.data_ptr(), None, None, st[0] if B > 1 else 0, st[1] if H > 1 else 0, st[2]), B, H, n, dev
 
 
 class Layout(C.Structure):

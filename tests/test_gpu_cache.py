@@ -552,3 +552,74 @@ def test_python_refusals():
         mog.diff_decode(c, None, **ok, lam=lam, lambda_init=0.5, gamma=gamma[:64])
     with pytest.raises(ValueError):  # an e4m3 cache has no MoG index
         mog.build(c, None, [64], mog.make_params(1, 2, 4, 64))
+
+
+# ---------------------------------------------------------- bounds, streams, large batches
+
+@pytest.mark.parametrize("lens,H,G,page", [((5000,), 1, 4, 16), ((3000, 10, 0, 4000), 3, 16, 64), ((2500,) * 3, 2, 9, 0)])
+def test_nothing_is_written_behind_scratch_and_output(lens, H, G, page):
+    m = Made(71, lens, H, page)
+    q = queries(72, m.B, H * G)
+    for diff in ([False, True] if G <= 8 else [False]):
+        need = (mog.diff_scratch_bytes if diff else mog.dense8_scratch_bytes)(m.B, H, H * G, m.n_max)
+        assert need > 0
+        buf = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device=DEV)
+        big = torch.full((m.B + 2, H * G, D), 7.5, device=DEV)
+        out, scratch = big[1:-1], buf[4096:4096 + need]
+        if diff:
+            lam, gamma = weights(73)
+            mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma, out=out, scratch=scratch)
+            check_diff(m, q, out, G, lam, 0.5, gamma, 1e-5)
+        else:
+            mog.dense_decode(*m.cache, m.lengths, m.n_max, q, out=out, scratch=scratch)
+            check_dense8(m, q, out, G)
+        assert (buf[:4096] == 0xA5).all() and (buf[4096 + need:] == 0xA5).all()
+        assert (big[0] == 7.5).all() and (big[-1] == 7.5).all()
+
+
+@pytest.mark.parametrize("n", [40, 1000])
+def test_large_batches_of_short_sequences(n):
+    """More units than CTAs: a warp per head folds one or two partials."""
+    g = torch.Generator().manual_seed(74)
+    lens = tuple(int(x) for x in torch.randint(0, n + 1, (300,), generator=g))
+    m = Made(75, lens, 2, 16)
+    q = queries(76, m.B, 4)
+    lam, gamma = weights(77)
+    assert mog.dense8_scratch_bytes(m.B, 2, 4, m.n_max) > 0
+    check_dense8(m, q, mog.dense_decode(*m.cache, m.lengths, m.n_max, q), 2)
+    check_diff(m, q, mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma), 2, lam, 0.5, gamma, 1e-5)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with scratch of its own."""
+    ms = [Made(78 + i, (20000 + 999 * i,), 2, 16 * i) for i in range(2)]
+    qs = [queries(80 + i, 1, 8) for i in range(2)]
+    want = [mog.dense_decode(*m.cache, m.lengths, m.n_max, q) for m, q in zip(ms, qs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            got[i].append(mog.dense_decode(*ms[i].cache, ms[i].lengths, ms[i].n_max, qs[i], stream=s))
+    for s in streams:
+        s.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_graphs_of_two_calls_with_their_own_scratch():
+    """Scratch that a captured call takes by itself belongs to the graph."""
+    m = Made(82, (9000, 400), 2, 64)
+    q = queries(83, 2, 8)
+    lam, gamma = weights(84)
+    want = (mog.dense_decode(*m.cache, m.lengths, m.n_max, q), mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = (mog.dense_decode(*m.cache, m.lengths, m.n_max, q), mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma))
+    for _ in range(3):
+        noise = [torch.full((1 << 20,), float("nan"), device=DEV) for _ in range(8)]  # takes freed memory outside
+        del noise
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -365,3 +365,43 @@ def test_serving_run(e4m3):
     assert int(pool.refs[live:].abs().sum()) == 0 and pool.status() == 0
     append([1] * batch)
     attend()
+
+
+def test_no_page_outside_the_plan_is_written():
+    """Pools and tables inside larger buffers: what is around them stays."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    big = [torch.randn((20, 2, 16, D), generator=g, device=DEV).bfloat16() for _ in range(2)]
+    keep = [b.clone() for b in big]
+    table = torch.full((6, 4), 77, dtype=torch.int32, device=DEV)
+    table[1:5] = -1
+    pool = mog.PagePool(big[0][2:-2], big[1][2:-2], 4, 4, block_table=table[1:5])
+    model = Model(16, 16, 4, 4)
+    for n, src in (([20, 0, 16, 3], [0, 0, 0, 3]), ([1, 1, 1, 1], [-1, 1, 2, 3]), ([0, 0, 0, 5], [1, 2, 3, 1])):
+        pool.grow(ints(n))
+        model.grow(n)
+        pool.assign(ints(src))
+        model.assign(src)
+        pool.compact()
+        model.compact()
+        same(pool, model, None)
+    assert (table[0] == 77).all() and (table[5] == 77).all()
+    at = torch.from_numpy(model.content).to(DEV)
+    for b, k in zip(big, keep):
+        assert torch.equal(b[:2], k[:2]) and torch.equal(b[-2:], k[-2:]) and torch.equal(b[2:-2], k[2:-2][at])
+
+
+def test_many_holders_of_one_last_page():
+    """4096 sequences that share a partly filled page all grow: all but the last copy it."""
+    B = 4096
+    pool, model = make(B + 8, 16, B, 2, H=1), Model(B + 8, 16, B, 2)
+    first = [5] + [0] * (B - 1)
+    pool.grow(ints(first))
+    model.grow(first)
+    pool.assign(ints([0] * B))
+    model.assign([0] * B)
+    before = [bits(t) for t in tensors(pool)]
+    model.content = np.arange(B + 8)
+    pool.grow(ints([1] * B))
+    model.grow([1] * B)
+    same(pool, model, before)
+    assert pool.status() == 0
