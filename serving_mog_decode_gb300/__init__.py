@@ -791,6 +791,7 @@ class PagePool:
                         len(pools))
         self.batch = batch
         self.pos, self.granted = torch.zeros_like(self.lengths), torch.zeros_like(self.lengths)
+        self._lib, self._ref = lib(), C.byref(self._s)
         self._pos_ptr, self._granted_ptr = self.pos.data_ptr(), self.granted.data_ptr()
 
     def cache(self, layer=0):
@@ -805,15 +806,15 @@ class PagePool:
         if s is None:
             with _there(self.device, stream):
                 return self._call(fn, None, *args)
-        rc = getattr(lib(), fn)(C.byref(self._s), *args, s)
+        rc = fn(self._ref, *args, s)
         if rc:
-            _check(rc, fn)
+            _check(rc, fn.__name__)
 
     def assign(self, src, stream=None):
         """Fork, reorder and free (mog_pages_assign): sequence b takes the pages and length that
         src[b] had (b: as it is; -1: none).  src: int32 [batch] on the device."""
         _check_counts(src, self.batch, self.device, "src")
-        self._call("mog_pages_assign", stream, src.data_ptr())
+        self._call(self._lib.mog_pages_assign, stream, src.data_ptr())
 
     def grow(self, n_new, stream=None):
         """Room for n_new[b] more tokens of every sequence (mog_pages_grow); a shared last page
@@ -821,12 +822,12 @@ class PagePool:
         rows, and how many (0 everywhere if there was no room: see status()).  They are the
         same two tensors every time: the next grow overwrites them."""
         _check_counts(n_new, self.batch, self.device, "n_new")
-        self._call("mog_pages_grow", stream, n_new.data_ptr(), self._pos_ptr, self._granted_ptr)
+        self._call(self._lib.mog_pages_grow, stream, n_new.data_ptr(), self._pos_ptr, self._granted_ptr)
         return self.pos, self.granted
 
     def compact(self, stream=None):
         """Move the pages in use to the front of the pools (mog_pages_compact)."""
-        self._call("mog_pages_compact", stream)
+        self._call(self._lib.mog_pages_compact, stream)
 
     def status(self, stream=None) -> int:
         """Wait for the stream, then read and clear the status of the calls so far: MOG_OK,
@@ -835,7 +836,7 @@ class PagePool:
         if s is None:
             with _there(self.device, stream):
                 return self.status()
-        return lib().mog_pages_status(C.byref(self._s), s)
+        return self._lib.mog_pages_status(self._ref, s)
 
 
 def kmeans_assign(x, cent, stream=None, with_recheck=False):

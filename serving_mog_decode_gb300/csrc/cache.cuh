@@ -4,9 +4,10 @@
 //
 // dense_decode8: softmax(tau q.K^T) V of an e4m3 cache whose row i stands for
 // k_scale[i]*code_i and v_scale[i]*code_i.  mog_diff_decode: the difference of two softmax
-// maps over one set of values, normalised.  Both are one split kernel and one merge kernel.
+// maps over one set of values, normalised.  Both are a split kernel and a fold of its partials,
+// or, for short caches, one kernel whose clusters take a unit each and fold it themselves.
 //
-// Split (k_cache_split): the 64-row tiles of all (sequence, KV head) units form one list;
+// Split (k_cache_split): the tiles (128 e4m3 rows, 64 of bf16) of all (sequence, KV head) units form one list;
 // CTA c takes tiles [c*chunk, (c+1)*chunk) of it, so ragged batches load every SM alike
 // (the lengths are read on the device: a captured graph replays with grown sequences).  Its
 // copies run ahead across unit borders.  Each unit that a CTA touches leaves one partial
