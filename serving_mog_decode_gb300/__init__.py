@@ -171,7 +171,7 @@ def _check_table(block_table, K):
 
 
 def _paged_cache(P):
-    k, v, t, rows = made = P.K, P.V, P.block_table, P.page_rows
+    k, v, t, rows = P.K, P.V, P.block_table, P.page_rows
     _check_table(t, k)
     shape, st = k.shape, k.stride()
     h, n = (1, 2) if P.heads_first else (2, 1)
@@ -180,7 +180,7 @@ def _paged_cache(P):
     per = t.shape[1]
     c = Cache(0, 0, k.data_ptr(), v.data_ptr(), None, None, st[0] if shape[0] > 1 else 0, st[h] if shape[h] > 1 else 0,
               st[n], 0, 0, 0, t.data_ptr(), rows, per, shape[0])
-    return made, (c, t.shape[0], shape[h], per * rows, k.device)
+    return c, t.shape[0], shape[h], per * rows, k.device
 
 
 def _cache(K, V):
@@ -189,9 +189,11 @@ def _cache(K, V):
     if isinstance(K, (KV8, PagedKV8)):
         return K.cache, K.batch, K.h_kv, K.positions, K.device
     if isinstance(K, PagedKV):
-        made = K._cache  # its mog_cache, with the attributes that it was made of
-        if made is None or any(x is not y for x, y in zip(made[0], (K.K, K.V, K.block_table, K.page_rows))):
-            made = K._cache = _paged_cache(K)
+        k, v, t = K.K, K.V, K.block_table
+        of = k, v, t, k.data_ptr(), v.data_ptr(), t.data_ptr(), K.page_rows, K.heads_first
+        made = K._cache  # its mog_cache, with what it was made of: the attributes may be set anew
+        if made is None or any(x is not y for x, y in zip(made[0][:3], of)) or made[0][3:] != of[3:]:
+            made = K._cache = of, _paged_cache(K)
         return made[1]
     torch = _torch()
     if V is None:
@@ -579,6 +581,8 @@ def dense_decode(K, V, lengths_dev, n_max, q, out=None, scratch=None, stream=Non
 def dense_decode_noalloc(K, V, lengths_dev, n_max, q, out, stream=None):
     """dense_decode whose scratch is the library's static device array: no device memory
     is allocated by this call (the caller supplies `out`)."""
+    if isinstance(K, (KV8, PagedKV8)):
+        raise ValueError("dense_decode_noalloc reads bf16 caches")
     B, H_kv = (q.shape[0], K.h_kv) if isinstance(K, PagedKV) else (K.shape[0], K.shape[1])
     _check_q_out(K, q, out)
     kv = _kv(K, V)

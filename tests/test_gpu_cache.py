@@ -550,6 +550,8 @@ def test_python_refusals():
             mog.diff_decode(c, None, **ok, lam=w, lambda_init=0.5)
     with pytest.raises(ValueError):
         mog.diff_decode(c, None, **ok, lam=lam, lambda_init=0.5, gamma=gamma[:64])
+    with pytest.raises(ValueError):
+        mog.dense_decode_noalloc(c, None, m.lengths, 64, q, torch.empty((1, 4, D), device=DEV))
     with pytest.raises(ValueError):  # an e4m3 cache has no MoG index
         mog.build(c, None, [64], mog.make_params(1, 2, 4, 64))
 
@@ -623,3 +625,17 @@ def test_graphs_of_two_calls_with_their_own_scratch():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_paged_cache_whose_attributes_are_set_anew():
+    """A PagedKV is read as it is at each call, in place of what an earlier call saw."""
+    a, b = Made(85, (300,), 2, 16, e4m3=False), Made(86, (300,), 2, 16, e4m3=False)
+    q = queries(87, 1, 4)
+    lam, gamma = weights(88)
+    pk = a.cache[0]
+    mog.diff_decode(pk, None, a.lengths, 300, q, lam, 0.5, gamma)
+    pk.K, pk.V, pk.block_table = b.cache[0].K, b.cache[0].V, b.table
+    check_diff(b, q, mog.diff_decode(pk, None, b.lengths, 300, q, lam, 0.5, gamma), 2, lam, 0.5, gamma, 1e-5, False)
+    pk.K.data = a.pools[0]  # (the same tensor object over other memory)
+    pk.V.data, pk.block_table.data = a.pools[1], a.table
+    check_diff(a, q, mog.diff_decode(pk, None, a.lengths, 300, q, lam, 0.5, gamma), 2, lam, 0.5, gamma, 1e-5, False)
