@@ -163,7 +163,7 @@ def queries(seed, B, HG):
 
 
 OUTS = [torch.float32, torch.bfloat16]
-LAYOUTS = [(0, True), (16, True), (64, False), (128, True)]
+LAYOUTS = [(0, True), (16, True), (64, False), (128, True), (256, True)]
 
 
 # ---------------------------------------------------------------------------- dense8
@@ -639,3 +639,38 @@ def test_a_paged_cache_whose_attributes_are_set_anew():
     pk.K.data = a.pools[0]  # (the same tensor object over other memory)
     pk.V.data, pk.block_table.data = a.pools[1], a.table
     check_diff(a, q, mog.diff_decode(pk, None, a.lengths, 300, q, lam, 0.5, gamma), 2, lam, 0.5, gamma, 1e-5, False)
+
+
+def test_pages_past_32_bit_offsets():
+    """Pools whose pages lie 128 KB apart over more than 4 GiB: stored, forked, moved and read."""
+    n_pages, R, apart = 40000, 16, 1 << 17
+    big = torch.zeros(n_pages * apart, dtype=torch.uint8, device=DEV)
+
+    def pool(at):
+        return big[at:].view(torch.float8_e4m3fn).as_strided((n_pages, 1, R, D), (apart, R * D, D, 1))
+
+    K, V = pool(0), pool(apart // 2)
+    scales = [torch.ones((n_pages, 1, R), device=DEV) for _ in range(2)]
+    refs = torch.ones(n_pages, dtype=torch.int32, device=DEV)  # all but the last pages are taken
+    refs[-40:] = 0
+    p = mog.PagePool(K, V, 2, 8, k_scale=scales[0], v_scale=scales[1], refs=refs)
+    n = torch.tensor([100, 0], dtype=torch.int32, device=DEV)
+    pos, granted = p.grow(n)
+    assert granted.tolist() == [100, 0] and int(p.block_table[0, 0]) == n_pages - 40
+    x = randn(gen(89), 2, 100, 2, D).bfloat16()
+    mog.kv_store(p.cache(), None, pos, granted, x[:, :, :1], x[:, :, 1:])
+    p.assign(torch.tensor([0, 0], dtype=torch.int32, device=DEV))
+    p.grow(torch.tensor([0, 1], dtype=torch.int32, device=DEV))  # a copied last page
+    p.lengths.fill_(100)                                          # (its new row is not written)
+    rows = [e4m3_nearest(x[0, :, i].double() / row_scale(x[0, :, i].double())[:, None])
+            * row_scale(x[0, :, i].double())[:, None] for i in range(2)]
+    q = queries(90, 2, 4)
+    ref, e, s = one_map(q[0].double(), *rows, 100, D ** -0.5)
+    out = mog.dense_decode(p.cache(), None, p.lengths, 128, q)
+    check(out[0], ref, e + 2 * weight_error(True, False) * s, "first")
+    ref, e, s = one_map(q[1].double(), *rows, 100, D ** -0.5)
+    check(out[1], ref, e + 2 * weight_error(True, False) * s, "copied")
+    p.refs[:100] = 0  # pages at the front come free: the sequences' pages move there
+    p.compact()
+    assert int(p.block_table.max()) < n_pages - 40 and p.status() == 0
+    assert torch.equal(mog.dense_decode(p.cache(), None, p.lengths, 128, q), out)
