@@ -464,7 +464,9 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
                 s[blk][i] = !DIFF ? d[blk][0][i] : WIDE ? d[blk][(i >> 1) & 1][i] : t >= 2 ? d[blk][1][i] : d[blk][0][i];
     }
 
-    // log2-domain logits; row of s[blk][i]: rowof(i)
+    // log2-domain logits; row of s[blk][i]: rowof(i).  They are rounded before the maximum is taken
+    // from them (no fused multiply-add in the exponent): the largest weight has to be 1 however
+    // large the logits.
     auto rowof = [&](int i) { return WIDE ? 2 * t + (i & 1) + 8 * (i >> 2) : g + 8 * (i >> 1); };
     auto colof = [](int i) { return WIDE ? (i >> 1) & 1 : i & 1; };
 #pragma unroll
