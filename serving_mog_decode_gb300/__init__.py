@@ -722,23 +722,29 @@ def kv_store(K, V, pos, count, k_new, v_new, stream=None):
     if s is None:
         with _there(dev, stream):
             return kv_store(K, V, pos, count, k_new, v_new)
-    shape, sk, sv = k_new.shape, k_new.stride(), v_new.stride()
-    for t in (k_new, v_new):
-        if (t.dtype is not torch.bfloat16 or len(shape) != 4 or t.shape != shape or shape[0] != B or shape[2] != H_kv
-                or shape[3] != 128 or t.device != dev):
-            raise ValueError(f"k_new and v_new must be bf16 tensors [{B}, T, {H_kv}, 128] on the cache's device")
+    shape = k_new.shape
+    if (len(shape) != 4 or k_new.dtype is not torch.bfloat16 or v_new.dtype is not torch.bfloat16
+            or v_new.shape != shape or shape[0] != B or shape[2] != H_kv or shape[3] != 128 or k_new.device != dev
+            or v_new.device != dev):
+        raise ValueError(f"k_new and v_new must be bf16 tensors [{B}, T, {H_kv}, 128] on the cache's device")
     T = shape[1]
-    if 1 in shape:  # a dim of one entry has no stride that counts
-        sk, sv = ([x if n > 1 else 0 for n, x in zip(shape, st)] for st in (sk, sv))
-    if sk[3] != 1 or sk[:3] != sv[:3] or sv[3] != 1:
+
+    def strides(t):  # 0 for a dim of one entry, whose stride does not count
+        sb, st, sh, sd = t.stride()
+        return sb if B > 1 else 0, st if T > 1 else 0, sh if H_kv > 1 else 0, sd
+
+    sk = strides(k_new)
+    if sk[3] != 1 or strides(v_new) != sk:
         raise ValueError("k_new and v_new must share strides, the last dim contiguous")
     _check_counts(pos, B, dev, "pos")
+    at = None
     if count is not None:
         _check_counts(count, B, dev, "count")
+        at = count.data_ptr()
     if T == 0:
         return
-    rc = lib().mog_kv_store(C.byref(c), B, H_kv, 128, T, pos.data_ptr(), None if count is None else count.data_ptr(),
-                            k_new.data_ptr(), v_new.data_ptr(), sk[0], sk[1], sk[2], s)
+    rc = lib().mog_kv_store(C.byref(c), B, H_kv, 128, T, pos.data_ptr(), at, k_new.data_ptr(), v_new.data_ptr(), sk[0],
+                            sk[1], sk[2], s)
     if rc:
         _check(rc, "mog_kv_store")
 

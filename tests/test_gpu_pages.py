@@ -236,8 +236,9 @@ def test_more_pools_than_one_copy_launch_holds():
     same(pool, model, before)
 
 
-def test_page_calls_in_a_graph():
-    pool = make(64, 16, 4, 8)
+@pytest.mark.parametrize("kw", [{}, dict(R=64, H=8)])  # growth in one launch, in two
+def test_page_calls_in_a_graph(kw):
+    pool = make(64, kw.get("R", 16), 4, 8, H=kw.get("H", 2))
     n, src = ints([30, 0, 0, 0]), ints([0, 0, 0, -1])
     pool.grow(n)
     one = ints([0, 1, 1, 1])
@@ -254,6 +255,26 @@ def test_page_calls_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((pool.block_table, pool.refs, pool.lengths), want))
         assert pos.tolist() == [30, 30, 30, 0] and granted.tolist() == [0, 1, 1, 1]
+
+
+def test_compaction_in_a_graph():
+    pool, model = make(64, 16, 4, 8), Model(64, 16, 4, 8)
+    before = [bits(t) for t in tensors(pool)]
+    src, n = ints([2, 3, -1, -1]), ints([0, 0, 70, 33])
+    for m, x in ((pool, ints([70, 33, 70, 33])), (model, [70, 33, 70, 33])):
+        m.grow(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pool.assign(src)
+        pool.compact()
+        pool.grow(n)
+    for _ in range(4):
+        graph.replay()
+        model.assign(src.tolist())
+        model.compact()
+        model.grow(n.tolist())
+        same(pool, model, before)
 
 
 def test_pool_refusals():
