@@ -150,7 +150,7 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
 // mog_kv_store: rows of new keys and values to their positions.  A row is 8 lanes' work, 16
 // elements a lane: with 16 lanes a row the kernel was bound by the instructions of its
 // addresses and of the elements' conversion, 45 us for 24K tokens of 8 heads in 16-row pages
-// (100 MB read, 50 MB written: 22 us).  Elements stay packed in pairs: their magnitudes' maximum and
+// (100 MB read, 50 MB written: 22 us), and takes 26 us so.  Elements stay packed in pairs: their magnitudes' maximum and
 // their scaling are bf16x2 instructions, exact both.
 // A row's e4m3 scale is the least power of two 2^e (e >= -126) with amax <= 448*2^e, so
 // that dividing by it is exact and the only rounding is the one to e4m3.
