@@ -515,7 +515,7 @@ typedef struct mog_cache {
 /*
  * dense_decode over an e4m3 cache: for every query head softmax(tau q.K^T) V over keys
  * [0, N_b), K and V the rows' values scale * code, tau = 1/sqrt(d).  A sequence without
- * rows gives zeros.
+ * rows gives zeros, and so does one whose logits are all -infinity.
  *  c           : MOG_CACHE_E4M3
  *  lengths_dev : int32[batch] on the device, clamped to [0, n_max]; n_max <= the cache's
  *                positions
@@ -537,7 +537,7 @@ int dense_decode8(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max,
  *   a   = softmax(tau q1.K1^T) V - lambda softmax(tau q2.K2^T) V,   tau = 1/sqrt(d/2)
  *   lambda = exp(l_q1 . l_k1) - exp(l_q2 . l_k2) + lambda_init
  *   out = (1 - lambda_init) * a / sqrt(mean(a^2) + eps) * gamma
- * over keys [0, N_b); a sequence without rows gives zeros.
+ * over keys [0, N_b); a map without rows, or whose logits are all -infinity, is zero.
  *  lam         : device f32 [lam_heads][4][d/2], the vectors l_q1, l_k1, l_q2, l_k2, with
  *                lam_heads 1 (shared by the heads) or h_q; 16-byte aligned
  *  gamma       : device f32 [d], 16-byte aligned, or NULL for ones;  eps > 0

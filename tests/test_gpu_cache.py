@@ -674,3 +674,19 @@ def test_pages_past_32_bit_offsets():
     p.compact()
     assert int(p.block_table.max()) < n_pages - 40 and p.status() == 0
     assert torch.equal(mog.dense_decode(p.cache(), None, p.lengths, 128, q), out)
+
+
+def test_diff_a_map_of_infinitely_small_logits_is_zero():
+    """-inf in the second half of every row: the first map alone is left."""
+    m = Made(91, (100,), 1, 0, e4m3=False)
+    q = queries(92, 1, 2).abs() + 0.5
+    m.cache[0][..., 64:] = float("-inf")
+    lam, gamma = weights(93)
+    out = mog.diff_decode(*m.cache, m.lengths, 100, q, lam, 0.5, gamma)
+    K, V = m.rows64[0][0, 0], m.rows64[1][0, 0]
+    a, e, s = one_map(q[0, :, :64].double(), K[:, :64], V, 100, 64 ** -0.5)
+    r = torch.sqrt((a * a).mean(-1, keepdim=True) + 1e-5)
+    E = e + 2 * weight_error(False, False) * s
+    ref = 0.5 * gamma.double() * a / r
+    rE = torch.sqrt((E * E).mean(-1, keepdim=True))
+    check(out[0], ref, 1.05 * (0.5 * gamma.double().abs() * E / r + ref.abs() * rE / r) + 16 * STEP * ref.abs(), "map")
