@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
     const uint32_t stages = smem_u32(csm);
     const int G2 = DIFF ? 2 * a.G : a.G;
     Cursor<T::ROWS> ci, cc;  // the next tile to copy, the next to compute
-    int cnt;
+    int cnt, pg = -1;  // tiles of this CTA; the page of the next tile's row group `lane`
     if (!CLUSTER) {
         pdl_trigger();
         const int total = total_tiles<T::ROWS>(a);
@@ -838,12 +838,15 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
         cnt = min(chunk, total - t0);
         if (cnt <= 0) return;
         ci.seek(a, t0);
-    } else {  // an equal share of one unit's tiles
+    } else {  // tiles rank, rank + cs, ... of one unit: the first one's pages are known before its length
         const int u = blockIdx.x / a.cs, rank = blockIdx.x - u * a.cs;
-        ci.b = u / a.h_kv, ci.h = u - ci.b * a.h_kv;
+        ci.b = u / a.h_kv, ci.h = u - ci.b * a.h_kv, ci.t = rank;
+        if constexpr (PAGED) {
+            const int lane = threadIdx.x & 31, col = (rank * T::ROWS + 16 * lane) >> a.pshift;
+            if (lane < T::ROWS / 16 && col < a.pps) pg = __ldg(a.bt + (int64_t)ci.b * a.pps + col);
+        }
         ci.load(a);
-        ci.t = (int)((int64_t)ci.nt * rank / a.cs);
-        cnt = (int)((int64_t)ci.nt * (rank + 1) / a.cs) - ci.t;
+        cnt = ci.nt > rank ? (ci.nt - rank - 1) / a.cs + 1 : 0;
         if (cnt == 0) {  // an empty partial
             for (int i = threadIdx.x; i < G2 * PART_W; i += CT_THREADS)
                 reinterpret_cast<float *>(csm + T::PART)[i] = i % PART_W == 0 ? -INFINITY : 0.f;
@@ -852,14 +855,14 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
         }
     }
     cc = ci;
-    int pg = 0;
-    tile_page<T, PAGED>(a, ci, pg);
+    if (!CLUSTER) tile_page<T, PAGED>(a, ci, pg);
     int ahead = 0;  // tiles whose copies have started
     auto feed = [&](uint32_t stage) {
         if (ahead < cnt) {
             issue<T, PAGED>(a, ci, pg, stage);
             if (++ahead < cnt) {
-                ci.next(a);
+                if (CLUSTER) ci.t += a.cs;
+                else ci.next(a);
                 tile_page<T, PAGED>(a, ci, pg);
             }
         }
@@ -878,7 +881,7 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
         __syncthreads();  // the tile is there, and the stage before it has been consumed
         feed(stages + (slot == 0 ? T::STAGES - 1 : slot - 1) * T::STAGE);
         compute<T, DIFF, PARTS>(st, qf, qs, stages + slot * T::STAGE);
-        const bool end = cc.last();
+        const bool end = !CLUSTER && cc.last();
         if (end || i == cnt - 1) {
             float *dst = CLUSTER ? reinterpret_cast<float *>(csm + T::PART)
                               : a.part + ((int64_t)blockIdx.x + unit) * G2 * PART_W;
@@ -887,7 +890,7 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
             st.init();
         }
         slot = slot + 1 == T::STAGES ? 0 : slot + 1;
-        cc.next(a);
+        if (!CLUSTER) cc.next(a);
         if (end) {
             unit = cc.b * a.h_kv + cc.h;
             load_q<E4M3, DIFF, WIDE>(qf, qs, a, unit);
