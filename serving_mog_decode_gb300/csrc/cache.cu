@@ -86,9 +86,10 @@ int cache_splits(int units, int n_max) {
 // the partials' way through L2, a launch and the scratch, but has no more than 8 CTAs for a
 // KV head.  It is taken while all clusters fit on the GPU together (two CTAs per SM, three
 // stages each) and no CTA has more than 8 tiles of 64 rows, 4 if there is not a CTA for every SM.
-// Kernel times, one launch against two: 8 KV heads and G = 4 of e4m3, 1000 tokens 5.5 us against
-// 6.3, 2000 7.0 against 6.6 (12 against 18 with the host's part), 4096 9.5 against 7.8;
-// 32 KV heads, 4096 tokens 10.7 against 13.1.  Clusters of 16 were slower throughout.
+// Kernel times, one launch against two: 8 KV heads and G = 4 of e4m3, 1000 tokens 5.1 us against
+// 6.4 (12 against 18 with the host's part), 2000 6.2 against 7.0, 4096 8.4 against 8.2 (2 KV heads
+// 8.2 against 6.8; differential over bf16 10.9 against 9.4); 32 KV heads, 4096 tokens 10.1
+// against 13.3.  Clusters of 16 were slower throughout.
 constexpr int CLUSTER_MAX = 8;
 
 int cache_cluster(int units, int n_max) {
