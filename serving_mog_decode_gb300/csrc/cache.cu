@@ -151,20 +151,23 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
 // mog_kv_store: rows of new keys and values to their positions.  A row is 8 lanes' work, 16
 // elements a lane: with 16 lanes a row the kernel was bound by the instructions of its
 // addresses and of the elements' conversion, 45 us for 24K tokens of 8 heads in 16-row pages
-// (100 MB read, 50 MB written: 22 us), and takes 26 us so.  Elements stay packed in pairs: their magnitudes' maximum and
+// (100 MB read, 50 MB written: 22 us), and takes 24 us so.  Elements stay packed in pairs: their magnitudes' maximum and
 // their scaling are bf16x2 instructions, exact both.
 // A row's e4m3 scale is the least power of two 2^e (e >= -126) with amax <= 448*2^e, so
 // that dividing by it is exact and the only rounding is the one to e4m3.
 // ------------------------------------------------------------------------------------
+// S: type of the strides, 32 bits where they all fit (the products that make an address are then one
+// instruction each: 24.4 us against 26.1 for the prompts above).
+template <class S>
 struct StoreArgs {
     uint8_t *K, *V;
     float *ks, *vs;
-    int64_t sb, sh, sn, ssb, ssh, ssn;
+    S sb, sh, sn, ssb, ssh, ssn;
     const int *bt;
     int pshift, pps, n_pages, n_cap;
     const int *pos, *count;
     const uint16_t *kn, *vn;
-    int64_t nb, nt, nh;  // elements between sequences, tokens and heads of the new rows
+    S nb, nt, nh;  // elements between sequences, tokens and heads of the new rows
     int t_max, h_kv;
 };
 
@@ -188,29 +191,29 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {  // bf16 pair -> two
     return c;
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs a) {
+template <bool E4M3, class S>
+__global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs<S> a) {
     const int b = blockIdx.y, lane = threadIdx.x % SR_LANES;
     const int count = a.count ? min(max(a.count[b], 0), a.t_max) : a.t_max;
     const int per = 2 * a.h_kv, rows = count * per;  // head fastest, then key or value, then token
-    const int64_t start = a.pos[b];
+    const int start = a.pos[b];
     const int step = gridDim.x * (SR_THREADS / SR_LANES), dt = step / per, dr = step - dt * per;
     int i = blockIdx.x * (SR_THREADS / SR_LANES) + threadIdx.x / SR_LANES;
     int t = i / per, r = i - t * per;
     // (whole groups enter or leave: the shuffles below stay inside one)
     const unsigned group = 0xffu << (threadIdx.x & 24);
     while (i < rows) {
-        int64_t slab[SR_ROWS], pos[SR_ROWS];
+        int slab[SR_ROWS], pos[SR_ROWS];
         const uint16_t *src[SR_ROWS];
         int head[SR_ROWS];  // >= h_kv: a value row
 #pragma unroll
         for (int u = 0; u < SR_ROWS; ++u) {
-            pos[u] = start + t;
+            pos[u] = (int)((unsigned)start + (unsigned)t);  // (past 2^31: negative, and so left out)
             head[u] = r;
             const bool ok = i < rows && pos[u] >= 0 && pos[u] < a.n_cap;
             slab[u] = !ok ? -1 : a.bt ? a.bt[(int64_t)b * a.pps + (pos[u] >> a.pshift)] : b;
             const int h = r >= a.h_kv ? r - a.h_kv : r;
-            src[u] = (r >= a.h_kv ? a.vn : a.kn) + b * a.nb + t * a.nt + h * a.nh + lane * 8;
+            src[u] = (r >= a.h_kv ? a.vn : a.kn) + (int64_t)b * a.nb + (int64_t)t * a.nt + (int64_t)h * a.nh + lane * 8;
             i = i < rows ? i + step : i;  // (stays below 2^31)
             t += dt;
             r += dr;
@@ -227,9 +230,9 @@ __global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs a) {
         for (int u = 0; u < SR_ROWS; ++u) {
             if (slab[u] < 0) continue;
             const bool val = head[u] >= a.h_kv;
-            const int64_t h = val ? head[u] - a.h_kv : head[u];
-            const int64_t row = a.bt ? pos[u] & ((1 << a.pshift) - 1) : pos[u];
-            uint8_t *dst = (val ? a.V : a.K) + slab[u] * a.sb + h * a.sh + row * a.sn;
+            const int h = val ? head[u] - a.h_kv : head[u];
+            const int row = a.bt ? pos[u] & ((1 << a.pshift) - 1) : pos[u];
+            uint8_t *dst = (val ? a.V : a.K) + (int64_t)slab[u] * a.sb + (int64_t)h * a.sh + (int64_t)row * a.sn;
             if (!E4M3) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4 *>(dst + 128 * k + lane * 16) = x[u][k];
@@ -261,22 +264,24 @@ __global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs a) {
             for (int k = 0; k < 4; ++k) c[k] = e4m3_pair(bf2_mul(w[2 * k], inv2)) | e4m3_pair(bf2_mul(w[2 * k + 1], inv2)) << 16;
             *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(c[0], c[1]);
             *reinterpret_cast<uint2 *>(dst + 64 + lane * 8) = make_uint2(c[2], c[3]);
-            if (lane == 0) (val ? a.vs : a.ks)[slab[u] * a.ssb + h * a.ssh + row * a.ssn] = pow2f(e);
+            if (lane == 0) (val ? a.vs : a.ks)[(int64_t)slab[u] * a.ssb + (int64_t)h * a.ssh + (int64_t)row * a.ssn] = pow2f(e);
         }
     }
 }
 
-cudaError_t launch_kv_store(const mog_cache *c, int batch, int h_kv, int t_max, const int32_t *pos,
-                            const int32_t *count, const void *kn, const void *vn, int64_t nb, int64_t nt,
-                            int64_t nh, cudaStream_t s) {
+template <class S>
+static cudaError_t launch_store(const mog_cache *c, int batch, int h_kv, int t_max, const int32_t *pos,
+                                const int32_t *count, const void *kn, const void *vn, int64_t nb, int64_t nt,
+                                int64_t nh, cudaStream_t s) {
     const bool e4 = c->type == MOG_CACHE_E4M3;
     const int es = e4 ? 1 : 2;
     const int64_t cap = c->block_table ? (int64_t)c->pages_per_seq * c->page_rows : c->n_cap;
-    StoreArgs a{static_cast<uint8_t *>(c->k), static_cast<uint8_t *>(c->v), c->k_scale, c->v_scale,
-                c->stride_b * es, c->stride_h * es, c->stride_n * es, c->scale_b, c->scale_h, c->scale_n,
-                c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
-                (int)(cap < INT32_MAX ? cap : INT32_MAX), pos, count, static_cast<const uint16_t *>(kn),
-                static_cast<const uint16_t *>(vn), nb, nt, nh, t_max, h_kv};
+    const StoreArgs<S> a{static_cast<uint8_t *>(c->k), static_cast<uint8_t *>(c->v), c->k_scale, c->v_scale,
+                         (S)(c->stride_b * es), (S)(c->stride_h * es), (S)(c->stride_n * es), (S)c->scale_b,
+                         (S)c->scale_h, (S)c->scale_n, c->block_table,
+                         c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
+                         (int)(cap < INT32_MAX ? cap : INT32_MAX), pos, count, static_cast<const uint16_t *>(kn),
+                         static_cast<const uint16_t *>(vn), (S)nb, (S)nt, (S)nh, t_max, h_kv};
     const int64_t rows = (int64_t)t_max * 2 * h_kv, per = SR_THREADS / SR_LANES;
     // up to 16 CTAs per SM; fewer rows: one per group of lanes
     const int64_t most = ceil_div64(16LL * num_sms(), batch);
@@ -285,6 +290,16 @@ cudaError_t launch_kv_store(const mog_cache *c, int batch, int h_kv, int t_max, 
     if (e4) k_kv_store<true><<<grid, SR_THREADS, 0, s>>>(a);
     else k_kv_store<false><<<grid, SR_THREADS, 0, s>>>(a);
     return cudaGetLastError();
+}
+
+cudaError_t launch_kv_store(const mog_cache *c, int batch, int h_kv, int t_max, const int32_t *pos,
+                            const int32_t *count, const void *kn, const void *vn, int64_t nb, int64_t nt,
+                            int64_t nh, cudaStream_t s) {
+    bool small = true;
+    for (int64_t x : {2 * c->stride_b, 2 * c->stride_h, 2 * c->stride_n, c->scale_b, c->scale_h, c->scale_n, nb, nt, nh})
+        small = small && x >= INT32_MIN && x <= INT32_MAX;
+    return small ? launch_store<int>(c, batch, h_kv, t_max, pos, count, kn, vn, nb, nt, nh, s)
+                 : launch_store<int64_t>(c, batch, h_kv, t_max, pos, count, kn, vn, nb, nt, nh, s);
 }
 
 }  // namespace mog

@@ -284,6 +284,26 @@ def test_dense8_on_another_stream():
     assert torch.equal(got, want) and torch.equal(again, want)
 
 
+def test_store_past_32_bit_strides():
+    """Sequences and new rows further apart than 2^31 elements."""
+    apart = (1 << 31) + 4096
+    big = torch.zeros(2 * apart, dtype=torch.uint8, device=DEV)
+    pools = [big[at:].view(torch.float8_e4m3fn).as_strided((2, 1, 4, D), (apart, 512, D, 1)) for at in (0, 1024)]
+    scales = [torch.ones((2, 1, 4), device=DEV) for _ in range(2)]
+    new = torch.zeros(apart + 4096, dtype=torch.bfloat16, device=DEV)
+    x = [new[at:].as_strided((2, 2, 1, D), (apart, D, D, 1)) for at in (0, 512)]
+    for i, t in enumerate(x):
+        t.copy_(randn(gen(94 + i), 2, 2, 1, D))
+    mog.kv_store(mog.KV8(*pools, *scales), None, torch.tensor([1, 2], dtype=torch.int32, device=DEV), None, *x)
+    for pool, sc, t in zip(pools, scales, x):
+        for b, p0 in ((0, 1), (1, 2)):
+            row = t[b, :, 0].double()
+            want = row_scale(row)
+            assert torch.equal(sc[b, 0, p0:p0 + 2].double(), want)
+            assert torch.equal(pool[b, 0, p0:p0 + 2].double(), e4m3_nearest(row / want[:, None]))
+            assert (pool[b, 0, :p0].double() == 0).all() and (pool[b, 0, p0 + 2:].double() == 0).all()
+
+
 def test_dense8_past_32_bit_offsets():
     """One head's rows spread over more than 4 GiB by their stride."""
     n, stride = 40000, 128 * 1024
