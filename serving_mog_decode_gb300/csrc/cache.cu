@@ -148,16 +148,17 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
 }
 
 // ------------------------------------------------------------------------------------
-// mog_kv_store: rows of new keys and values to their positions.  A row is 8 lanes' work, 16
-// elements a lane: with 16 lanes a row the kernel was bound by the instructions of its
-// addresses and of the elements' conversion, 45 us for 24K tokens of 8 heads in 16-row pages
-// (100 MB read, 50 MB written: 22 us), and takes 24 us so.  Elements stay packed in pairs: their magnitudes' maximum and
-// their scaling are bf16x2 instructions, exact both.
+// mog_kv_store: rows of new keys and values to their positions.  A row is the work of four
+// lanes, 32 elements each, four 16-byte loads in flight: the kernel is bound by the instructions
+// of a row's addresses as much as by HBM, and fewer lanes share them among more elements (24K
+// tokens of 8 heads in 16-row pages, 100 MB read, 50 MB written, 22 us of HBM time: 16 lanes 45 us,
+// 8 lanes 24, 4 lanes 21.6 with part of the rows in L2, 27.7 without).  Elements stay packed in pairs:
+// their magnitudes' maximum and their scaling are bf16x2 instructions, exact both.
 // A row's e4m3 scale is the least power of two 2^e (e >= -126) with amax <= 448*2^e, so
 // that dividing by it is exact and the only rounding is the one to e4m3.
 // ------------------------------------------------------------------------------------
 // S: type of the strides, 32 bits where they all fit (the products that make an address are then one
-// instruction each: 24.4 us against 26.1 for the prompts above).
+// instruction each: 24.4 us against 26.1 with eight lanes a row).
 template <class S>
 struct StoreArgs {
     uint8_t *K, *V;
@@ -171,9 +172,7 @@ struct StoreArgs {
     int t_max, h_kv;
 };
 
-// Rows of a group of lanes in flight together: page numbers are loaded for all of them, then
-// elements, before any of them is rounded.
-constexpr int SR_THREADS = 256, SR_ROWS = 2, SR_LANES = 8;
+constexpr int SR_THREADS = 256, SR_LANES = 4, SR_VECS = 16 / SR_LANES;  // 16-byte pieces of a row per lane
 
 __device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {  // (a NaN half gives way)
     uint32_t r;
@@ -200,72 +199,65 @@ __global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs<S> a) {
     const int step = gridDim.x * (SR_THREADS / SR_LANES), dt = step / per, dr = step - dt * per;
     int i = blockIdx.x * (SR_THREADS / SR_LANES) + threadIdx.x / SR_LANES;
     int t = i / per, r = i - t * per;
-    // (whole groups enter or leave: the shuffles below stay inside one)
-    const unsigned group = 0xffu << (threadIdx.x & 24);
-    while (i < rows) {
-        int slab[SR_ROWS], pos[SR_ROWS];
-        const uint16_t *src[SR_ROWS];
-        int head[SR_ROWS];  // >= h_kv: a value row
-#pragma unroll
-        for (int u = 0; u < SR_ROWS; ++u) {
-            pos[u] = (int)((unsigned)start + (unsigned)t);  // (past 2^31: negative, and so left out)
-            head[u] = r;
-            const bool ok = i < rows && pos[u] >= 0 && pos[u] < a.n_cap;
-            slab[u] = !ok ? -1 : a.bt ? a.bt[(int64_t)b * a.pps + (pos[u] >> a.pshift)] : b;
-            const int h = r >= a.h_kv ? r - a.h_kv : r;
-            src[u] = (r >= a.h_kv ? a.vn : a.kn) + (int64_t)b * a.nb + (int64_t)t * a.nt + (int64_t)h * a.nh + lane * 8;
-            i = i < rows ? i + step : i;  // (stays below 2^31)
-            t += dt;
-            r += dr;
-            if (r >= per) r -= per, ++t;
+    // (whole groups of lanes enter or leave: the shuffles below stay inside one)
+    const unsigned group = ((1u << SR_LANES) - 1u) << (threadIdx.x & (32 - SR_LANES));
+    for (; i < rows; i += step) {  // (rows and step stay below 2^30)
+        const bool val = r >= a.h_kv;
+        const int h = val ? r - a.h_kv : r;
+        const int pos = (int)((unsigned)start + (unsigned)t);  // (past 2^31: negative, and so left out)
+        const uint16_t *src = (val ? a.vn : a.kn) + (int64_t)b * a.nb + (int64_t)t * a.nt + (int64_t)h * a.nh + lane * 8;
+        t += dt;
+        r += dr;
+        if (r >= per) r -= per, ++t;
+        if (pos < 0 || pos >= a.n_cap) continue;
+        int slab = b, row = pos;
+        if (a.bt) {
+            slab = a.bt[(int64_t)b * a.pps + (pos >> a.pshift)];
+            row = pos & ((1 << a.pshift) - 1);
+            if ((unsigned)slab >= (unsigned)a.n_pages) continue;
         }
-        uint4 x[SR_ROWS][2];  // elements 8*lane .. and 64 + 8*lane ..
+        uint32_t w[4 * SR_VECS];  // piece k: elements 8*(lane + SR_LANES*k) ..
 #pragma unroll
-        for (int u = 0; u < SR_ROWS; ++u) {
-            if (a.bt && slab[u] >= a.n_pages) slab[u] = -1;
+        for (int k = 0; k < SR_VECS; ++k) {
+            const uint4 x = ldg_nc16(src + 8 * SR_LANES * k);
+            w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+        }
+        uint8_t *dst = (val ? a.V : a.K) + (int64_t)slab * a.sb + (int64_t)h * a.sh + (int64_t)row * a.sn;
+        if (!E4M3) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) x[u][k] = slab[u] >= 0 ? ldg_nc16(src[u] + 64 * k) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < SR_VECS; ++k)
+                *reinterpret_cast<uint4 *>(dst + 16 * (lane + SR_LANES * k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            continue;
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4 * SR_VECS; ++k) m = bf2_max(m, w[k] & 0x7fff7fffu);
+        float amax = fmaxf(bf_lo(m), bf_hi(m));
+        if (amax == INFINITY) {  // the largest finite magnitude instead
+            amax = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4 * SR_VECS; ++k) {
+                const float p = fabsf(bf_lo(w[k])), q = fabsf(bf_hi(w[k]));
+                amax = fmaxf(amax, fmaxf(p < INFINITY ? p : 0.f, q < INFINITY ? q : 0.f));
+            }
         }
 #pragma unroll
-        for (int u = 0; u < SR_ROWS; ++u) {
-            if (slab[u] < 0) continue;
-            const bool val = head[u] >= a.h_kv;
-            const int h = val ? head[u] - a.h_kv : head[u];
-            const int row = a.bt ? pos[u] & ((1 << a.pshift) - 1) : pos[u];
-            uint8_t *dst = (val ? a.V : a.K) + (int64_t)slab[u] * a.sb + (int64_t)h * a.sh + (int64_t)row * a.sn;
-            if (!E4M3) {
+        for (int o = 1; o < SR_LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
+        // amax = m * 2^E, 1 <= m < 2: 448 = 1.75 * 2^8
+        const int bits = __float_as_int(amax), E = (bits >> 23) - 127;
+        int e = E - 8 + ((bits & 0x7fffff) > 0x600000);
+        e = amax > 0.f ? max(e, -126) : 0;
+        const uint32_t inv = (uint32_t)(127 - e) << 7, inv2 = inv | inv << 16;  // 2^-e twice, -126 <= -e <= 126
+        // (a product below bf16's normal range rounds, but e4m3 has only 0 there)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4 *>(dst + 128 * k + lane * 16) = x[u][k];
-                continue;
-            }
-            const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-            uint32_t m = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m = bf2_max(m, w[k] & 0x7fff7fffu);
-            float amax = fmaxf(bf_lo(m), bf_hi(m));
-            if (amax == INFINITY) {  // the largest finite magnitude instead
-                amax = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float p = fabsf(bf_lo(w[k])), q = fabsf(bf_hi(w[k]));
-                    amax = fmaxf(amax, fmaxf(p < INFINITY ? p : 0.f, q < INFINITY ? q : 0.f));
-                }
-            }
-#pragma unroll
-            for (int o = 1; o < SR_LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
-            // amax = m * 2^E, 1 <= m < 2: 448 = 1.75 * 2^8
-            const int bits = __float_as_int(amax), E = (bits >> 23) - 127;
-            int e = E - 8 + ((bits & 0x7fffff) > 0x600000);
-            e = amax > 0.f ? max(e, -126) : 0;
-            const uint32_t inv = (uint32_t)(127 - e) << 7, inv2 = inv | inv << 16;  // 2^-e twice, -126 <= -e <= 126
-            // (a product below bf16's normal range rounds, but e4m3 has only 0 there)
+        for (int k = 0; k < SR_VECS; ++k) {
             uint32_t c[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] = e4m3_pair(bf2_mul(w[2 * k], inv2)) | e4m3_pair(bf2_mul(w[2 * k + 1], inv2)) << 16;
-            *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(c[0], c[1]);
-            *reinterpret_cast<uint2 *>(dst + 64 + lane * 8) = make_uint2(c[2], c[3]);
-            if (lane == 0) (val ? a.vs : a.ks)[(int64_t)slab[u] * a.ssb + (int64_t)h * a.ssh + (int64_t)row * a.ssn] = pow2f(e);
+            for (int j = 0; j < 4; ++j) c[j] = e4m3_pair(bf2_mul(w[4 * k + j], inv2));
+            *reinterpret_cast<uint2 *>(dst + 8 * (lane + SR_LANES * k)) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
         }
+        if (lane == 0)
+            (val ? a.vs : a.ks)[(int64_t)slab * a.ssb + (int64_t)h * a.ssh + (int64_t)row * a.ssn] = pow2f(e);
     }
 }
 
