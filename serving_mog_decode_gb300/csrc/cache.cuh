@@ -24,11 +24,12 @@
 // e4m3 rows are read by 16-byte loads in the order the fragments want (dimensions are
 // permuted alike in K and q, and back in the output), then widened in registers to fp16,
 // which holds every e4m3 value exactly.  q enters as fp16 scaled by a power of two of its
-// own, so that its elements down to 2^-29 of the largest are exact.  Weights enter the P.V
-// product as fp16 (2^14 * p * v_scale / running power of two >= v_scale): high part alone
-// (2^-12 relative) when the output is rounded to bf16, high + low parts (2^-22) when it
-// stays fp32.  bf16 rows go through ldmatrix; their weights are bf16 high + low parts for
-// a bf16 output (2^-17) and three parts (2^-24) for an fp32 one.  All sums are fp32.
+// own, so that its elements down to 2^-29 of the largest are exact.  Weights p * v_scale enter
+// the P.V product as fp16, 2^14 times their share of a running unit: high part alone
+// (2^-11 relative) when the output is rounded to bf16, high + low parts (2^-22) when it
+// stays fp32, and no better than 2^-39 of the unit.  The unit is at most 2^11 times the largest weight
+// of a row that is not zero (new_unit).  bf16 rows go through ldmatrix; their weights are bf16
+// high + low parts for a bf16 output (2^-16) and three parts (2^-24) for an fp32 one.  All sums are fp32.
 //
 // Bound by: HBM in the narrow form (whole steps: 1M e4m3 tokens, 8 KV heads, G = 4: 312 us,
 // 7.1 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 316 us, 6.8 TB/s); the
@@ -47,7 +48,9 @@ namespace mog {
 constexpr int CT_WARPS = 4;
 constexpr int CL_PER_SM = 2, CL_STAGES = 3;  // CTAs per SM and stages of the cluster form: short caches, latency
 constexpr int CT_THREADS = 32 * CT_WARPS;
-constexpr float W_SCALE = 16384.f;  // 2^14: scale of fp16 weights
+constexpr int W_EXP = 14;           // fp16 weights: 2^14 times their share of the unit
+constexpr int V_RANGE = 10 << 23;   // value scales within 2^10 of the unit's are in order (a difference of float bits)
+constexpr int V_NONE = 0x7fffffff;  // no unit yet
 
 // A tile is copied by the whole CTA, 2 KB of neighbouring rows per instruction, and each
 // warp consumes BLK blocks of 16 of its rows.  Stages are aligned to 128 bytes: 16 bytes off,
@@ -251,8 +254,11 @@ template <bool WIDE>
 struct State {
     static constexpr int NT = WIDE ? 16 : 8;
     float o[NT][4];
-    float m[2], l[2];  // maximum (log2 domain); this lane's share of the sum
-    float vr;  // e4m3: power of two >= every v_scale seen (0: none yet); o is in units of vr / W_SCALE
+    float m[2], l[2];  // what logits are relative to (log2 domain): their maximum, but see new_unit; this lane's share of the sum
+    // e4m3: bits of the least value scale in order; the largest is 2^ve, and o is in units of
+    // 2^(m + ve - W_EXP) (the same in all lanes)
+    int vlo;
+    __device__ __forceinline__ int ve() const { return (vlo >> 23) - 127 + (V_RANGE >> 23); }
     __device__ __forceinline__ void init() {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -260,7 +266,7 @@ struct State {
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
-        vr = 0.f;
+        vlo = V_NONE;
     }
     static __device__ __forceinline__ int col(int e) { return WIDE ? e >> 1 : e & 1; }
 };
@@ -408,6 +414,105 @@ __device__ __forceinline__ void k_frag(uint32_t (&a)[4], uint32_t sk, int ks, co
     }
 }
 
+// The largest of a column's values.
+template <bool WIDE>
+__device__ __forceinline__ float column_max(float x) {
+#pragma unroll
+    for (int o = WIDE ? 1 : 4; o < (WIDE ? 4 : 32); o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+// Row (of a block of 16) and column (of the lane's two) of logit i.
+template <bool WIDE>
+__device__ __forceinline__ int logit_row(int i) {
+    const int lane = threadIdx.x & 31;
+    return WIDE ? 2 * (lane & 3) + (i & 1) + 8 * (i >> 2) : (lane >> 2) + 8 * (i >> 1);
+}
+template <bool WIDE>
+__device__ __forceinline__ constexpr int logit_col(int i) { return WIDE ? (i >> 1) & 1 : i & 1; }
+
+__device__ __forceinline__ int exp_above(float x) { return (__float_as_int(x) >> 23) - 126; }  // |x| < 2^that, x >= 0
+
+// e4m3: a unit for a tile with value scales out of order.  Weights 2^s * v_scale are held in fp16
+// as shares of the unit 2^(m + ve).  While the scales stay between 2^(ve - 10) and 2^ve the unit
+// follows the largest logit alone.  A scale outside may belong to a row of zeros (kv_store gives it
+// the scale 1) or to one without weight; a unit made for it would leave the other rows' weights
+// no bits.  So rows of zeros are left out (their scale in the stage becomes 0), and m becomes the
+// largest s + log2 v_scale of the rest, less ve.  It may end above or below the largest logit: bounds keep the
+// sum, which counts rows of zeros too, and o, which may hold more than this tile brings, inside fp32.
+// mine: the bits of the scale of row `lane`;  there: is that row in the cache.
+template <class T, int NS>
+__device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T::BLK][NS], float (&mx)[2], int mine,
+                                         bool there, uint32_t sv, uint32_t vsc) {
+    constexpr bool WIDE = T::WIDE;
+    constexpr int INF = 0x7f800000;
+    static_assert(!T::E4M3 || T::WROWS == 32, "a lane per row");
+    const int lane = threadIdx.x & 31;
+    auto made = [](int hi) { return (max((hi >> 23) + 1, 15) << 23) - V_RANGE; };  // (ve >= -112)
+    int hi = __reduce_max_sync(0xffffffffu, mine < INF ? mine : 0);
+    if (st.vlo == V_NONE && hi - __reduce_min_sync(0xffffffffu, there ? mine : INF) <= V_RANGE) {
+        st.vlo = made(hi);  // the first tile, in order within itself
+        return;
+    }
+    uint32_t any = 0;
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+        const uint4 x = lds16(sv + swz_v<T::E4M3>(lane, ch));
+        any |= x.x | x.y | x.z | x.w;
+    }
+    const bool zero = (any & 0x7f7f7f7fu) == 0 && mine < INF;
+    if (zero) asm volatile("st.shared.u32 [%0], %1;" ::"r"(vsc + 4 * lane), "r"(0) : "memory");
+    hi = __reduce_max_sync(0xffffffffu, mine < INF && !zero ? mine : 0);
+    __syncwarp();
+    const int ve_old = st.ve();
+    if (st.vlo == V_NONE || (hi > 0 && (unsigned)(hi - st.vlo) > V_RANGE)) st.vlo = made(hi);
+    int ve = st.ve();
+    float far[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int blk = 0; blk < T::BLK; ++blk)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int v = __float_as_int(lds4(vsc + 4 * (16 * blk + logit_row<WIDE>(i)))) & 0x7fffffff;
+            // (rounded up: a weight must not pass the unit)
+            const float x = v > 0 && v < INF ? __fadd_ru(s[blk][i], (float)((v >> 23) - 126 - ve)) : -INFINITY;
+            far[logit_col<WIDE>(i)] = fmaxf(far[logit_col<WIDE>(i)], x);
+        }
+    // a row of the largest logit would pass 2^80: a smaller ve (v_scale * 2^(W_EXP - ve) stays finite)
+    float least = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        far[c] = column_max<WIDE>(far[c]);
+        if (far[c] > -INFINITY) least = fminf(least, fmaxf(far[c] - mx[c], -512.f) + 80.f);
+    }
+    const int less = max((int)-warp_max(-least), max(-100, -112 - ve));
+    ve += less;
+    st.vlo += less * (1 << 23);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int d = ve_old - ve;
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < State<WIDE>::NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (State<WIDE>::col(e) == c) big = fmaxf(big, fabsf(st.o[i][e]));
+        big = column_max<WIDE>(big);
+        const float sum = column_max<WIDE>(st.l[c]);
+        float m = fmaxf(__fadd_ru(far[c], (float)-less), mx[c] - 90.f);                   // this tile's terms of the sum: 2^90
+        if (sum > 0.f) m = fmaxf(m, st.m[c] + (float)(max(exp_above(sum), -30) - 90));      // the sum: 2^90
+        if (big > 0.f) m = fmaxf(m, __fadd_ru(st.m[c], (float)(d + max(exp_above(big), -30) - 54)));  // o: 2^54
+        if (m == -INFINITY) continue;  // (nothing so far)
+        m = ceilf(m);
+        const float fl = ex2(st.m[c] - m), fo = ex2(fminf(st.m[c] - m + (float)d, 126.f));
+        st.l[c] *= fl;
+#pragma unroll
+        for (int i = 0; i < State<WIDE>::NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (State<WIDE>::col(e) == c) st.o[i][e] *= fo;
+        st.m[c] = mx[c] = m;
+    }
+}
+
 // This warp's rows of a tile.
 //
 // The products of one tile start from zero on the tensor cores, which truncate their sums,
@@ -472,8 +577,8 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
     // log2-domain logits; row of s[blk][i]: rowof(i).  They are rounded before the maximum is taken
     // from them (no fused multiply-add in the exponent): the largest weight has to be 1 however
     // large the logits.
-    auto rowof = [&](int i) { return WIDE ? 2 * t + (i & 1) + 8 * (i >> 2) : g + 8 * (i >> 1); };
-    auto colof = [](int i) { return WIDE ? (i >> 1) & 1 : i & 1; };
+    auto rowof = [](int i) { return logit_row<WIDE>(i); };
+    auto colof = [](int i) { return logit_col<WIDE>(i); };
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
         float k[4];  // scales of this lane's rows of the block (narrow: two of them)
@@ -496,35 +601,31 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
             for (int i = 0; i < NS; ++i)
                 if (!((rows >> (16 * blk + rowof(i))) & 1u)) s[blk][i] = -INFINITY;
     }
-    float inv = 0.f;
-    if (E4M3) {
-        const float mine = fabsf(lds4(sc + 4 * (T::ROWS + lane % T::WROWS)));
-        if (__any_sync(0xffffffffu, mine > st.vr)) {  // a larger value scale: new unit
-            const float vr = pow2f(min(max((__float_as_int(warp_max(mine)) >> 23) - 126, -100), 127));
-            const float f = st.vr / vr;
-#pragma unroll
-            for (int i = 0; i < State<WIDE>::NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st.o[i][e] *= f;
-            st.vr = vr;
-        }
-        inv = st.vr > 0.f ? W_SCALE / st.vr : 0.f;  // (rows whose scales are all 0 have no unit yet)
-    }
 
     // maxima, rescale factors, weights
-    float al[2], sh[2];
+    float al[2], sh[2], mx[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        float mx = -INFINITY;
+        mx[c] = -INFINITY;
 #pragma unroll
         for (int blk = 0; blk < BLK; ++blk)
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                if (colof(i) == c) mx = fmaxf(mx, s[blk][i]);
+                if (colof(i) == c) mx[c] = fmaxf(mx[c], s[blk][i]);
+        mx[c] = column_max<WIDE>(mx[c]);
+    }
+    float inv = 0.f;
+    if (E4M3) {
+        const int mine = __float_as_int(lds4(sc + 4 * (T::ROWS + lane))) & 0x7fffffff;
+        const bool there = (rows >> lane) & 1u;
+        if (__any_sync(0xffffffffu, there && (unsigned)(mine - st.vlo) > V_RANGE))
+            new_unit<T>(st, s, mx, mine, there, sv, sc + 4 * T::ROWS);
+        inv = pow2f(W_EXP - st.ve());
+    }
 #pragma unroll
-        for (int o = WIDE ? 1 : 4; o < (WIDE ? 4 : 32); o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int c = 0; c < 2; ++c) {
         // the shift: 0 until a row has been seen, so that no infinities are subtracted
-        const float mn = fmaxf(st.m[c], mx);
+        const float mn = fmaxf(st.m[c], mx[c]);
         sh[c] = mn == -INFINITY ? 0.f : mn;
         al[c] = ex2(st.m[c] - sh[c]);
         st.m[c] = mn;
@@ -663,7 +764,7 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
     constexpr int SW = S::NT * 4 * 32;  // words of a warp's accumulators
     static_assert(T::XCH == 2 * SW * 4 && T::AUX >= T::XCH, "two states fit in a stage");
     if (E4M3) {  // to the values' own unit
-        const float u = st.vr / W_SCALE;
+        const float u = pow2f(st.vlo == V_NONE ? 0 : st.ve() - W_EXP);
 #pragma unroll
         for (int i = 0; i < S::NT; ++i)
 #pragma unroll

@@ -1,0 +1,142 @@
+"""e4m3 decode where value rows are of very different size: rows of zeros (which kv_store gives the
+scale 1) among small ones, large rows without weight, rows that lose their weight later.
+
+The bounds are those of test_gpu_cache, per output element and relative to sum p |v|.  To
+them the kernel adds 2^-39 of its unit per row, and the unit is at most 2^11 times the largest weight
+p * v_scale among a warp's rows that are not zero: 2^-28 of that weight for each of the few hundred
+rows of a warp, whose codes are of comparable size here: 2^-20 of sum p |v|, inside the bounds' 2^-15.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import serving_mog_decode_gb300 as mog
+from serving_mog_decode_gb300 import buildlib
+from test_gpu_cache import D, DEV, OUTS, check_dense8, check_diff, gen, queries, randn, weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    buildlib.build()
+    mog.lib()
+
+
+class Stored:
+    """Rows k, v (float [H, n, D]) of one sequence, written by kv_store, in 64 bits as stored."""
+
+    def __init__(self, k, v, slack):
+        self.H, n = k.shape[:2]
+        self.lens, self.B, self.n_max = (n,), 1, n + slack
+        codes = [torch.zeros((1, self.H, n + slack, D), device=DEV).to(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.full((1, self.H, n + slack), float("nan"), device=DEV) for _ in range(2)]
+        self.cache = mog.KV8(*codes, *scales), None
+        self.lengths = torch.tensor([n], dtype=torch.int32, device=DEV)
+        new = [x.transpose(0, 1)[None].bfloat16().contiguous() for x in (k, v)]
+        mog.kv_store(*self.cache, torch.zeros_like(self.lengths), None, *new)
+        self.rows64 = [c[:, :, :n].double() * s[:, :, :n].double()[..., None] for c, s in zip(codes, scales)]
+
+
+def check_all(m, q, G, out_type):
+    """dense_decode and (up to 8 heads) diff_decode over the cache."""
+    out = torch.empty(q.shape, dtype=out_type, device=DEV)
+    check_dense8(m, q, mog.dense_decode(*m.cache, m.lengths, m.n_max, q, out=out), G)
+    if G <= 8:
+        lam, gamma = weights(7)
+        mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma, eps=1e-30, out=out)
+        check_diff(m, q, out, G, lam, 0.5, gamma, 1e-30)
+
+
+FORMS = pytest.mark.parametrize("G,slack", [(1, 0), (4, 0), (4, 3000), (5, 3000), (8, 0), (9, 0), (16, 3000)])
+
+
+@pytest.mark.parametrize("out_type", OUTS)
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-6, 1e-8, 1e-12])
+@FORMS
+def test_rows_of_zeros_among_small_rows(G, slack, size, out_type):
+    """Whole tiles of zeros, and single rows of zeros in every other tile."""
+    g = gen(1)
+    H, n = 2, 700
+    k, v = 0.3 * randn(g, H, n, D), size * randn(g, H, n, D)
+    v[:, :40] = 0
+    v[:, ::16] = 0
+    v[:, 320:480] = 0
+    check_all(Stored(k, v, slack), 0.3 * queries(2, 1, H * G), G, out_type)
+
+
+@pytest.mark.parametrize("out_type", OUTS)
+@pytest.mark.parametrize("at", [(70,), (0, 1, 2), tuple(range(64, 128)), (699,)])
+@FORMS
+def test_large_rows_that_some_heads_do_not_see(G, slack, at, out_type):
+    """Rows 2^40 times the others: every other head gives them e^-100 of the rest's weight, the
+    others all of it."""
+    g = gen(3)
+    H, n = 2, 700
+    k, v = 0.3 * randn(g, H, n, D), 1e-3 * randn(g, H, n, D)
+    q = 0.3 * queries(4, 1, H * G)
+    for d in (0, 64):
+        k[..., d], q[..., d] = 0, 0
+        k[:, list(at), d] = -100.0
+        q[:, ::2, d] = 8.0
+        q[:, 1::2, d] = -8.0
+    v[:, list(at)] *= 2.0 ** 40
+    check_all(Stored(k, v, slack), q, G, out_type)
+
+
+@pytest.mark.parametrize("out_type", OUTS)
+@pytest.mark.parametrize("first,later,gap", [(2.0 ** 30, 1e-3, 40.0), (2.0 ** 100, 1e-20, 180.0), (0.0, 1e-30, 0.0)])
+@FORMS
+def test_large_rows_that_lose_their_weight(G, slack, first, later, gap, out_type):
+    """Rows `first` in size, then rows `later` in size whose logits are `gap` above theirs."""
+    g = gen(5)
+    H, n, lead = 2, 900, 200
+    k, v = 0.3 * randn(g, H, n, D), randn(g, H, n, D)
+    q = 0.3 * queries(6, 1, H * G)
+    for d in (0, 64):
+        k[..., d], q[..., d] = 0, 11.0
+        k[:, lead:, d] = gap
+    v[:, :lead] *= first
+    v[:, lead:] *= later
+    m = Stored(k, v, slack)
+    if later > 1e-18:
+        return check_all(m, q, G, out_type)
+    # (below the floor of check_dense8's comparison: the same values times 2^60 are the same output times 2^60)
+    out = torch.empty(q.shape, dtype=out_type, device=DEV)
+    mog.dense_decode(*m.cache, m.lengths, m.n_max, q, out=out)
+    m.rows64[1] = m.rows64[1] * 2.0 ** 60
+    check_dense8(m, q, (out.float() * 2.0 ** 60).to(out_type), G)
+
+
+@pytest.mark.parametrize("out_type", OUTS)
+@pytest.mark.parametrize("G", [4, 9])
+@pytest.mark.parametrize("sink", [False, True])
+def test_a_long_flat_tail_beside_one_row(G, sink, out_type):
+    """300,000 rows of e^-12 of the largest row's weight each, which together outweigh it; that row's
+    values zero, or like the others'."""
+    g = gen(8)
+    n = 300000
+    k, v = torch.zeros((1, n, D), device=DEV), 1e-6 * (1 + 0.2 * randn(g, 1, n, D))
+    q = 0.1 * queries(9, 1, G)
+    for d in (0, 64):
+        q[..., d] = 8.0
+        k[:, 5, d] = 12.0 * D ** 0.5 / 16
+    v[:, ::1000] = 0
+    if sink:
+        v[:, 5] = 0
+    check_all(Stored(k, v, 0), q, G, out_type)
+
+
+@pytest.mark.parametrize("G", [4, 9])
+def test_a_row_of_zeros_whose_scale_is_infinite_shows(G):
+    """scale * code is NaN there, as in the definition."""
+    g = gen(10)
+    k, v = 0.3 * randn(g, 2, 200, D), 1e-6 * randn(g, 2, 200, D)
+    v[:, ::16] = 0
+    m = Stored(k, v, 0)
+    q = queries(11, 1, 2 * G)
+    m.cache[0].v_scale[0, 0, 48] = float("inf")
+    out = mog.dense_decode(*m.cache, m.lengths, m.n_max, q)
+    assert torch.isnan(out[0, :G]).all() and torch.isfinite(out[0, G:]).all()
