@@ -136,8 +136,8 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
     const int splits = std::min(cache_splits(batch * h_kv, n_max), per_sm * num_sms());
     while (a.cs > 1 && a.cs / 2 >= ceil_div64(n_max, rows)) a.cs /= 2;  // as many CTAs as tiles do
     const cudaError_t e = e4 ? launch_split8(a, d, out, diff != nullptr, bf_out, wide, splits, s)
-                          : bf_out ? pick_split<false, true, 2>(a, d, out, wide, splits, s)
-                                   : pick_split<false, true, 3>(a, d, out, wide, splits, s);
+                          : bf_out ? pick_split<false, true, true>(a, d, out, wide, splits, s)
+                                   : pick_split<false, true, false>(a, d, out, wide, splits, s);
     if (e != cudaSuccess || a.cs) return e;
     // a unit has splits / units partials and one more: a CTA per head from about five
     if (splits > 4 * batch * h_kv)

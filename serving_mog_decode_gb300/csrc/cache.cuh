@@ -25,11 +25,10 @@
 // permuted alike in K and q, and back in the output), then widened in registers to fp16,
 // which holds every e4m3 value exactly.  q enters as fp16 scaled by a power of two of its
 // own, so that its elements down to 2^-29 of the largest are exact.  Weights p * v_scale enter
-// the P.V product as fp16, 2^14 times their share of a running unit: high part alone
-// (2^-11 relative) when the output is rounded to bf16, high + low parts (2^-22) when it
-// stays fp32, and no better than 2^-39 of the unit.  The unit is at most 2^11 times the largest weight
-// of a row that is not zero (new_unit).  bf16 rows go through ldmatrix; their weights are bf16
-// high + low parts for a bf16 output (2^-16) and three parts (2^-24) for an fp32 one.  All sums are fp32.
+// the P.V product as fp16, 2^14 times their share of a running unit: high + low parts (2^-22
+// relative), or the high part alone (2^-11; weight_parts), and no better than 2^-39 of the unit.  The unit is at most 2^11 times the largest weight
+// of a row that is not zero (new_unit).  bf16 rows go through ldmatrix; their weights are three bf16
+// parts (2^-24), or two for a bf16 output (2^-16).  All sums are fp32.
 //
 // Bound by: HBM in the narrow form (whole steps: 1M e4m3 tokens, 8 KV heads, G = 4: 312 us,
 // 7.1 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 316 us, 6.8 TB/s); the
@@ -49,6 +48,14 @@ constexpr int CT_WARPS = 4;
 constexpr int CL_PER_SM = 2, CL_STAGES = 3;  // CTAs per SM and stages of the cluster form: short caches, latency
 constexpr int CT_THREADS = 32 * CT_WARPS;
 constexpr int W_EXP = 14;           // fp16 weights: 2^14 times their share of the unit
+// 16-bit parts that a weight of the second product is held in.  A bf16 output takes one less where that
+// is worth something: bf16 weights stay within 2^-16 of theirs, a 256th of the output's half step,
+// and the step is 1% to 4% faster (2 x 4K tokens, G = 4: 11.3 us against 11.6; 4 x 128K, G = 5: 313 against 316);
+// one fp16 part, within 2^-11, an eighth of that half step, is for the wide form alone (16 heads, 512K: 172 us
+// against 202; the narrow form: 1M tokens, G = 4: 308 against 311).
+constexpr int weight_parts(bool e4m3, bool wide, bool bf16_out) {
+    return (e4m3 ? 2 : 3) - (bf16_out && (wide || !e4m3) ? 1 : 0);
+}
 constexpr int V_RANGE = 10 << 23;   // value scales within 2^10 of the unit's are in order (a difference of float bits)
 constexpr int V_NONE = 0x7fffffff;  // no unit yet
 
@@ -920,13 +927,13 @@ __device__ __forceinline__ void cluster_end(const CacheArgs &a, const DiffArgs &
 
 // CLUSTER: the form with a cluster of a.cs CTAs per unit (a kernel of its own: the two in one cost
 // the split form registers and 14% of its speed).
-template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS, bool CLUSTER>
+template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, bool BF16OUT, bool CLUSTER>
 __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
     extern __shared__ __align__(128) uint8_t csm[];
     __shared__ Exchange ex;
     __shared__ QShared qs;  // (wide)
     using T = Tile<E4M3, WIDE, CLUSTER>;
-    constexpr bool BF16OUT = PARTS == (E4M3 ? 1 : 2);  // (the parts go by the output's type)
+    constexpr int PARTS = weight_parts(E4M3, WIDE, BF16OUT);
     const uint32_t stages = smem_u32(csm);
     const int G2 = DIFF ? 2 * a.G : a.G;
     Cursor<T::ROWS> ci, cc;  // the next tile to copy, the next to compute
@@ -1001,10 +1008,10 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
     if (CLUSTER) cluster_end<T, DIFF, BF16OUT>(a, d, out, stages, unit);
 }
 
-template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, int PARTS>
+template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, bool BF16OUT>
 static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out, int splits, cudaStream_t s) {
     const int smem = a.cs ? Tile<E4M3, WIDE, true>::SMEM : Tile<E4M3, WIDE>::SMEM;
-    const auto fn = a.cs ? k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS, true> : k_cache_split<E4M3, WIDE, PAGED, DIFF, PARTS, false>;
+    const auto fn = a.cs ? k_cache_split<E4M3, WIDE, PAGED, DIFF, BF16OUT, true> : k_cache_split<E4M3, WIDE, PAGED, DIFF, BF16OUT, false>;
     const cudaError_t e = ensure_smem((const void *)fn, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1023,12 +1030,12 @@ static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out
 
 // The instance for a call: launches it (a.cs > 0: as clusters, one launch; else the split of
 // `splits` CTAs, whose partials k_cache_merge folds).
-template <bool E4M3, bool DIFF, int PARTS>
+template <bool E4M3, bool DIFF, bool BF16OUT>
 static cudaError_t pick_split(const CacheArgs &a, const DiffArgs &d, void *out, bool wide, int splits, cudaStream_t s) {
-    if (a.bt) return wide ? launch_split<E4M3, true, true, DIFF, PARTS>(a, d, out, splits, s)
-                          : launch_split<E4M3, false, true, DIFF, PARTS>(a, d, out, splits, s);
-    return wide ? launch_split<E4M3, true, false, DIFF, PARTS>(a, d, out, splits, s)
-                : launch_split<E4M3, false, false, DIFF, PARTS>(a, d, out, splits, s);
+    if (a.bt) return wide ? launch_split<E4M3, true, true, DIFF, BF16OUT>(a, d, out, splits, s)
+                          : launch_split<E4M3, false, true, DIFF, BF16OUT>(a, d, out, splits, s);
+    return wide ? launch_split<E4M3, true, false, DIFF, BF16OUT>(a, d, out, splits, s)
+                : launch_split<E4M3, false, false, DIFF, BF16OUT>(a, d, out, splits, s);
 }
 
 cudaError_t launch_split8(const CacheArgs &a, const DiffArgs &d, void *out, bool diff, bool bf_out, bool wide, int splits,

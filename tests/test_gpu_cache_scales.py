@@ -140,3 +140,29 @@ def test_a_row_of_zeros_whose_scale_is_infinite_shows(G):
     m.cache[0].v_scale[0, 0, 48] = float("inf")
     out = mog.dense_decode(*m.cache, m.lengths, m.n_max, q)
     assert torch.isnan(out[0, :G]).all() and torch.isfinite(out[0, G:]).all()
+
+
+@pytest.mark.parametrize("slack", [0, 3000])
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("n", [1, 5])
+def test_bf16_outputs_up_to_eight_heads_are_rounded_once(n, G, slack):
+    """Equal keys, so that every weight is 1/n and each output is the mean of n values: within half a bf16
+    step of it and the fp32 form's error (weights 2^-22, sums 2^-16).  Weights in one fp16 part, all off by the
+    same 2^-11 or less, would carry a few outputs over the next border."""
+    g = gen(12)
+    H = 8
+    k, v = torch.ones((1, H, n, D), device=DEV), randn(g, 1, H, n, D).abs() + 0.1
+    scale = v.amax(-1) / 448.0 * (1 + 0.3 * torch.rand((1, H, n), generator=g, device=DEV))
+    codes = [x.to(torch.float8_e4m3fn) for x in (k, v / scale[..., None])]
+    caps = [torch.zeros((1, H, n + slack, D), device=DEV).to(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones((1, H, n + slack), device=DEV) for _ in range(2)]
+    for c, x in zip(caps, codes):
+        c[:, :, :n].view(torch.uint8).copy_(x.view(torch.uint8))
+    scales[1][:, :, :n] = scale
+    lengths = torch.tensor([n], dtype=torch.int32, device=DEV)
+    q = queries(13, 1, H * G)
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+    mog.dense_decode(mog.KV8(*caps, *scales), None, lengths, n + slack, q, out=out)
+    ref = (codes[1].double() * scale.double()[..., None]).mean(2)[0].repeat_interleave(G, 0)
+    half = 2.0 ** (torch.floor(torch.log2(ref)) - 8)
+    assert ((out[0].double() - ref).abs() <= half + (2.0 ** -16 + 2.0 ** -22) * ref).all()
