@@ -625,7 +625,8 @@ int mog_pages_grow(const mog_pages *p, const int32_t *n_new_dev, int32_t *pos_de
  * Move the pages in use to the front of the pools: with n_live pages held, the live pages
  * behind the first n_live move, in ascending order, to the free places among them, and the
  * block table and refs follow.  Afterwards pages [n_live, n_pages) are free.  A mog_handle
- * built over the old table is no longer valid.
+ * built over the old table is no longer valid.  If pages move, an entry outside the pool, or whose
+ * page refs count as free, stays as it is and is reported.
  */
 int mog_pages_compact(const mog_pages *p, void *stream);
 

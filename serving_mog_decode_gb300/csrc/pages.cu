@@ -17,8 +17,9 @@
 
 namespace mog {
 
-// Work buffer (int32): header, the list of copies (sources, destinations), and per page
-// the free pages found (grow) or the new place of a page that moves (compact).
+// Work buffer (int32): header, the list of copies (sources, destinations), and n_pages entries:
+// the free pages found (grow) or, of a page that moves or is moved to, the number of its copy (compact;
+// other entries are what earlier calls left, so that a number counts only if its copy names the page).
 constexpr int PW_HEAD = 64;
 enum { PW_STATUS = 0, PW_COPIES = 1, PW_LIVE = 2 };
 
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(PL_THREADS) k_pages_plan(PagesArgs a) {
     __syncthreads();
     for (int i = tid; i < movers; i += PL_THREADS) {  // holes == movers
         const int from = a.src()[i], to = a.dst()[i];
-        a.map()[from] = to;
+        a.map()[from] = a.map()[to] = i;
         a.refs[to] = a.refs[from];
         a.refs[from] = 0;
     }
@@ -329,10 +330,16 @@ __global__ void __launch_bounds__(CP_THREADS) k_pages_copy(PagesArgs a, PoolArgs
         const int64_t live = a.work[PW_LIVE], entries = (int64_t)a.batch * a.pps;
         for (int64_t i = blockIdx.x * (int64_t)CP_THREADS + threadIdx.x; i < entries; i += (int64_t)gridDim.x * CP_THREADS) {
             const int p = a.table[i];
-            if (p < live && p >= -1) continue;
-            const int to = p >= live && p < a.n_pages ? a.map()[p] : -1;
-            if (to >= 0 && to < live) a.table[i] = to;
-            else atomicOr(a.work + PW_STATUS, PAGES_BAD_INDEX);  // a page that nothing is counted to hold
+            if (p == -1) continue;
+            bool bad = (unsigned)p >= (unsigned)a.n_pages;
+            if (!bad) {
+                const int c = a.map()[p];
+                const bool listed = (unsigned)c < (unsigned)n;
+                const int from = listed ? a.src()[c] : -1, to = listed ? a.dst()[c] : -1;
+                if (from == p) a.table[i] = to;
+                else bad = p == to || p >= live;  // refs had it free: nothing is counted to hold it
+            }
+            if (bad) atomicOr(a.work + PW_STATUS, PAGES_BAD_INDEX);  // (the entry stays)
         }
     }
     copy_pages(a, pl, n, blockIdx.x, gridDim.x, threadIdx.x);

@@ -1,0 +1,55 @@
+"""PagePool over state that the caller has broken, or set anew: reported or refused, and other sequences'
+rows stay theirs."""
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import serving_mog_decode_gb300 as mog
+from serving_mog_decode_gb300 import buildlib
+from test_gpu_pages import DEV, bits, ints, make, tensors
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    buildlib.build()
+    mog.lib()
+
+
+def row_bytes(pool, b):
+    """The bytes of sequence b's pages in every pool, in the sequence's order."""
+    used = -(-int(pool.lengths[b]) // pool.page_rows)
+    pages = pool.block_table[b, :used].long()
+    return [bits(t)[pages] for t in tensors(pool)]
+
+
+@pytest.mark.parametrize("grown", [False, True])  # (an earlier call's list in the work buffer)
+@pytest.mark.parametrize("slot", [0, 5])          # a page in front of the moved ones, one behind
+def test_compaction_reports_a_held_page_that_refs_count_as_free(slot, grown):
+    R, n = 16, 6 * 16
+    pool = make(64, R, 4, 8)
+    if grown:
+        pool.grow(ints([n] * 4))
+    else:  # the same state, in a work buffer that no call has written
+        pool.block_table[:, :6] = torch.arange(24, device=DEV, dtype=torch.int32).view(4, 6)
+        pool.lengths.fill_(n)
+        pool.refs[:24] = 1
+    pool.assign(ints([-1, 1, 2, 3]))  # pages 0 .. 5 come free, 18 pages live
+    page = 3 * 6 + slot if slot else 6
+    b, at = (3, slot) if slot else (1, 0)
+    assert int(pool.block_table[b, at]) == page and pool.status() == 0
+    pool.refs[page] = 0
+    others = [x for x in range(1, 4) if x != b]
+    keep = {x: row_bytes(pool, x) for x in others}
+    pool.compact()
+    assert pool.status() == 5
+    assert int(pool.block_table[b, at]) == page
+    for x in others:
+        assert all(torch.equal(got, want) for got, want in zip(row_bytes(pool, x), keep[x]))
+    table = pool.block_table.clone()
+    table[b, at] = -1
+    held = torch.bincount(table[table >= 0].long(), minlength=64).int()
+    assert torch.equal(held, pool.refs)  # every other entry and its count moved together
