@@ -59,11 +59,9 @@ class PagedKV:
 
     def __init__(self, K, V, block_table, page_rows, heads_first=True):
         torch = _torch()
-        for t in (K, V):
-            if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1 or not t.is_cuda:
-                raise ValueError("page pools must be CUDA bf16 tensors with 4 dims, last contiguous")
-        if K.shape != V.shape or K.stride() != V.stride():
-            raise ValueError("K and V pools must share shape and strides")
+        _check_pools(K, V)
+        if not (K.is_cuda and V.is_cuda):
+            raise ValueError("page pools must be CUDA tensors")
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
             raise ValueError("block_table must be a contiguous int32 tensor [B, pages_per_seq]")
         self.K, self.V, self.block_table, self.page_rows = K, V, block_table, page_rows
@@ -74,6 +72,7 @@ class PagedKV:
 
     def struct(self) -> KV:
         K = self.K
+        _check_pools(K, self.V)  # (the attributes may have been set anew)
         sh, sn = (K.stride(1), K.stride(2)) if self.heads_first else (K.stride(2), K.stride(1))
         return KV(K.data_ptr(), self.V.data_ptr(), K.stride(0), sh, sn, self.block_table.data_ptr(),
                   self.page_rows, self.block_table.shape[1])
@@ -170,8 +169,17 @@ def _check_table(block_table, K):
         raise ValueError("block_table must be a contiguous int32 tensor [B, pages_per_seq] on the pools' device")
 
 
+def _check_pools(K, V):
+    bf16, st = _torch().bfloat16, K.stride()
+    if K.dtype is not bf16 or V.dtype is not bf16 or len(st) != 4 or st[3] != 1:
+        raise ValueError("page pools must be bf16 tensors with 4 dims, last contiguous")
+    if K.shape != V.shape or st != V.stride():
+        raise ValueError("K and V pools must share shape and strides")
+
+
 def _paged_cache(P):
     k, v, t, rows = P.K, P.V, P.block_table, P.page_rows
+    _check_pools(k, v)
     _check_table(t, k)
     shape, st = k.shape, k.stride()
     h, n = (1, 2) if P.heads_first else (2, 1)
@@ -190,7 +198,8 @@ def _cache(K, V):
         return K.cache, K.batch, K.h_kv, K.positions, K.device
     if isinstance(K, PagedKV):
         k, v, t = K.K, K.V, K.block_table
-        of = k, v, t, k.data_ptr(), v.data_ptr(), t.data_ptr(), K.page_rows, K.heads_first
+        of = (k, v, t, k.data_ptr(), v.data_ptr(), t.data_ptr(), k.shape, v.shape, t.shape, k.stride(), v.stride(),
+              t.stride(), K.page_rows, K.heads_first)
         made = K._cache  # its mog_cache, with what it was made of: the attributes may be set anew
         if made is None or any(x is not y for x, y in zip(made[0][:3], of)) or made[0][3:] != of[3:]:
             made = K._cache = of, _paged_cache(K)

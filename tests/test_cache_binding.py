@@ -1,0 +1,55 @@
+"""What the binding refuses before any device work: pools, streams and attributes that the cache and page
+calls cannot take.  Host tensors stand in for device ones, as far as a check looks."""
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import serving_mog_decode_gb300 as mog
+
+
+def paged(**kw):
+    """A PagedKV over host tensors, with attributes set anew."""
+    p = object.__new__(mog.PagedKV)
+    pool = torch.zeros((8, 2, 16, 128), dtype=torch.bfloat16)
+    base = dict(K=pool, V=pool.clone(), block_table=torch.zeros((3, 2), dtype=torch.int32), page_rows=16,
+                heads_first=True, h_kv=2, device=pool.device, _cache=None)
+    for name, value in {**base, **kw}.items():
+        setattr(p, name, value)
+    return p
+
+
+SHORT = torch.zeros((7, 2, 16, 128), dtype=torch.bfloat16)
+WIDE = torch.zeros((8, 2, 32, 128), dtype=torch.bfloat16)[:, :, :16]
+HALF = torch.zeros((8, 2, 16, 128), dtype=torch.float16)
+
+
+@pytest.mark.parametrize("kw", [dict(V=SHORT), dict(V=WIDE), dict(V=HALF), dict(K=HALF, V=HALF),
+                                dict(K=WIDE[..., ::2], V=WIDE[..., ::2])])
+def test_a_paged_cache_set_anew_to_pools_that_do_not_match_is_refused(kw):
+    assert mog._cache(paged(), None)[1:4] == (3, 2, 32)
+    for read in (lambda p: mog._cache(p, None), lambda p: p.struct()):
+        with pytest.raises(ValueError, match="pools"):
+            read(paged(**kw))
+        p = paged()
+        read(p)
+        for name, value in kw.items():
+            setattr(p, name, value)
+        with pytest.raises(ValueError, match="pools"):
+            read(p)
+
+
+def test_a_paged_cache_whose_tensors_take_another_shape_in_place_is_read_anew():
+    big = torch.zeros((8, 2, 16, 128), dtype=torch.bfloat16)
+    p = paged(K=big[:], V=big[:])
+    c, batch, h_kv, positions, _ = mog._cache(p, None)
+    assert (c.n_pages, c.stride_b, batch, positions) == (8, 4096, 3, 32)
+    p.K.data, p.V.data = big[::2], big[::2]  # (the same addresses)
+    c = mog._cache(p, None)[0]
+    assert (c.n_pages, c.stride_b) == (4, 8192)
+    p.K.data = big  # K alone
+    with pytest.raises(ValueError, match="pools"):
+        mog._cache(p, None)
+    p.K.data, p.block_table.data = big[::2], torch.zeros((5, 1), dtype=torch.int32)
+    assert mog._cache(p, None)[1:4] == (5, 2, 16)
