@@ -758,6 +758,15 @@ def kv_store(K, V, pos, count, k_new, v_new, stream=None):
         _check(rc, "mog_kv_store")
 
 
+def _pool_desc(t):
+    """mog_page_pool of a tensor whose first dim is the pages."""
+    n, size = t.shape[0], t.element_size()
+    page = t.numel() // n if n else 0
+    if page == 0 or (n > 1 and t.stride(0) < page):
+        raise ValueError("page pools must hold pages that do not overlap")
+    return PagePoolDesc(t.data_ptr(), (t.stride(0) if n > 1 else page) * size, page * size)
+
+
 class PagePool:
     """Sequences that share the pages of one or more paged caches (mog_pages): a block table
     [batch, pages_per_seq], the sequences' lengths and the pages' holders, all on the device.
@@ -778,6 +787,8 @@ class PagePool:
         if len({len(x) for x in lists}) != 1 or not self.K:
             raise ValueError("K, V and their scales must have one tensor per layer each")
         first = self.K[0]
+        if first.dim() != 4 or first.shape[0] == 0:
+            raise ValueError("page pools must have 4 dims and a page")
         self.device, n_pages = first.device, first.shape[0]
         self.heads_first, self.page_rows = heads_first, first.shape[2 if heads_first else 1]
         pools = [t for x in lists for t in x]
@@ -802,9 +813,7 @@ class PagePool:
         need = C.c_size_t(0)
         _check(lib().mog_pages_work_bytes(n_pages, batch, C.byref(need)), "mog_pages_work_bytes")
         self.work = torch.zeros(need.value // 4, dtype=torch.int32, device=self.device)
-        self._descs = (PagePoolDesc * len(pools))(*[
-            PagePoolDesc(t.data_ptr(), max(t.stride(0), t[0].numel()) * t.element_size(),
-                         t[0].numel() * t.element_size()) for t in pools])
+        self._descs = (PagePoolDesc * len(pools))(*map(_pool_desc, pools))
         self._s = Pages(n_pages, self.page_rows, batch, pages_per_seq, self.block_table.data_ptr(),
                         self.lengths.data_ptr(), self.refs.data_ptr(), self.work.data_ptr(), need.value, self._descs,
                         len(pools))

@@ -53,3 +53,17 @@ def test_a_paged_cache_whose_tensors_take_another_shape_in_place_is_read_anew():
         mog._cache(p, None)
     p.K.data, p.block_table.data = big[::2], torch.zeros((5, 1), dtype=torch.int32)
     assert mog._cache(p, None)[1:4] == (5, 2, 16)
+
+
+def test_pools_whose_pages_overlap_are_refused():
+    """An expanded pool has one page of memory: strides taken for more would lead out of it."""
+    pool = torch.zeros((8, 2, 16, 128), dtype=torch.bfloat16)
+    d = mog._pool_desc(pool)
+    assert (d.base, d.page_stride, d.page_bytes) == (pool.data_ptr(), 8192, 8192)
+    d = mog._pool_desc(pool[1::2])
+    assert (d.page_stride, d.page_bytes) == (16384, 8192)
+    d = mog._pool_desc(pool[2:3].as_strided((1, 2, 16, 128), (1, 2048, 128, 1)))  # (the stride of one page counts for nothing)
+    assert (d.page_stride, d.page_bytes) == (8192, 8192)
+    for bad in (pool[:1].expand(8, -1, -1, -1), pool.view(-1).as_strided((8, 2, 16, 128), (2048, 2048, 128, 1)), pool[:0]):
+        with pytest.raises(ValueError, match="overlap"):
+            mog._pool_desc(bad)

@@ -53,3 +53,10 @@ def test_compaction_reports_a_held_page_that_refs_count_as_free(slot, grown):
     table[b, at] = -1
     held = torch.bincount(table[table >= 0].long(), minlength=64).int()
     assert torch.equal(held, pool.refs)  # every other entry and its count moved together
+
+
+def test_pools_whose_pages_overlap_are_refused():
+    K = torch.zeros((8, 2, 16, 128), dtype=torch.bfloat16, device=DEV)
+    for bad in (K[:1].expand(8, -1, -1, -1), K[:0]):
+        with pytest.raises(ValueError):
+            mog.PagePool(bad, bad, 2, 4)
