@@ -124,7 +124,16 @@ def _check_rows8(K, V, k_scale, v_scale):
         raise ValueError("the last dim of K and V must be 128")
 
 
-class KV8:
+class _Fixed:
+    """An object whose attributes stay as they were made: its C structure holds their addresses."""
+
+    def __setattr__(self, name, value):
+        if "_made" in self.__dict__:
+            raise AttributeError(f"a {type(self).__name__} is fixed once it is made: {name} cannot be set")
+        object.__setattr__(self, name, value)
+
+
+class KV8(_Fixed):
     """A contiguous e4m3 KV cache: codes K, V float8_e4m3fn [B, H_kv, n_cap, 128] and a scale
     per row, k_scale, v_scale float32 [B, H_kv, n_cap] (value = scale * code).  Pass it as K
     (with V=None) to dense_decode, diff_decode and kv_store.  The tensors are fixed once it
@@ -137,9 +146,10 @@ class KV8:
         self.positions = K.shape[2]
         self.cache = Cache(1, K.shape[2], K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                            *_strides(K)[:2], K.stride(2), *_strides(k_scale), None, 0, 0, 0)
+        self._made = True
 
 
-class PagedKV8:
+class PagedKV8(_Fixed):
     """A paged e4m3 KV cache: page pools K, V float8_e4m3fn [pages, H_kv, page_rows, 128]
     (heads_first) or [pages, page_rows, H_kv, 128], a scale per row, k_scale, v_scale float32
     of the pools' first three dims, and an int32 block table [B, pages_per_seq] on the device.
@@ -160,6 +170,7 @@ class PagedKV8:
         self.cache = Cache(1, 0, K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ks[0], ks[h],
                            ks[n], ss[0], ss[h], ss[n], block_table.data_ptr(), page_rows, block_table.shape[1],
                            K.shape[0])
+        self._made = True
 
 
 def _check_table(block_table, K):
@@ -767,14 +778,15 @@ def _pool_desc(t):
     return PagePoolDesc(t.data_ptr(), (t.stride(0) if n > 1 else page) * size, page * size)
 
 
-class PagePool:
+class PagePool(_Fixed):
     """Sequences that share the pages of one or more paged caches (mog_pages): a block table
     [batch, pages_per_seq], the sequences' lengths and the pages' holders, all on the device.
 
     K, V: page pools [pages, H_kv, page_rows, 128] (heads_first) or [pages, page_rows, H_kv, 128],
     one tensor each or a list with one per layer, bf16, or float8_e4m3fn with k_scale, v_scale.  A page's
     elements must be contiguous.  block_table, lengths, refs: existing state, int32, used as it
-    is; by default every sequence is empty.  No method waits for the GPU but status()."""
+    is; by default every sequence is empty.  The tensors are fixed once it is made; their contents may change between
+    calls.  No method waits for the GPU but status()."""
 
     def __init__(self, K, V, batch, pages_per_seq, heads_first=True, k_scale=None, v_scale=None, block_table=None,
                  lengths=None, refs=None):
@@ -821,13 +833,13 @@ class PagePool:
         self.pos, self.granted = torch.zeros_like(self.lengths), torch.zeros_like(self.lengths)
         self._lib, self._ref = lib(), C.byref(self._s)
         self._pos_ptr, self._granted_ptr = self.pos.data_ptr(), self.granted.data_ptr()
+        self._layers = list(zip(*lists))  # what cache() hands out: the pools that the calls copy
+        self._made = True
 
     def cache(self, layer=0):
         """The paged cache of a layer (PagedKV or PagedKV8), for the calls that take one."""
-        if self.k_scale is None:
-            return PagedKV(self.K[layer], self.V[layer], self.block_table, self.page_rows, self.heads_first)
-        return PagedKV8(self.K[layer], self.V[layer], self.k_scale[layer], self.v_scale[layer], self.block_table,
-                        self.page_rows, self.heads_first)
+        return (PagedKV if self.k_scale is None else PagedKV8)(*self._layers[layer], self.block_table, self.page_rows,
+                                                               self.heads_first)
 
     def _call(self, fn, stream, *args):
         s = _here(self.device, stream)

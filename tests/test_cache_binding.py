@@ -67,3 +67,13 @@ def test_pools_whose_pages_overlap_are_refused():
     for bad in (pool[:1].expand(8, -1, -1, -1), pool.view(-1).as_strided((8, 2, 16, 128), (2048, 2048, 128, 1)), pool[:0]):
         with pytest.raises(ValueError, match="overlap"):
             mog._pool_desc(bad)
+
+
+def test_what_a_descriptor_was_made_of_cannot_be_set_anew():
+    for cls in (mog.KV8, mog.PagedKV8, mog.PagePool):
+        x = object.__new__(cls)
+        x.K, x._made = 1, True
+        for name in ("K", "block_table"):
+            with pytest.raises(AttributeError, match="fixed"):
+                setattr(x, name, 2)
+        assert x.K == 1

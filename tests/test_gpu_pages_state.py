@@ -60,3 +60,21 @@ def test_pools_whose_pages_overlap_are_refused():
     for bad in (K[:1].expand(8, -1, -1, -1), K[:0]):
         with pytest.raises(ValueError):
             mog.PagePool(bad, bad, 2, 4)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_pool_and_its_caches_keep_their_tensors(e4m3):
+    """A state tensor set anew would be read by cache() and not by grow, assign and compact."""
+    pool = make(8, 16, 2, 4, e4m3=e4m3)
+    for name in ("block_table", "lengths", "refs", "K", "pos"):
+        with pytest.raises(AttributeError, match="fixed"):
+            setattr(pool, name, getattr(pool, name))
+    want = pool.cache()
+    pool.K[0] = torch.zeros_like(pool.K[0])  # (the list is the caller's to change, the pool's tensors are not)
+    got = pool.cache()
+    assert got.K is want.K and got.V is want.V and got.block_table is pool.block_table
+    if e4m3:
+        for c in (got, mog.KV8(want.K, want.V, want.k_scale, want.v_scale)):
+            for name in ("K", "k_scale", "batch"):
+                with pytest.raises(AttributeError, match="fixed"):
+                    setattr(c, name, getattr(c, name))
