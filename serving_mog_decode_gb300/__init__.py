@@ -618,6 +618,8 @@ class _there:
 
     def __init__(self, dev, stream):
         torch = _torch()
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
         self.cms = [torch.cuda.device(dev)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):

@@ -77,3 +77,10 @@ def test_what_a_descriptor_was_made_of_cannot_be_set_anew():
             with pytest.raises(AttributeError, match="fixed"):
                 setattr(x, name, 2)
         assert x.K == 1
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Taken as it is, the work would go to the current stream of the cache's device instead."""
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        mog._there(torch.device("cuda", 0), stream)

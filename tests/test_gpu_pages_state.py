@@ -78,3 +78,12 @@ def test_a_pool_and_its_caches_keep_their_tensors(e4m3):
             for name in ("K", "k_scale", "batch"):
                 with pytest.raises(AttributeError, match="fixed"):
                     setattr(c, name, getattr(c, name))
+
+
+def test_calls_on_a_stream_of_the_cache_s_device():
+    pool = make(16, 16, 2, 4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    pos, granted = pool.grow(ints([20, 3]), stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert pos.tolist() == [0, 0] and granted.tolist() == [20, 3] and pool.status(stream=s) == 0
