@@ -69,10 +69,13 @@ class PagedKV:
         self.h_kv = K.shape[1] if heads_first else K.shape[2]
         self.device = K.device
         self._cache = None  # (made when a call first needs it)
+        self._checked = K, V
 
     def struct(self) -> KV:
-        K = self.K
-        _check_pools(K, self.V)  # (the attributes may have been set anew)
+        K, V = self.K, self.V
+        if self._checked[0] is not K or self._checked[1] is not V:  # (set anew)
+            _check_pools(K, V)
+            self._checked = K, V
         sh, sn = (K.stride(1), K.stride(2)) if self.heads_first else (K.stride(2), K.stride(1))
         return KV(K.data_ptr(), self.V.data_ptr(), K.stride(0), sh, sn, self.block_table.data_ptr(),
                   self.page_rows, self.block_table.shape[1])
@@ -209,11 +212,11 @@ def _cache(K, V):
         return K.cache, K.batch, K.h_kv, K.positions, K.device
     if isinstance(K, PagedKV):
         k, v, t = K.K, K.V, K.block_table
-        of = (k, v, t, k.data_ptr(), v.data_ptr(), t.data_ptr(), k.shape, v.shape, t.shape, k.stride(), v.stride(),
-              t.stride(), K.page_rows, K.heads_first)
+        of = (k.data_ptr(), v.data_ptr(), t.data_ptr(), k.shape, v.shape, t.shape, k.stride(), v.stride(), t.stride(),
+              K.page_rows, K.heads_first)
         made = K._cache  # its mog_cache, with what it was made of: the attributes may be set anew
-        if made is None or any(x is not y for x, y in zip(made[0][:3], of)) or made[0][3:] != of[3:]:
-            made = K._cache = of, _paged_cache(K)
+        if made is None or made[2] is not k or made[3] is not v or made[4] is not t or made[0] != of:
+            made = K._cache = of, _paged_cache(K), k, v, t
         return made[1]
     torch = _torch()
     if V is None:

@@ -14,7 +14,7 @@ def paged(**kw):
     p = object.__new__(mog.PagedKV)
     pool = torch.zeros((8, 2, 16, 128), dtype=torch.bfloat16)
     base = dict(K=pool, V=pool.clone(), block_table=torch.zeros((3, 2), dtype=torch.int32), page_rows=16,
-                heads_first=True, h_kv=2, device=pool.device, _cache=None)
+                heads_first=True, h_kv=2, device=pool.device, _cache=None, _checked=(None, None))
     for name, value in {**base, **kw}.items():
         setattr(p, name, value)
     return p

@@ -14,7 +14,8 @@ if not torch.cuda.is_available():
 
 import serving_mog_decode_gb300 as mog
 from serving_mog_decode_gb300 import buildlib
-from test_gpu_cache import D, DEV, OUTS, check_dense8, check_diff, gen, queries, randn, weights
+from test_gpu_cache import (D, DEV, OUTS, STEP, Made, check, check_dense8, check_diff, gen, one_map, queries, randn,
+                            weight_error, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +167,41 @@ def test_bf16_outputs_up_to_eight_heads_are_rounded_once(n, G, slack):
     ref = (codes[1].double() * scale.double()[..., None]).mean(2)[0].repeat_interleave(G, 0)
     half = 2.0 ** (torch.floor(torch.log2(ref)) - 8)
     assert ((out[0].double() - ref).abs() <= half + (2.0 ** -16 + 2.0 ** -22) * ref).all()
+
+
+@pytest.mark.parametrize("out_type", OUTS)
+@pytest.mark.parametrize("half", [0, 1])
+@pytest.mark.parametrize("G,slack", [(2, 0), (2, 3000), (5, 0), (5, 3000), (8, 3000)])
+def test_diff_rows_infinite_in_one_half(G, slack, half, out_type):
+    """bf16 rows with -inf in one half: without weight in that map, with their usual one in the other.  Each
+    map's reference and bound go over the rows that it sees."""
+    H, n, w = 1, 300, D // 2
+    m = Made(14, (n,), H, 0, e4m3=False, slack=slack)
+    q = queries(15, 1, H * G).abs() + 0.5
+    rows = [7, 64, 299]
+    m.cache[0][0, 0, rows, half * w:(half + 1) * w] = float("-inf")
+    lam, gamma = weights(16)
+    out = torch.empty(q.shape, dtype=out_type, device=DEV)
+    mog.diff_decode(*m.cache, m.lengths, m.n_max, q, lam, 0.5, gamma, out=out)
+    seen = torch.ones(n, dtype=torch.bool, device=DEV)
+    seen[rows] = False
+    maps = []
+    for j in range(2):
+        K, V = m.cache[0][0, 0, :n].double(), m.cache[1][0, 0, :n].double()
+        if j == half:
+            K, V = K[seen], V[seen]
+        at = slice(j * w, (j + 1) * w)
+        maps.append(one_map(q[0, :, at].double(), K[:, at], V, len(V), w ** -0.5))
+    bf = out_type == torch.bfloat16
+    L = lam.double()
+    weight = torch.exp((L[0] * L[1]).sum()) - torch.exp((L[2] * L[3]).sum()) + 0.5
+    (a1, e1, s1), (a2, e2, s2) = maps
+    a = a1 - weight * a2
+    r = torch.sqrt((a * a).mean(-1, keepdim=True) + 1e-5)
+    gm = 0.5 * gamma.double()
+    ref = a / r * gm
+    # as in check_diff
+    dw = 200 * STEP * (weight.abs() + 2 * torch.exp((L[:2].abs().prod(0)).sum()))
+    E = e1 + weight.abs() * e2 + (2 * weight_error(False, bf) + 4 * STEP) * (s1 + weight.abs() * s2) + dw * s2
+    bound = 1.05 * (E / r * gm.abs() + ref.abs() * torch.sqrt((E * E).mean(-1, keepdim=True)) / r) + 16 * STEP * ref.abs()
+    check(out[0], ref, bound + (2.0 ** -8 * ref.abs() if bf else 0), half)
