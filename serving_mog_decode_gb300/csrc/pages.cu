@@ -238,10 +238,10 @@ __device__ __forceinline__ void grow_plan(const PagesArgs &a, const int *n_new, 
     }
     __syncthreads();
     for (int b = tid; b < a.batch; b += PL_THREADS) {
-        const int len = a.lengths[b];
+        const int len = a.lengths[b], n = n_new[b];  // (n_new may be pos or granted of the call before)
         pos[b] = len;
-        granted[b] = n_new[b];
-        a.lengths[b] = len + n_new[b];
+        granted[b] = n;
+        a.lengths[b] = len + n;
     }
 }
 

@@ -87,3 +87,15 @@ def test_calls_on_a_stream_of_the_cache_s_device():
     pos, granted = pool.grow(ints([20, 3]), stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert pos.tolist() == [0, 0] and granted.tolist() == [20, 3] and pool.status(stream=s) == 0
+
+
+@pytest.mark.parametrize("name", ["pos", "granted", "lengths"])
+def test_grow_by_what_an_earlier_growth_returned(name):
+    """n_new in the tensors that grow writes."""
+    pool = make(40, 16, 3, 12)
+    pool.grow(ints([5, 0, 20]))
+    pool.grow(ints([1, 2, 3]))
+    n, before = getattr(pool, name).tolist(), pool.lengths.tolist()
+    pos, granted = pool.grow(getattr(pool, name))
+    assert granted.tolist() == n and pos.tolist() == before
+    assert pool.lengths.tolist() == [x + y for x, y in zip(before, n)] and pool.status() == 0
