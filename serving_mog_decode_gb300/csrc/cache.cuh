@@ -30,10 +30,10 @@
 // of a row that is not zero (new_unit).  bf16 rows go through ldmatrix; their weights are three bf16
 // parts (2^-24), or two for a bf16 output (2^-16).  All sums are fp32.
 //
-// Bound by: HBM in the narrow form (whole steps: 1M e4m3 tokens, 8 KV heads, G = 4: 312 us,
-// 7.1 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 316 us, 6.8 TB/s); the
-// wide form too over bf16 rows (G = 5: 320 us), but over e4m3 rows by the latencies of its
-// chains (G = 5, 4 x 128K: 220 us, 5.0 TB/s; 45% of issue slots, 39% of the tensor pipe).
+// Bound by: HBM in the narrow form (whole steps: 1M e4m3 tokens, 8 KV heads, G = 4: 313 us,
+// 7.1 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 310 us, 6.9 TB/s; over e4m3 rows
+// 171 us, 6.5 TB/s); the wide form too over bf16 rows (G = 5: 315 us), but over e4m3 rows by the latencies of its
+// chains (G = 5, 4 x 128K: 217 us, 5.1 TB/s; 43% of issue slots, 37% of the tensor pipe).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -446,6 +446,8 @@ __device__ __forceinline__ int exp_above(float x) { return (__float_as_int(x) >>
 // no bits.  So rows of zeros are left out (their scale in the stage becomes 0), and m becomes the
 // largest s + log2 v_scale of the rest, less ve.  It may end above or below the largest logit: bounds keep the
 // sum, which counts rows of zeros too, and o, which may hold more than this tile brings, inside fp32.
+// A cache with such a tile everywhere (every 16th row zero, the rest's scales 2^-14) is read in 419 us in place
+// of 315 (1M tokens, G = 4) and 283 in place of 202 (512K, G = 16).
 // mine: the bits of the scale of row `lane`;  there: is that row in the cache.
 template <class T, int NS>
 __device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T::BLK][NS], float (&mx)[2], int mine,

@@ -8,7 +8,10 @@
 // is partly filled and shared is the last one of every sequence that holds it.
 //
 // These calls are bound by launch latency and dependent reads on the table's side, by HBM
-// where they copy pages (read once, written once).  Metadata of a call is planned by one
+// where they copy pages (read once, written once).  A growth by one token without copies takes 3.7 us for 8
+// sequences of one layer and 5.9 for 64 of 32 layers, whose copy kernel finds nothing to do (8.8 with e4m3
+// rows: 128 pools, two copy kernels).  Only the holders of one last page that all grow at
+// once are walked quadratically: 1024 of them take 58 us, 4096 take 460.  Metadata of a call is planned by one
 // CTA (a page pool has at most a few hundred thousand pages: their holder counts come from
 // L2), page bytes are copied by the whole GPU in a second kernel, launched early and
 // waiting for the plan (programmatic dependent launch); small growth is one launch.
