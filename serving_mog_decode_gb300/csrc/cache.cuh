@@ -65,6 +65,9 @@ constexpr int V_NONE = 0x7fffffff;  // no unit yet
 template <bool E4M3_, bool WIDE_, bool CLUSTER = false>
 struct Tile {
     static constexpr bool E4M3 = E4M3_, WIDE = WIDE_;
+    // A unit's first tile is looked at before its products, where a warp has one tile or a few (1000 tokens: 5.6 us
+    // against 5.8 after them); elsewhere that would cost registers (8 x 16-64K, 32 KV heads: 403 against 381).
+    static constexpr bool EARLY = CLUSTER;
     static constexpr int BLK = E4M3 ? 2 : 1;              // blocks of 16 rows per warp
     static constexpr int WROWS = 16 * BLK;                // rows per warp
     static constexpr int ROWS = CT_WARPS * WROWS;
@@ -265,6 +268,7 @@ struct State {
     // e4m3: bits of the least value scale in order; the largest is 2^ve, and o is in units of
     // 2^(m + ve - W_EXP) (the same in all lanes)
     int vlo;
+    float rise;  // e4m3: how far m has risen since new_unit last looked
     __device__ __forceinline__ int ve() const { return (vlo >> 23) - 127 + (V_RANGE >> 23); }
     __device__ __forceinline__ void init() {
 #pragma unroll
@@ -274,6 +278,7 @@ struct State {
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
         vlo = V_NONE;
+        rise = 0.f;
     }
     static __device__ __forceinline__ int col(int e) { return WIDE ? e >> 1 : e & 1; }
 };
@@ -439,41 +444,58 @@ __device__ __forceinline__ constexpr int logit_col(int i) { return WIDE ? (i >> 
 
 __device__ __forceinline__ int exp_above(float x) { return (__float_as_int(x) >> 23) - 126; }  // |x| < 2^that, x >= 0
 
+constexpr int F32_INF = 0x7f800000;
+// vlo for a largest scale with the bits hi (ve >= -112).
+__device__ __forceinline__ int scale_floor(int hi) { return (max((hi >> 23) + 1, 15) << 23) - V_RANGE; }
+
+// e4m3, a tile's value rows: zero: is row `lane` all zeros (with a finite scale);  hi: the bits of the largest
+// finite scale.  If the tile is a unit's first, without rows of zeros, and its scales are in order,
+// they set the range (true).
+template <bool WIDE>
+__device__ __forceinline__ bool first_tile(State<WIDE> &st, int mine, bool there, uint32_t sv, bool &zero, int &hi) {
+    const int lane = threadIdx.x & 31;
+    uint32_t any = 0;
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {  // (the row's chunks in an order without bank conflicts)
+        const uint4 x = lds16(sv + lane * MOG_D + (((ch + lane) & 7) << 4));
+        any |= x.x | x.y | x.z | x.w;
+    }
+    zero = (any & 0x7f7f7f7fu) == 0 && mine < F32_INF;
+    hi = __reduce_max_sync(0xffffffffu, mine < F32_INF ? mine : 0);
+    if (st.vlo == V_NONE && hi - __reduce_min_sync(0xffffffffu, there ? mine : F32_INF) <= V_RANGE &&
+        !__any_sync(0xffffffffu, there && zero)) {
+        st.vlo = scale_floor(hi);
+        return true;
+    }
+    return false;
+}
+
 // e4m3: a unit for a tile with value scales out of order.  Weights 2^s * v_scale are held in fp16
-// as shares of the unit 2^(m + ve).  While the scales stay between 2^(ve - 10) and 2^ve the unit
-// follows the largest logit alone.  A scale outside may belong to a row of zeros (kv_store gives it
-// the scale 1) or to one without weight; a unit made for it would leave the other rows' weights
-// no bits.  So rows of zeros are left out (their scale in the stage becomes 0), and m becomes the
-// largest s + log2 v_scale of the rest, less ve.  It may end above or below the largest logit: bounds keep the
-// sum, which counts rows of zeros too, and o, which may hold more than this tile brings, inside fp32.
-// A cache with such a tile everywhere (every 16th row zero, the rest's scales 2^-14) is read in 419 us in place
-// of 315 (1M tokens, G = 4) and 283 in place of 202 (512K, G = 16).
+// as shares of the unit 2^(m + ve).  While the scales stay between 2^(ve - 10) and 2^ve, and m rises by
+// less than 2^10 in all, the unit follows the largest logit alone.  A scale outside may belong to
+// a row of zeros (kv_store gives it the scale 1) or to one without weight, and a row of zeros may have the largest
+// logit; a unit made for it would leave the other rows' weights no bits.  So rows of zeros are
+// left out (their scale in the stage becomes 0), and m becomes the largest s + log2 v_scale of the rest, less ve, or
+// what o holds, if that is more.  It may end above or below the largest logit: bounds keep the sum, which counts
+// rows of zeros too, inside fp32.
+// A cache with such a tile everywhere (every 16th row zero, the rest's scales 2^-14) is read in 409 us in place
+// of 316 (1M tokens, G = 4) and 277 in place of 204 (512K, G = 16).
 // mine: the bits of the scale of row `lane`;  there: is that row in the cache.
 template <class T, int NS>
 __device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T::BLK][NS], float (&mx)[2], int mine,
                                          bool there, uint32_t sv, uint32_t vsc) {
     constexpr bool WIDE = T::WIDE;
-    constexpr int INF = 0x7f800000;
     static_assert(!T::E4M3 || T::WROWS == 32, "a lane per row");
     const int lane = threadIdx.x & 31;
-    auto made = [](int hi) { return (max((hi >> 23) + 1, 15) << 23) - V_RANGE; };  // (ve >= -112)
-    int hi = __reduce_max_sync(0xffffffffu, mine < INF ? mine : 0);
-    if (st.vlo == V_NONE && hi - __reduce_min_sync(0xffffffffu, there ? mine : INF) <= V_RANGE) {
-        st.vlo = made(hi);  // the first tile, in order within itself
-        return;
-    }
-    uint32_t any = 0;
-#pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
-        const uint4 x = lds16(sv + swz_v<T::E4M3>(lane, ch));
-        any |= x.x | x.y | x.z | x.w;
-    }
-    const bool zero = (any & 0x7f7f7f7fu) == 0 && mine < INF;
+    st.rise = 0.f;
+    bool zero;
+    int hi;
+    if (first_tile(st, mine, there, sv, zero, hi) && !T::EARLY) return;
     if (zero) asm volatile("st.shared.u32 [%0], %1;" ::"r"(vsc + 4 * lane), "r"(0) : "memory");
-    hi = __reduce_max_sync(0xffffffffu, mine < INF && !zero ? mine : 0);
+    hi = __reduce_max_sync(0xffffffffu, mine < F32_INF && !zero ? mine : 0);
     __syncwarp();
     const int ve_old = st.ve();
-    if (st.vlo == V_NONE || (hi > 0 && (unsigned)(hi - st.vlo) > V_RANGE)) st.vlo = made(hi);
+    if (st.vlo == V_NONE || (hi > 0 && (unsigned)(hi - st.vlo) > V_RANGE)) st.vlo = scale_floor(hi);
     int ve = st.ve();
     float far[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -482,7 +504,7 @@ __device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T:
         for (int i = 0; i < NS; ++i) {
             const int v = __float_as_int(lds4(vsc + 4 * (16 * blk + logit_row<WIDE>(i)))) & 0x7fffffff;
             // (rounded up: a weight must not pass the unit)
-            const float x = v > 0 && v < INF ? __fadd_ru(s[blk][i], (float)((v >> 23) - 126 - ve)) : -INFINITY;
+            const float x = v > 0 && v < F32_INF ? __fadd_ru(s[blk][i], (float)((v >> 23) - 126 - ve)) : -INFINITY;
             far[logit_col<WIDE>(i)] = fmaxf(far[logit_col<WIDE>(i)], x);
         }
     // a row of the largest logit would pass 2^80: a smaller ve (v_scale * 2^(W_EXP - ve) stays finite)
@@ -508,7 +530,7 @@ __device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T:
         const float sum = column_max<WIDE>(st.l[c]);
         float m = fmaxf(__fadd_ru(far[c], (float)-less), mx[c] - 90.f);                   // this tile's terms of the sum: 2^90
         if (sum > 0.f) m = fmaxf(m, st.m[c] + (float)(max(exp_above(sum), -30) - 90));      // the sum: 2^90
-        if (big > 0.f) m = fmaxf(m, __fadd_ru(st.m[c], (float)(d + max(exp_above(big), -30) - 54)));  // o: 2^54
+        if (big > 0.f) m = fmaxf(m, __fadd_ru(st.m[c], (float)(d + max(exp_above(big), -30) - 30)));  // o: 2^30
         if (m == -INFINITY) continue;  // (nothing so far)
         m = ceilf(m);
         const float fl = ex2(st.m[c] - m), fo = ex2(fminf(st.m[c] - m + (float)d, 126.f));
@@ -537,6 +559,15 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
     constexpr uint32_t ALL = (uint32_t)((1ull << T::WROWS) - 1);
     const uint32_t rows = (__float_as_uint(lds4(stage + T::MASK + 4 * (wr / 32))) >> (wr % 32)) & ALL;
     if (rows == 0) return;
+
+    int mine = 0;  // e4m3: the bits of the value scale of row `lane`
+    bool fresh = false;
+    if (E4M3 && T::EARLY) {
+        mine = __float_as_int(lds4(sc + 4 * (T::ROWS + lane))) & 0x7fffffff;
+        bool zero;
+        int hi;
+        if (st.vlo == V_NONE) fresh = first_tile(st, mine, (rows >> lane) & 1u, sv, zero, hi);
+    }
 
     // Logits s[blk][i]: narrow: rows g (i = 0, 1) and g+8 (2, 3) of columns 2t, 2t+1 (even and
     // odd i); wide: columns g (i = 0, 1, 4, 5) and g+8 of rows 2t, 2t+1 (0..3), 2t+8, 2t+9.
@@ -625,9 +656,11 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
     }
     float inv = 0.f;
     if (E4M3) {
-        const int mine = __float_as_int(lds4(sc + 4 * (T::ROWS + lane))) & 0x7fffffff;
+        if (!T::EARLY) mine = __float_as_int(lds4(sc + 4 * (T::ROWS + lane))) & 0x7fffffff;
         const bool there = (rows >> lane) & 1u;
-        if (__any_sync(0xffffffffu, there && (unsigned)(mine - st.vlo) > V_RANGE))
+        // (infinite at first)
+        st.rise = T::EARLY && fresh ? 0.f : st.rise + fmaxf(fmaxf(mx[0] - st.m[0], mx[1] - st.m[1]), 0.f);
+        if (__any_sync(0xffffffffu, (there && (unsigned)(mine - st.vlo) > V_RANGE) || st.rise > 10.f))
             new_unit<T>(st, s, mx, mine, there, sv, sc + 4 * T::ROWS);
         inv = pow2f(W_EXP - st.ve());
     }

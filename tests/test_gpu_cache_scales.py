@@ -130,6 +130,25 @@ def test_a_long_flat_tail_beside_one_row(G, sink, out_type):
     check_all(Stored(k, v, 0), q, G, out_type)
 
 
+@pytest.mark.parametrize("out_type", OUTS)
+@pytest.mark.parametrize("steps", [1, 40])
+@pytest.mark.parametrize("size", [1.0, 100.0])
+@FORMS
+def test_rows_of_zeros_with_the_largest_logits(G, slack, size, steps, out_type):
+    """Values whose scales are near the 1 that a row of zeros has, and rows of zeros that take nearly all the
+    weight: one first row, or a row in every tile, each a little above the one before."""
+    g = gen(17)
+    H, n = 2, 40 * 32
+    k, v = 0.3 * randn(g, H, n, D), size * randn(g, H, n, D)
+    q = 0.3 * queries(18, 1, H * G)
+    at = torch.arange(steps, device=DEV) * 32
+    for d in (0, 64):
+        k[..., d], q[..., d] = 0, 11.0
+        k[:, at, d] = 30.0 * (1 + torch.arange(steps, device=DEV)) / steps
+    v[:, at] = 0
+    check_all(Stored(k, v, slack), q, G, out_type)
+
+
 @pytest.mark.parametrize("G", [4, 9])
 def test_a_row_of_zeros_whose_scale_is_infinite_shows(G):
     """scale * code is NaN there, as in the definition."""
