@@ -30,10 +30,10 @@
 // of a row that is not zero (new_unit).  bf16 rows go through ldmatrix; their weights are three bf16
 // parts (2^-24), or two for a bf16 output (2^-16).  All sums are fp32.
 //
-// Bound by: HBM in the narrow form (whole steps: 1M e4m3 tokens, 8 KV heads, G = 4: 313 us,
-// 7.1 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 310 us, 6.9 TB/s; over e4m3 rows
+// Bound by: HBM in the narrow form (whole steps: 1M e4m3 tokens, 8 KV heads, G = 4: 315 us,
+// 7.0 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 310 us, 6.9 TB/s; over e4m3 rows
 // 171 us, 6.5 TB/s); the wide form too over bf16 rows (G = 5: 315 us), but over e4m3 rows by the latencies of its
-// chains (G = 5, 4 x 128K: 217 us, 5.1 TB/s; 43% of issue slots, 37% of the tensor pipe).
+// chains (G = 5, 4 x 128K: 220 us, 5.0 TB/s; 43% of issue slots, 37% of the tensor pipe).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -51,8 +51,8 @@ constexpr int W_EXP = 14;           // fp16 weights: 2^14 times their share of t
 // 16-bit parts that a weight of the second product is held in.  A bf16 output takes one less where that
 // is worth something: bf16 weights stay within 2^-16 of theirs, a 256th of the output's half step,
 // and the step is 1% to 4% faster (2 x 4K tokens, G = 4: 11.3 us against 11.6; 4 x 128K, G = 5: 313 against 316);
-// one fp16 part, within 2^-11, an eighth of that half step, is for the wide form alone (16 heads, 512K: 172 us
-// against 202; the narrow form: 1M tokens, G = 4: 308 against 311).
+// one fp16 part, within 2^-11, an eighth of that half step, is for the wide form alone (16 heads, 512K: 174 us
+// against 204; the narrow form: 1M tokens, G = 4: 308 against 311).
 constexpr int weight_parts(bool e4m3, bool wide, bool bf16_out) {
     return (e4m3 ? 2 : 3) - (bf16_out && (wide || !e4m3) ? 1 : 0);
 }
@@ -73,7 +73,7 @@ struct Tile {
     static constexpr int ROWS = CT_WARPS * WROWS;
     // Three CTAs per SM, but two of the wide e4m3 form: it is bound by the latencies of its
     // longer chains, which 255 registers (32 rows a warp in flight, no spills) hide better than
-    // a third CTA (16 heads, 512K: 202 us against 231 with three CTAs and 16 rows a warp).
+    // a third CTA (16 heads, 512K: 204 us against 231 with three CTAs and 16 rows a warp).
     static constexpr int PER_SM = CLUSTER ? CL_PER_SM : E4M3 && WIDE ? 2 : 3;
     static constexpr int ROW = E4M3 ? MOG_D : 2 * MOG_D;  // bytes
     static constexpr int KV = ROWS * ROW;                 // bytes of the K or V tile: 16 KB
