@@ -516,7 +516,7 @@ typedef struct mog_cache {
  * dense_decode over an e4m3 cache: for every query head softmax(tau q.K^T) V over keys
  * [0, N_b), K and V the rows' values scale * code, tau = 1/sqrt(d).  A sequence without
  * rows gives zeros, and so does one whose logits are all -infinity.  Value scales may lie any
- * way: a row's weight * scale is held to 2^-22 of it, or to 2^-28 of the largest one of a row that
+ * way: a row's weight * scale is held to 2^-22 of it, or to 2^-24 of the largest one of a row that
  * is not zero where that is more (bf16 outputs of more than 8 heads per KV head, or 4
  * differential ones: 2^-11).
  *  c           : MOG_CACHE_E4M3

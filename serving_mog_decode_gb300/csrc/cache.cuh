@@ -26,7 +26,7 @@
 // which holds every e4m3 value exactly.  q enters as fp16 scaled by a power of two of its
 // own, so that its elements down to 2^-29 of the largest are exact.  Weights p * v_scale enter
 // the P.V product as fp16, 2^14 times their share of a running unit: high + low parts (2^-22
-// relative), or the high part alone (2^-11; weight_parts), and no better than 2^-39 of the unit.  The unit is at most 2^11 times the largest weight
+// relative), or the high part alone (2^-11; weight_parts), and no better than 2^-39 of the unit.  The unit is at most 2^15 times the largest weight
 // of a row that is not zero (new_unit).  bf16 rows go through ldmatrix; their weights are three bf16
 // parts (2^-24), or two for a bf16 output (2^-16).  All sums are fp32.
 //
@@ -57,6 +57,7 @@ constexpr int weight_parts(bool e4m3, bool wide, bool bf16_out) {
     return (e4m3 ? 2 : 3) - (bf16_out && (wide || !e4m3) ? 1 : 0);
 }
 constexpr int V_RANGE = 10 << 23;   // value scales within 2^10 of the unit's are in order (a difference of float bits)
+constexpr float M_RISE = 4.f;       // m may rise by 2^4 before rows of zeros are looked for again
 constexpr int V_NONE = 0x7fffffff;  // no unit yet
 
 // A tile is copied by the whole CTA, 2 KB of neighbouring rows per instruction, and each
@@ -472,7 +473,7 @@ __device__ __forceinline__ bool first_tile(State<WIDE> &st, int mine, bool there
 
 // e4m3: a unit for a tile with value scales out of order.  Weights 2^s * v_scale are held in fp16
 // as shares of the unit 2^(m + ve).  While the scales stay between 2^(ve - 10) and 2^ve, and m rises by
-// less than 2^10 in all, the unit follows the largest logit alone.  A scale outside may belong to
+// less than 2^4 in all, the unit follows the largest logit alone.  A scale outside may belong to
 // a row of zeros (kv_store gives it the scale 1) or to one without weight, and a row of zeros may have the largest
 // logit; a unit made for it would leave the other rows' weights no bits.  So rows of zeros are
 // left out (their scale in the stage becomes 0), and m becomes the largest s + log2 v_scale of the rest, less ve, or
@@ -660,7 +661,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
         const bool there = (rows >> lane) & 1u;
         // (infinite at first)
         st.rise = T::EARLY && fresh ? 0.f : st.rise + fmaxf(fmaxf(mx[0] - st.m[0], mx[1] - st.m[1]), 0.f);
-        if (__any_sync(0xffffffffu, (there && (unsigned)(mine - st.vlo) > V_RANGE) || st.rise > 10.f))
+        if (__any_sync(0xffffffffu, (there && (unsigned)(mine - st.vlo) > V_RANGE) || st.rise > M_RISE))
             new_unit<T>(st, s, mx, mine, there, sv, sc + 4 * T::ROWS);
         inv = pow2f(W_EXP - st.ve());
     }

@@ -2,9 +2,9 @@
 scale 1) among small ones, large rows without weight, rows that lose their weight later.
 
 The bounds are those of test_gpu_cache, per output element and relative to sum p |v|.  To
-them the kernel adds 2^-39 of its unit per row, and the unit is at most 2^11 times the largest weight
-p * v_scale among a warp's rows that are not zero: 2^-28 of that weight for each of the few hundred
-rows of a warp, whose codes are of comparable size here: 2^-20 of sum p |v|, inside the bounds' 2^-15.
+them the kernel adds 2^-39 of its unit per row, and the unit is at most 2^15 times the largest weight
+p * v_scale among a warp's rows that are not zero: 2^-24 of that weight for each of the few hundred
+rows of a warp, whose codes are of comparable size here: 2^-16 of sum p |v|, inside the bounds' 2^-15.
 """
 import pytest
 
