@@ -484,11 +484,15 @@ int mog_check_bounded_wait(int32_t limit, int32_t arrive, int32_t *scratch_dev, 
  * ------------------------------------------------------------------------------------ */
 
 /*
- * A KV cache of bf16 or e4m3 rows in device memory, contiguous or paged (mog_kv's layouts).
+ * A KV cache of bf16, e4m3 or int8 rows in device memory, contiguous or paged (mog_kv's layouts).
  *  type MOG_CACHE_BF16 : rows as mog_kv; k_scale, v_scale NULL.
  *  type MOG_CACHE_E4M3 : one byte per element (fp8 e4m3), and one fp32 scale >= 0 per row
  *    of K and of V: the row of position n stands for scale * code.  Scales of (b, h, n) at
  *    b*scale_b + h*scale_h + n*scale_n floats (pages: page, h, row in page).
+ *  type MOG_CACHE_I8 : one byte per element (int8), and one fp32 scale per block of block_rows
+ *    positions of K and of V: the row of position n stands for scale * code.  Scales of
+ *    (b, h, n) at b*scale_b + h*scale_h + (n / block_rows)*scale_n floats (pages: page, h, row
+ *    in page / block_rows).  block_rows is 16, 32, 64 or 128, and at most page_rows.
  *  stride_b, stride_h, stride_n are in elements, multiples of 16 bytes, stride_n >= d;
  *  base pointers 16-byte aligned.
  *  Contiguous: block_table NULL, positions [0, n_cap).  Paged: page_rows a power of two
@@ -497,6 +501,7 @@ int mog_check_bounded_wait(int32_t limit, int32_t arrive, int32_t *scratch_dev, 
  */
 #define MOG_CACHE_BF16 0
 #define MOG_CACHE_E4M3 1
+#define MOG_CACHE_I8 3
 typedef struct mog_cache {
     int32_t type;
     int32_t n_cap;
@@ -506,6 +511,7 @@ typedef struct mog_cache {
     int64_t scale_b, scale_h, scale_n;
     const int32_t *block_table; /* NULL: contiguous */
     int32_t page_rows, pages_per_seq, n_pages;
+    int32_t block_rows;         /* MOG_CACHE_I8: rows of a scale (read for no other type) */
 } mog_cache;
 
 /* Element type of an output: fp32, or bf16 rounded once from fp32. */
@@ -513,13 +519,13 @@ typedef struct mog_cache {
 #define MOG_OUT_BF16 1
 
 /*
- * dense_decode over an e4m3 cache: for every query head softmax(tau q.K^T) V over keys
+ * dense_decode over an 8-bit cache: for every query head softmax(tau q.K^T) V over keys
  * [0, N_b), K and V the rows' values scale * code, tau = 1/sqrt(d).  A sequence without
  * rows gives zeros, and so does one whose logits are all -infinity.  Value scales may lie any
  * way: a row's weight * scale is held to 2^-22 of it, or to 2^-24 of the largest one of a row that
  * is not zero where that is more (bf16 outputs of more than 8 heads per KV head, or 4
  * differential ones: 2^-11).
- *  c           : MOG_CACHE_E4M3
+ *  c           : MOG_CACHE_E4M3 or MOG_CACHE_I8
  *  lengths_dev : int32[batch] on the device, clamped to [0, n_max]; n_max <= the cache's
  *                positions
  *  q_dev       : bf16 [batch][h_q][d];  out_dev: out_type [batch][h_q][d]
@@ -544,7 +550,7 @@ int dense_decode8(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max,
  *  lam         : device f32 [lam_heads][4][d/2], the vectors l_q1, l_k1, l_q2, l_k2, with
  *                lam_heads 1 (shared by the heads) or h_q; 16-byte aligned
  *  gamma       : device f32 [d], 16-byte aligned, or NULL for ones;  eps > 0
- * Caches of both types; the other arguments as dense_decode8.  h_q / h_kv <= 8.
+ * Caches of every type; the other arguments as dense_decode8.  h_q / h_kv <= 8.
  */
 typedef struct mog_diff_params {
     const float *lam;
@@ -571,10 +577,74 @@ int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_ma
  * amax <= 448 * 2^e, amax the row's largest finite magnitude (scale 1 if that is 0); its
  * codes are x / 2^e (exact) rounded to nearest even, infinities saturated, NaN kept.  Rows
  * must not be stored twice by one call (pages shared by two sequences that both write).
+ *
+ * An int8 block's scale is s = max(held, amax * fp32(1/127), 2^-126), amax the largest finite
+ * magnitude among its new rows and `held` its scale if it holds rows (positions of the block before
+ * pos[b], which earlier stores wrote; else 0: a block whose first row is written starts afresh,
+ * and what lies behind the new rows counts for nothing).  The new rows' codes are x * (1/s) rounded to
+ * nearest even, infinities +-127; if s > held, the codes that the block holds become code * (held/s)
+ * rounded to nearest even.  A NaN among the new rows makes the scale NaN, and so every row of
+ * the block, whose codes stay as they are.  Products and quotients are rounded to fp32.
  */
 int mog_kv_store(const mog_cache *c, int32_t batch, int32_t h_kv, int32_t d, int32_t t_max,
                  const int32_t *pos_dev, const int32_t *count_dev, const void *k_new_dev,
                  const void *v_new_dev, int64_t new_b, int64_t new_t, int64_t new_h, void *stream);
+
+/*
+ * Read rows of a cache back as bf16: position pos[b] + t, t < count[b], of sequence b goes to
+ * k_out, v_out (strides as mog_kv_store's new rows), 8-bit rows as scale * code rounded to fp32 and
+ * then to bf16.  Rows of positions outside the cache, or in no page, and rows t >= count[b] are left
+ * as they are.  count NULL: t_max for every sequence.
+ */
+int mog_kv_load(const mog_cache *c, int32_t batch, int32_t h_kv, int32_t d, int32_t t_max,
+                const int32_t *pos_dev, const int32_t *count_dev, void *k_out_dev, void *v_out_dev,
+                int64_t out_b, int64_t out_t, int64_t out_h, void *stream);
+
+/*
+ * Rotary positions of the first rot_dim dimensions of a row of d: pair i, (a, b), of a row at
+ * position p becomes factor * (a cos x - b sin x, b cos x + a sin x), x = p * f_i; the other
+ * dimensions stay.
+ *  turns   : device int64 [rot_dim/2]: f_i / 2 pi as a 64-bit binary fraction of a turn
+ *            (round(f_i / 2 pi * 2^64) mod 2^64), so that the angle of any position is exact
+ *            to 2^-32 of a turn; 8-byte aligned
+ *  rot_dim : a multiple of 16, at most d
+ *  layout  : MOG_ROPE_HALVES: pair i is dimensions i, i + rot_dim/2; MOG_ROPE_PAIRS: 2i, 2i + 1
+ *  factor  : multiplies the turned dimensions (the attention factor of scaled contexts; else 1)
+ * Computed in fp32 and rounded once, to bf16.
+ */
+#define MOG_ROPE_HALVES 0
+#define MOG_ROPE_PAIRS 1
+typedef struct mog_rope {
+    const int64_t *turns;
+    int32_t rot_dim, layout;
+    float factor;
+} mog_rope;
+
+/*
+ * Turn rows: out = x turned by its positions (inverse != 0: by the negative angles, the transpose).
+ *  pos_dev : int32 [batch], token t of sequence b at position pos[b] + t; or with pos_each != 0
+ *            int32 [batch][t_max], a position of each token's own.  Any int32.
+ *  x, out  : bf16, element (b, t, h, j) at b*s[0] + t*s[1] + h*s[2] + j; strides multiples of 8,
+ *            16-byte aligned; out may be x itself, and must not overlap it otherwise
+ * Rows t >= count[b] of out are left as they are; count NULL: t_max each.  t_max * heads <= 2^30.
+ */
+int mog_rope_apply(const mog_rope *rope, int32_t batch, int32_t heads, int32_t d, int32_t t_max,
+                   const int32_t *pos_dev, int32_t pos_each, const int32_t *count_dev, int32_t inverse,
+                   const void *x_dev, const int64_t *x_strides, void *out_dev, const int64_t *out_strides,
+                   void *stream);
+
+/*
+ * A step's rows in one launch: queries turned into q_out, keys turned and stored with the values at
+ * the positions pos[b] + t that also turn them.  The result is that of mog_rope_apply on the queries and the keys
+ * (rounded to bf16), then mog_kv_store: its arguments, its rows left out, caches of every type.
+ * Queries are turned whether or not their position is in the cache.  q_out may be q itself.
+ * t_max * (h_q + 2 h_kv) <= 2^30.
+ */
+int mog_rope_store(const mog_cache *c, const mog_rope *rope, int32_t batch, int32_t h_kv, int32_t h_q,
+                   int32_t d, int32_t t_max, const int32_t *pos_dev, const int32_t *count_dev,
+                   const void *q_dev, const int64_t *q_strides, void *q_out_dev,
+                   const int64_t *q_out_strides, const void *k_new_dev, const void *v_new_dev,
+                   const int64_t *new_strides, void *stream);
 
 /*
  * The pages of a paged cache shared by sequences.  All state is in device memory and owned

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -86,7 +87,12 @@ class Cache(C.Structure):
                 ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("stride_b", C.c_int64),
                 ("stride_h", C.c_int64), ("stride_n", C.c_int64), ("scale_b", C.c_int64),
                 ("scale_h", C.c_int64), ("scale_n", C.c_int64), ("block_table", C.c_void_p),
-                ("page_rows", C.c_int32), ("pages_per_seq", C.c_int32), ("n_pages", C.c_int32)]
+                ("page_rows", C.c_int32), ("pages_per_seq", C.c_int32), ("n_pages", C.c_int32),
+                ("block_rows", C.c_int32)]
+
+
+class RopeParams(C.Structure):
+    _fields_ = [("turns", C.c_void_p), ("rot_dim", C.c_int32), ("layout", C.c_int32), ("factor", C.c_float)]
 
 
 class DiffParams(C.Structure):
@@ -176,6 +182,68 @@ class PagedKV8(_Fixed):
         self._made = True
 
 
+def _check_rows_i8(K, V, k_scale, v_scale, rows, block_rows):
+    """rows: the dim of K that block_rows divides into blocks (positions, or a page's rows)."""
+    torch = _torch()
+    for t in (K, V):
+        if t.dtype != torch.int8 or t.dim() != 4 or t.stride(3) != 1 or not t.is_cuda:
+            raise ValueError("K and V must be CUDA int8 tensors with 4 dims, last contiguous")
+    if K.shape != V.shape or K.stride() != V.stride() or V.device != K.device:
+        raise ValueError("K and V must share shape, strides and device")
+    if K.shape[3] != 128:
+        raise ValueError("the last dim of K and V must be 128")
+    if block_rows not in (16, 32, 64, 128):
+        raise ValueError("block_rows must be 16, 32, 64 or 128")
+    shape = list(K.shape[:3])
+    shape[rows] = -(-shape[rows] // block_rows)
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or list(t.shape) != shape or t.device != K.device:
+            raise ValueError(f"the scales must be float32 tensors {shape} on K's device")
+    if k_scale.stride() != v_scale.stride():
+        raise ValueError("the scales must share strides")
+
+
+class KVI8(_Fixed):
+    """A contiguous int8 KV cache with a scale per block of positions: codes K, V int8
+    [B, H_kv, n_cap, 128], k_scale, v_scale float32 [B, H_kv, ceil(n_cap / block_rows)], block_rows
+    16, 32, 64 or 128 (value = scale * code).  Pass it as K (with V=None) to dense_decode, diff_decode,
+    kv_store, kv_load and rope_store.  The tensors are fixed once it is made."""
+
+    def __init__(self, K, V, k_scale, v_scale, block_rows):
+        _check_rows_i8(K, V, k_scale, v_scale, 2, block_rows)
+        self.K, self.V, self.k_scale, self.v_scale, self.block_rows = K, V, k_scale, v_scale, block_rows
+        self.batch, self.h_kv, self.device = K.shape[0], K.shape[1], K.device
+        self.positions = K.shape[2]
+        self.cache = Cache(3, K.shape[2], K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                           *_strides(K)[:2], K.stride(2), *_strides(k_scale), None, 0, 0, 0, block_rows)
+        self._made = True
+
+
+class PagedKVI8(_Fixed):
+    """A paged int8 KV cache with a scale per block of a page's rows: page pools K, V int8
+    [pages, H_kv, page_rows, 128] (heads_first) or [pages, page_rows, H_kv, 128], k_scale, v_scale
+    float32 with page_rows / block_rows in place of page_rows and without the last dim, and an int32 block
+    table [B, pages_per_seq] on the device.  block_rows: 16, 32, 64 or 128, at most page_rows.
+    Pass it as K (with V=None) where a KVI8 goes.  The tensors are fixed once it is made; the
+    block table's entries may change between calls."""
+
+    def __init__(self, K, V, k_scale, v_scale, block_table, page_rows, block_rows, heads_first=True):
+        h, n = (1, 2) if heads_first else (2, 1)
+        _check_rows_i8(K, V, k_scale, v_scale, n, block_rows)
+        _check_table(block_table, K)
+        if K.shape[n] != page_rows or block_rows > page_rows:
+            raise ValueError("page_rows must be the pools' rows per page, and block_rows at most that")
+        self.K, self.V, self.k_scale, self.v_scale, self.block_rows = K, V, k_scale, v_scale, block_rows
+        self.block_table, self.page_rows, self.heads_first = block_table, page_rows, heads_first
+        self.batch, self.h_kv = block_table.shape[0], K.shape[h]
+        self.positions, self.device = block_table.shape[1] * page_rows, K.device
+        ks, ss = _strides(K), _strides(k_scale)
+        self.cache = Cache(3, 0, K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), ks[0], ks[h],
+                           ks[n], ss[0], ss[h], ss[n], block_table.data_ptr(), page_rows, block_table.shape[1],
+                           K.shape[0], block_rows)
+        self._made = True
+
+
 def _check_table(block_table, K):
     torch = _torch()
     if (block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous()
@@ -205,10 +273,13 @@ def _paged_cache(P):
     return c, t.shape[0], shape[h], per * rows, k.device
 
 
+_ROWS8 = (KV8, PagedKV8, KVI8, PagedKVI8)  # caches of 8-bit rows
+
+
 def _cache(K, V):
-    """(mog_cache, batch, KV heads, positions, device) of a KV8, a PagedKV8, a PagedKV or two
-    bf16 tensors [B, H_kv, n_cap, 128]."""
-    if isinstance(K, (KV8, PagedKV8)):
+    """(mog_cache, batch, KV heads, positions, device) of a KV8, PagedKV8, KVI8 or PagedKVI8, a
+    PagedKV or two bf16 tensors [B, H_kv, n_cap, 128]."""
+    if isinstance(K, _ROWS8):
         return K.cache, K.batch, K.h_kv, K.positions, K.device
     if isinstance(K, PagedKV):
         k, v, t = K.K, K.V, K.block_table
@@ -220,7 +291,7 @@ def _cache(K, V):
         return made[1]
     torch = _torch()
     if V is None:
-        raise ValueError("this call takes K and V tensors, or a PagedKV, KV8 or PagedKV8 as K")
+        raise ValueError("this call takes K and V tensors, or a PagedKV, KV8, PagedKV8, KVI8 or PagedKVI8 as K")
     shape, st, dev = K.shape, K.stride(), K.device
     if (K.dtype is not torch.bfloat16 or V.dtype is not torch.bfloat16 or len(shape) != 4 or shape[3] != 128
             or st[3] != 1 or V.shape != shape or V.stride() != st or dev.type != "cuda" or V.device != dev):
@@ -283,6 +354,9 @@ _SIGS = {
     "mog_diff_decode_scratch_bytes": (C.c_int, [C.c_int32] * 5 + [_P]),
     "mog_diff_decode": (C.c_int, [_P, _P] + [C.c_int32] * 5 + [_P, _P, _P, C.c_int32, _P, C.c_size_t, _P]),
     "mog_kv_store": (C.c_int, [_P] + [C.c_int32] * 4 + [_P] * 4 + [C.c_int64] * 3 + [_P]),
+    "mog_kv_load": (C.c_int, [_P] + [C.c_int32] * 4 + [_P] * 4 + [C.c_int64] * 3 + [_P]),
+    "mog_rope_apply": (C.c_int, [_P] + [C.c_int32] * 4 + [_P, C.c_int32, _P, C.c_int32] + [_P] * 5),
+    "mog_rope_store": (C.c_int, [_P, _P] + [C.c_int32] * 5 + [_P] * 10),
     "mog_pages_work_bytes": (C.c_int, [C.c_int32, C.c_int32, _P]),
     "mog_pages_assign": (C.c_int, [_P, _P, _P]),
     "mog_pages_grow": (C.c_int, [_P, _P, _P, _P, _P]),
@@ -339,7 +413,7 @@ def _kv(K, V):
     if isinstance(K, PagedKV):
         return K.struct()
     torch = _torch()
-    if isinstance(K, (KV8, PagedKV8)) or V is None:
+    if isinstance(K, _ROWS8) or V is None:
         raise ValueError("this call takes bf16 K and V tensors, or a PagedKV as K")
     for t in (K, V):
         if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1 or not t.is_cuda:
@@ -581,9 +655,9 @@ def _check_q_out(K, q, out):
 
 
 def dense_decode(K, V, lengths_dev, n_max, q, out=None, scratch=None, stream=None):
-    """Full-scan exact attention.  q: bf16 [B, H_q, d] -> out f32 [B, H_q, d].  Over an e4m3
-    cache (K a KV8 or PagedKV8; dense_decode8) `out` may also be bf16."""
-    if isinstance(K, (KV8, PagedKV8)):
+    """Full-scan exact attention.  q: bf16 [B, H_q, d] -> out f32 [B, H_q, d].  Over an 8-bit
+    cache (K a KV8, PagedKV8, KVI8 or PagedKVI8; dense_decode8) `out` may also be bf16."""
+    if isinstance(K, _ROWS8):
         return _cache_decode("dense_decode8", K, V, lengths_dev, n_max, q, None, out, scratch, stream)
     torch = _torch()
     B, H_kv = (q.shape[0], K.h_kv) if isinstance(K, PagedKV) else (K.shape[0], K.shape[1])
@@ -604,7 +678,7 @@ def dense_decode(K, V, lengths_dev, n_max, q, out=None, scratch=None, stream=Non
 def dense_decode_noalloc(K, V, lengths_dev, n_max, q, out, stream=None):
     """dense_decode whose scratch is the library's static device array: no device memory
     is allocated by this call (the caller supplies `out`)."""
-    if isinstance(K, (KV8, PagedKV8)):
+    if isinstance(K, _ROWS8):
         raise ValueError("dense_decode_noalloc reads bf16 caches")
     B, H_kv = (q.shape[0], K.h_kv) if isinstance(K, PagedKV) else (K.shape[0], K.shape[1])
     _check_q_out(K, q, out)
@@ -706,8 +780,8 @@ def diff_decode(K, V, lengths_dev, n_max, q, lam, lambda_init, gamma=None, eps=1
                 stream=None):
     """Differential decode attention (mog_diff_decode): a head is two halves of 64, q bf16
     [B, H_q, 128] = [q1 | q2] over keys [k1 | k2] and values of 128; the second softmax map is
-    subtracted lambda times and the result normalised.  K, V: bf16 tensors, or K a PagedKV, KV8
-    or PagedKV8.  lam: float32 [4, 64] or [H_q, 4, 64], the vectors l_q1, l_k1, l_q2, l_k2 of
+    subtracted lambda times and the result normalised.  K, V: bf16 tensors, or K a PagedKV, KV8,
+    PagedKV8, KVI8 or PagedKVI8.  lam: float32 [4, 64] or [H_q, 4, 64], the vectors l_q1, l_k1, l_q2, l_k2 of
     lambda = exp(l_q1.l_k1) - exp(l_q2.l_k2) + lambda_init; gamma: float32 [128] norm weights
     or None.  -> out f32 (or bf16 if given so) [B, H_q, 128]."""
     torch = _torch()
@@ -730,7 +804,7 @@ def diff_scratch_bytes(batch, h_kv, h_q, n_max) -> int:
 
 
 def dense8_scratch_bytes(batch, h_kv, h_q, n_max) -> int:
-    """Bytes of dense_decode's scratch over an e4m3 cache, on the current device."""
+    """Bytes of dense_decode's scratch over an 8-bit cache, on the current device."""
     return _scratch_bytes("dense_decode8", batch, h_kv, h_q, n_max, _torch().cuda.current_device()
                           if _torch().cuda.is_available() else -1)
 
@@ -740,7 +814,8 @@ def kv_store(K, V, pos, count, k_new, v_new, stream=None):
     strides of whole 16-byte chunks, alike for both, last dim contiguous), token t < count[b] of
     sequence b to position pos[b] + t; pos, count int32 [B] on the device, count None for T
     each.  K, V: bf16 tensors [B, H_kv, n_cap, 128], or K a PagedKV, KV8 or PagedKV8 (rounded
-    to e4m3 with a power-of-two scale per row)."""
+    to e4m3 with a power-of-two scale per row), KVI8 or PagedKVI8 (rounded to int8 with a scale per
+    block of positions, which grows with the rows that join the block)."""
     torch = _torch()
     c, B, H_kv, _, dev = _cache(K, V)
     s = _here(dev, stream)
@@ -774,6 +849,207 @@ def kv_store(K, V, pos, count, k_new, v_new, stream=None):
         _check(rc, "mog_kv_store")
 
 
+def _row_strides(t, shape, dev, name, write=False):
+    """Element strides between sequences, tokens and heads of bf16 rows [B, T, H, 128]."""
+    torch = _torch()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on {dev}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"the last dim of {name} must be contiguous")
+    if write and any(s == 0 and n > 1 for s, n in zip(st, shape)):
+        raise ValueError(f"{name} is written: its rows must not share memory")
+    return tuple(s if n > 1 else 0 for s, n in zip(st[:3], shape))
+
+
+def _strides3(s):
+    return (C.c_int64 * 3)(*s)
+
+
+def kv_load(K, V, pos, count, k_out, v_out, stream=None):
+    """Read rows of a cache back as bf16 (mog_kv_load): position pos[b] + t, t < count[b], of sequence
+    b to k_out[b, t], v_out[b, t]; k_out, v_out bf16 [B, T, H_kv, 128] of the same strides, pos, count
+    int32 [B] on the device, count None for T each.  K, V: any cache that kv_store takes.  Rows
+    behind count[b], outside the cache or in no page stay as they are.  -> (k_out, v_out)."""
+    c, B, H_kv, _, dev = _cache(K, V)
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return kv_load(K, V, pos, count, k_out, v_out)
+    if k_out.dim() != 4 or k_out.shape[0] != B:
+        raise ValueError(f"k_out must be a bf16 tensor [{B}, T, {H_kv}, 128] on the cache's device")
+    T = k_out.shape[1]
+    shape = (B, T, H_kv, 128)
+    st = _row_strides(k_out, shape, dev, "k_out", True)
+    if _row_strides(v_out, shape, dev, "v_out", True) != st:
+        raise ValueError("k_out and v_out must share strides")
+    _check_counts(pos, B, dev, "pos")
+    if count is not None:
+        _check_counts(count, B, dev, "count")
+    if T:
+        _check(lib().mog_kv_load(C.byref(c), B, H_kv, 128, T, pos.data_ptr(),
+                                 None if count is None else count.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), *st, s),
+               "mog_kv_load")
+    return k_out, v_out
+
+
+def rope_frequencies(rot_dim=128, base=10000.0, scaling=None):
+    """(radians per position of each pair of rotary dimensions, attention factor), as Python floats:
+    base^(-2i/rot_dim) and 1, or scaled for contexts longer than the one trained on by scaling, a
+    dict with "type" and "factor":
+      "linear"  every frequency divided by the factor
+      "ntk"     the base raised to base * factor^(rot_dim / (rot_dim - 2))
+      "yarn"    divided by the factor below beta_slow (1) turns over original_len positions, kept above
+                beta_fast (32), blended linearly in the pair's number between; attention factor
+                0.1 ln(factor) + 1 unless given as "attention_factor"
+      "bands"   divided by the factor below low (1) turns over original_len, kept above high (4),
+                blended linearly in the turns between"""
+    def plain(b):
+        return [b ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+
+    if scaling is None:
+        return plain(base), 1.0
+    kind, x = scaling["type"], float(scaling["factor"])
+    if not x > 0:
+        raise ValueError("a scaling's factor must be positive")
+    if kind == "linear":
+        return [f / x for f in plain(base)], 1.0
+    if kind == "ntk":
+        if rot_dim <= 2:
+            raise ValueError("ntk scaling needs more than one pair")
+        return plain(base * x ** (rot_dim / (rot_dim - 2))), 1.0
+    if kind not in ("yarn", "bands"):
+        raise ValueError(f"unknown scaling type {kind!r}")
+    n = float(scaling["original_len"])
+    f = plain(base)
+    if kind == "yarn":
+        def pair(turns):  # the pair that makes so many turns over the original length
+            return rot_dim * math.log(n / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        lo = max(math.floor(pair(scaling.get("beta_fast", 32.0))), 0)
+        hi = min(math.ceil(pair(scaling.get("beta_slow", 1.0))), rot_dim - 1)
+        keep = [1 - min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(len(f))]
+        scale = scaling.get("attention_factor")
+        if scale is None:
+            scale = 0.1 * math.log(x) + 1 if x > 1 else 1.0
+    else:
+        low, high = float(scaling.get("low", 1.0)), float(scaling.get("high", 4.0))
+        if not high > low:
+            raise ValueError("bands scaling needs high > low")
+        keep = [min(max((n * g / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for g in f]
+        scale = 1.0
+    return [g / x * (1 - k) + g * k for g, k in zip(f, keep)], float(scale)
+
+
+class Rope(_Fixed):
+    """Rotary positions of the first rot_dim dimensions of a head (a multiple of 16 up to 128), for rope and
+    rope_store; made once and kept.  interleaved: pairs of neighbouring dimensions 2i, 2i + 1;
+    otherwise i, i + rot_dim/2.  Frequencies: rope_frequencies(rot_dim, base, scaling), or
+    inv_freq (radians per position, rot_dim/2 of them, a sequence or a float64 tensor).  factor: the
+    attention factor of the turned dimensions (default: the scaling's, or 1).  device: default
+    inv_freq's if that is a CUDA tensor, else the current one."""
+
+    def __init__(self, rot_dim=128, base=10000.0, interleaved=False, scaling=None, inv_freq=None, factor=None,
+                 device=None):
+        torch = _torch()
+        if rot_dim % 16 or not 16 <= rot_dim <= 128:
+            raise ValueError("rot_dim must be a multiple of 16 from 16 to 128")
+        if inv_freq is not None and scaling is not None:
+            raise ValueError("inv_freq and scaling exclude each other")
+        of_scaling = 1.0
+        if inv_freq is None:
+            inv_freq, of_scaling = rope_frequencies(rot_dim, base, scaling)
+        f = torch.as_tensor(inv_freq, dtype=torch.float64)
+        if f.shape != (rot_dim // 2,):
+            raise ValueError(f"inv_freq must have {rot_dim // 2} entries")
+        self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
+        self.factor = float(of_scaling if factor is None else factor)
+        if not math.isfinite(self.factor):
+            raise ValueError("factor must be finite")
+        # turns per position as a 64-bit fraction: two exact steps of 32 bits
+        x = f / (2 * math.pi)
+        x = (x - torch.trunc(x)) * 2.0 ** 32
+        high = torch.floor(x)
+        low = torch.floor((x - high) * 2.0 ** 32)
+        high = high - 2.0 ** 32 * torch.floor((high + 2.0 ** 31) / 2.0 ** 32)
+        turns = high.long() * (1 << 32) + low.long()
+        if device is None:
+            device = f.device if f.is_cuda else torch.device("cuda", torch.cuda.current_device())
+        self.turns = turns.to(device)
+        self.device = self.turns.device
+        self._s = RopeParams(self.turns.data_ptr(), rot_dim, 1 if interleaved else 0, self.factor)
+        self._made = True
+
+
+def rope(x, pos, by, count=None, out=None, inverse=False, stream=None):
+    """Turn rows by their positions (mog_rope_apply): x bf16 [B, T, H, 128] (strides of whole 16-byte
+    chunks, last dim contiguous), pos int32 on the device, [B] (token t of sequence b at pos[b] + t)
+    or [B, T]; by: a Rope.  inverse: by the negative angles, which is also the gradient's way
+    back.  out: like x, or x itself; a new tensor by default.  Rows t >= count[b] (int32 [B] or None)
+    of out are not written.  -> out."""
+    torch = _torch()
+    dev = x.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return rope(x, pos, by, count, out, inverse)
+    if x.dim() != 4 or x.shape[3] != 128:
+        raise ValueError("x must be a bf16 tensor [B, T, H, 128]")
+    B, T, H = x.shape[:3]
+    xs = _row_strides(x, x.shape, dev, "x", out is x)
+    if by.device != dev:
+        raise ValueError(f"the Rope is on {by.device}, x on {dev}")
+    each = pos.dim() == 2
+    if (pos.dtype is not torch.int32 or pos.shape != ((B, T) if each else (B,)) or not pos.is_contiguous()
+            or pos.device != dev):
+        raise ValueError(f"pos must be a contiguous int32 tensor [{B}] or [{B}, {T}] on x's device")
+    if count is not None:
+        _check_counts(count, B, dev, "count")
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    os_ = _row_strides(out, x.shape, dev, "out", True)
+    if out.numel():
+        _check(lib().mog_rope_apply(C.byref(by._s), B, H, 128, T, pos.data_ptr(), each,
+                                    None if count is None else count.data_ptr(), bool(inverse), x.data_ptr(),
+                                    _strides3(xs), out.data_ptr(), _strides3(os_), s), "mog_rope_apply")
+    return out
+
+
+def rope_store(K, V, pos, count, q, k_new, v_new, rope, q_out=None, stream=None):
+    """A step's rows in one launch (mog_rope_store): queries q bf16 [B, T, H_q, 128] turned into q_out (like
+    q, or q itself; a new tensor by default), keys k_new turned and stored with the values v_new, bf16
+    [B, T, H_kv, 128], at the positions pos[b] + t that also turn them.  As rope on q and k_new, then
+    kv_store: K, V, pos and count as there; rope: a Rope.  -> q_out."""
+    torch = _torch()
+    c, B, H_kv, _, dev = _cache(K, V)
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return rope_store(K, V, pos, count, q, k_new, v_new, rope, q_out)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != 128:
+        raise ValueError(f"q must be a bf16 tensor [{B}, T, H_q, 128] on the cache's device")
+    T, H_q = q.shape[1:3]
+    qs = _row_strides(q, q.shape, dev, "q", q_out is q)
+    ks = _row_strides(k_new, (B, T, H_kv, 128), dev, "k_new")
+    if _row_strides(v_new, (B, T, H_kv, 128), dev, "v_new") != ks:
+        raise ValueError("k_new and v_new must share strides")
+    if rope.device != dev:
+        raise ValueError(f"the Rope is on {rope.device}, the cache on {dev}")
+    _check_counts(pos, B, dev, "pos")
+    if count is not None:
+        _check_counts(count, B, dev, "count")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    os_ = _row_strides(q_out, q.shape, dev, "q_out", True)
+    if T:
+        rc = lib().mog_rope_store(C.byref(c), C.byref(rope._s), B, H_kv, H_q, 128, T, pos.data_ptr(),
+                                  None if count is None else count.data_ptr(), q.data_ptr(), _strides3(qs),
+                                  q_out.data_ptr(), _strides3(os_), k_new.data_ptr(), v_new.data_ptr(), _strides3(ks), s)
+        if rc:
+            _check(rc, "mog_rope_store")
+    return q_out
+
+
 def _pool_desc(t):
     """mog_page_pool of a tensor whose first dim is the pages."""
     n, size = t.shape[0], t.element_size()
@@ -788,7 +1064,8 @@ class PagePool(_Fixed):
     [batch, pages_per_seq], the sequences' lengths and the pages' holders, all on the device.
 
     K, V: page pools [pages, H_kv, page_rows, 128] (heads_first) or [pages, page_rows, H_kv, 128],
-    one tensor each or a list with one per layer, bf16, or float8_e4m3fn with k_scale, v_scale.  A page's
+    one tensor each or a list with one per layer, bf16, or float8_e4m3fn or int8 with k_scale, v_scale
+    (as PagedKV8's or PagedKVI8's; an int8 page's scales take a multiple of 16 bytes).  A page's
     elements must be contiguous.  block_table, lengths, refs: existing state, int32, used as it
     is; by default every sequence is empty.  The tensors are fixed once it is made; their contents may change between
     calls.  No method waits for the GPU but status()."""
@@ -809,12 +1086,25 @@ class PagePool(_Fixed):
         self.device, n_pages = first.device, first.shape[0]
         self.heads_first, self.page_rows = heads_first, first.shape[2 if heads_first else 1]
         pools = [t for x in lists for t in x]
-        rows = torch.float8_e4m3fn if len(lists) == 4 else torch.bfloat16
+        rows = (torch.bfloat16 if len(lists) == 2 else torch.int8 if first.dtype == torch.int8
+                else torch.float8_e4m3fn)
         if any(t.dtype != rows or t.dim() != 4 or t.shape != first.shape for t in self.K + self.V) or any(
                 t.dtype != torch.float32 or t.dim() != 3 for x in lists[2:] for t in x):
-            raise ValueError("K and V must be bf16 pools of one shape, or float8_e4m3fn with float32 k_scale and v_scale")
+            raise ValueError("K and V must be bf16 pools of one shape, or float8_e4m3fn or int8 with float32 k_scale "
+                             "and v_scale")
+        scales = list(first.shape[:3])  # the scales' dims
+        self.block_rows = None
+        if rows == torch.int8:
+            n = 2 if heads_first else 1
+            per = lists[2][0].shape[n]
+            if per == 0 or self.page_rows % per or self.page_rows // per not in (16, 32, 64, 128):
+                raise ValueError("an int8 page's scales must stand for blocks of 16, 32, 64 or 128 rows")
+            scales[n], self.block_rows = per, self.page_rows // per
+            if lists[2][0][0].numel() % 4:
+                raise ValueError("an int8 page's scales must take a multiple of 16 bytes (page copies)")
         for t in pools:
-            if not t.is_cuda or t.device != self.device or t.shape[:3] != first.shape[:3] or not t[0].is_contiguous():
+            if not t.is_cuda or t.device != self.device or not t[0].is_contiguous() or (
+                    list(t.shape[:3]) != (scales if t.dim() == 3 else list(first.shape[:3]))):
                 raise ValueError("page pools must share a CUDA device and their first three dims, a page contiguous")
         for name, t, shape in (("block_table", block_table, (batch, pages_per_seq)), ("lengths", lengths, (batch,)),
                                ("refs", refs, (n_pages,))):
@@ -842,7 +1132,9 @@ class PagePool(_Fixed):
         self._made = True
 
     def cache(self, layer=0):
-        """The paged cache of a layer (PagedKV or PagedKV8), for the calls that take one."""
+        """The paged cache of a layer (PagedKV, PagedKV8 or PagedKVI8), for the calls that take one."""
+        if self.block_rows is not None:
+            return PagedKVI8(*self._layers[layer], self.block_table, self.page_rows, self.block_rows, self.heads_first)
         return (PagedKV if self.k_scale is None else PagedKV8)(*self._layers[layer], self.block_table, self.page_rows,
                                                                self.heads_first)
 

@@ -900,11 +900,15 @@ extern "C" int mog_check_bounded_wait(int32_t limit, int32_t arrive, int32_t *sc
 // Layout of a mog_cache; n positions of it are used.
 static int check_cache(const mog_cache *c, int64_t n) {
     if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return MOG_ERR_INVALID_ARG;
-    if (c->type != MOG_CACHE_BF16 && c->type != MOG_CACHE_E4M3) return MOG_ERR_INVALID_ARG;
-    const bool e4 = c->type == MOG_CACHE_E4M3;
-    if (e4 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale)) return MOG_ERR_INVALID_ARG;
-    if (e4 && (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3)) return MOG_ERR_INVALID_ARG;
-    const int64_t m = e4 ? 15 : 7;
+    if (c->type != MOG_CACHE_BF16 && c->type != MOG_CACHE_E4M3 && c->type != MOG_CACHE_I8) return MOG_ERR_INVALID_ARG;
+    const bool row8 = c->type != MOG_CACHE_BF16;
+    if (row8 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale)) return MOG_ERR_INVALID_ARG;
+    if (row8 && (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3)) return MOG_ERR_INVALID_ARG;
+    if (c->type == MOG_CACHE_I8) {
+        if (c->block_rows < 16 || c->block_rows > 128 || log2_exact(c->block_rows) < 0) return MOG_ERR_SHAPE;
+        if (c->block_table && c->block_rows > c->page_rows) return MOG_ERR_SHAPE;
+    }
+    const int64_t m = row8 ? 15 : 7;
     if (c->stride_n < MOG_D || ((c->stride_b | c->stride_h | c->stride_n) & m)) return MOG_ERR_SHAPE;
     if (c->stride_b < 0 || c->stride_h < 0) return MOG_ERR_SHAPE;
     if (c->block_table) {
@@ -956,7 +960,7 @@ extern "C" int dense_decode8(const mog_cache *c, const int32_t *lengths_dev, int
     size_t need = 0;
     const int st = dense_decode8_scratch_bytes(batch, h_kv, h_q, d, n_max, &need);
     if (st != MOG_OK) return st;
-    if (!c || c->type != MOG_CACHE_E4M3) return MOG_ERR_INVALID_ARG;
+    if (!c || c->type == MOG_CACHE_BF16) return MOG_ERR_INVALID_ARG;
     return cache_decode(c, lengths_dev, n_max, batch, h_kv, h_q, q_dev, nullptr, out_dev, out_type, scratch_dev, need,
                         scratch_bytes, stream, "dense_decode8 launch");
 }
@@ -992,8 +996,88 @@ extern "C" int mog_kv_store(const mog_cache *c, int32_t batch, int32_t h_kv, int
     if (!pos_dev || !k_new_dev || !v_new_dev) return MOG_ERR_INVALID_ARG;
     if (!aligned16(k_new_dev) || !aligned16(v_new_dev)) return MOG_ERR_INVALID_ARG;
     if ((new_b | new_t | new_h) & 7) return MOG_ERR_SHAPE;
+    if (c->type == MOG_CACHE_I8) {
+        RowsIn r{};
+        r.k = k_new_dev, r.v = v_new_dev, r.ks[0] = new_b, r.ks[1] = new_t, r.ks[2] = new_h;
+        r.h_kv = h_kv, r.t_max = t_max, r.pos = pos_dev, r.count = count_dev;
+        CK(launch_rows_i8(c, batch, r, static_cast<cudaStream_t>(stream)));
+        return MOG_OK;
+    }
     CK(launch_kv_store(c, batch, h_kv, t_max, pos_dev, count_dev, k_new_dev, v_new_dev, new_b, new_t, new_h,
                        static_cast<cudaStream_t>(stream)));
+    return MOG_OK;
+}
+
+extern "C" int mog_kv_load(const mog_cache *c, int32_t batch, int32_t h_kv, int32_t d, int32_t t_max,
+                           const int32_t *pos_dev, const int32_t *count_dev, void *k_out_dev, void *v_out_dev,
+                           int64_t out_b, int64_t out_t, int64_t out_h, void *stream) {
+    if (batch <= 0 || h_kv <= 0 || t_max <= 0) return MOG_ERR_INVALID_ARG;
+    if (d != MOG_D || batch > 65535 || (int64_t)t_max * 2 * h_kv > (1 << 30)) return MOG_ERR_SHAPE;
+    const int st = check_cache(c, 1);
+    if (st != MOG_OK) return st;
+    if (!pos_dev || !k_out_dev || !v_out_dev) return MOG_ERR_INVALID_ARG;
+    if (!aligned16(k_out_dev) || !aligned16(v_out_dev)) return MOG_ERR_INVALID_ARG;
+    if ((out_b | out_t | out_h) & 7) return MOG_ERR_SHAPE;
+    RowsIn r{};
+    r.ks[0] = out_b, r.ks[1] = out_t, r.ks[2] = out_h;
+    r.h_kv = h_kv, r.t_max = t_max, r.pos = pos_dev, r.count = count_dev;
+    CK(launch_kv_load(c, batch, r, k_out_dev, v_out_dev, static_cast<cudaStream_t>(stream)));
+    return MOG_OK;
+}
+
+// ------------------------------------------------------------------------ rotary positions
+
+static int check_rope(const mog_rope *r) {
+    if (!r || !r->turns || ((uintptr_t)r->turns & 7)) return MOG_ERR_INVALID_ARG;
+    if (r->rot_dim < 16 || r->rot_dim > MOG_D || r->rot_dim % 16) return MOG_ERR_SHAPE;
+    if (r->layout != MOG_ROPE_HALVES && r->layout != MOG_ROPE_PAIRS) return MOG_ERR_INVALID_ARG;
+    return std::isfinite(r->factor) ? MOG_OK : MOG_ERR_INVALID_ARG;
+}
+
+static int check_rows(const void *p, const int64_t *strides) {
+    if (!p || !aligned16(p)) return MOG_ERR_INVALID_ARG;
+    return (strides[0] | strides[1] | strides[2]) & 7 ? MOG_ERR_SHAPE : MOG_OK;
+}
+
+extern "C" int mog_rope_apply(const mog_rope *rope, int32_t batch, int32_t heads, int32_t d, int32_t t_max,
+                              const int32_t *pos_dev, int32_t pos_each, const int32_t *count_dev, int32_t inverse,
+                              const void *x_dev, const int64_t *x_strides, void *out_dev, const int64_t *out_strides,
+                              void *stream) {
+    if (batch <= 0 || heads <= 0 || t_max <= 0 || !x_strides || !out_strides) return MOG_ERR_INVALID_ARG;
+    if (d != MOG_D || batch > 65535 || (int64_t)t_max * heads > (1 << 30)) return MOG_ERR_SHAPE;
+    int st = check_rope(rope);
+    if (st != MOG_OK) return st;
+    if (!pos_dev) return MOG_ERR_INVALID_ARG;
+    if ((st = check_rows(x_dev, x_strides)) != MOG_OK || (st = check_rows(out_dev, out_strides)) != MOG_OK) return st;
+    RowsIn r{};
+    r.q = x_dev, r.qo = out_dev, r.h_q = heads, r.t_max = t_max, r.pos = pos_dev, r.count = count_dev;
+    for (int i = 0; i < 3; ++i) r.qs[i] = x_strides[i], r.os[i] = out_strides[i];
+    r.each = pos_each != 0, r.inverse = inverse != 0, r.rope = rope;
+    CK(launch_rope(nullptr, batch, r, static_cast<cudaStream_t>(stream)));
+    return MOG_OK;
+}
+
+extern "C" int mog_rope_store(const mog_cache *c, const mog_rope *rope, int32_t batch, int32_t h_kv, int32_t h_q,
+                              int32_t d, int32_t t_max, const int32_t *pos_dev, const int32_t *count_dev,
+                              const void *q_dev, const int64_t *q_strides, void *q_out_dev,
+                              const int64_t *q_out_strides, const void *k_new_dev, const void *v_new_dev,
+                              const int64_t *new_strides, void *stream) {
+    if (batch <= 0 || h_kv <= 0 || h_q <= 0 || t_max <= 0) return MOG_ERR_INVALID_ARG;
+    if (!q_strides || !q_out_strides || !new_strides) return MOG_ERR_INVALID_ARG;
+    if (d != MOG_D || batch > 65535 || (int64_t)t_max * (h_q + 2LL * h_kv) > (1 << 30)) return MOG_ERR_SHAPE;
+    int st = check_rope(rope);
+    if (st != MOG_OK) return st;
+    if ((st = check_cache(c, 1)) != MOG_OK) return st;
+    if (!pos_dev) return MOG_ERR_INVALID_ARG;
+    if ((st = check_rows(q_dev, q_strides)) != MOG_OK || (st = check_rows(q_out_dev, q_out_strides)) != MOG_OK ||
+        (st = check_rows(k_new_dev, new_strides)) != MOG_OK || (st = check_rows(v_new_dev, new_strides)) != MOG_OK)
+        return st;
+    RowsIn r{};
+    r.q = q_dev, r.qo = q_out_dev, r.k = k_new_dev, r.v = v_new_dev;
+    for (int i = 0; i < 3; ++i) r.qs[i] = q_strides[i], r.os[i] = q_out_strides[i], r.ks[i] = new_strides[i];
+    r.h_q = h_q, r.h_kv = h_kv, r.t_max = t_max, r.pos = pos_dev, r.count = count_dev, r.rope = rope;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CK(c->type == MOG_CACHE_I8 ? launch_rows_i8(c, batch, r, s) : launch_rope(c, batch, r, s));
     return MOG_OK;
 }
 

@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "cache.cuh"
+#include "rows.cuh"
 
 namespace mog {
 
@@ -121,21 +122,22 @@ static cudaError_t launch_merge(cudaStream_t s, bool diff, bool bf_out, const Ca
 cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
                                 const void *q, const mog_diff_params *diff, int out_type, void *out, float *scratch,
                                 cudaStream_t s) {
-    const bool e4 = c->type == MOG_CACHE_E4M3, bf_out = out_type == MOG_OUT_BF16;
-    const int es = e4 ? 1 : 2;
+    const bool i8 = c->type == MOG_CACHE_I8, row8 = i8 || c->type == MOG_CACHE_E4M3, bf_out = out_type == MOG_OUT_BF16;
+    const int es = row8 ? 1 : 2;
     CacheArgs a{static_cast<const uint8_t *>(c->k), static_cast<const uint8_t *>(c->v), c->k_scale, c->v_scale,
                 c->stride_b * es, c->stride_h * es, c->stride_n * es, c->scale_b, c->scale_h, c->scale_n,
-                c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
+                i8 ? log2_exact(c->block_rows) : 0, c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
                 lengths, n_max, batch, h_kv, G, static_cast<const uint16_t *>(q), scratch,
                 (float)(LOG2E / sqrt(diff ? MOG_D / 2.0 : (double)MOG_D)), cache_cluster(batch * h_kv, n_max)};
     DiffArgs d{};
     if (diff) d = DiffArgs{diff->lam, diff->lam_heads > 1 ? 4 * (MOG_D / 2) : 0, diff->gamma, diff->lambda_init, diff->eps};
     const bool wide = (diff ? 2 : 1) * G > 8;
-    const int per_sm = !e4 ? 3 : wide ? Tile<true, true>::PER_SM : Tile<true, false>::PER_SM;
-    const int rows = !e4 ? 64 : wide ? Tile<true, true>::ROWS : Tile<true, false>::ROWS;
+    const int per_sm = !row8 ? 3 : wide ? Tile<true, true>::PER_SM : Tile<true, false>::PER_SM;
+    const int rows = !row8 ? 64 : wide ? Tile<true, true>::ROWS : Tile<true, false>::ROWS;
     const int splits = std::min(cache_splits(batch * h_kv, n_max), per_sm * num_sms());
     while (a.cs > 1 && a.cs / 2 >= ceil_div64(n_max, rows)) a.cs /= 2;  // as many CTAs as tiles do
-    const cudaError_t e = e4 ? launch_split8(a, d, out, diff != nullptr, bf_out, wide, splits, s)
+    const cudaError_t e = i8 ? launch_spliti8(a, d, out, diff != nullptr, bf_out, wide, splits, s)
+                          : row8 ? launch_split8(a, d, out, diff != nullptr, bf_out, wide, splits, s)
                           : bf_out ? pick_split<false, true, true>(a, d, out, wide, splits, s)
                                    : pick_split<false, true, false>(a, d, out, wide, splits, s);
     if (e != cudaSuccess || a.cs) return e;
@@ -174,22 +176,6 @@ struct StoreArgs {
 };
 
 constexpr int SR_THREADS = 256, SR_LANES = 4, SR_VECS = 16 / SR_LANES;  // 16-byte pieces of a row per lane
-
-__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {  // (a NaN half gives way)
-    uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {  // bf16 pair -> two codes
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(bf_hi(w)), "f"(bf_lo(w)));
-    return c;
-}
 
 template <bool E4M3, class S>
 __global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs<S> a) {
@@ -230,25 +216,8 @@ __global__ void __launch_bounds__(SR_THREADS) k_kv_store(StoreArgs<S> a) {
                 *reinterpret_cast<uint4 *>(dst + 16 * (lane + SR_LANES * k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             continue;
         }
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 4 * SR_VECS; ++k) m = bf2_max(m, w[k] & 0x7fff7fffu);
-        float amax = fmaxf(bf_lo(m), bf_hi(m));
-        if (amax == INFINITY) {  // the largest finite magnitude instead
-            amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4 * SR_VECS; ++k) {
-                const float p = fabsf(bf_lo(w[k])), q = fabsf(bf_hi(w[k]));
-                amax = fmaxf(amax, fmaxf(p < INFINITY ? p : 0.f, q < INFINITY ? q : 0.f));
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < SR_LANES; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
-        // amax = m * 2^E, 1 <= m < 2: 448 = 1.75 * 2^8
-        const int bits = __float_as_int(amax), E = (bits >> 23) - 127;
-        int e = E - 8 + ((bits & 0x7fffff) > 0x600000);
-        e = amax > 0.f ? max(e, -126) : 0;
-        const uint32_t inv = (uint32_t)(127 - e) << 7, inv2 = inv | inv << 16;  // 2^-e twice, -126 <= -e <= 126
+        const int e = e4m3_row_exp<SR_LANES>(w, group);
+        const uint32_t inv2 = bf2_pow2_neg(e);
         // (a product below bf16's normal range rounds, but e4m3 has only 0 there)
 #pragma unroll
         for (int k = 0; k < SR_VECS; ++k) {

@@ -1,29 +1,30 @@
-// cache.cuh -- decode attentions over a mog_cache (bf16 or e4m3 rows, contiguous or paged):
-// the kernel that reads the cache.  Its instances are compiled in cache.cu (bf16 rows) and
-// cache8.cu (e4m3 rows).
+// cache.cuh -- decode attentions over a mog_cache (bf16, e4m3 or int8 rows, contiguous or paged):
+// the kernel that reads the cache.  Its instances are compiled in cache.cu (bf16 rows), cache8.cu
+// (e4m3 rows) and cachei8.cu (int8 rows).
 //
-// dense_decode8: softmax(tau q.K^T) V of an e4m3 cache whose row i stands for
+// dense_decode8: softmax(tau q.K^T) V of an 8-bit cache whose row i stands for
 // k_scale[i]*code_i and v_scale[i]*code_i.  mog_diff_decode: the difference of two softmax
 // maps over one set of values, normalised.  Both are a split kernel and a fold of its partials,
 // or, for short caches, one kernel whose clusters take a unit each and fold it themselves.
 //
-// Split (k_cache_split): the tiles (128 e4m3 rows, 64 of bf16) of all (sequence, KV head) units form one list;
+// Split (k_cache_split): the tiles (128 8-bit rows, 64 of bf16) of all (sequence, KV head) units form one list;
 // CTA c takes tiles [c*chunk, (c+1)*chunk) of it, so ragged batches load every SM alike
 // (the lengths are read on the device: a captured graph replays with grown sequences).  Its
 // copies run ahead across unit borders.  Each unit that a CTA touches leaves one partial
 // (max, sum, acc per head) in slot c + unit, which no other pair (c, unit) shares, because
 // along the list either c or the unit grows by one.
 //
-// One warp takes 16 rows (bf16) or 32 (e4m3) of each tile.  Up to 8 columns (query heads, or
+// One warp takes 16 rows (bf16) or 32 (8-bit) of each tile.  Up to 8 columns (query heads, or
 // the two maps of up to 4 differential heads) sit in N of m16n8k16 with the rows in M
 // ("narrow"); up to 16 columns sit in M with the rows in N ("wide").  Either way a value
 // row is read once for all of them, and no column of the product is padding at its limit.
 // The wide form needs no transposition between the two products (its weights leave the first
 // one in the layout that the second takes) and a maximum over 4 lanes instead of 8.
 //
-// e4m3 rows are read by 16-byte loads in the order the fragments want (dimensions are
+// 8-bit rows are read by 16-byte loads in the order the fragments want (dimensions are
 // permuted alike in K and q, and back in the output), then widened in registers to fp16,
-// which holds every e4m3 value exactly.  q enters as fp16 scaled by a power of two of its
+// which holds every e4m3 and int8 value exactly.  The scale of an int8 block is copied to each of its rows
+// in the stage, so that all 8-bit rows are alike from there on.  q enters as fp16 scaled by a power of two of its
 // own, so that its elements down to 2^-29 of the largest are exact.  Weights p * v_scale enter
 // the P.V product as fp16, 2^14 times their share of a running unit: high + low parts (2^-22
 // relative), or the high part alone (2^-11; weight_parts), and no better than 2^-39 of the unit.  The unit is at most 2^15 times the largest weight
@@ -63,25 +64,25 @@ constexpr int V_NONE = 0x7fffffff;  // no unit yet
 // A tile is copied by the whole CTA, 2 KB of neighbouring rows per instruction, and each
 // warp consumes BLK blocks of 16 of its rows.  Stages are aligned to 128 bytes: 16 bytes off,
 // the copies of the same kernel were 5% slower (1M e4m3 tokens, 8 heads: 329 against 316 us).
-template <bool E4M3_, bool WIDE_, bool CLUSTER = false>
+template <bool ROW8_, bool WIDE_, bool CLUSTER = false, bool I8_ = false>
 struct Tile {
-    static constexpr bool E4M3 = E4M3_, WIDE = WIDE_;
+    static constexpr bool ROW8 = ROW8_, WIDE = WIDE_, I8 = I8_;  // 8-bit rows (e4m3 or int8); up to 16 columns; int8
     // A unit's first tile is looked at before its products, where a warp has one tile or a few (1000 tokens: 5.6 us
     // against 5.8 after them); elsewhere that would cost registers (8 x 16-64K, 32 KV heads: 403 against 381).
     static constexpr bool EARLY = CLUSTER;
-    static constexpr int BLK = E4M3 ? 2 : 1;              // blocks of 16 rows per warp
+    static constexpr int BLK = ROW8 ? 2 : 1;              // blocks of 16 rows per warp
     static constexpr int WROWS = 16 * BLK;                // rows per warp
     static constexpr int ROWS = CT_WARPS * WROWS;
     // Three CTAs per SM, but two of the wide e4m3 form: it is bound by the latencies of its
     // longer chains, which 255 registers (32 rows a warp in flight, no spills) hide better than
     // a third CTA (16 heads, 512K: 204 us against 231 with three CTAs and 16 rows a warp).
-    static constexpr int PER_SM = CLUSTER ? CL_PER_SM : E4M3 && WIDE ? 2 : 3;
-    static constexpr int ROW = E4M3 ? MOG_D : 2 * MOG_D;  // bytes
+    static constexpr int PER_SM = CLUSTER ? CL_PER_SM : ROW8 && WIDE ? 2 : 3;
+    static constexpr int ROW = ROW8 ? MOG_D : 2 * MOG_D;  // bytes
     static constexpr int KV = ROWS * ROW;                 // bytes of the K or V tile: 16 KB
     static constexpr int AUX = 2 * KV;                    // K scales, V scales
-    static constexpr int MASK = AUX + (E4M3 ? 2 * ROWS * 4 : 0);  // bit per row
+    static constexpr int MASK = AUX + (ROW8 ? 2 * ROWS * 4 : 0);  // bit per row
     static constexpr int STAGE = MASK + 128;              // rows stay aligned to 128 bytes
-    static constexpr int STAGES = CLUSTER ? CL_STAGES : E4M3 && WIDE ? 3 : 2;   // 32 KB each: 96 KB or more in flight per SM
+    static constexpr int STAGES = CLUSTER ? CL_STAGES : ROW8 && WIDE ? 3 : 2;   // 32 KB each: 96 KB or more in flight per SM
     static constexpr int COLS = WIDE ? 16 : 8;
     static constexpr int XCH = 2 * COLS * MOG_D * 4;      // two warps' accumulators, in a consumed stage
     // a cluster's CTA leaves its partial behind that in stage 0, or behind the stages
@@ -94,6 +95,7 @@ struct CacheArgs {
     const float *ks, *vs;
     int64_t sb, sh, sn;     // bytes between pages (or sequences), heads, rows
     int64_t ssb, ssh, ssn;  // the same of the scales, in floats
+    int sshift;             // log2 of the rows of a scale (int8; else 0)
     const int *bt;
     int pshift, pps, n_pages;
     const int *lengths;
@@ -194,13 +196,13 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int src
 // Shared-memory position of a 16-byte chunk of a row, conflict-free for the readers.  e4m3
 // (128-byte rows): K is read at rows r, r+1 and chunks t (t < 4), V at rows 0, 2, 4, 6 (+1,
 // +8) and two neighbouring chunks.  bf16 (256-byte rows): ldmatrix.
-template <bool E4M3>
+template <bool ROW8>
 __device__ __forceinline__ uint32_t swz_k(int row, int ch) {
-    return E4M3 ? (uint32_t)(row * MOG_D + ((ch ^ ((row & 1) << 2)) << 4)) : swz(row, ch);
+    return ROW8 ? (uint32_t)(row * MOG_D + ((ch ^ ((row & 1) << 2)) << 4)) : swz(row, ch);
 }
-template <bool E4M3>
+template <bool ROW8>
 __device__ __forceinline__ uint32_t swz_v(int row, int ch) {
-    return E4M3 ? (uint32_t)(row * MOG_D + ((ch ^ (row & 6)) << 4)) : swz(row, ch);
+    return ROW8 ? (uint32_t)(row * MOG_D + ((ch ^ (row & 6)) << 4)) : swz(row, ch);
 }
 
 // Page of the tile's 16-row group `lane`, loaded one tile ahead of its use (unchecked: a
@@ -218,7 +220,7 @@ __device__ __forceinline__ void tile_page(const CacheArgs &a, const Cursor<T::RO
 // masked; they are never read.
 template <class T, bool PAGED>
 __device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<T::ROWS> &c, int pg, uint32_t stage) {
-    constexpr bool E4M3 = T::E4M3;
+    constexpr bool ROW8 = T::ROW8;
     constexpr int CH = T::ROW / 16;        // chunks per row
     constexpr int RP = CT_THREADS / CH;    // rows per instruction: 16 or 8
     const int tid = threadIdx.x, lane = tid & 31, ch = tid % CH, r0 = tid / CH;
@@ -234,16 +236,16 @@ __device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<T::ROWS> 
         if (PAGED) off += page * a.sb;
         off = ok ? off : 0;
         const int bytes = ok ? 16 : 0;
-        cp_async16(stage + swz_k<E4M3>(r, ch), a.K + off, bytes);
-        cp_async16(stage + T::KV + swz_v<E4M3>(r, ch), a.V + off, bytes);
+        cp_async16(stage + swz_k<ROW8>(r, ch), a.K + off, bytes);
+        cp_async16(stage + T::KV + swz_v<ROW8>(r, ch), a.V + off, bytes);
     }
     // thread r: row r's scales and whether it is there
     if (tid >= T::ROWS) return;
     const int page = PAGED ? __shfl_sync(0xffffffffu, pg, tid / 16) : c.b;
     const bool ok = tid < left && (!PAGED || (unsigned)page < (unsigned)a.n_pages);
-    if (E4M3) {
-        const int64_t row = PAGED ? (first + tid) & pmask : first + tid;
-        const int64_t so = ok ? page * a.ssb + c.h * a.ssh + row * a.ssn : 0;
+    if (ROW8) {
+        const int row = PAGED ? (first + tid) & pmask : first + tid;
+        const int64_t so = ok ? page * a.ssb + c.h * a.ssh + (int64_t)(T::I8 ? row >> a.sshift : row) * a.ssn : 0;
         cp_async4(stage + T::AUX + 4 * tid, a.ks + so, ok ? 4 : 0);
         cp_async4(stage + T::AUX + 4 * (T::ROWS + tid), a.vs + so, ok ? 4 : 0);
     }
@@ -296,7 +298,7 @@ typedef uint4 QShared[8][32];
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // One column's fragment pieces: this lane's dimensions of each of the 8 steps.
-template <bool E4M3, bool DIFF, bool WIDE>
+template <bool ROW8, bool DIFF, bool WIDE>
 __device__ __forceinline__ float load_column(uint32_t (&w)[8][2], const CacheArgs &a, int unit, int c) {
     const int t = threadIdx.x & 3;
     int map, head;
@@ -304,7 +306,7 @@ __device__ __forceinline__ float load_column(uint32_t (&w)[8][2], const CacheArg
     const bool have = head < a.G;
     unit = min(unit, a.batch * a.h_kv - 1);  // (lengths that change under a call must not lead out of q)
     const uint16_t *row = a.q + ((int64_t)unit * a.G + (have ? head : 0)) * MOG_D;
-    if (!E4M3) {
+    if (!ROW8) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
             const bool use = have && (!DIFF || (ks >> 2) == map);
@@ -346,10 +348,10 @@ __device__ __forceinline__ float load_column(uint32_t (&w)[8][2], const CacheArg
 }
 
 // (wide: the caller puts a CTA barrier between the last reads of qs, this, and the next reads)
-template <bool E4M3, bool DIFF, bool WIDE>
+template <bool ROW8, bool DIFF, bool WIDE>
 __device__ __forceinline__ void load_q(QF &qf, QShared &qs, const CacheArgs &a, int unit) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const float f = load_column<E4M3, DIFF, WIDE>(qf.b, a, unit, g);
+    const float f = load_column<ROW8, DIFF, WIDE>(qf.b, a, unit, g);
     if (!WIDE) {
         qf.f[0] = __shfl_sync(0xffffffffu, f, 8 * t);
         qf.f[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
@@ -357,7 +359,7 @@ __device__ __forceinline__ void load_q(QF &qf, QShared &qs, const CacheArgs &a, 
     }
     uint32_t w[8][2];
     qf.f[0] = f;
-    qf.f[1] = load_column<E4M3, DIFF, WIDE>(w, a, unit, g + 8);
+    qf.f[1] = load_column<ROW8, DIFF, WIDE>(w, a, unit, g + 8);
     if (threadIdx.x < 32) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) qs[ks][lane] = make_uint4(qf.b[ks][0], w[ks][0], qf.b[ks][1], w[ks][1]);
@@ -371,13 +373,24 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <bool E4M3>
+template <bool ROW8>
 __device__ __forceinline__ void mma_t(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if (E4M3) mma_f16(d, a, b0, b1);
+    if (ROW8) mma_f16(d, a, b0, b1);
     else mma_bf16(d, a, b0, b1);
 }
-// four e4m3 bytes -> two fp16 pairs (exact)
+// four 8-bit codes -> two fp16 pairs (exact).  int8: u = code + 128 is the low byte of the fp16 number
+// 1024 + u, from which 1152 is taken.
+template <bool I8>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if (I8) {
+        w ^= 0x80808080u;
+        lo = __byte_perm(w, 0x64646464u, 0x4140);
+        hi = __byte_perm(w, 0x64646464u, 0x4342);
+        const uint32_t bias = 0x64806480u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(lo), "r"(bias));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(hi), "r"(bias));
+        return;
+    }
     asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
@@ -389,9 +402,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // The largest part of (x, y) that 16 bits hold, and what is left.
-template <bool E4M3>
+template <bool ROW8>
 __device__ __forceinline__ uint32_t part16(float &x, float &y) {
-    if (E4M3) {
+    if (ROW8) {
         const __half2 h = __floats2half2_rn(x, y);
         const float2 f = __half22float2(h);
         x -= f.x, y -= f.y;
@@ -416,14 +429,14 @@ __device__ __forceinline__ float2 lds8(uint32_t addr) {
 
 // 16 rows by 16 dimensions of K: {rows g | rows g+8} x {dimension pairs 0 | 1} of step ks, as
 // the operand with rows in M; its halves (0, 2) and (1, 3) are the two with 8 rows in N.
-template <bool E4M3>
+template <bool ROW8, bool I8>
 __device__ __forceinline__ void k_frag(uint32_t (&a)[4], uint32_t sk, int ks, const uint4 &wa, const uint4 &wb) {
-    if (E4M3) {
-        widen(word(wa, ks & 3), a[0], a[2]);
-        widen(word(wb, ks & 3), a[1], a[3]);
+    if (ROW8) {
+        widen<I8>(word(wa, ks & 3), a[0], a[2]);
+        widen<I8>(word(wb, ks & 3), a[1], a[3]);
     } else {
         const int lane = threadIdx.x & 31, mat = lane >> 3, r8 = lane & 7;
-        ldsm_x4(sk + swz_k<E4M3>((mat & 1) * 8 + r8, 2 * ks + (mat >> 1)), a[0], a[1], a[2], a[3]);
+        ldsm_x4(sk + swz_k<ROW8>((mat & 1) * 8 + r8, 2 * ks + (mat >> 1)), a[0], a[1], a[2], a[3]);
     }
 }
 
@@ -452,7 +465,7 @@ __device__ __forceinline__ int scale_floor(int hi) { return (max((hi >> 23) + 1,
 // e4m3, a tile's value rows: zero: is row `lane` all zeros (with a finite scale);  hi: the bits of the largest
 // finite scale.  If the tile is a unit's first, without rows of zeros, and its scales are in order,
 // they set the range (true).
-template <bool WIDE>
+template <bool WIDE, bool I8>
 __device__ __forceinline__ bool first_tile(State<WIDE> &st, int mine, bool there, uint32_t sv, bool &zero, int &hi) {
     const int lane = threadIdx.x & 31;
     uint32_t any = 0;
@@ -461,7 +474,7 @@ __device__ __forceinline__ bool first_tile(State<WIDE> &st, int mine, bool there
         const uint4 x = lds16(sv + lane * MOG_D + (((ch + lane) & 7) << 4));
         any |= x.x | x.y | x.z | x.w;
     }
-    zero = (any & 0x7f7f7f7fu) == 0 && mine < F32_INF;
+    zero = (any & (I8 ? 0xffffffffu : 0x7f7f7f7fu)) == 0 && mine < F32_INF;
     hi = __reduce_max_sync(0xffffffffu, mine < F32_INF ? mine : 0);
     if (st.vlo == V_NONE && hi - __reduce_min_sync(0xffffffffu, there ? mine : F32_INF) <= V_RANGE &&
         !__any_sync(0xffffffffu, there && zero)) {
@@ -486,12 +499,12 @@ template <class T, int NS>
 __device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T::BLK][NS], float (&mx)[2], int mine,
                                          bool there, uint32_t sv, uint32_t vsc) {
     constexpr bool WIDE = T::WIDE;
-    static_assert(!T::E4M3 || T::WROWS == 32, "a lane per row");
+    static_assert(!T::ROW8 || T::WROWS == 32, "a lane per row");
     const int lane = threadIdx.x & 31;
     st.rise = 0.f;
     bool zero;
     int hi;
-    if (first_tile(st, mine, there, sv, zero, hi) && !T::EARLY) return;
+    if (first_tile<WIDE, T::I8>(st, mine, there, sv, zero, hi) && !T::EARLY) return;
     if (zero) asm volatile("st.shared.u32 [%0], %1;" ::"r"(vsc + 4 * lane), "r"(0) : "memory");
     hi = __reduce_max_sync(0xffffffffu, mine < F32_INF && !zero ? mine : 0);
     __syncwarp();
@@ -552,7 +565,7 @@ __device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T:
 // it): summing a 1M-token sequence on the tensor cores alone drifted by 1.1e-5.
 template <class T, bool DIFF, int PARTS>
 __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const QShared &qs, uint32_t stage) {
-    constexpr bool E4M3 = T::E4M3, WIDE = T::WIDE;
+    constexpr bool ROW8 = T::ROW8, WIDE = T::WIDE;
     constexpr int BLK = T::BLK;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, mat = lane >> 3, r8 = lane & 7;
     const int wr = (threadIdx.x >> 5) * T::WROWS;  // this warp's first row (a multiple of 16)
@@ -563,11 +576,11 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 
     int mine = 0;  // e4m3: the bits of the value scale of row `lane`
     bool fresh = false;
-    if (E4M3 && T::EARLY) {
+    if (ROW8 && T::EARLY) {
         mine = __float_as_int(lds4(sc + 4 * (T::ROWS + lane))) & 0x7fffffff;
         bool zero;
         int hi;
-        if (st.vlo == V_NONE) fresh = first_tile(st, mine, (rows >> lane) & 1u, sv, zero, hi);
+        if (st.vlo == V_NONE) fresh = first_tile<WIDE, T::I8>(st, mine, (rows >> lane) & 1u, sv, zero, hi);
     }
 
     // Logits s[blk][i]: narrow: rows g (i = 0, 1) and g+8 (2, 3) of columns 2t, 2t+1 (even and
@@ -581,11 +594,11 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint4 wa[BLK], wb[BLK];
-            if (E4M3) {
+            if (ROW8) {
 #pragma unroll
                 for (int blk = 0; blk < BLK; ++blk) {
-                    wa[blk] = lds16(sk + swz_k<E4M3>(16 * blk + g, t + 4 * j));
-                    wb[blk] = lds16(sk + swz_k<E4M3>(16 * blk + g + 8, t + 4 * j));
+                    wa[blk] = lds16(sk + swz_k<ROW8>(16 * blk + g, t + 4 * j));
+                    wb[blk] = lds16(sk + swz_k<ROW8>(16 * blk + g + 8, t + 4 * j));
                 }
             }
 #pragma unroll
@@ -597,13 +610,13 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
                 for (int blk = 0; blk < BLK; ++blk) {
                     uint32_t a[4];
-                    k_frag<E4M3>(a, sk, ks, wa[blk], wb[blk]);
+                    k_frag<ROW8, T::I8>(a, sk, ks, wa[blk], wb[blk]);
                     float (&dd)[NS] = d[blk][acc];
                     if (WIDE) {
-                        mma_t<E4M3>(reinterpret_cast<float (&)[4]>(dd[0]), qa, a[0], a[2]);
-                        mma_t<E4M3>(reinterpret_cast<float (&)[4]>(dd[NS - 4]), qa, a[1], a[3]);
+                        mma_t<ROW8>(reinterpret_cast<float (&)[4]>(dd[0]), qa, a[0], a[2]);
+                        mma_t<ROW8>(reinterpret_cast<float (&)[4]>(dd[NS - 4]), qa, a[1], a[3]);
                     } else {
-                        mma_t<E4M3>(reinterpret_cast<float (&)[4]>(dd[0]), a, qf.b[ks][0], qf.b[ks][1]);
+                        mma_t<ROW8>(reinterpret_cast<float (&)[4]>(dd[0]), a, qf.b[ks][0], qf.b[ks][1]);
                     }
                 }
             }
@@ -623,15 +636,15 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
         float k[4];  // scales of this lane's rows of the block (narrow: two of them)
-        if (E4M3 && WIDE) {
+        if (ROW8 && WIDE) {
             const float2 x = lds8(sc + 4 * (16 * blk + 2 * t)), y = lds8(sc + 4 * (16 * blk + 2 * t + 8));
             k[0] = x.x, k[1] = x.y, k[2] = y.x, k[3] = y.y;
-        } else if (E4M3) {
+        } else if (ROW8) {
             k[0] = lds4(sc + 4 * (16 * blk + g)), k[1] = lds4(sc + 4 * (16 * blk + g + 8));
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const float kk = E4M3 ? k[WIDE ? (i & 1) + 2 * (i >> 2) : i >> 1] : 1.f;
+            const float kk = ROW8 ? k[WIDE ? (i & 1) + 2 * (i >> 2) : i >> 1] : 1.f;
             s[blk][i] *= kk * qf.f[colof(i)];
         }
     }
@@ -656,7 +669,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
         mx[c] = column_max<WIDE>(mx[c]);
     }
     float inv = 0.f;
-    if (E4M3) {
+    if (ROW8) {
         if (!T::EARLY) mine = __float_as_int(lds4(sc + 4 * (T::ROWS + lane))) & 0x7fffffff;
         const bool there = (rows >> lane) & 1u;
         // (infinite at first)
@@ -678,10 +691,10 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
         float v[4];
-        if (E4M3 && WIDE) {
+        if (ROW8 && WIDE) {
             const float2 x = lds8(sc + 4 * (T::ROWS + 16 * blk + 2 * t)), y = lds8(sc + 4 * (T::ROWS + 16 * blk + 2 * t + 8));
             v[0] = x.x * inv, v[1] = x.y * inv, v[2] = y.x * inv, v[3] = y.y * inv;
-        } else if (E4M3) {
+        } else if (ROW8) {
             v[0] = lds4(sc + 4 * (T::ROWS + 16 * blk + g)) * inv, v[1] = lds4(sc + 4 * (T::ROWS + 16 * blk + g + 8)) * inv;
         }
 #pragma unroll
@@ -689,13 +702,13 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
             float x = ex2(s[blk][i] - sh[colof(i)]), y = ex2(s[blk][i + 1] - sh[colof(i + 1)]);
             st.l[colof(i)] += x;
             st.l[colof(i + 1)] += y;
-            if (E4M3) {
+            if (ROW8) {
                 x *= v[WIDE ? 2 * (i >> 2) : i >> 1];
                 y *= v[WIDE ? 1 + 2 * (i >> 2) : i >> 1];
             }
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
-                const uint32_t h = part16<E4M3>(x, y);
+                const uint32_t h = part16<ROW8>(x, y);
                 pf[blk][k][i / 2] = WIDE ? h : movmatrix_t(h);
             }
         }
@@ -711,10 +724,10 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
             for (int k = PARTS - 1; k >= 0; --k) {
                 if (WIDE) {
                     const uint32_t p[4] = {pf[blk][k][0], pf[blk][k][1], pf[blk][k][NS / 2 - 2], pf[blk][k][NS / 2 - 1]};
-                    mma_t<E4M3>(d[0], p, a[blk][0], a[blk][2]);
-                    mma_t<E4M3>(d[WIDE ? 1 : 0], p, a[blk][1], a[blk][3]);
+                    mma_t<ROW8>(d[0], p, a[blk][0], a[blk][2]);
+                    mma_t<ROW8>(d[WIDE ? 1 : 0], p, a[blk][1], a[blk][3]);
                 } else {
-                    mma_t<E4M3>(d[0], a[blk], pf[blk][k][0], pf[blk][k][1]);
+                    mma_t<ROW8>(d[0], a[blk], pf[blk][k][0], pf[blk][k][1]);
                 }
             }
 #pragma unroll
@@ -725,7 +738,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
                 o = fmaf(o, al[State<WIDE>::col(e)], d[k][e]);
             }
     };
-    if (E4M3) {
+    if (ROW8) {
         // rows 2t, 2t+1, 2t+8, 2t+9 of a block, dimensions 16g .. 16g+15: word w holds
         // dimensions 16g + 4w .. +3, the sets 0 and 1 of mt = 2w, then of 2w + 1
         uint4 x[BLK][4];
@@ -733,15 +746,15 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
         for (int blk = 0; blk < BLK; ++blk)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[blk][i] = lds16(sv + swz_v<E4M3>(16 * blk + 2 * t + (i & 1) + 8 * (i >> 1), g));
+                x[blk][i] = lds16(sv + swz_v<ROW8>(16 * blk + 2 * t + (i & 1) + 8 * (i >> 1), g));
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
             uint32_t a[BLK][4];
 #pragma unroll
             for (int blk = 0; blk < BLK; ++blk) {
-                widen(__byte_perm(word(x[blk][0], mt >> 1), word(x[blk][1], mt >> 1), sel), a[blk][0], a[blk][1]);
-                widen(__byte_perm(word(x[blk][2], mt >> 1), word(x[blk][3], mt >> 1), sel), a[blk][2], a[blk][3]);
+                widen<T::I8>(__byte_perm(word(x[blk][0], mt >> 1), word(x[blk][1], mt >> 1), sel), a[blk][0], a[blk][1]);
+                widen<T::I8>(__byte_perm(word(x[blk][2], mt >> 1), word(x[blk][3], mt >> 1), sel), a[blk][2], a[blk][3]);
             }
             add(mt, a);
         }
@@ -749,7 +762,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             uint32_t a[BLK][4];
-            ldsm_x4_t(sv + swz_v<E4M3>((mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0][0], a[0][1], a[0][2], a[0][3]);
+            ldsm_x4_t(sv + swz_v<ROW8>((mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0][0], a[0][1], a[0][2], a[0][3]);
             add(mt, a);
         }
     }
@@ -801,12 +814,12 @@ __device__ __forceinline__ void state_fold(State<WIDE> &st, const float *x, cons
 
 template <class T, bool DIFF>
 __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex, const CacheArgs &a, float *dst) {
-    constexpr bool E4M3 = T::E4M3, WIDE = T::WIDE;
+    constexpr bool ROW8 = T::ROW8, WIDE = T::WIDE;
     using S = State<WIDE>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     constexpr int SW = S::NT * 4 * 32;  // words of a warp's accumulators
     static_assert(T::XCH == 2 * SW * 4 && T::AUX >= T::XCH, "two states fit in a stage");
-    if (E4M3) {  // to the values' own unit
+    if (ROW8) {  // to the values' own unit
         const float u = pow2f(st.vlo == V_NONE ? 0 : st.ve() - W_EXP);
 #pragma unroll
         for (int i = 0; i < S::NT; ++i)
@@ -839,8 +852,8 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
         if (WIDE) {
             // o[2 mt + k][2c + e]: e4m3: dimension 16(2t + e) + 2 mt + k; bf16: 16 mt + 8 k + 2t + e
 #pragma unroll
-            for (int i = 0; i < S::NT; i += E4M3 ? 4 : 1) {
-                if (E4M3) {
+            for (int i = 0; i < S::NT; i += ROW8 ? 4 : 1) {
+                if (ROW8) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         *reinterpret_cast<float4 *>(r + 16 * (2 * t + e) + i) =
@@ -854,7 +867,7 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
             // o[mt][c + 2 k]: e4m3: dimension 16 g + 2 mt + k; bf16: 16 mt + 8 k + g
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (E4M3) {
+                if (ROW8) {
                     *reinterpret_cast<float2 *>(r + 16 * g + 2 * i) = make_float2(st.o[i][c], st.o[i][c + 2]);
                 } else {
                     r[16 * i + g] = st.o[i][c];
@@ -963,13 +976,13 @@ __device__ __forceinline__ void cluster_end(const CacheArgs &a, const DiffArgs &
 
 // CLUSTER: the form with a cluster of a.cs CTAs per unit (a kernel of its own: the two in one cost
 // the split form registers and 14% of its speed).
-template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, bool BF16OUT, bool CLUSTER>
-__global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
+template <bool ROW8, bool WIDE, bool PAGED, bool DIFF, bool BF16OUT, bool CLUSTER, bool I8>
+__global__ void __launch_bounds__(CT_THREADS, Tile<ROW8, WIDE, CLUSTER, I8>::PER_SM) k_cache_split(CacheArgs a, DiffArgs d, void *out) {
     extern __shared__ __align__(128) uint8_t csm[];
     __shared__ Exchange ex;
     __shared__ QShared qs;  // (wide)
-    using T = Tile<E4M3, WIDE, CLUSTER>;
-    constexpr int PARTS = weight_parts(E4M3, WIDE, BF16OUT);
+    using T = Tile<ROW8, WIDE, CLUSTER, I8>;
+    constexpr int PARTS = weight_parts(ROW8, WIDE, BF16OUT);
     const uint32_t stages = smem_u32(csm);
     const int G2 = DIFF ? 2 * a.G : a.G;
     Cursor<T::ROWS> ci, cc;  // the next tile to copy, the next to compute
@@ -1016,7 +1029,7 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
     for (int s = 0; s < T::STAGES - 1; ++s) feed(stages + s * T::STAGE);
     int unit = cc.b * a.h_kv + cc.h;
     QF qf;
-    load_q<E4M3, DIFF, WIDE>(qf, qs, a, unit);
+    load_q<ROW8, DIFF, WIDE>(qf, qs, a, unit);
     State<WIDE> st;
     st.init();
     int slot = 0;
@@ -1037,17 +1050,18 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<E4M3, WIDE, CLUSTER>::PER_SM)
         if (!CLUSTER) cc.next(a);
         if (end) {
             unit = cc.b * a.h_kv + cc.h;
-            load_q<E4M3, DIFF, WIDE>(qf, qs, a, unit);
+            load_q<ROW8, DIFF, WIDE>(qf, qs, a, unit);
         }
     }
     cp_async_wait<0>();
     if (CLUSTER) cluster_end<T, DIFF, BF16OUT>(a, d, out, stages, unit);
 }
 
-template <bool E4M3, bool WIDE, bool PAGED, bool DIFF, bool BF16OUT>
+template <bool ROW8, bool WIDE, bool PAGED, bool DIFF, bool BF16OUT, bool I8>
 static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out, int splits, cudaStream_t s) {
-    const int smem = a.cs ? Tile<E4M3, WIDE, true>::SMEM : Tile<E4M3, WIDE>::SMEM;
-    const auto fn = a.cs ? k_cache_split<E4M3, WIDE, PAGED, DIFF, BF16OUT, true> : k_cache_split<E4M3, WIDE, PAGED, DIFF, BF16OUT, false>;
+    const int smem = a.cs ? Tile<ROW8, WIDE, true>::SMEM : Tile<ROW8, WIDE>::SMEM;
+    const auto fn = a.cs ? k_cache_split<ROW8, WIDE, PAGED, DIFF, BF16OUT, true, I8>
+                         : k_cache_split<ROW8, WIDE, PAGED, DIFF, BF16OUT, false, I8>;
     const cudaError_t e = ensure_smem((const void *)fn, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1066,15 +1080,17 @@ static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out
 
 // The instance for a call: launches it (a.cs > 0: as clusters, one launch; else the split of
 // `splits` CTAs, whose partials k_cache_merge folds).
-template <bool E4M3, bool DIFF, bool BF16OUT>
+template <bool ROW8, bool DIFF, bool BF16OUT, bool I8 = false>
 static cudaError_t pick_split(const CacheArgs &a, const DiffArgs &d, void *out, bool wide, int splits, cudaStream_t s) {
-    if (a.bt) return wide ? launch_split<E4M3, true, true, DIFF, BF16OUT>(a, d, out, splits, s)
-                          : launch_split<E4M3, false, true, DIFF, BF16OUT>(a, d, out, splits, s);
-    return wide ? launch_split<E4M3, true, false, DIFF, BF16OUT>(a, d, out, splits, s)
-                : launch_split<E4M3, false, false, DIFF, BF16OUT>(a, d, out, splits, s);
+    if (a.bt) return wide ? launch_split<ROW8, true, true, DIFF, BF16OUT, I8>(a, d, out, splits, s)
+                          : launch_split<ROW8, false, true, DIFF, BF16OUT, I8>(a, d, out, splits, s);
+    return wide ? launch_split<ROW8, true, false, DIFF, BF16OUT, I8>(a, d, out, splits, s)
+                : launch_split<ROW8, false, false, DIFF, BF16OUT, I8>(a, d, out, splits, s);
 }
 
 cudaError_t launch_split8(const CacheArgs &a, const DiffArgs &d, void *out, bool diff, bool bf_out, bool wide, int splits,
                           cudaStream_t s);
+cudaError_t launch_spliti8(const CacheArgs &a, const DiffArgs &d, void *out, bool diff, bool bf_out, bool wide, int splits,
+                           cudaStream_t s);
 
 }  // namespace mog

@@ -153,6 +153,20 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
 cudaError_t launch_kv_store(const mog_cache *c, int batch, int h_kv, int t_max, const int32_t *pos,
                             const int32_t *count, const void *kn, const void *vn, int64_t nb, int64_t nt,
                             int64_t nh, cudaStream_t s);
+// Rows of new tokens: queries in and out, keys and values; strides in elements between sequences,
+// tokens and heads.  rope may be null (stores), k and v too (rotary positions alone).
+struct RowsIn {
+    const void *q, *k, *v;
+    void *qo;
+    int64_t qs[3], os[3], ks[3];
+    int h_q, h_kv, t_max;
+    const int32_t *pos, *count;
+    int each, inverse;
+    const mog_rope *rope;
+};
+cudaError_t launch_rope(const mog_cache *c, int batch, const RowsIn &r, cudaStream_t s);     // not int8 caches
+cudaError_t launch_rows_i8(const mog_cache *c, int batch, const RowsIn &r, cudaStream_t s);  // with or without rope
+cudaError_t launch_kv_load(const mog_cache *c, int batch, const RowsIn &r, void *ko, void *vo, cudaStream_t s);
 enum { PAGES_FULL = 1, PAGES_BAD_INDEX = 2 };  // status bits of a pages work buffer
 size_t pages_work_ints(int n_pages, int batch);
 cudaError_t launch_pages_assign(const mog_pages *p, const int32_t *src, cudaStream_t s);
