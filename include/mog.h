@@ -567,6 +567,30 @@ int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_ma
                     void *scratch_dev, size_t scratch_bytes, void *stream);
 
 /*
+ * Cross attention: t_max query tokens of each sequence, or one, to the rows [0, N_b) of a bf16
+ * cache, all of which every one of them sees: out = softmax(tau q.K^T) V per token and head, tau =
+ * 1/sqrt(d).  A sequence without rows, and a query whose logits are all -infinity, give zeros.
+ *  c           : MOG_CACHE_BF16, strides below 2^39 elements; stride_b = 0: the same rows for every
+ *                sequence
+ *  lengths_dev : int32[batch] on the device, clamped to [0, n_max]; n_max <= the cache's positions
+ *  count_dev   : int32[batch] query tokens, clamped to [0, t_max], or NULL: t_max each.  Rows of
+ *                out behind them are left as they are
+ *  q_dev, out_dev : bf16, element (b, t, h, j) at b*s[0] + t*s[1] + h*s[2] + j, strides multiples of
+ *                8, 16-byte aligned; they must not overlap
+ *  scratch_dev : at least mog_cross_scratch_bytes() bytes, 16-byte aligned (0 bytes: may be NULL), no
+ *                initial contents needed, not shared by calls that overlap on the GPU
+ * Products of bf16 with fp32 sums; the weights are rounded to bf16 for the second one, an error of the
+ * size of the output's own rounding.  d must be 128, h_q / h_kv <= 16, batch * h_kv <= 65535, t_max *
+ * h_q <= 2^30, n_max <= 2^30.  Should a bounded wait inside the kernel run out, its rows are NaN.
+ */
+int mog_cross_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max,
+                            int32_t n_max, size_t *bytes);
+int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                     int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev,
+                     const void *q_dev, const int64_t *q_strides, void *out_dev,
+                     const int64_t *out_strides, void *scratch_dev, size_t scratch_bytes, void *stream);
+
+/*
  * Write new keys and values into a cache: token t < count[b] of sequence b goes to position
  * pos[b] + t.  Positions outside the cache, or in no page, are left out.
  *  pos_dev, count_dev   : int32[batch] on the device; count NULL: t_max for every sequence

@@ -354,6 +354,8 @@ _SIGS = {
     "mog_diff_decode_scratch_bytes": (C.c_int, [C.c_int32] * 5 + [_P]),
     "mog_diff_decode": (C.c_int, [_P, _P] + [C.c_int32] * 5 + [_P, _P, _P, C.c_int32, _P, C.c_size_t, _P]),
     "mog_kv_store": (C.c_int, [_P] + [C.c_int32] * 4 + [_P] * 4 + [C.c_int64] * 3 + [_P]),
+    "mog_cross_scratch_bytes": (C.c_int, [C.c_int32] * 6 + [_P]),
+    "mog_cross_attend": (C.c_int, [_P, _P] + [C.c_int32] * 6 + [_P] * 6 + [C.c_size_t, _P]),
     "mog_kv_load": (C.c_int, [_P] + [C.c_int32] * 4 + [_P] * 4 + [C.c_int64] * 3 + [_P]),
     "mog_rope_apply": (C.c_int, [_P] + [C.c_int32] * 4 + [_P, C.c_int32, _P, C.c_int32] + [_P] * 5),
     "mog_rope_store": (C.c_int, [_P, _P] + [C.c_int32] * 5 + [_P] * 10),
@@ -807,6 +809,72 @@ def dense8_scratch_bytes(batch, h_kv, h_q, n_max) -> int:
     """Bytes of dense_decode's scratch over an 8-bit cache, on the current device."""
     return _scratch_bytes("dense_decode8", batch, h_kv, h_q, n_max, _torch().cuda.current_device()
                           if _torch().cuda.is_available() else -1)
+
+
+@functools.lru_cache(maxsize=512)
+def _cross_scratch(B, H_kv, H_q, T, n_max, dev_index) -> int:
+    need = C.c_size_t(0)
+    _check(lib().mog_cross_scratch_bytes(B, H_kv, H_q, 128, T, n_max, C.byref(need)), "mog_cross_attend")
+    return need.value
+
+
+def cross_scratch_bytes(batch, h_kv, h_q, t_max, n_max) -> int:
+    """Bytes of cross_attend's scratch on the current device."""
+    return _cross_scratch(batch, h_kv, h_q, t_max, n_max, _torch().cuda.current_device()
+                          if _torch().cuda.is_available() else -1)
+
+
+def cross_attend(K, V, lengths_dev, n_max, q, count=None, out=None, scratch=None, stream=None):
+    """Cross attention (mog_cross_attend): q bf16 [B, T, H_q, 128], T query tokens of each sequence (any
+    strides of whole 16-byte chunks, last dim contiguous), to the rows [0, lengths_dev[b]) of a bf16
+    cache, K, V [B, H_kv, n_cap, 128] (expanded over the batch, too) or K a PagedKV; every token sees every row.
+    count: int32 [B] query tokens of each sequence, or None for T; rows of out behind them are not
+    written.  out: bf16 like q, a new tensor by default.  8-bit caches: dense_decode for one token,
+    kv_load for more.  -> out."""
+    torch = _torch()
+    if isinstance(K, _ROWS8):
+        raise ValueError("cross_attend reads bf16 caches: dense_decode takes 8-bit ones for one token, kv_load reads them back")
+    c, B, H_kv, positions, dev = _cache(K, V)
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return cross_attend(K, V, lengths_dev, n_max, q, count, out, scratch)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != 128:
+        raise ValueError(f"q must be a bf16 tensor [{B}, T, H_q, 128] on the cache's device")
+    shape = q.shape
+    T, H_q = shape[1], shape[2]
+    qs = _row_strides(q, shape, dev, "q")
+    _check_counts(lengths_dev, B, dev, "lengths_dev")
+    if count is not None:
+        _check_counts(count, B, dev, "count")
+    if not 1 <= n_max <= positions:
+        raise ValueError(f"n_max must be between 1 and the cache's {positions} positions")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    os_ = _row_strides(out, shape, dev, "out", True)
+    if T == 0 or B == 0:
+        return out
+    nbytes = _cross_scratch(B, H_kv, H_q, T, n_max, dev.index)
+    own = None
+    if scratch is None:
+        if nbytes:
+            own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+        at = own
+    elif scratch.device != dev or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous tensor on the cache's device")
+    else:
+        nbytes = scratch.numel() * scratch.element_size()
+        at = scratch.data_ptr()
+    try:
+        rc = lib().mog_cross_attend(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, T,
+                                    None if count is None else count.data_ptr(), q.data_ptr(), _strides3(qs),
+                                    out.data_ptr(), _strides3(os_), at, nbytes, s)
+    finally:
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+    if rc:
+        _check(rc, "mog_cross_attend")
+    return out
 
 
 def kv_store(K, V, pos, count, k_new, v_new, stream=None):

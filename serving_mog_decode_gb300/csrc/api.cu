@@ -1025,6 +1025,39 @@ extern "C" int mog_kv_load(const mog_cache *c, int32_t batch, int32_t h_kv, int3
     return MOG_OK;
 }
 
+extern "C" int mog_cross_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max,
+                                       int32_t n_max, size_t *bytes) {
+    if (!bytes || batch <= 0 || h_kv <= 0 || h_q <= 0 || t_max <= 0 || n_max <= 0) return MOG_ERR_INVALID_ARG;
+    if (d != MOG_D || h_q % h_kv != 0 || h_q / h_kv > MOG_MAX_G) return MOG_ERR_SHAPE;
+    if (n_max > (1 << 30) || (int64_t)batch * h_kv > 65535 || (int64_t)t_max * h_q > (1 << 30)) return MOG_ERR_SHAPE;
+    *bytes = cross_scratch(batch, h_kv, h_q / h_kv, t_max, n_max);
+    return MOG_OK;
+}
+
+static int check_rows(const void *p, const int64_t *strides);
+
+extern "C" int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                                int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev,
+                                const void *q_dev, const int64_t *q_strides, void *out_dev,
+                                const int64_t *out_strides, void *scratch_dev, size_t scratch_bytes, void *stream) {
+    size_t need = 0;
+    int st = mog_cross_scratch_bytes(batch, h_kv, h_q, d, t_max, n_max, &need);
+    if (st != MOG_OK) return st;
+    if (!c || c->type != MOG_CACHE_BF16) return MOG_ERR_INVALID_ARG;
+    if ((st = check_cache(c, n_max)) != MOG_OK) return st;
+    for (int64_t x : {c->stride_b, c->stride_h, c->stride_n})
+        if (x >= (int64_t)1 << 39) return MOG_ERR_SHAPE;  // (a tensor map's strides are below 2^40 bytes)
+    if (!lengths_dev || !q_strides || !out_strides || (need && !scratch_dev)) return MOG_ERR_INVALID_ARG;
+    if ((st = check_rows(q_dev, q_strides)) != MOG_OK || (st = check_rows(out_dev, out_strides)) != MOG_OK) return st;
+    if (!aligned16(scratch_dev)) return MOG_ERR_INVALID_ARG;
+    if (scratch_bytes < need) return MOG_ERR_ARENA_TOO_SMALL;
+    RowsIn r{};
+    r.q = q_dev, r.qo = out_dev, r.h_q = h_q, r.h_kv = h_kv, r.t_max = t_max, r.count = count_dev;
+    for (int i = 0; i < 3; ++i) r.qs[i] = q_strides[i], r.os[i] = out_strides[i];
+    const cudaError_t e = launch_cross(c, lengths_dev, n_max, batch, r, static_cast<float *>(scratch_dev), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOG_OK : cuda_fail(e, "mog_cross_attend launch");
+}
+
 // ------------------------------------------------------------------------ rotary positions
 
 static int check_rope(const mog_rope *r) {

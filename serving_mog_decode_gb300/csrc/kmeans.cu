@@ -1761,12 +1761,7 @@ static AssignJob build_job(const Dev &dv, int t) {
 
 static cudaError_t set_smem(const void *fn, size_t bytes) { return ensure_smem(fn, bytes); }
 
-// cuTensorMapEncodeTiled, reached through the runtime's driver entry point.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-static EncodeTiledFn encode_fn() {
+EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static bool tried = false;
     if (!tried) {

@@ -11,6 +11,14 @@
 
 namespace mog {
 
+// cuTensorMapEncodeTiled, reached through the runtime's driver entry point (kmeans.cu); null if the
+// driver has none.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 // ------------------------------------------------------------------------- mbarriers
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

@@ -164,3 +164,25 @@ def test_int8_cache_shapes_are_checked():
             mog.KVI8(rows, rows, ks, vs, block)
     with pytest.raises(ValueError, match="CUDA int8"):
         mog.KVI8(K, K, s, s, 32)
+
+
+def test_cross_refusals(lib):
+    def cross(c=None, lengths=P, n_max=1 << 20, batch=2, h_kv=8, h_q=32, d=128, t=4, q=P, qs=S3, out=P, os_=S3, scratch=P,
+              nbytes=1 << 40):
+        c = c if c is not None else cache(type=0, k_scale=None, v_scale=None)
+        return lib.mog_cross_attend(C.byref(c), lengths, n_max, batch, h_kv, h_q, d, t, None, q, qs, out, os_, scratch,
+                                    nbytes, None)
+
+    assert cross(cache()) == ARG and cross(cache(type=0)) == ARG
+    for kw, why in [(dict(k=None), ARG), (dict(v=ODD.value), ARG), (dict(stride_n=64), SHAPE), (dict(n_cap=100), SHAPE),
+                    (dict(stride_b=1 << 39), SHAPE), (dict(stride_h=1 << 39), SHAPE), (dict(stride_n=1 << 39), SHAPE),
+                    (dict(block_table=P.value, page_rows=24, pages_per_seq=1 << 18, n_pages=4), SHAPE)]:
+        assert cross(cache(**dict(dict(type=0, k_scale=None, v_scale=None), **kw))) == why, kw
+    for kw, why in [(dict(lengths=None), ARG), (dict(n_max=0), ARG), (dict(n_max=(1 << 20) + 1), SHAPE),
+                    (dict(n_max=(1 << 30) + 1), SHAPE), (dict(batch=0), ARG), (dict(h_kv=0), ARG), (dict(h_q=0), ARG),
+                    (dict(h_q=33), SHAPE), (dict(h_kv=1, h_q=17), SHAPE), (dict(batch=8192), SHAPE), (dict(d=64), SHAPE),
+                    (dict(t=0), ARG), (dict(t=1 << 26), SHAPE), (dict(q=None), ARG), (dict(q=ODD), ARG), (dict(out=ODD), ARG),
+                    (dict(qs=S_ODD), SHAPE), (dict(os_=S_ODD), SHAPE), (dict(qs=None), ARG), (dict(scratch=None), ARG),
+                    (dict(scratch=ODD), ARG), (dict(nbytes=16), SMALL)]:
+        assert cross(**kw) == why, kw
+    assert mog.cross_scratch_bytes(8, 16, 16, 500, 1500) == 0 and mog.cross_scratch_bytes(1, 1, 1, 1, 1 << 20) > 0
