@@ -10,8 +10,8 @@
 //
 //   warps 0-3, 4-7  softmax of stream 0, 1: a thread has one query row; it reads its 128 logits from
 //                   tensor memory, takes the running maximum, and writes the weights back as bf16 where the logits were
-//   warp 8          issues the MMAs: S = Q K^T (128 x 128 x 128) and O += P V, P from tensor memory
-//   warp 9          TMA copies of K and V tiles through a ring of 32 KB slots, in the order of their use
+//   warps 8, 9      issue the MMAs of stream 0, 1: S = Q K^T (128 x 128 x 128) and O += P V, P from tensor memory
+//   warp 10         TMA copies of K and V tiles through a ring of 32 KB slots, in the order of their use
 //
 // Tensor memory holds S (then P) and O of both streams, 512 columns.  O is rescaled only when a row's
 // maximum has risen by more than 2^8 since the last time: weights are then at most 2^8, and O and
@@ -29,12 +29,15 @@ namespace mog {
 constexpr int CX_M = 128, CX_KEYS = 128;         // query rows and keys of a tile
 constexpr int CX_TILE = CX_KEYS * MOG_D * 2;     // bytes of a tile (K, V or Q): two halves of 64 dimensions
 constexpr int CX_HALF = CX_TILE / 2;
-constexpr int CX_SLOTS = 5;
-constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 9;  // (warps 10, 11 fill the third warpgroup)
+// Slots of 32 KB.  Two query tiles: one ring of five.  One query tile: its second one's place is a sixth, and
+// each stream has a ring of three of its own: a barrier's waiter has to have seen the phase before the one it
+// waits for, which a slot that the streams take in turn would not give.
+constexpr int CX_SLOTS = 6, CX_RING = 5, CX_OWN = 3;
+constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 10;  // (warp 11 fills the third warpgroup)
 // Registers: 168 a thread at launch; the softmax warps take 208, the others leave theirs at 80
 // (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
 constexpr int CX_REGS_MORE = 208, CX_REGS_LESS = 80;
-constexpr int CX_SMEM = (2 + CX_SLOTS) * CX_TILE + 1024;
+constexpr int CX_SMEM = (2 + CX_RING) * CX_TILE + 1024;
 constexpr int CX_PART = MOG_D + 4;               // floats of a partial: maximum, sum, 2 unused, accumulators
 constexpr float CX_RISE = 8.f;                   // log2 of the rise of a maximum that O is rescaled for
 
@@ -122,8 +125,21 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 struct CrossBars {
-    uint64_t full[CX_SLOTS], free[CX_SLOTS], s_full[2], p_full[2], o_full[2];
+    uint64_t full[CX_SLOTS], free[CX_SLOTS], s_full[2], p_full[2], o_full[2], v_tail;
 };
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+// Zeros in rows [row, row + n) of a tile, by a warp.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int row, int n) {
+    for (int i = row * 8 + (threadIdx.x & 31); i < (row + n) * 8; i += 32) {
+        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + 16 * i), "r"(0) : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + CX_HALF + 16 * i), "r"(0) : "memory");
+    }
+}
 
 // One output row (or partial), 32 dimensions from `c` on.
 __device__ __forceinline__ void put32(uint16_t *row, int c, const float (&v)[32]) {
@@ -150,22 +166,25 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     split_tiles(len, a.splits, split, first, nt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw = smem_u32(cx_raw);
-    const uint32_t sQ = (raw + 1023u) & ~1023u, sR = sQ + 2 * CX_TILE;
+    const uint32_t sQ = (raw + 1023u) & ~1023u, sR = sQ + (pair ? 2 : 1) * CX_TILE;
+    const int ways = pair ? 1 : 2, ring = pair ? CX_RING : CX_OWN;  // rings, and their slots
     auto bar = [&](const uint64_t &x) { return smem_u32(&x); };
     // tiles of stream s, and its j-th
     auto n_of = [&](int s) { return pair ? nt : (nt - s + 1) >> 1; };
     auto tile_of = [&](int s, int j) { return first + (pair ? j : 2 * j + s); };
+    const int tail = nt > 0 ? max(0, (first + nt) * CX_KEYS - len) : 0;  // rows of the last tile behind the sequence's end
 
     if (tid == 0) {
         for (int i = 0; i < CX_SLOTS; ++i) {
             mbar_init(bar(bars.full[i]), 1);
-            mbar_init(bar(bars.free[i]), 1);
+            mbar_init(bar(bars.free[i]), pair ? 2 : 1);  // (both streams use a tile)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(bars.s_full[i]), 1);
             mbar_init(bar(bars.p_full[i]), CX_M);
             mbar_init(bar(bars.o_full[i]), 1);
         }
+        mbar_init(bar(bars.v_tail), 1);
         fence_barrier_init();
         s_fail = 0;
     }
@@ -193,132 +212,107 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     auto tO = [&](int s) { return tmem + (uint32_t)(256 + s * 128); };
 
     if (warp >= CX_MMA) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CX_REGS_LESS));
-    if (warp == CX_LOAD) {
-        // ------------------------------------------------------------------ copies
-        const int gr = PAGED ? min(CX_KEYS, 1 << a.pshift) : CX_KEYS, ng = CX_KEYS / gr;  // rows of a copy, copies of a tile
-        int issued = 0;
-        bool ok = true;
-        auto load = [&](const CUtensorMap *map, int tile, bool value) {
-            const int slot = issued % CX_SLOTS, round = issued / CX_SLOTS;
-            if (round > 0) ok = ok && mbar_wait(bar(bars.free[slot]), (round - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            const uint32_t dst = sR + slot * CX_TILE;
-            const int key = tile * CX_KEYS + lane * gr;  // lane g: the tile's g-th copy
-            int page = 0;
-            bool there = lane < ng && key < len;
-            if (PAGED && there) {
-                page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
-                there = (unsigned)page < (unsigned)a.n_pages;
-            }
-            const unsigned have = __ballot_sync(0xffffffffu, there);
-            if (PAGED && value) {  // a page that is none: its weights are zero, and so must its values be finite
-                const unsigned none = __ballot_sync(0xffffffffu, lane < ng && key < len) & ~have;
-                if (none) {
-                    for (int g = 0; g < ng; ++g)
-                        if (none >> g & 1)
-                            for (int i = lane; i < 2 * gr * 8; i += 32) {
-                                const uint32_t at = dst + (i >= gr * 8 ? CX_HALF - gr * 128 : 0) + g * gr * 128 + 16 * i;
-                                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-                            }
-                    fence_proxy_async();
-                    __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CX_REGS_LESS));
+        if (warp == CX_LOAD) {
+            // -------------------------------------------------------------- copies
+            const int gr = PAGED ? min(CX_KEYS, 1 << a.pshift) : CX_KEYS, ng = CX_KEYS / gr;  // rows of a copy, copies of a tile
+            int issued[2] = {0, 0};  // copies of each ring
+            bool ok = true;
+            auto load = [&](int s, const CUtensorMap *map, int tile, bool value) {
+                const int i = issued[s], slot = s * CX_OWN + i % ring, round = i / ring;
+                if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.free[slot]), (round - 1) & 1));
+                if (!ok) return;
+                const uint32_t dst = sR + slot * CX_TILE;
+                const int key = tile * CX_KEYS + lane * gr;  // lane g: the tile's g-th copy
+                int page = 0;
+                const bool seen = lane < ng && key < len;
+                bool there = seen;
+                if (PAGED && seen) {
+                    page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
+                    there = (unsigned)page < (unsigned)a.n_pages;
                 }
-            }
-            if (lane == 0) mbar_expect_tx(bar(bars.full[slot]), (uint32_t)__popc(have) * gr * 256);
-            __syncwarp();
-            if (there) {
-                const int row = PAGED ? key & ((1 << a.pshift) - 1) : key;
-                const int c2 = PAGED ? h : h * a.hmul, c3 = PAGED ? page : b * a.bmul;
-                tma_load_4d(dst + lane * gr * 128, map, 0, row, c2, c3, bar(bars.full[slot]));
-                tma_load_4d(dst + CX_HALF + lane * gr * 128, map, 64, row, c2, c3, bar(bars.full[slot]));
-            }
-            ++issued;
-        };
-        if (pair) {
-            for (int j = 0; j < nt && ok; ++j) {
-                load(&kmap, first + j, false);
-                load(&vmap, first + j, true);
-            }
-        } else {
-            if (nt > 0) load(&kmap, first, false);
-            if (nt > 1) load(&kmap, first + 1, false);
-            for (int j = 0; j < nt && ok; ++j) {
-                load(&vmap, first + j, true);
-                if (j + 2 < nt) load(&kmap, first + j + 2, false);
-            }
-        }
-        if (!ok) atomicExch(&s_fail, 1);
-        // no copy outlives the CTA
-        for (int i = max(0, issued - CX_SLOTS); i < issued; ++i) mbar_wait(bar(bars.full[i % CX_SLOTS]), (i / CX_SLOTS) & 1);
-    } else if (warp == CX_MMA) {
-        // -------------------------------------------------------------------- MMAs
-        constexpr uint32_t ID_S = idesc_bf16_f32(CX_M, CX_KEYS), ID_O = idesc_bf16_f32(CX_M, MOG_D) | 1u << 16;
-        bool ok = true;
-        // copies in the order of their use; a slot is free once its last MMA is through
-        auto index_of = [&](bool value, int s, int j) {  // number of the copy that stream s's j-th tile needs
-            if (pair) return 2 * j + (value ? 1 : 0);
-            const int t = 2 * j + s;
-            if (!value) return t < 2 ? t : 2 * t - 1;
-            return t + min(2 + t, nt);  // (all K tiles up to t + 1 come before it)
-        };
-        auto wait_copy = [&](int i) { ok = ok && mbar_wait(bar(bars.full[i % CX_SLOTS]), (i / CX_SLOTS) & 1); };
-        auto mma_s = [&](int s, int j) {
-            const int i = index_of(false, s, j);
-            wait_copy(i);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t q = sQ + (pair ? s : 0) * CX_TILE, k = sR + (i % CX_SLOTS) * CX_TILE;
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = (ks >> 2) * CX_HALF + (ks & 3) * 32;
-                    tc_mma(tS(s), smem_desc_sw128(q + off), smem_desc_sw128(k + off), ID_S, ks != 0);
+                const unsigned have = __ballot_sync(0xffffffffu, there);
+                if (PAGED && value) {  // a page that is none: its weights are zero, and so must its values be finite
+                    const unsigned none = __ballot_sync(0xffffffffu, seen && !there);
+                    for (int g = 0; none >> g; ++g)
+                        if (none >> g & 1) zero_rows(dst, g * gr, gr);
+                    if (none) fence_proxy_async();
                 }
-                tc_commit(bar(bars.s_full[s]));
-                if (!pair || s == 1) tc_commit(bar(bars.free[i % CX_SLOTS]));
+                __syncwarp();
+                if (lane == 0) mbar_expect_tx(bar(bars.full[slot]), (uint32_t)__popc(have) * gr * 256);
+                __syncwarp();
+                if (there) {
+                    const int row = PAGED ? key & ((1 << a.pshift) - 1) : key;
+                    const int c2 = PAGED ? h : h * a.hmul, c3 = PAGED ? page : b * a.bmul;
+                    tma_load_4d(dst + lane * gr * 128, map, 0, row, c2, c3, bar(bars.full[slot]));
+                    tma_load_4d(dst + CX_HALF + lane * gr * 128, map, 64, row, c2, c3, bar(bars.full[slot]));
+                }
+                ++issued[s];
+            };
+            // in the order of their use: of a ring K, V, K, V, ...
+            for (int t = 0; t < min(nt, ways); ++t) load(t, &kmap, first + t, false);
+            for (int t = 0; t < nt && ok; ++t) {
+                const int s = pair ? 0 : t & 1;
+                load(s, &vmap, first + t, true);
+                if (t + ways < nt && ok) load(s, &kmap, first + t + ways, false);
             }
-            __syncwarp();
-        };
-        auto mma_o = [&](int s, int j) {
-            const int i = index_of(true, s, j);
-            wait_copy(i);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            const uint32_t v = sR + (i % CX_SLOTS) * CX_TILE;
-            const int left = len - tile_of(s, j) * CX_KEYS;
-            if (left < CX_KEYS && (!pair || s == 0)) {
+            if (tail > 0 && ok) {
                 // rows behind the sequence's end: their weights are zero, and so must their values be finite
-                for (int x = left * 8 + lane; x < CX_KEYS * 8; x += 32) {
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v + 16 * x), "r"(0) : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(v + CX_HALF + 16 * x), "r"(0) : "memory");
-                }
+                const int s = pair ? 0 : (nt - 1) & 1, i = issued[s] - 1, slot = s * CX_OWN + i % ring;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.full[slot]), (i / ring) & 1));
+                zero_rows(sR + slot * CX_TILE, CX_KEYS - tail, tail);
                 fence_proxy_async();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bars.v_tail));
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.p_full[s]), j & 1));
-            if (!ok) return;
-            tc_fence_after();
-            if (lane == 0) {
+            if (!ok) atomicExch(&s_fail, 1);
+            // no copy outlives the CTA
+            for (int s = 0; s < ways; ++s)
+                for (int i = max(0, issued[s] - ring); i < issued[s]; ++i) mbar_wait(bar(bars.full[s * CX_OWN + i % ring]), (i / ring) & 1);
+        } else if (warp < CX_MMA + 2) {
+            // ---------------------------------------------------------------- MMAs
+            // A warp's one thread issues a stream's; the two queue up, so that the tensor cores go on while one waits.
+            if (elect_one()) {
+                constexpr uint32_t ID_S = idesc_bf16_f32(CX_M, CX_KEYS), ID_O = idesc_bf16_f32(CX_M, MOG_D) | 1u << 16;
+                const int s = warp - CX_MMA, n = n_of(s);
+                const uint64_t qd = smem_desc_sw128(sQ + (pair ? s : 0) * CX_TILE), kd = smem_desc_sw128(sR), vd = v_desc(sR);
+                bool ok = true;
+                auto slot_of = [&](int i) {  // of copy i of the stream's ring, once it is there
+                    const int slot = (pair ? 0 : s * CX_OWN) + i % ring;
+                    ok = ok && mbar_wait(bar(bars.full[slot]), (i / ring) & 1);
+                    return slot;
+                };
+                auto mma_s = [&](int slot) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) tc_mma_ts(tO(s), tS(s) + 8 * ks, v_desc(v + ks * 2048), ID_O, (j | ks) != 0);
-                if (!pair || s == 1) tc_commit(bar(bars.free[i % CX_SLOTS]));
-                if (j + 1 == n_of(s)) tc_commit(bar(bars.o_full[s]));
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const int off = ((ks >> 2) * CX_HALF + (ks & 3) * 32) >> 4;
+                        tc_mma(tS(s), qd + off, kd + off + slot * (CX_TILE >> 4), ID_S, ks != 0);
+                    }
+                    tc_commit(bar(bars.s_full[s]));
+                    tc_commit(bar(bars.free[slot]));
+                };
+                if (n > 0) {
+                    const int slot = slot_of(0);
+                    if (ok) mma_s(slot);
+                }
+                for (int j = 0; j < n && ok; ++j) {
+                    const bool more = j + 1 < n;
+                    const int v = slot_of(2 * j + 1), k = more ? slot_of(2 * j + 2) : 0;
+                    if (tail > 0 && tile_of(s, j) + 1 == first + nt) ok = ok && mbar_wait(bar(bars.v_tail), 0);
+                    ok = ok && mbar_wait(bar(bars.p_full[s]), j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_ts(tO(s), tS(s) + 8 * ks, vd + ks * (2048 >> 4) + v * (CX_TILE >> 4), ID_O, ks != 0 || j != 0);
+                    tc_commit(bar(bars.free[v]));
+                    if (more) mma_s(k);
+                    else tc_commit(bar(bars.o_full[s]));
+                }
+                if (!ok) atomicExch(&s_fail, 1);
             }
             __syncwarp();
-        };
-        for (int s = 0; s < 2; ++s)
-            if (n_of(s) > 0) mma_s(s, 0);
-        for (int j = 0; j < n_of(0) && ok; ++j)
-            for (int s = 0; s < 2; ++s) {
-                if (j >= n_of(s) || !ok) continue;
-                mma_o(s, j);
-                if (ok && j + 1 < n_of(s)) mma_s(s, j + 1);
-            }
-        if (!ok) atomicExch(&s_fail, 1);
-    }
+        }
     } else {
         // ----------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CX_REGS_MORE));

@@ -93,6 +93,7 @@ CASES = [  # lens, T, H, G, page
     ((300, 5, 640), 30, 2, 4, 0), ((1500, 700), 50, 2, 5, 0), ((1000,), 17, 1, 16, 0), ((127, 128, 129), 100, 1, 3, 16),
     ((500, 33), 40, 2, 8, 32), ((1111, 2000), 1, 2, 4, 64), ((777,), 200, 2, 2, 128), ((900, 300), 70, 1, 7, 256),
     ((20000,), 3, 2, 5, 64), ((20000, 9000), 1, 4, 4, 0), ((6000,), 300, 1, 1, 16),
+    ((20000, 19000, 20000, 17000), 16, 16, 5, 64), ((15000, 16384), 80, 20, 4, 0),  # long streams, one query tile and two
 ]
 
 
