@@ -10,8 +10,8 @@
 //
 //   warps 0-3, 4-7  softmax of stream 0, 1: a thread has one query row; it reads its 128 logits from
 //                   tensor memory, takes the running maximum, and writes the weights back as bf16 where the logits were
-//   warps 8, 9      issue the MMAs of stream 0, 1: S = Q K^T (128 x 128 x 128) and O += P V, P from tensor memory
-//   warp 10         TMA copies of K and V tiles through a ring of 32 KB slots, in the order of their use
+//   warp 8          issues the MMAs: S = Q K^T (128 x 128 x 128) and O += P V, P from tensor memory
+//   warp 9          TMA copies of K and V tiles through a ring of 32 KB slots, in the order of their use
 //
 // Tensor memory holds S (then P) and O of both streams, 512 columns.  O is rescaled only when a row's
 // maximum has risen by more than 2^8 since the last time: weights are then at most 2^8, and O and
@@ -29,11 +29,10 @@ namespace mog {
 constexpr int CX_M = 128, CX_KEYS = 128;         // query rows and keys of a tile
 constexpr int CX_TILE = CX_KEYS * MOG_D * 2;     // bytes of a tile (K, V or Q): two halves of 64 dimensions
 constexpr int CX_HALF = CX_TILE / 2;
-// Slots of 32 KB.  Two query tiles: one ring of five.  One query tile: its second one's place is a sixth, and
-// each stream has a ring of three of its own: a barrier's waiter has to have seen the phase before the one it
-// waits for, which a slot that the streams take in turn would not give.
+// Slots of 32 KB.  Two query tiles: one ring of five.  One query tile: the second one's place is a sixth, and each
+// stream has a ring of three of its own.
 constexpr int CX_SLOTS = 6, CX_RING = 5, CX_OWN = 3;
-constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 10;  // (warp 11 fills the third warpgroup)
+constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 9;  // (warps 10, 11 fill the third warpgroup)
 // Registers: 168 a thread at launch; the softmax warps take 208, the others leave theirs at 80
 // (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
 constexpr int CX_REGS_MORE = 208, CX_REGS_LESS = 80;
@@ -96,6 +95,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+// After tmem_wait_ld: loaded values are not used before this point.
+__device__ __forceinline__ void settle(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -125,7 +129,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 struct CrossBars {
-    uint64_t full[CX_SLOTS], free[CX_SLOTS], s_full[2], p_full[2], o_full[2], v_tail;
+    uint64_t full[CX_SLOTS];  // a copy is there
+    // The logits of a stream's even and odd tiles.  That tile j + 1's are there says also that all earlier MMAs are
+    // through, and so that V of tile j and K of tile j + 1 are free: the only signal that the copying warp needs.  It may
+    // be a tile late with its wait, which is why even and odd ones have a barrier each.
+    uint64_t s_full[2][2];
+    uint64_t p_full[2][2];    // a stream's weights, of each half of the keys
+    uint64_t o_full[2], v_tail;
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -141,12 +151,14 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int row, int n) {
     }
 }
 
-// One output row (or partial), 32 dimensions from `c` on.
-__device__ __forceinline__ void put32(uint16_t *row, int c, const float (&v)[32]) {
+// 32 dimensions from 32 c on of row `r` of a warp's 32 output rows, as bf16 in shared memory: 16-byte chunk ch
+// of a row at chunk ch ^ (r & 7), without bank conflicts for a row a lane and for 16 lanes a row.
+__device__ __forceinline__ void put32(uint32_t out, int r, int c, const float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(row + c + 8 * i) = make_uint4(cvt_bf2(v[8 * i], v[8 * i + 1]), cvt_bf2(v[8 * i + 2], v[8 * i + 3]),
-                                                                 cvt_bf2(v[8 * i + 4], v[8 * i + 5]), cvt_bf2(v[8 * i + 6], v[8 * i + 7]));
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out + r * 256 + (((4 * c + i) ^ (r & 7)) << 4)),
+                     "r"(cvt_bf2(v[8 * i], v[8 * i + 1])), "r"(cvt_bf2(v[8 * i + 2], v[8 * i + 3])),
+                     "r"(cvt_bf2(v[8 * i + 4], v[8 * i + 5])), "r"(cvt_bf2(v[8 * i + 6], v[8 * i + 7])) : "memory");
 }
 
 template <bool PAGED>
@@ -174,14 +186,10 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     auto tile_of = [&](int s, int j) { return first + (pair ? j : 2 * j + s); };
     const int tail = nt > 0 ? max(0, (first + nt) * CX_KEYS - len) : 0;  // rows of the last tile behind the sequence's end
 
-    if (tid == 0) {
-        for (int i = 0; i < CX_SLOTS; ++i) {
-            mbar_init(bar(bars.full[i]), 1);
-            mbar_init(bar(bars.free[i]), pair ? 2 : 1);  // (both streams use a tile)
-        }
+    if (tid == CX_LOAD * 32) {
+        for (int i = 0; i < CX_SLOTS; ++i) mbar_init(bar(bars.full[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(bars.s_full[i]), 1);
-            mbar_init(bar(bars.p_full[i]), CX_M);
+            for (int k = 0; k < 2; ++k) mbar_init(bar(bars.s_full[i][k]), 1), mbar_init(bar(bars.p_full[i][k]), CX_M);
             mbar_init(bar(bars.o_full[i]), 1);
         }
         mbar_init(bar(bars.v_tail), 1);
@@ -192,18 +200,61 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         tmem_alloc(smem_u32(&s_tmem), 512);
         tmem_relinquish();
     }
-    // queries: rows of 256 bytes in the layout that the K tiles have
-    for (int i = tid; i < (pair ? 2 : 1) * CX_M * 16; i += CX_THREADS) {
-        const int r = i >> 4, ch = i & 15, row = row0 + r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < rows && nt > 0) {
-            const int t = row / a.G, g = row - t * a.G;
-            x = ldg_nc16(a.q + b * a.qb + t * a.qt + (int64_t)(h * a.G + g) * a.qh + 8 * ch);
+    // copies, by their warp
+    const int gr = PAGED ? min(CX_KEYS, 1 << a.pshift) : CX_KEYS, ng = CX_KEYS / gr;  // rows of a copy, copies of a tile
+    int issued[2] = {0, 0};  // copies of each ring
+    bool copies_ok = true;
+    auto load = [&](int s, const CUtensorMap *map, int tile, bool value) {
+        const int i = issued[s], slot = s * CX_OWN + i % ring, round = i / ring;
+        if (round > 0) {  // copy i - ring, V of tile f - 1 or K of tile f, has been used
+            const int f = (i - ring + 1) >> 1;
+            copies_ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.s_full[pair ? 1 : s][f & 1]), (f >> 1) & 1));
         }
-        const uint32_t at = sQ + (r >> 7) * CX_TILE + (ch >> 3) * CX_HALF + (r & 127) * 128 + (((ch ^ r) & 7) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+        if (!copies_ok) return;
+        const uint32_t dst = sR + slot * CX_TILE;
+        const int key = tile * CX_KEYS + lane * gr;  // lane g: the tile's g-th copy
+        int page = 0;
+        const bool seen = lane < ng && key < len;
+        bool there = seen;
+        if (PAGED && seen) {
+            page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
+            there = (unsigned)page < (unsigned)a.n_pages;
+        }
+        const unsigned have = __ballot_sync(0xffffffffu, there);
+        if (PAGED && value) {  // a page that is none: its weights are zero, and so must its values be finite
+            const unsigned none = __ballot_sync(0xffffffffu, seen && !there);
+            for (int g = 0; none >> g; ++g)
+                if (none >> g & 1) zero_rows(dst, g * gr, gr);
+            if (none) fence_proxy_async();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(bar(bars.full[slot]), (uint32_t)__popc(have) * gr * 256);
+        __syncwarp();
+        if (there) {
+            const int row = PAGED ? key & ((1 << a.pshift) - 1) : key;
+            const int c2 = PAGED ? h : h * a.hmul, c3 = PAGED ? page : b * a.bmul;
+            tma_load_4d(dst + lane * gr * 128, map, 0, row, c2, c3, bar(bars.full[slot]));
+            tma_load_4d(dst + CX_HALF + lane * gr * 128, map, 64, row, c2, c3, bar(bars.full[slot]));
+        }
+        ++issued[s];
+    };
+    if (warp == CX_LOAD) {  // the first keys, before all else
+        __syncwarp();  // (its first lane has made the barriers)
+        for (int t = 0; t < min(nt, ways); ++t) load(t, &kmap, first + t, false);
     }
-    fence_proxy_async();
+    // queries: rows of 256 bytes in the layout that the K tiles have
+    if (warp != CX_LOAD && nt > 0) {
+        for (int i = tid < CX_LOAD * 32 ? tid : tid - 32; i < (pair ? 2 : 1) * CX_M * 16; i += CX_THREADS - 32) {
+            const int r = i >> 4, ch = i & 15, row = row0 + r;
+            const int t = row / a.G, g = row - t * a.G;
+            const uint32_t at = sQ + (r >> 7) * CX_TILE + (ch >> 3) * CX_HALF + (r & 127) * 128 + (((ch ^ r) & 7) << 4);
+            const bool in = row < rows;
+            cp_async16(at, a.q + (in ? b * a.qb + t * a.qt + (int64_t)(h * a.G + g) * a.qh + 8 * ch : 0), in ? 16 : 0);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -215,47 +266,13 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CX_REGS_LESS));
         if (warp == CX_LOAD) {
             // -------------------------------------------------------------- copies
-            const int gr = PAGED ? min(CX_KEYS, 1 << a.pshift) : CX_KEYS, ng = CX_KEYS / gr;  // rows of a copy, copies of a tile
-            int issued[2] = {0, 0};  // copies of each ring
-            bool ok = true;
-            auto load = [&](int s, const CUtensorMap *map, int tile, bool value) {
-                const int i = issued[s], slot = s * CX_OWN + i % ring, round = i / ring;
-                if (round > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.free[slot]), (round - 1) & 1));
-                if (!ok) return;
-                const uint32_t dst = sR + slot * CX_TILE;
-                const int key = tile * CX_KEYS + lane * gr;  // lane g: the tile's g-th copy
-                int page = 0;
-                const bool seen = lane < ng && key < len;
-                bool there = seen;
-                if (PAGED && seen) {
-                    page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
-                    there = (unsigned)page < (unsigned)a.n_pages;
-                }
-                const unsigned have = __ballot_sync(0xffffffffu, there);
-                if (PAGED && value) {  // a page that is none: its weights are zero, and so must its values be finite
-                    const unsigned none = __ballot_sync(0xffffffffu, seen && !there);
-                    for (int g = 0; none >> g; ++g)
-                        if (none >> g & 1) zero_rows(dst, g * gr, gr);
-                    if (none) fence_proxy_async();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_expect_tx(bar(bars.full[slot]), (uint32_t)__popc(have) * gr * 256);
-                __syncwarp();
-                if (there) {
-                    const int row = PAGED ? key & ((1 << a.pshift) - 1) : key;
-                    const int c2 = PAGED ? h : h * a.hmul, c3 = PAGED ? page : b * a.bmul;
-                    tma_load_4d(dst + lane * gr * 128, map, 0, row, c2, c3, bar(bars.full[slot]));
-                    tma_load_4d(dst + CX_HALF + lane * gr * 128, map, 64, row, c2, c3, bar(bars.full[slot]));
-                }
-                ++issued[s];
-            };
             // in the order of their use: of a ring K, V, K, V, ...
-            for (int t = 0; t < min(nt, ways); ++t) load(t, &kmap, first + t, false);
-            for (int t = 0; t < nt && ok; ++t) {
+            for (int t = 0; t < nt && copies_ok; ++t) {
                 const int s = pair ? 0 : t & 1;
                 load(s, &vmap, first + t, true);
-                if (t + ways < nt && ok) load(s, &kmap, first + t + ways, false);
+                if (t + ways < nt && copies_ok) load(s, &kmap, first + t + ways, false);
             }
+            bool ok = copies_ok;
             if (tail > 0 && ok) {
                 // rows behind the sequence's end: their weights are zero, and so must their values be finite
                 const int s = pair ? 0 : (nt - 1) & 1, i = issued[s] - 1, slot = s * CX_OWN + i % ring;
@@ -269,45 +286,77 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
             // no copy outlives the CTA
             for (int s = 0; s < ways; ++s)
                 for (int i = max(0, issued[s] - ring); i < issued[s]; ++i) mbar_wait(bar(bars.full[s * CX_OWN + i % ring]), (i / ring) & 1);
-        } else if (warp < CX_MMA + 2) {
+        } else if (warp == CX_MMA) {
             // ---------------------------------------------------------------- MMAs
-            // A warp's one thread issues a stream's; the two queue up, so that the tensor cores go on while one waits.
+            // One thread, the streams in turn: while it waits for the weights of one, the MMAs of the other run.
             if (elect_one()) {
                 constexpr uint32_t ID_S = idesc_bf16_f32(CX_M, CX_KEYS), ID_O = idesc_bf16_f32(CX_M, MOG_D) | 1u << 16;
-                const int s = warp - CX_MMA, n = n_of(s);
-                const uint64_t qd = smem_desc_sw128(sQ + (pair ? s : 0) * CX_TILE), kd = smem_desc_sw128(sR), vd = v_desc(sR);
+                const uint64_t qd = smem_desc_sw128(sQ), kd = smem_desc_sw128(sR), vd = v_desc(sR);
                 bool ok = true;
-                auto slot_of = [&](int i) {  // of copy i of the stream's ring, once it is there
-                    const int slot = (pair ? 0 : s * CX_OWN) + i % ring;
-                    ok = ok && mbar_wait(bar(bars.full[slot]), (i / ring) & 1);
+                int at0 = 0, at1 = CX_OWN;  // the next slot of each ring, and its phase
+                uint32_t phase0 = 0, phase1 = 0;
+                auto next_copy = [&](int &at, uint32_t &phase, int end) {  // its slot, once it is there
+                    const int slot = at;
+                    ok = ok && mbar_wait(bar(bars.full[slot]), phase);
+                    if (++at == end) at -= ring, phase ^= 1;
                     return slot;
                 };
-                auto mma_s = [&](int slot) {
+                auto mma_s = [&](int s, int j, int slot) {
+                    const uint64_t q = qd + (pair ? s : 0) * (CX_TILE >> 4), k = kd + slot * (CX_TILE >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const int off = ((ks >> 2) * CX_HALF + (ks & 3) * 32) >> 4;
-                        tc_mma(tS(s), qd + off, kd + off + slot * (CX_TILE >> 4), ID_S, ks != 0);
+                        tc_mma(tS(s), q + off, k + off, ID_S, ks != 0);
                     }
-                    tc_commit(bar(bars.s_full[s]));
-                    tc_commit(bar(bars.free[slot]));
+                    tc_commit(bar(bars.s_full[s][j & 1]));
                 };
-                if (n > 0) {
-                    const int slot = slot_of(0);
-                    if (ok) mma_s(slot);
-                }
-                for (int j = 0; j < n && ok; ++j) {
-                    const bool more = j + 1 < n;
-                    const int v = slot_of(2 * j + 1), k = more ? slot_of(2 * j + 2) : 0;
-                    if (tail > 0 && tile_of(s, j) + 1 == first + nt) ok = ok && mbar_wait(bar(bars.v_tail), 0);
-                    ok = ok && mbar_wait(bar(bars.p_full[s]), j & 1);
-                    if (!ok) break;
-                    tc_fence_after();
+                // stream s's j-th tile; v, k: the slots of its values and of the next tile's keys
+                auto step = [&](int s, int j, int v, int k, bool more) {
+                    const uint64_t d = vd + v * (CX_TILE >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc_mma_ts(tO(s), tS(s) + 8 * ks, vd + ks * (2048 >> 4) + v * (CX_TILE >> 4), ID_O, ks != 0 || j != 0);
-                    tc_commit(bar(bars.free[v]));
-                    if (more) mma_s(k);
+                    for (int c = 0; c < 2; ++c) {
+                        ok = ok && mbar_wait(bar(bars.p_full[s][c]), j & 1);
+                        if (!ok) return;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 4 * c; ks < 4 * c + 4; ++ks)
+                            tc_mma_ts(tO(s), tS(s) + 8 * ks, d + ks * (2048 >> 4), ID_O, ks != 0 || j != 0);
+                    }
+                    if (more) mma_s(s, j + 1, k);
                     else tc_commit(bar(bars.o_full[s]));
+                };
+                if (pair) {
+                    if (nt > 0) {
+                        const int k = next_copy(at0, phase0, CX_RING);
+                        if (ok) mma_s(0, 0, k), mma_s(1, 0, k);
+                    }
+                    for (int j = 0; j < nt && ok; ++j) {
+                        const bool more = j + 1 < nt;
+                        const int v = next_copy(at0, phase0, CX_RING), k = more ? next_copy(at0, phase0, CX_RING) : 0;
+                        if (!more && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail), 0);
+                        step(0, j, v, k, more);
+                        if (ok) step(1, j, v, k, more);
+                    }
+                } else {
+                    if (nt > 0) {
+                        const int k = next_copy(at0, phase0, CX_OWN);
+                        if (ok) mma_s(0, 0, k);
+                    }
+                    if (nt > 1 && ok) {
+                        const int k = next_copy(at1, phase1, 2 * CX_OWN);
+                        if (ok) mma_s(1, 0, k);
+                    }
+                    for (int j = 0; 2 * j < nt && ok; ++j) {
+                        bool more = 2 * j + 2 < nt;
+                        int v = next_copy(at0, phase0, CX_OWN), k = more ? next_copy(at0, phase0, CX_OWN) : 0;
+                        if (2 * j + 1 == nt && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail), 0);
+                        step(0, j, v, k, more);
+                        if (2 * j + 1 >= nt || !ok) break;
+                        more = 2 * j + 3 < nt;
+                        v = next_copy(at1, phase1, 2 * CX_OWN), k = more ? next_copy(at1, phase1, 2 * CX_OWN) : 0;
+                        if (2 * j + 2 == nt && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail), 0);
+                        step(1, j, v, k, more);
+                    }
                 }
                 if (!ok) atomicExch(&s_fail, 1);
             }
@@ -336,39 +385,49 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 groups = __ballot_sync(0xffffffffu, (unsigned)page < (unsigned)a.n_pages);
                 page_of(j + 1);
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.s_full[s]), j & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.s_full[s][j & 1]), (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
             uint32_t x[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS(s) + lanes + 32 * c, x[c]);
-            tmem_wait_ld();
             float(&v)[128] = reinterpret_cast<float(&)[128]>(x);
-            if (left < CX_KEYS || (PAGED && groups != (1u << (CX_KEYS >> gshift)) - 1u)) {
+            const bool cut = left < CX_KEYS || (PAGED && groups != (1u << (CX_KEYS >> gshift)) - 1u);
+            tmem_ld32_nowait(tS(s) + lanes, x[0]);
+            tmem_ld32_nowait(tS(s) + lanes + 32, x[1]);
+            tmem_wait_ld();
+            settle(x[0]), settle(x[1]);
+            tmem_ld32_nowait(tS(s) + lanes + 64, x[2]);  // (while the maximum of the first ones is taken)
+            tmem_ld32_nowait(tS(s) + lanes + 96, x[3]);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < CX_KEYS; ++i)
-                    if (i >= left || (PAGED && !(groups >> (i >> gshift) & 1u))) v[i] = -INFINITY;
+            for (int c = 0; c < 2; ++c) {
+                if (c == 1) {
+                    tmem_wait_ld();
+                    settle(x[2]), settle(x[3]);
+                }
+                if (cut) {
+#pragma unroll
+                    for (int i = 64 * c; i < 64 * c + 64; ++i)
+                        if (i >= left || (PAGED && !(groups >> (i >> gshift) & 1u))) v[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 64 * c; i < 64 * c + 64; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], v[i + k], v[i + 4 + k]);
             }
-            float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-            for (int i = 4; i < CX_KEYS; i += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mx[k] = i + 4 < CX_KEYS ? fmax3(mx[k], v[i + k], v[(i + 4 + k) % CX_KEYS]) : fmaxf(mx[k], v[i + k]);
             float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2, f = a.scale2;
-            // Logits so large that a rounded maximum could leave a weight over 2: rounded first, so that
-            // the largest weight is 1.
-            if (__any_sync(0xffffffffu, fabsf(top) > 16777216.f && fabsf(top) < INFINITY)) {
-#pragma unroll
-                for (int i = 0; i < CX_KEYS; ++i) v[i] = __fmul_rn(v[i], f);
-                f = 1.f;
-            }
+            const bool big = fabsf(top) > 16777216.f && fabsf(top) < INFINITY;
             const float mn = fmaxf(m, top);
-            if (j == 0) {
-                m = mn;
-            } else {
-                const bool need = mn > m + CX_RISE;
-                if (__any_sync(0xffffffffu, need)) {
+            if (j == 0) m = mn;
+            const bool need = mn > m + CX_RISE;
+            if (__any_sync(0xffffffffu, big || need)) {
+                // Logits so large that a rounded maximum could leave a weight over 2: rounded first, so that the
+                // largest weight is 1.
+                if (__any_sync(0xffffffffu, big)) {
+#pragma unroll
+                    for (int i = 0; i < CX_KEYS; ++i) v[i] = __fmul_rn(v[i], f);
+                    f = 1.f;
+                }
+                if (__any_sync(0xffffffffu, need)) {  // (not of the first tile)
                     const float al = need ? ex2(m - mn) : 1.f;
                     if (need) m = mn;
                     l *= al;
@@ -377,6 +436,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                         uint32_t o[32];
                         tmem_ld32_nowait(tO(s) + lanes + 32 * c, o);
                         tmem_wait_ld();
+                        settle(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
                         tmem_st32(tO(s) + lanes + 32 * c, o);
@@ -398,13 +458,13 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                     p[i] = cvt_bf2(y0, y1);
                 }
                 tmem_st32(tS(s) + lanes + 32 * c, p);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(bars.p_full[s][c]));  // (the product starts on the first half)
             }
             float s0, s1;
             unpack2(add2(sum[0], sum[1]), s0, s1);
             l += s0 + s1;
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar(bars.p_full[s]));
         }
         // ----------------------------------------------------------------- outputs
         const int row = row0 + (pair ? s * CX_M : 0) + r;
@@ -439,8 +499,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         const bool failed = *(volatile int *)&s_fail != 0;
         if (pair || s == 0) {
             const bool write = row < rows;
-            const int t = row / a.G, g = row - t * a.G;
-            uint16_t *dst = a.out + b * a.ob + t * a.ot + (int64_t)(h * a.G + g) * a.oh;
+            const uint32_t stage = sQ + (pair ? s : 0) * CX_TILE + (warp & 3) * 32 * 256;  // (the queries have been read)
             float *part = a.part + (((int64_t)split * gridDim.y + u) * a.rows_pad + row) * CX_PART;
             const float inv = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (nothing seen: zeros; a sum that is NaN stays)
             mine *= inv, his *= inv;
@@ -464,10 +523,23 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<float4 *>(part + 4 + 32 * c + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                } else if (write) {
-                    put32(dst, 32 * c, o);
+                } else {
+                    put32(stage, lane, c, o);
                 }
                 __syncwarp();
+            }
+            if (a.splits == 1) {
+                // two rows at a time, 16 lanes each
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const int k = 2 * i + (lane >> 4), ch = lane & 15, to = row - lane + k;
+                    uint4 x;
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                 : "r"(stage + k * 256 + ((ch ^ (k & 7)) << 4)));
+                    if (to >= rows) continue;
+                    const int t = to / a.G, g = to - t * a.G;
+                    *reinterpret_cast<uint4 *>(a.out + b * a.ob + t * a.ot + (int64_t)(h * a.G + g) * a.oh + 8 * ch) = x;
+                }
             }
         }
         tc_fence_before();
