@@ -576,7 +576,8 @@ int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_ma
  *  count_dev   : int32[batch] query tokens, clamped to [0, t_max], or NULL: t_max each.  Rows of
  *                out behind them are left as they are
  *  q_dev, out_dev : bf16, element (b, t, h, j) at b*s[0] + t*s[1] + h*s[2] + j, strides multiples of
- *                8, 16-byte aligned; they must not overlap
+ *                8, 16-byte aligned; they must not overlap.  q's strides are >= 0 and below 2^35; that of
+ *                the tokens or heads may be 0 only if there is one (that of the sequences always)
  *  scratch_dev : at least mog_cross_scratch_bytes() bytes, 16-byte aligned (0 bytes: may be NULL), no
  *                initial contents needed, not shared by calls that overlap on the GPU
  * Products of bf16 with fp32 sums; the weights are rounded to bf16 for the second one, an error of the

@@ -1051,6 +1051,10 @@ extern "C" int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, 
     if ((st = check_rows(q_dev, q_strides)) != MOG_OK || (st = check_rows(out_dev, out_strides)) != MOG_OK) return st;
     if (!aligned16(scratch_dev)) return MOG_ERR_INVALID_ARG;
     if (scratch_bytes < need) return MOG_ERR_ARENA_TOO_SMALL;
+    // the queries' tensor map: rows of their own for every token and head
+    for (int i = 0; i < 3; ++i)
+        if (q_strides[i] < 0 || q_strides[i] >= (int64_t)1 << 35) return MOG_ERR_SHAPE;
+    if ((t_max > 1 && q_strides[1] == 0) || (h_q > 1 && q_strides[2] == 0)) return MOG_ERR_SHAPE;
     RowsIn r{};
     r.q = q_dev, r.qo = out_dev, r.h_q = h_q, r.h_kv = h_kv, r.t_max = t_max, r.count = count_dev;
     for (int i = 0; i < 3; ++i) r.qs[i] = q_strides[i], r.os[i] = out_strides[i];

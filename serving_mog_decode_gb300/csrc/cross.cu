@@ -3,15 +3,22 @@
 //
 //   out = softmax(tau q.K^T) V     per query token and head, over the keys [0, N_b)
 //
-// The T x G query rows that share a KV head are packed (token, then head), 128 to a tile.  A CTA
-// has two streams over tiles of 128 keys: two query tiles that share every key tile, or, where only one
-// is left, one query tile whose streams take alternate key tiles and are joined at the end.  While the
-// softmax of one stream runs, the tensor cores work for the other:
+// The query rows that share a KV head are packed (token, then head), as many whole tokens as fit 128 rows to
+// a tile.  A CTA has two streams over tiles of 128 keys: two query tiles that share every key tile ("pair"), or,
+// where only one is left, one query tile whose streams take alternate key tiles and are joined at the end.  While
+// the softmax of one stream runs, the tensor cores work for the other:
 //
 //   warps 0-3, 4-7  softmax of stream 0, 1: a thread has one query row; it reads its 128 logits from
 //                   tensor memory, takes the running maximum, and writes the weights back as bf16 where the logits were
 //   warp 8          issues the MMAs: S = Q K^T (128 x 128 x 128) and O += P V, P from tensor memory
 //   warp 9          TMA copies of K and V tiles through a ring of 32 KB slots, in the order of their use
+//   warp 10         TMA copies of the query tiles
+//
+// Work: an item is a pair of query tiles of a (sequence, KV head).  Lengths and counts are read on the device (a
+// captured graph replays with others).  Either a CTA, one per SM, takes whole items, the longest sequences' first
+// and in a snake (c, 2C - 1 - c, 2C + c, ...); or the key tiles of all items form one list, in units of two
+// tile products, of which each CTA takes an equal share (sequences alike: of what whole rounds leave).  The parts of an item that several CTAs have are partials (at most
+// two a CTA), which k_cross_merge folds.  cross_grid has the rule.  The copies of a CTA's next item run ahead.
 //
 // Tensor memory holds S (then P) and O of both streams, 512 columns.  O is rescaled only when a row's
 // maximum has risen by more than 2^8 since the last time: weights are then at most 2^8, and O and
@@ -29,43 +36,267 @@ namespace mog {
 constexpr int CX_M = 128, CX_KEYS = 128;         // query rows and keys of a tile
 constexpr int CX_TILE = CX_KEYS * MOG_D * 2;     // bytes of a tile (K, V or Q): two halves of 64 dimensions
 constexpr int CX_HALF = CX_TILE / 2;
-// Slots of 32 KB.  Two query tiles: one ring of five.  One query tile: the second one's place is a sixth, and each
-// stream has a ring of three of its own.
-constexpr int CX_SLOTS = 6, CX_RING = 5, CX_OWN = 3;
-constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 9;  // (warps 10, 11 fill the third warpgroup)
+constexpr int CX_RING = 5;                       // slots of K and V tiles
+constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 9, CX_Q = 10;  // (warp 11 fills the third warpgroup)
+constexpr int CX_SORT = 64;                      // sequences that whole items are sorted over
 // Registers: 168 a thread at launch; the softmax warps take 208, the others leave theirs at 80
 // (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
 constexpr int CX_REGS_MORE = 208, CX_REGS_LESS = 80;
 constexpr int CX_SMEM = (2 + CX_RING) * CX_TILE + 1024;
-constexpr int CX_PART = MOG_D + 4;               // floats of a partial: maximum, sum, 2 unused, accumulators
+constexpr int CX_PART = MOG_D + 4;               // floats of a partial row: maximum, sum, 2 unused, accumulators
 constexpr float CX_RISE = 8.f;                   // log2 of the rise of a maximum that O is rescaled for
 
 struct CrossArgs {
-    const uint16_t *q;
     uint16_t *out;
-    int64_t qb, qt, qh, ob, ot, oh;
+    int64_t ob, ot, oh;
     const int *lengths, *count;
-    int n_max, t_max, h_kv, G;
+    int n_max, t_max, batch, h_kv, G;
+    int tokens;      // of a query tile
+    int qmul;        // 0 where the queries of all sequences are one in memory
     const int *bt;
     int pshift, pps, n_pages;
     int bmul, hmul;  // contiguous: 0 where all sequences (heads) are one in memory
     float scale2;    // tau * log2(e)
-    float *part;     // splits > 1: [split][unit][row][CX_PART]
-    int splits, rows_pad;
+    float *part;     // [2 * CTAs][part_rows][CX_PART]: of CTA c, slot 2c: the item that it does not begin, 2c + 1: that it does not end
+    int part_rows;
+    int whole;       // whole items
 };
 
-// Query rows of sequence b that share a KV head.
-__device__ __forceinline__ int cross_rows(const CrossArgs &a, int b) {
-    const int t = a.count ? min(max(a.count[b], 0), a.t_max) : a.t_max;
-    return t * a.G;
-}
+// A sequence as items of each of its KV heads: `pairs` of two query tiles, `units` units each, and one of a
+// single query tile (`half` units) if half > 0.  An item without keys is a unit of its own (its rows are zeros).
+struct CrossSeq {
+    int count, len, nt, pairs, units, half;
+    __device__ __forceinline__ void load(const CrossArgs &a, int b) {
+        count = a.count ? min(max(a.count[b], 0), a.t_max) : a.t_max;
+        len = min(max(a.lengths[b], 0), a.n_max);
+        nt = (int)(((unsigned)len + CX_KEYS - 1) / CX_KEYS);
+        const int tiles = (count + a.tokens - 1) / a.tokens;
+        pairs = tiles >> 1;
+        units = max(nt, 1);
+        half = tiles & 1 ? max((nt + 1) >> 1, 1) : 0;
+    }
+    __device__ __forceinline__ int items() const { return pairs + (half > 0); }  // of a KV head
+    __device__ __forceinline__ int64_t cost() const { return (int64_t)pairs * units + half; }
+};
 
-// Key tiles [first, first + n) of split s of a sequence of `len` keys.
-__device__ __forceinline__ void split_tiles(int len, int splits, int s, int &first, int &n) {
-    const int nt = (int)(((unsigned)len + CX_KEYS - 1) / CX_KEYS);
-    const int per = (nt + splits - 1) / splits;
-    first = min(s * per, nt);
-    n = min(per, nt - first);
+// Whole items: sequences by their number of key tiles, the longest first, and where each one's items end in that
+// order.  n = 0: not sorted; `items` of every (sequence, KV head), real or not.
+struct CrossOrder {
+    int n, items;
+    uint8_t seq[CX_SORT];
+    int end[CX_SORT];
+    // (by the whole CTA; followed by a barrier)
+    __device__ __forceinline__ void make(const CrossArgs &a, int (&need)[CX_SORT], int (&key)[CX_SORT]) {
+        const int tid = threadIdx.x, per = ((a.t_max + a.tokens - 1) / a.tokens + 1) / 2;
+        const bool sort = a.batch <= CX_SORT && (int64_t)a.batch * a.h_kv * per > gridDim.x;
+        if (tid == 0) n = sort ? a.batch : 0, items = per;
+        if (!sort) return;
+        if (tid < a.batch) {
+            CrossSeq c;
+            c.load(a, tid);
+            need[tid] = c.items() * a.h_kv, key[tid] = c.nt;
+        }
+        __syncthreads();
+        if (tid < a.batch) {
+            int rank = 0;
+            int e = need[tid];
+            for (int i = 0; i < a.batch; ++i)
+                if (key[i] > key[tid] || (key[i] == key[tid] && i < tid)) ++rank, e += need[i];
+            seq[rank] = (uint8_t)tid, end[rank] = e;
+        }
+    }
+};
+
+// What a CTA works on next: `n` key tiles from `first` on of an item.
+struct Segment {
+    CrossSeq q;
+    int b, h, x;      // sequence, KV head, item
+    int at;           // its unit in the item
+    int64_t left;     // units of the CTA from here on;  whole items: how many it has had
+    bool pair, begins, ends;
+    int first, nt;
+    // Equal shares: the list's units, a share.  Sequences alike: CTAs first take `rounds` whole items each (`skipped`
+    // in all), in step with one another, so that those of a KV head read its tiles from L2 at the same time; the
+    // list is of the other items, pairs and then halves.
+    int64_t total, chunk, skipped, index;
+    int rounds;
+    bool even;
+
+    __device__ __forceinline__ int units() const { return x < q.pairs ? q.units : q.half; }
+    __device__ __forceinline__ void set(int64_t most) {
+        pair = x < q.pairs;
+        const int n = (int)min((int64_t)(units() - at), most);
+        begins = at == 0, ends = at + n == units();
+        first = pair ? at : 2 * at;
+        nt = min(pair ? n : 2 * n, q.nt - first);
+    }
+    // The CTA's first segment; false if it has none (called by full warps).
+    __device__ __forceinline__ bool start(const CrossArgs &a, const CrossOrder &o) {
+        left = 0;
+        if (a.whole) return take(a, o);
+        plan(a, gridDim.x);
+        if (rounds) return round(a);
+        return share(a);
+    }
+    // Equal shares: how the work is laid out (called by full warps).
+    __device__ __forceinline__ void plan(const CrossArgs &a, int ctas) {
+        all_units(a);
+        rounds = 0;
+        if (even) {
+            q.load(a, 0);
+            const int64_t units = (int64_t)a.batch * a.h_kv, p = units * q.pairs;
+            rounds = (int)(p / ctas);
+            skipped = (int64_t)rounds * ctas;
+            total = (p - skipped) * q.units + units * q.half;
+        }
+        chunk = max((total + ctas - 1) / ctas, (int64_t)CX_LEAST);
+    }
+    static constexpr int CX_LEAST = 3;  // units of a share: fewer are not worth a CTA's start
+    // sequences alike: the next whole item
+    __device__ __forceinline__ bool round(const CrossArgs &a) {
+        item(a, left++ * gridDim.x + blockIdx.x);
+        q.load(a, b);
+        set(INT64_MAX);
+        return true;
+    }
+    // sequences alike: pair item i, or half item i - all pairs
+    __device__ __forceinline__ void item(const CrossArgs &a, int64_t i) {
+        const int64_t p = (int64_t)a.batch * a.h_kv * q.pairs, u = i < p ? i / q.pairs : i - p;
+        x = i < p ? (int)(i - u * q.pairs) : q.pairs;
+        b = (int)(u / a.h_kv), h = (int)(u - (int64_t)b * a.h_kv);
+        index = i, at = 0;
+    }
+    // the CTA's share of the list (called by full warps unless the sequences are alike)
+    __device__ __forceinline__ bool share(const CrossArgs &a) {
+        rounds = 0;
+        const int64_t p = (int64_t)blockIdx.x * chunk;
+        if (p >= total) return false;
+        left = min(chunk, total - p);
+        seek(a, p);
+        set(left);
+        return true;
+    }
+    // whole items: the next one of the snake
+    __device__ __forceinline__ bool take(const CrossArgs &a, const CrossOrder &o) {
+        while (true) {
+            const int64_t i = left * gridDim.x + (left & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            ++left;
+            if (o.n == 0) {  // one item each, or too many sequences to sort: the sequences as they are
+                const int64_t unit = i / o.items;
+                if (unit >= (int64_t)a.batch * a.h_kv) return false;
+                b = (int)(unit / a.h_kv), h = (int)(unit - (int64_t)b * a.h_kv), x = (int)(i - unit * o.items);
+                q.load(a, b);
+                if (x < q.items()) break;
+            } else {
+                int k = 0;
+                while (k < o.n && o.end[k] <= i) ++k;
+                if (k == o.n) return false;
+                b = o.seq[k];
+                q.load(a, b);
+                const int r = (int)(i - (k ? o.end[k - 1] : 0)), n = max(q.items(), 1);
+                h = min(r / n, a.h_kv - 1), x = r - r / n * n;
+                break;
+            }
+        }
+        at = 0;
+        set(INT64_MAX);
+        return true;
+    }
+    // units of all sequences, and whether these are alike
+    __device__ __forceinline__ void all_units(const CrossArgs &a) {
+        const int lane = threadIdx.x & 31;
+        CrossSeq f;
+        f.load(a, 0);
+        int64_t s = 0;
+        bool same = true;
+        for (int i = lane; i < a.batch; i += 32) {
+            CrossSeq c;
+            c.load(a, i);
+            s += c.cost() * a.h_kv;
+            same = same && c.nt == f.nt && c.pairs == f.pairs && c.half == f.half;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        total = s;
+        even = __all_sync(0xffffffffu, same) && s > 0;
+    }
+    // The item that holds unit p of the list (p < total; called by full warps unless the sequences are alike).
+    __device__ __forceinline__ void seek(const CrossArgs &a, int64_t p) {
+        if (even) {
+            const int64_t pairs = (int64_t)a.batch * a.h_kv * q.pairs, first = (pairs - skipped) * q.units;
+            const int64_t i = p < first ? p / q.units : (p - first) / q.half, n = p < first ? i * q.units : first + i * q.half;
+            item(a, (p < first ? skipped : pairs) + i);
+            at = (int)(p - n);
+            q.load(a, b);
+            return;
+        }
+        const int lane = threadIdx.x & 31;
+        int64_t base = 0;
+        b = a.batch - 1;
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+            CrossSeq c;
+            int64_t mine = 0;
+            if (b0 + lane < a.batch) c.load(a, b0 + lane), mine = c.cost() * a.h_kv;
+            int64_t end = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += v;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, base + end > p);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                b = b0 + l;
+                base += __shfl_sync(0xffffffffu, end - mine, l);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, end, 31);
+        }
+        q.load(a, b);
+        const int64_t c = max(q.cost(), (int64_t)1), r = p - base;
+        h = min((int)(r / c), a.h_kv - 1);
+        const int64_t o = r - h * c;
+        x = min((int)(o / q.units), q.pairs);
+        at = (int)(o - (int64_t)x * q.units);
+    }
+    __device__ __forceinline__ bool next(const CrossArgs &a, const CrossOrder &o) {
+        if (a.whole) return take(a, o);
+        if (rounds) return left < rounds ? round(a) : share(a);
+        left -= min((int64_t)(units() - at), left);
+        if (left <= 0) return false;
+        if (even) {
+            item(a, index + 1);
+            q.load(a, b);
+            set(left);
+            return true;
+        }
+        at = 0;
+        if (++x >= q.items()) {
+            x = 0;
+            if (++h == a.h_kv) {
+                h = 0;
+                do {
+                    if (++b >= a.batch) return false;  // (lengths that changed under the call)
+                    q.load(a, b);
+                } while (q.count == 0);
+            }
+        }
+        set(left);
+        return true;
+    }
+    // tiles of stream s, its j-th; rows of the last tile behind the sequence's end
+    __device__ __forceinline__ int n_of(int s) const { return pair ? nt : (nt - s + 1) >> 1; }
+    __device__ __forceinline__ int tile_of(int s, int j) const { return first + (pair ? j : 2 * j + s); }
+    __device__ __forceinline__ int tail() const { return max(0, (first + nt) * CX_KEYS - q.len); }
+};
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
 }
 
 // V tile, [128 keys][64 dims] twice, as the MN-major operand B (N = dimensions, K = keys): 64
@@ -125,19 +356,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// the two softmax groups' barrier
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-struct CrossBars {
-    uint64_t full[CX_SLOTS];  // a copy is there
-    // The logits of a stream's even and odd tiles.  That tile j + 1's are there says also that all earlier MMAs are
-    // through, and so that V of tile j and K of tile j + 1 are free: the only signal that the copying warp needs.  It may
-    // be a tile late with its wait, which is why even and odd ones have a barrier each.
-    uint64_t s_full[2][2];
-    uint64_t p_full[2][2];    // a stream's weights, of each half of the keys
-    uint64_t o_full[2], v_tail;
-};
-
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+    return x;
+}
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -151,109 +377,85 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int row, int n) {
     }
 }
 
-// 32 dimensions from 32 c on of row `r` of a warp's 32 output rows, as bf16 in shared memory: 16-byte chunk ch
-// of a row at chunk ch ^ (r & 7), without bank conflicts for a row a lane and for 16 lanes a row.
-__device__ __forceinline__ void put32(uint32_t out, int r, int c, const float (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(out + r * 256 + (((4 * c + i) ^ (r & 7)) << 4)),
-                     "r"(cvt_bf2(v[8 * i], v[8 * i + 1])), "r"(cvt_bf2(v[8 * i + 2], v[8 * i + 3])),
-                     "r"(cvt_bf2(v[8 * i + 4], v[8 * i + 5])), "r"(cvt_bf2(v[8 * i + 6], v[8 * i + 7])) : "memory");
+// Bit i: key k + i of a tile is behind the sequence's end (`left` keys of it are not), or in no page (bit j of
+// groups: the page of keys j << gshift .. is one; gshift >= 4).
+template <bool PAGED>
+__device__ __forceinline__ uint32_t dead_keys(int k, int left, unsigned groups, int gshift) {
+    uint32_t dead = left >= k + 32 ? 0u : left <= k ? 0xffffffffu : 0xffffffffu << (left - k);
+    if (PAGED) {
+        if (!(groups >> (k >> gshift) & 1u)) dead |= 0xffffu;
+        if (!(groups >> ((k + 16) >> gshift) & 1u)) dead |= 0xffff0000u;
+    }
+    return dead;
 }
 
+// Barriers.  Every wait is for the phase after the last one that its waiter has seen.
+struct CrossBars {
+    uint64_t full[CX_RING];  // a copy is there
+    // Copies that fall free together (V of a tile and K of the next one) are a group; the slot of its last one says so.
+    uint64_t free[CX_RING];
+    uint64_t q_full, q_free;  // the item's queries are there; their place, which the outputs pass through, is free
+    uint64_t s_full[2];       // a stream's logits
+    uint64_t p_full[2][2];    // its weights, of each half of the keys
+    uint64_t o_full[2], o_free[2];  // its sums are through; have been read
+    uint64_t j_full, j_free;  // one query tile: stream 1's maxima and sums are there; have been read
+    uint64_t v_tail[4];       // an item's last V: its rows behind the sequence's end are zero (the ring holds 2 such at most)
+};
+
 template <bool PAGED>
-__global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __grid_constant__ CUtensorMap qmap,
+                                                         const __grid_constant__ CUtensorMap kmap,
                                                          const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ uint8_t cx_raw[];
     __shared__ __align__(8) CrossBars bars;
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
-    __shared__ float2 s_ml[CX_M];
-    const int u = blockIdx.y, b = u / a.h_kv, h = u - b * a.h_kv, split = blockIdx.z;
-    const int rows = cross_rows(a, b), row0 = blockIdx.x * 2 * CX_M;
-    if (row0 >= rows) return;
-    const bool pair = row0 + CX_M < rows;  // two query tiles
-    const int len = min(max(a.lengths[b], 0), a.n_max);
-    int first, nt;
-    split_tiles(len, a.splits, split, first, nt);
+    pdl_trigger();  // (k_cross_merge waits for the whole grid)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t raw = smem_u32(cx_raw);
-    const uint32_t sQ = (raw + 1023u) & ~1023u, sR = sQ + (pair ? 2 : 1) * CX_TILE;
-    const int ways = pair ? 1 : 2, ring = pair ? CX_RING : CX_OWN;  // rings, and their slots
+    // A warp's place in the list, in shared memory: it is looked at between items only.
+    __shared__ Segment s_seg[CX_THREADS / 32];
+    __shared__ CrossOrder s_order;
+    if (a.whole) {
+        s_order.make(a, *reinterpret_cast<int(*)[CX_SORT]>(cx_raw), *reinterpret_cast<int(*)[CX_SORT]>(cx_raw + 4 * CX_SORT));
+        __syncthreads();
+    }
+    Segment &g = s_seg[warp];
+    {
+        Segment first;
+        if (!first.start(a, s_order)) return;
+        if (lane == 0) g = first;
+        __syncwarp();
+    }
+    auto next_item = [&]() {  // (by a whole warp)
+        __syncwarp();
+        int more = 0;
+        if (lane == 0) more = g.next(a, s_order);
+        more = __shfl_sync(0xffffffffu, more, 0);
+        __syncwarp();
+        return more != 0;
+    };
+    const uint32_t sQ = (smem_u32(cx_raw) + 1023u) & ~1023u, sR = sQ + 2 * CX_TILE;
     auto bar = [&](const uint64_t &x) { return smem_u32(&x); };
-    // tiles of stream s, and its j-th
-    auto n_of = [&](int s) { return pair ? nt : (nt - s + 1) >> 1; };
-    auto tile_of = [&](int s, int j) { return first + (pair ? j : 2 * j + s); };
-    const int tail = nt > 0 ? max(0, (first + nt) * CX_KEYS - len) : 0;  // rows of the last tile behind the sequence's end
-
+    float2 *s_ml = reinterpret_cast<float2 *>(cx_raw + (sQ + CX_TILE - smem_u32(cx_raw)));  // (one query tile: the other's place)
     if (tid == CX_LOAD * 32) {
-        for (int i = 0; i < CX_SLOTS; ++i) mbar_init(bar(bars.full[i]), 1);
+        for (int i = 0; i < CX_RING; ++i) mbar_init(bar(bars.full[i]), 1), mbar_init(bar(bars.free[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            for (int k = 0; k < 2; ++k) mbar_init(bar(bars.s_full[i][k]), 1), mbar_init(bar(bars.p_full[i][k]), CX_M);
+            mbar_init(bar(bars.s_full[i]), 1);
+            for (int k = 0; k < 2; ++k) mbar_init(bar(bars.p_full[i][k]), CX_M);
             mbar_init(bar(bars.o_full[i]), 1);
+            mbar_init(bar(bars.o_free[i]), CX_M);
         }
-        mbar_init(bar(bars.v_tail), 1);
+        mbar_init(bar(bars.q_full), 1);
+        mbar_init(bar(bars.q_free), 2 * CX_M);
+        mbar_init(bar(bars.j_full), CX_M);
+        mbar_init(bar(bars.j_free), CX_M);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(bars.v_tail[i]), 1);
         fence_barrier_init();
         s_fail = 0;
     }
     if (warp == CX_MMA) {
         tmem_alloc(smem_u32(&s_tmem), 512);
         tmem_relinquish();
-    }
-    // copies, by their warp
-    const int gr = PAGED ? min(CX_KEYS, 1 << a.pshift) : CX_KEYS, ng = CX_KEYS / gr;  // rows of a copy, copies of a tile
-    int issued[2] = {0, 0};  // copies of each ring
-    bool copies_ok = true;
-    auto load = [&](int s, const CUtensorMap *map, int tile, bool value) {
-        const int i = issued[s], slot = s * CX_OWN + i % ring, round = i / ring;
-        if (round > 0) {  // copy i - ring, V of tile f - 1 or K of tile f, has been used
-            const int f = (i - ring + 1) >> 1;
-            copies_ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.s_full[pair ? 1 : s][f & 1]), (f >> 1) & 1));
-        }
-        if (!copies_ok) return;
-        const uint32_t dst = sR + slot * CX_TILE;
-        const int key = tile * CX_KEYS + lane * gr;  // lane g: the tile's g-th copy
-        int page = 0;
-        const bool seen = lane < ng && key < len;
-        bool there = seen;
-        if (PAGED && seen) {
-            page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
-            there = (unsigned)page < (unsigned)a.n_pages;
-        }
-        const unsigned have = __ballot_sync(0xffffffffu, there);
-        if (PAGED && value) {  // a page that is none: its weights are zero, and so must its values be finite
-            const unsigned none = __ballot_sync(0xffffffffu, seen && !there);
-            for (int g = 0; none >> g; ++g)
-                if (none >> g & 1) zero_rows(dst, g * gr, gr);
-            if (none) fence_proxy_async();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_expect_tx(bar(bars.full[slot]), (uint32_t)__popc(have) * gr * 256);
-        __syncwarp();
-        if (there) {
-            const int row = PAGED ? key & ((1 << a.pshift) - 1) : key;
-            const int c2 = PAGED ? h : h * a.hmul, c3 = PAGED ? page : b * a.bmul;
-            tma_load_4d(dst + lane * gr * 128, map, 0, row, c2, c3, bar(bars.full[slot]));
-            tma_load_4d(dst + CX_HALF + lane * gr * 128, map, 64, row, c2, c3, bar(bars.full[slot]));
-        }
-        ++issued[s];
-    };
-    if (warp == CX_LOAD) {  // the first keys, before all else
-        __syncwarp();  // (its first lane has made the barriers)
-        for (int t = 0; t < min(nt, ways); ++t) load(t, &kmap, first + t, false);
-    }
-    // queries: rows of 256 bytes in the layout that the K tiles have
-    if (warp != CX_LOAD && nt > 0) {
-        for (int i = tid < CX_LOAD * 32 ? tid : tid - 32; i < (pair ? 2 : 1) * CX_M * 16; i += CX_THREADS - 32) {
-            const int r = i >> 4, ch = i & 15, row = row0 + r;
-            const int t = row / a.G, g = row - t * a.G;
-            const uint32_t at = sQ + (r >> 7) * CX_TILE + (ch >> 3) * CX_HALF + (r & 127) * 128 + (((ch ^ r) & 7) << 4);
-            const bool in = row < rows;
-            cp_async16(at, a.q + (in ? b * a.qb + t * a.qt + (int64_t)(h * a.G + g) * a.qh + 8 * ch : 0), in ? 16 : 0);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async();
     }
     tc_fence_before();
     __syncthreads();
@@ -265,285 +467,436 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     if (warp >= CX_MMA) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CX_REGS_LESS));
         if (warp == CX_LOAD) {
-            // -------------------------------------------------------------- copies
-            // in the order of their use: of a ring K, V, K, V, ...
-            for (int t = 0; t < nt && copies_ok; ++t) {
-                const int s = pair ? 0 : t & 1;
-                load(s, &vmap, first + t, true);
-                if (t + ways < nt && copies_ok) load(s, &kmap, first + t + ways, false);
-            }
-            bool ok = copies_ok;
-            if (tail > 0 && ok) {
-                // rows behind the sequence's end: their weights are zero, and so must their values be finite
-                const int s = pair ? 0 : (nt - 1) & 1, i = issued[s] - 1, slot = s * CX_OWN + i % ring;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.full[slot]), (i / ring) & 1));
-                zero_rows(sR + slot * CX_TILE, CX_KEYS - tail, tail);
-                fence_proxy_async();
+            // -------------------------------------------------------------- copies of K and V
+            const int gr = PAGED ? min(CX_KEYS, 1 << a.pshift) : CX_KEYS, ng = CX_KEYS / gr;  // rows of a copy, copies of a tile
+            int slot = 0, issued = 0, tails = 0, b = 0, h = 0, len = 0;
+            // bits by slot: the next phase of full; its occupant is the first of a group of two; the next phase of free
+            uint32_t fullp = 0, two = 0, freep = 0;
+            bool ok = true;
+            auto load = [&](const CUtensorMap *map, int tile, bool value, bool first_of_two) {
+                if (issued >= CX_RING) {  // the slot's last occupant has been used
+                    const int w = two >> slot & 1 ? (slot + 1 == CX_RING ? 0 : slot + 1) : slot;
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.free[w]), (freep >> w & 1) ^ 1));
+                }
+                if (!ok) return;
+                const uint32_t dst = sR + slot * CX_TILE;
+                const int key = tile * CX_KEYS + lane * gr;  // lane g: the tile's g-th copy
+                int page = 0;
+                const bool seen = lane < ng && key < len;
+                bool there = seen;
+                if (PAGED && seen) {
+                    page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
+                    there = (unsigned)page < (unsigned)a.n_pages;
+                }
+                const unsigned have = __ballot_sync(0xffffffffu, there);
+                if (PAGED && value) {  // a page that is none: its weights are zero, and so must its values be finite
+                    const unsigned none = __ballot_sync(0xffffffffu, seen && !there);
+                    for (int i = 0; none >> i; ++i)
+                        if (none >> i & 1) zero_rows(dst, i * gr, gr);
+                    if (none) fence_proxy_async();
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(bars.v_tail));
-            }
+                if (lane == 0) mbar_expect_tx(bar(bars.full[slot]), (uint32_t)__popc(have) * gr * 256);
+                __syncwarp();
+                if (there) {
+                    const int row = PAGED ? key & ((1 << a.pshift) - 1) : key;
+                    const int c2 = PAGED ? h : h * a.hmul, c3 = PAGED ? page : b * a.bmul;
+                    tma_load_4d(dst + lane * gr * 128, map, 0, row, c2, c3, bar(bars.full[slot]));
+                    tma_load_4d(dst + CX_HALF + lane * gr * 128, map, 64, row, c2, c3, bar(bars.full[slot]));
+                }
+                const uint32_t bit = 1u << slot;
+                fullp ^= bit;
+                two = first_of_two ? two | bit : two & ~bit;
+                if (!first_of_two) freep ^= bit;
+                ++issued;
+                slot = slot + 1 == CX_RING ? 0 : slot + 1;
+            };
+            do {
+                // in the order of their use
+                const int ways = g.pair ? 1 : 2, nt = g.nt, first = g.first;
+                b = g.b, h = g.h, len = g.q.len;
+                for (int t = 0; t < min(nt, ways) && ok; ++t) load(&kmap, first + t, false, t + 1 < min(nt, ways));
+                for (int t = 0; t < nt && ok; ++t) {
+                    const bool more = t + ways < nt;
+                    load(&vmap, first + t, true, more);
+                    if (more && ok) load(&kmap, first + t + ways, false, false);
+                }
+                if (nt > 0 && g.tail() > 0 && ok) {
+                    // rows behind the sequence's end: their weights are zero, and so must their values be finite
+                    const int last = slot == 0 ? CX_RING - 1 : slot - 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.full[last]), (fullp >> last & 1) ^ 1));
+                    zero_rows(sR + last * CX_TILE, CX_KEYS - g.tail(), g.tail());
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(bars.v_tail[tails++ & 3]));
+                }
+            } while (ok && next_item());
             if (!ok) atomicExch(&s_fail, 1);
             // no copy outlives the CTA
-            for (int s = 0; s < ways; ++s)
-                for (int i = max(0, issued[s] - ring); i < issued[s]; ++i) mbar_wait(bar(bars.full[s * CX_OWN + i % ring]), (i / ring) & 1);
+            for (int i = 0; i < min(issued, CX_RING); ++i) mbar_wait(bar(bars.full[i]), (fullp >> i & 1) ^ 1);
         } else if (warp == CX_MMA) {
             // ---------------------------------------------------------------- MMAs
             // One thread, the streams in turn: while it waits for the weights of one, the MMAs of the other run.
             if (elect_one()) {
                 constexpr uint32_t ID_S = idesc_bf16_f32(CX_M, CX_KEYS), ID_O = idesc_bf16_f32(CX_M, MOG_D) | 1u << 16;
                 const uint64_t qd = smem_desc_sw128(sQ), kd = smem_desc_sw128(sR), vd = v_desc(sR);
-                bool ok = true;
-                int at0 = 0, at1 = CX_OWN;  // the next slot of each ring, and its phase
-                uint32_t phase0 = 0, phase1 = 0;
-                auto next_copy = [&](int &at, uint32_t &phase, int end) {  // its slot, once it is there
+                bool ok = true, pair = false;
+                int at = 0;                         // the next slot of the ring
+                uint32_t phase = 0, seg = 0, tails = 0;
+                uint32_t pp0 = 0, pp1 = 0;          // the next phase of the streams' p_full
+                auto next_copy = [&]() {            // its slot, once it is there
                     const int slot = at;
                     ok = ok && mbar_wait(bar(bars.full[slot]), phase);
-                    if (++at == end) at -= ring, phase ^= 1;
+                    if (++at == CX_RING) at = 0, phase ^= 1;
                     return slot;
                 };
-                auto mma_s = [&](int s, int j, int slot) {
+                auto mma_s = [&](int s, int slot) {
                     const uint64_t q = qd + (pair ? s : 0) * (CX_TILE >> 4), k = kd + slot * (CX_TILE >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const int off = ((ks >> 2) * CX_HALF + (ks & 3) * 32) >> 4;
                         tc_mma(tS(s), q + off, k + off, ID_S, ks != 0);
                     }
-                    tc_commit(bar(bars.s_full[s][j & 1]));
+                    tc_commit(bar(bars.s_full[s]));
                 };
-                // stream s's j-th tile; v, k: the slots of its values and of the next tile's keys
-                auto step = [&](int s, int j, int v, int k, bool more) {
+                // a tile of stream s; v, k: the slots of its values and of the next tile's keys
+                auto step = [&](int s, bool opens, int v, int k, bool more) {
                     const uint64_t d = vd + v * (CX_TILE >> 4);
+                    uint32_t &pp = s ? pp1 : pp0;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        ok = ok && mbar_wait(bar(bars.p_full[s][c]), j & 1);
+                        ok = ok && mbar_wait(bar(bars.p_full[s][c]), pp);
                         if (!ok) return;
                         tc_fence_after();
 #pragma unroll
                         for (int ks = 4 * c; ks < 4 * c + 4; ++ks)
-                            tc_mma_ts(tO(s), tS(s) + 8 * ks, d + ks * (2048 >> 4), ID_O, ks != 0 || j != 0);
+                            tc_mma_ts(tO(s), tS(s) + 8 * ks, d + ks * (2048 >> 4), ID_O, ks != 0 || !opens);
                     }
-                    if (more) mma_s(s, j + 1, k);
+                    pp ^= 1;
+                    if (more) mma_s(s, k);
                     else tc_commit(bar(bars.o_full[s]));
                 };
-                if (pair) {
-                    if (nt > 0) {
-                        const int k = next_copy(at0, phase0, CX_RING);
-                        if (ok) mma_s(0, 0, k), mma_s(1, 0, k);
+                do {
+                    const int nt = g.nt, tail = g.tail();
+                    pair = g.pair;
+                    if (nt == 0) continue;
+                    ok = ok && mbar_wait(bar(bars.q_full), seg & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (pair) {
+                        const int k0 = next_copy();
+                        if (!ok) break;
+                        mma_s(0, k0), mma_s(1, k0);
+                        tc_commit(bar(bars.free[k0]));
+                        for (int s = 0; s < 2 && seg > 0; ++s) ok = ok && mbar_wait(bar(bars.o_free[s]), (seg - 1) & 1);
+                        for (int j = 0; j < nt && ok; ++j) {
+                            const bool more = j + 1 < nt;
+                            const int v = next_copy(), k = more ? next_copy() : v;
+                            if (!more && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail[tails & 3]), (tails >> 2) & 1);
+                            if (ok) step(0, j == 0, v, k, more);
+                            if (ok) step(1, j == 0, v, k, more);
+                            if (!ok) break;
+                            tc_commit(bar(bars.free[k]));
+                        }
+                    } else {
+                        int k0 = next_copy();
+                        if (ok) mma_s(0, k0);
+                        if (nt > 1 && ok) {
+                            k0 = next_copy();
+                            if (ok) mma_s(1, k0);
+                        }
+                        if (!ok) break;
+                        tc_commit(bar(bars.free[k0]));
+                        for (int s = 0; s < 2 && seg > 0; ++s) ok = ok && mbar_wait(bar(bars.o_free[s]), (seg - 1) & 1);
+                        for (int t = 0; t < nt && ok; t += 2) {
+                            bool more = t + 2 < nt;
+                            int v = next_copy(), k = more ? next_copy() : v;
+                            if (t + 1 == nt && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail[tails & 3]), (tails >> 2) & 1);
+                            if (ok) step(0, t == 0, v, k, more);
+                            if (!ok) break;
+                            tc_commit(bar(bars.free[k]));
+                            if (t + 1 >= nt) break;
+                            more = t + 3 < nt;
+                            v = next_copy(), k = more ? next_copy() : v;
+                            if (t + 2 == nt && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail[tails & 3]), (tails >> 2) & 1);
+                            if (ok) step(1, t == 0, v, k, more);
+                            if (!ok) break;
+                            tc_commit(bar(bars.free[k]));
+                        }
                     }
-                    for (int j = 0; j < nt && ok; ++j) {
-                        const bool more = j + 1 < nt;
-                        const int v = next_copy(at0, phase0, CX_RING), k = more ? next_copy(at0, phase0, CX_RING) : 0;
-                        if (!more && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail), 0);
-                        step(0, j, v, k, more);
-                        if (ok) step(1, j, v, k, more);
-                    }
-                } else {
-                    if (nt > 0) {
-                        const int k = next_copy(at0, phase0, CX_OWN);
-                        if (ok) mma_s(0, 0, k);
-                    }
-                    if (nt > 1 && ok) {
-                        const int k = next_copy(at1, phase1, 2 * CX_OWN);
-                        if (ok) mma_s(1, 0, k);
-                    }
-                    for (int j = 0; 2 * j < nt && ok; ++j) {
-                        bool more = 2 * j + 2 < nt;
-                        int v = next_copy(at0, phase0, CX_OWN), k = more ? next_copy(at0, phase0, CX_OWN) : 0;
-                        if (2 * j + 1 == nt && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail), 0);
-                        step(0, j, v, k, more);
-                        if (2 * j + 1 >= nt || !ok) break;
-                        more = 2 * j + 3 < nt;
-                        v = next_copy(at1, phase1, 2 * CX_OWN), k = more ? next_copy(at1, phase1, 2 * CX_OWN) : 0;
-                        if (2 * j + 2 == nt && tail > 0) ok = ok && mbar_wait(bar(bars.v_tail), 0);
-                        step(1, j, v, k, more);
-                    }
-                }
+                    ++seg;
+                    tails += tail > 0;
+                } while (ok && g.next(a, s_order));
                 if (!ok) atomicExch(&s_fail, 1);
+            }
+            __syncwarp();
+        } else if (warp == CX_Q) {
+            // ---------------------------------------------------------------- copies of the queries
+            if (lane == 0) {
+                const uint32_t bytes = (uint32_t)(a.tokens * a.G) * 256;  // of a tile; tokens from t_max on are zeros
+                uint32_t seg = 0;
+                bool ok = true;
+                do {
+                    if (g.nt == 0) continue;
+                    if (seg > 0) ok = mbar_wait(bar(bars.q_free), (seg - 1) & 1);
+                    if (!ok) break;
+                    const int n = g.pair ? 2 : 1;
+                    mbar_expect_tx(bar(bars.q_full), n * bytes);
+                    for (int i = 0; i < n; ++i)
+                        for (int d = 0; d < 2; ++d)
+                            tma_load_5d(sQ + i * CX_TILE + d * CX_HALF, &qmap, 64 * d, 0, (2 * g.x + i) * a.tokens, g.h, g.b * a.qmul,
+                                        bar(bars.q_full));
+                    ++seg;
+                } while (g.next(a, s_order));
+                if (!ok) atomicExch(&s_fail, 1);
+                if (seg > 0) mbar_wait(bar(bars.q_full), (seg - 1) & 1);  // no copy outlives the CTA
             }
             __syncwarp();
         }
     } else {
         // ----------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CX_REGS_MORE));
-        const int s = warp >> 2, r = tid & 127, n = n_of(s);
+        const int s = warp >> 2, r = tid & 127, gshift = PAGED ? min(a.pshift, 7) : 7;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-        float m = -INFINITY, l = 0.f;
+        uint32_t sp = 0, op0 = 0, op1 = 0, joins = 0;       // the next phases of s_full and both o_full
+        const bool row = r < a.tokens * a.G;  // (the rows behind the tile's tokens hold anything)
         bool ok = true;
-        int page = 0, gshift = 0;  // paged: the page of the next tile's group `lane`
-        auto page_of = [&](int j) {
-            if (!PAGED || j >= n) return;
-            const int key = tile_of(s, j) * CX_KEYS + (lane << gshift);
-            page = -1;
-            if (lane < CX_KEYS >> gshift && key < len) page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
-        };
-        if (PAGED) gshift = min(a.pshift, 7);
-        page_of(0);
-        for (int j = 0; j < n; ++j) {
-            const int left = len - tile_of(s, j) * CX_KEYS;
-            unsigned groups = 0xffffffffu;
-            if (PAGED) {
-                groups = __ballot_sync(0xffffffffu, (unsigned)page < (unsigned)a.n_pages);
-                page_of(j + 1);
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.s_full[s][j & 1]), (j >> 1) & 1));
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t x[4][32];
-            float(&v)[128] = reinterpret_cast<float(&)[128]>(x);
-            const bool cut = left < CX_KEYS || (PAGED && groups != (1u << (CX_KEYS >> gshift)) - 1u);
-            tmem_ld32_nowait(tS(s) + lanes, x[0]);
-            tmem_ld32_nowait(tS(s) + lanes + 32, x[1]);
-            tmem_wait_ld();
-            settle(x[0]), settle(x[1]);
-            tmem_ld32_nowait(tS(s) + lanes + 64, x[2]);  // (while the maximum of the first ones is taken)
-            tmem_ld32_nowait(tS(s) + lanes + 96, x[3]);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (c == 1) {
-                    tmem_wait_ld();
-                    settle(x[2]), settle(x[3]);
+        do {
+            const int n = g.n_of(s), n1 = g.n_of(1), len = g.q.len;
+            const bool pair = g.pair;
+            const int tile0 = g.tile_of(s, 0), tiles = pair ? 1 : 2;  // the stream's tiles: tile0, tile0 + tiles, ...
+            const int *bt = PAGED ? a.bt + (int64_t)g.b * a.pps : nullptr;
+            float m = -INFINITY, l = 0.f;
+            int page = 0;  // paged: the page of the next tile's group `lane`
+            auto page_of = [&](int j) {
+                if (!PAGED || j >= n) return;
+                const int key = (tile0 + j * tiles) * CX_KEYS + (lane << gshift);
+                page = -1;
+                if (lane < CX_KEYS >> gshift && key < len) page = __ldg(bt + (key >> a.pshift));
+            };
+            page_of(0);
+            for (int j = 0; j < n && ok; ++j) {
+                const int left = len - (tile0 + j * tiles) * CX_KEYS;
+                unsigned groups = 0xffffffffu;
+                if (PAGED) {
+                    groups = __ballot_sync(0xffffffffu, (unsigned)page < (unsigned)a.n_pages);
+                    page_of(j + 1);
                 }
-                if (cut) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.s_full[s]), sp));
+                sp ^= 1;
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t x[4][32];
+                float(&v)[128] = reinterpret_cast<float(&)[128]>(x);
+                const bool cut = left < CX_KEYS || (PAGED && groups != (1u << (CX_KEYS >> gshift)) - 1u);
+                tmem_ld32_nowait(tS(s) + lanes, x[0]);
+                tmem_ld32_nowait(tS(s) + lanes + 32, x[1]);
+                tmem_wait_ld();
+                settle(x[0]), settle(x[1]);
+                tmem_ld32_nowait(tS(s) + lanes + 64, x[2]);  // (while the maximum of the first ones is taken)
+                tmem_ld32_nowait(tS(s) + lanes + 96, x[3]);
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 64 * c; i < 64 * c + 64; ++i)
-                        if (i >= left || (PAGED && !(groups >> (i >> gshift) & 1u))) v[i] = -INFINITY;
-                }
-#pragma unroll
-                for (int i = 64 * c; i < 64 * c + 64; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], v[i + k], v[i + 4 + k]);
-            }
-            float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2, f = a.scale2;
-            const bool big = fabsf(top) > 16777216.f && fabsf(top) < INFINITY;
-            const float mn = fmaxf(m, top);
-            if (j == 0) m = mn;
-            const bool need = mn > m + CX_RISE;
-            if (__any_sync(0xffffffffu, big || need)) {
-                // Logits so large that a rounded maximum could leave a weight over 2: rounded first, so that the
-                // largest weight is 1.
-                if (__any_sync(0xffffffffu, big)) {
-#pragma unroll
-                    for (int i = 0; i < CX_KEYS; ++i) v[i] = __fmul_rn(v[i], f);
-                    f = 1.f;
-                }
-                if (__any_sync(0xffffffffu, need)) {  // (not of the first tile)
-                    const float al = need ? ex2(m - mn) : 1.f;
-                    if (need) m = mn;
-                    l *= al;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32_nowait(tO(s) + lanes + 32 * c, o);
+                for (int c = 0; c < 2; ++c) {
+                    if (c == 1) {
                         tmem_wait_ld();
-                        settle(o);
+                        settle(x[2]), settle(x[3]);
+                    }
+                    if (cut) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                        tmem_st32(tO(s) + lanes + 32 * c, o);
+                        for (int w = 2 * c; w < 2 * c + 2; ++w) {
+                            const uint32_t dead = dead_keys<PAGED>(32 * w, left, groups, gshift);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (dead >> i & 1) v[32 * w + i] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 64 * c; i < 64 * c + 64; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], v[i + k], v[i + 4 + k]);
+                }
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2, f = a.scale2;
+                const bool big = row && fabsf(top) > 16777216.f && fabsf(top) < INFINITY;
+                const float mn = fmaxf(m, top);
+                if (j == 0) m = mn;
+                const bool need = row && mn > m + CX_RISE;
+                if (__any_sync(0xffffffffu, big || need)) {
+                    // Logits so large that a rounded maximum could leave a weight over 2: rounded first, so that the
+                    // largest weight is 1.
+                    if (__any_sync(0xffffffffu, big)) {
+#pragma unroll
+                        for (int i = 0; i < CX_KEYS; ++i) v[i] = __fmul_rn(v[i], f);
+                        f = 1.f;
+                    }
+                    if (__any_sync(0xffffffffu, need)) {  // (not of the first tile)
+                        const float al = need ? ex2(m - mn) : 1.f;
+                        if (need) m = mn;
+                        l *= al;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32_nowait(tO(s) + lanes + 32 * c, o);
+                            tmem_wait_ld();
+                            settle(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                            tmem_st32(tO(s) + lanes + 32 * c, o);
+                        }
                     }
                 }
-            }
-            const float sh = m == -INFINITY ? 0.f : -m;
-            const uint64_t f2 = f32x2(f, f), sh2 = f32x2(sh, sh);
-            uint64_t sum[2] = {0, 0};
+                const float sh = m == -INFINITY ? 0.f : -m;
+                const uint64_t f2 = f32x2(f, f), sh2 = f32x2(sh, sh);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t p[32];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t p[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float y0, y1;
-                    unpack2(fma2(f32x2(v[64 * c + 2 * i], v[64 * c + 2 * i + 1]), f2, sh2), y0, y1);
-                    y0 = ex2(y0), y1 = ex2(y1);
-                    sum[i & 1] = add2(sum[i & 1], f32x2(y0, y1));
-                    p[i] = cvt_bf2(y0, y1);
+                    for (int i = 0; i < 32; ++i) {
+                        float y0, y1;
+                        unpack2(fma2(f32x2(v[64 * c + 2 * i], v[64 * c + 2 * i + 1]), f2, sh2), y0, y1);
+                        y0 = ex2(y0), y1 = ex2(y1);
+                        sum[i & 1] = add2(sum[i & 1], f32x2(y0, y1));
+                        p[i] = cvt_bf2(y0, y1);
+                    }
+                    tmem_st32(tS(s) + lanes + 32 * c, p);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar(bars.p_full[s][c]));  // (the product starts on the first half)
                 }
-                tmem_st32(tS(s) + lanes + 32 * c, p);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(bar(bars.p_full[s][c]));  // (the product starts on the first half)
+                float s0, s1;
+                unpack2(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
             }
-            float s0, s1;
-            unpack2(add2(sum[0], sum[1]), s0, s1);
-            l += s0 + s1;
-        }
-        // ----------------------------------------------------------------- outputs
-        const int row = row0 + (pair ? s * CX_M : 0) + r;
-        if (n > 0) ok = ok && mbar_wait(bar(bars.o_full[s]), 0);
-        if (!pair && n_of(1 - s) > 0) ok = ok && mbar_wait(bar(bars.o_full[1 - s]), 0);  // (the ring is idle then)
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) atomicExch(&s_fail, 1);
-        tc_fence_after();
-        float *xch = reinterpret_cast<float *>(cx_raw + (sR - raw));  // [dimension][row]
-        float mine = 1.f, his = 0.f;
-        if (!pair) {
-            if (s == 1) {
-                s_ml[r] = make_float2(m, l);
-                if (ok && n > 0)
+            // ------------------------------------------------------------- outputs
+            const bool some = g.nt > 0, reads = some && (pair || s == 0), join = some && !pair;
+            if (join) {  // stream 1's maxima and sums to stream 0, which reads both O
+                if (s == 1) {
+                    if (joins > 0) ok = ok && mbar_wait(bar(bars.j_free), (joins - 1) & 1);
+                    s_ml[r] = make_float2(m, l);
+                    mbar_arrive(bar(bars.j_full));
+                } else {
+                    ok = ok && mbar_wait(bar(bars.j_full), joins & 1);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (reads && ok) {
+                if (join || s == 0) ok = mbar_wait(bar(bars.o_full[0]), op0);
+                if (join ? n1 > 0 : s == 1) ok = ok && mbar_wait(bar(bars.o_full[1]), op1);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (some) op0 ^= 1;
+            if (n1 > 0) op1 ^= 1;
+            if (!ok) atomicExch(&s_fail, 1);
+            tc_fence_after();
+            if (pair || s == 0) {
+                float mine = 1.f, his = 0.f;
+                if (join) {
+                    const float2 ml = s_ml[r];
+                    mbar_arrive(bar(bars.j_free));
+                    const float mn = fmaxf(m, ml.x), sh = mn == -INFINITY ? 0.f : mn;
+                    mine = ex2(m - sh), his = n1 > 0 ? ex2(ml.x - sh) : 0.f;
+                    m = mn;
+                    l = l * mine + (n1 > 0 ? ml.y * his : 0.f);
+                }
+                const bool failed = !ok || *(volatile int *)&s_fail != 0, whole = g.begins && g.ends;
+                if (whole) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;  // (nothing seen: zeros; a sum that is NaN stays)
+                    mine *= inv, his *= inv;
+                }
+                if (failed) mine = __int_as_float(0x7fffffff);  // a wait gave up: NaN, not a wrong number
+                // A warp's 32 rows pass through its part of the query tile, to leave in whole rows: 16-byte chunk ch
+                // of a row at chunk ch ^ (row & 7), without bank conflicts for a row a lane and for 16 lanes a row.
+                const int t0 = (2 * g.x + (pair ? s : 0)) * a.tokens;           // the tile's first token
+                const int live = min(a.tokens, g.q.count - t0) * a.G;          // its rows
+                const int w0 = (warp & 3) * 32, k0 = lane >> 4, ch = lane & 15;  // the warp's first row; what a lane copies
+                const uint32_t stage = sQ + (pair ? s : 0) * CX_TILE + w0 * 256;
+                const int G = a.G, dt = 2 / G, dg = 2 - dt * G;
+                int t = (w0 + k0) / G, hd = w0 + k0 - t * G;
+                uint16_t *dst = a.out + g.b * a.ob + t0 * a.ot + (int64_t)(g.h * G) * a.oh + 8 * ch;
+                float *part = a.part + ((2 * (int64_t)blockIdx.x + (g.begins ? 1 : 0)) * a.part_rows + (pair ? s * CX_M : 0)) * CX_PART;
+                if (!whole && r < live) *reinterpret_cast<float2 *>(part + (int64_t)r * CX_PART) = make_float2(failed ? mine : m, l);
+                auto get = [&](int c, float(&o)[32]) {  // 32 dimensions of the thread's row
+                    if (ok) {
+                        tmem_ld32(tO(s) + lanes + 32 * c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= mine;
+                        if (join && n1 > 0) {
+                            float o1[32];
+                            tmem_ld32(tO(1) + lanes + 32 * c, o1);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] += o1[i] * his;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = mine;
+                    }
+                };
+                auto o_read = [&]() {
+                    tc_fence_before();
+                    mbar_arrive(bar(bars.o_free[s]));
+                    if (join) mbar_arrive(bar(bars.o_free[1]));
+                };
+                auto staged = [&]() {  // the outputs have left the query tile
+                    __syncwarp();
+                    fence_proxy_async();
+                    mbar_arrive(bar(bars.q_free));
+                    if (join) mbar_arrive(bar(bars.q_free));  // (in place of stream 1, which may be an item ahead)
+                };
+                auto put = [&](int k, uint4 x) {  // 16 lanes' row k of the warp's; every second one in turn
+                    if (w0 + k < live) *reinterpret_cast<uint4 *>(dst + t * a.ot + hd * a.oh) = x;
+                    t += dt, hd += dg;
+                    if (hd >= G) hd -= G, ++t;
+                };
+                if (!some) {  // no keys: zeros (the query tile may be the next item's already)
+                    for (int k = k0; k < 32; k += 2) put(k, make_uint4(0, 0, 0, 0));
+                } else if (whole) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
-                        tmem_ld32(tO(1) + lanes + 32 * c, o);
+                        get(c, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) xch[(32 * c + i) * CX_M + r] = o[i];
+                        for (int i = 0; i < 4; ++i)
+                            sts16(stage + lane * 256 + (((4 * c + i) ^ (lane & 7)) << 4), cvt_bf2(o[8 * i], o[8 * i + 1]),
+                                  cvt_bf2(o[8 * i + 2], o[8 * i + 3]), cvt_bf2(o[8 * i + 4], o[8 * i + 5]), cvt_bf2(o[8 * i + 6], o[8 * i + 7]));
                     }
-            }
-            softmax_sync();
-            if (s == 0) {
-                const float2 ml = s_ml[r];
-                const float mn = fmaxf(m, ml.x), sh = mn == -INFINITY ? 0.f : mn;
-                mine = ex2(m - sh), his = n_of(1) > 0 ? ex2(ml.x - sh) : 0.f;
-                m = mn;
-                l = l * mine + ml.y * his;
-            }
-        }
-        const bool failed = *(volatile int *)&s_fail != 0;
-        if (pair || s == 0) {
-            const bool write = row < rows;
-            const uint32_t stage = sQ + (pair ? s : 0) * CX_TILE + (warp & 3) * 32 * 256;  // (the queries have been read)
-            float *part = a.part + (((int64_t)split * gridDim.y + u) * a.rows_pad + row) * CX_PART;
-            const float inv = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (nothing seen: zeros; a sum that is NaN stays)
-            mine *= inv, his *= inv;
-            if (a.splits > 1 && write) *reinterpret_cast<float2 *>(part) = make_float2(failed ? __int_as_float(0x7fffffff) : m, l);
+                    o_read();
+                    __syncwarp();
+                    uint4 y[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float o[32];
-                if (n > 0) {
-                    tmem_ld32(tO(s) + lanes + 32 * c, o);
+                    for (int i = 0; i < 16; ++i) y[i] = lds16(stage + (k0 + 2 * i) * 256 + ((ch ^ ((k0 + 2 * i) & 7)) << 4));
+                    staged();  // (before the stores leave)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) put(k0 + 2 * i, y[i]);
                 } else {
+                    // a partial, fp32, 64 dimensions at a time
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
-                }
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
+                        get(c, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    o[i] *= mine;
-                    if (!pair && n_of(1) > 0) o[i] += xch[(32 * c + i) * CX_M + r] * his;
-                    if (failed) o[i] = __int_as_float(0x7fffffff);  // a wait gave up: NaN, not a wrong number
-                }
-                if (write && a.splits > 1) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4 *>(part + 4 + 32 * c + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                } else {
-                    put32(stage, lane, c, o);
+                        for (int i = 0; i < 8; ++i)
+                            sts16(stage + lane * 256 + (((8 * (c & 1) + i) ^ (lane & 7)) << 4), __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                                  __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+                        if (c & 1) {
+                            __syncwarp();
+#pragma unroll 4
+                            for (int k = k0; k < 32; k += 2) {
+                                const uint4 x = lds16(stage + k * 256 + ((ch ^ (k & 7)) << 4));
+                                if (w0 + k < live) *reinterpret_cast<uint4 *>(part + (int64_t)(w0 + k) * CX_PART + 4 + 32 * (c - 1) + 4 * ch) = x;
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    o_read();
+                    staged();
                 }
                 __syncwarp();
             }
-            if (a.splits == 1) {
-                // two rows at a time, 16 lanes each
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    const int k = 2 * i + (lane >> 4), ch = lane & 15, to = row - lane + k;
-                    uint4 x;
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                                 : "r"(stage + k * 256 + ((ch ^ (k & 7)) << 4)));
-                    if (to >= rows) continue;
-                    const int t = to / a.G, g = to - t * a.G;
-                    *reinterpret_cast<uint4 *>(a.out + b * a.ob + t * a.ot + (int64_t)(h * a.G + g) * a.oh + 8 * ch) = x;
-                }
-            }
-        }
-        tc_fence_before();
+            joins += join;
+        } while (next_item());
     }
+    tc_fence_before();
     __syncthreads();
     if (warp == CX_MMA) {
         tc_fence_after();
@@ -551,109 +904,131 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     }
 }
 
-// Folds the partials of the splits: a warp per query row, four dimensions a lane.
-__global__ void __launch_bounds__(256) k_cross_merge(CrossArgs a, int units) {
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+// Folds the partials of an item that several CTAs share: boundary blockIdx.x + 1 of the chunks lies inside it,
+// and is the first one that does; a warp per query row, four dimensions a lane.
+__global__ void __launch_bounds__(256) k_cross_merge(CrossArgs a, int ctas) {
     const int lane = threadIdx.x & 31;
-    const int64_t per = (int64_t)a.t_max * a.G;
-    if (i >= units * per) return;
-    const int u = (int)(i / per), row = (int)(i - u * per), b = u / a.h_kv, h = u - b * a.h_kv;
-    if (row >= cross_rows(a, b)) return;
-    const float *p = a.part + ((int64_t)u * a.rows_pad + row) * CX_PART;
-    const int64_t step = (int64_t)units * a.rows_pad * CX_PART;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool nan = false;
-    for (int k = 0; k < a.splits; k += 4) {
-        float2 ml[4];
-        float4 v[4];
+    Segment g;
+    g.plan(a, ctas);
+    const int64_t chunk = g.chunk, p = (blockIdx.x + 1) * chunk;
+    if (p < g.total) g.seek(a, p);
+    pdl_wait();  // (by every block: nothing behind this kernel starts before k_cross has ended)
+    if (p >= g.total) return;
+    const int64_t begin = p - g.at, end = begin + g.units();
+    if (g.at == 0 || begin < (int64_t)blockIdx.x * chunk) return;
+    const int parts = (int)((end - 1) / chunk) - blockIdx.x + 1;  // of CTAs blockIdx.x ..
+    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < a.part_rows; row += gridDim.y * 8) {
+        const int r = row & (CX_M - 1), tile = 2 * g.x + (row >= CX_M);
+        const int t = tile * a.tokens + r / a.G, hd = r % a.G;
+        if (r >= a.tokens * a.G || t >= g.q.count || (g.x >= g.q.pairs && row >= CX_M)) continue;
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool nan = false;
+        for (int k = 0; k < parts; k += 4) {
+            float2 ml[4];
+            float4 v[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const bool ok = k + x < a.splits;
-            const float *r = p + (k + x) * step;
-            ml[x] = ok ? __ldcg(reinterpret_cast<const float2 *>(r)) : make_float2(-INFINITY, 0.f);
-            v[x] = ok ? __ldcg(reinterpret_cast<const float4 *>(r + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+            for (int x = 0; x < 4; ++x) {
+                const bool ok = k + x < parts;
+                const int64_t slot = 2 * ((int64_t)blockIdx.x + k + x) + (k + x == 0 ? 1 : 0);
+                const float *from = a.part + (slot * a.part_rows + row) * CX_PART;
+                ml[x] = ok ? __ldcg(reinterpret_cast<const float2 *>(from)) : make_float2(-INFINITY, 0.f);
+                v[x] = ok ? __ldcg(reinterpret_cast<const float4 *>(from + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            nan |= ml[x].x != ml[x].x;
-            const float mn = fmaxf(m, ml[x].x), sh = mn == -INFINITY ? 0.f : mn;
-            const float f = ex2(m - sh), g = ex2(ml[x].x - sh);
-            m = mn;
-            l = l * f + ml[x].y * g;
-            acc.x = acc.x * f + v[x].x * g, acc.y = acc.y * f + v[x].y * g;
-            acc.z = acc.z * f + v[x].z * g, acc.w = acc.w * f + v[x].w * g;
+            for (int x = 0; x < 4; ++x) {
+                nan |= ml[x].x != ml[x].x;
+                const float mn = fmaxf(m, ml[x].x), sh = mn == -INFINITY ? 0.f : mn;
+                const float f = ex2(m - sh), e = ex2(ml[x].x - sh);
+                m = mn;
+                l = l * f + ml[x].y * e;
+                acc.x = acc.x * f + v[x].x * e, acc.y = acc.y * f + v[x].y * e;
+                acc.z = acc.z * f + v[x].z * e, acc.w = acc.w * f + v[x].w * e;
+            }
         }
+        const float inv = nan ? __int_as_float(0x7fffffff) : l == 0.f ? 0.f : 1.f / l;
+        uint16_t *dst = a.out + g.b * a.ob + t * a.ot + (int64_t)(g.h * a.G + hd) * a.oh + 4 * lane;
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_bf2(acc.x * inv, acc.y * inv), cvt_bf2(acc.z * inv, acc.w * inv));
     }
-    const float inv = nan ? __int_as_float(0x7fffffff) : l == 0.f ? 0.f : 1.f / l;
-    const int t = row / a.G, g = row - t * a.G;
-    uint16_t *dst = a.out + b * a.ob + t * a.ot + (int64_t)(h * a.G + g) * a.oh + 4 * lane;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_bf2(acc.x * inv, acc.y * inv), cvt_bf2(acc.z * inv, acc.w * inv));
 }
 
-// Splits of the keys for `ctas` CTAs over up to `tiles` key tiles: the number whose waves end first,
-// in tile times, a CTA's start and end costing about 6 and the fold of the partials about 12.
-int cross_splits(int64_t ctas, int64_t tiles) {
-    const int64_t sms = num_sms();
-    int best = 1;
-    int64_t cost = INT64_MAX;
-    for (int s = 1; s <= 64 && (s == 1 || tiles >= 4LL * s); ++s) {
-        const int64_t c = ceil_div64(ctas * s, sms) * (ceil_div64(tiles, s) + 6) + (s > 1 ? 12 : 0);
-        if (c < cost) cost = c, best = s;
-    }
-    return best;
+// The grid and its work, by what the largest lengths and counts make of it.  Equal shares cost partials (up to 256 KB
+// written and read by each CTA) and their fold, as much as about 8 units of work; whole items leave the SMs
+// with unequal ones (8 sequences, 16 heads, 500 tokens to 375 .. 1500 rows: whole items 36 us, equal shares 105).
+static void cross_grid(int batch, int h_kv, int G, int t_max, int n_max, int64_t &ctas, int &whole) {
+    const int64_t tiles = ceil_div64(t_max, CX_M / G), nt = ceil_div64(n_max, CX_KEYS), per = ceil_div64(tiles, 2);
+    const int64_t units = (int64_t)batch * h_kv, all = units * (tiles / 2 * nt + tiles % 2 * ceil_div64(nt, 2));
+    const int64_t sms = num_sms(), longest = tiles > 1 ? nt : ceil_div64(nt, 2);
+    whole = units * per <= (1 << 30) && ceil_div64(units * per, sms) * longest <= all / sms + 8;
+    ctas = std::min(sms, whole ? units * per : ceil_div64(all, Segment::CX_LEAST));
 }
 
-static bool row_map(CUtensorMap *map, const void *base, int64_t rows, int64_t h, int64_t b, int64_t sn, int64_t sh,
-                    int64_t sb, int box_rows) {
+// Tensor map of bf16 rows, `dims` of which the first is a row's 128 elements; strides in elements, of no account for a
+// dim of one entry.  Boxes of 64 elements by `box`.  False if TMA cannot describe it.
+static bool row_map(CUtensorMap *map, const void *base, int n, const int64_t *dims, const int64_t *strides, const int *box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)MOG_D, (cuuint64_t)rows, (cuuint64_t)h, (cuuint64_t)b};
-    // (a dim of one entry: any stride)
-    const cuuint64_t strides[3] = {(cuuint64_t)sn * 2, h > 1 ? (cuuint64_t)sh * 2 : 256, b > 1 ? (cuuint64_t)sb * 2 : 256};
-    for (int i = 0; i < 3; ++i)
-        if (strides[i] == 0 || (strides[i] & 15) || strides[i] >= (1ull << 40)) return false;
-    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < n; ++i) {
+        d[i] = (cuuint64_t)dims[i], bx[i] = (cuuint32_t)box[i], es[i] = 1;
+        if (i == 0) continue;
+        st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i] * 2 : 256;
+        if (st[i - 1] == 0 || (st[i - 1] & 15) || st[i - 1] >= (1ull << 40)) return false;
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void *>(base), d, st, bx, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+static int cross_part_rows(int G, int t_max) { return t_max > CX_M / G ? 2 * CX_M : CX_M; }
+
 size_t cross_scratch(int batch, int h_kv, int G, int t_max, int n_max) {
-    const int64_t rows = (int64_t)t_max * G, qt = ceil_div64(rows, 2 * CX_M), units = (int64_t)batch * h_kv;
-    const int splits = cross_splits(units * qt, ceil_div64(n_max, CX_KEYS));
-    return splits > 1 ? (size_t)splits * units * rows * CX_PART * sizeof(float) : 0;
+    int64_t ctas;
+    int whole;
+    cross_grid(batch, h_kv, G, t_max, n_max, ctas, whole);
+    return whole ? 0 : (size_t)2 * ctas * cross_part_rows(G, t_max) * CX_PART * sizeof(float);
 }
 
 cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, int batch, const RowsIn &r, float *scratch,
                          cudaStream_t s) {
     CrossArgs a{};
-    a.q = static_cast<const uint16_t *>(r.q), a.out = static_cast<uint16_t *>(r.qo);
-    a.qb = r.qs[0], a.qt = r.qs[1], a.qh = r.qs[2], a.ob = r.os[0], a.ot = r.os[1], a.oh = r.os[2];
-    a.lengths = lengths, a.count = r.count, a.n_max = n_max, a.t_max = r.t_max, a.h_kv = r.h_kv, a.G = r.h_q / r.h_kv;
+    a.out = static_cast<uint16_t *>(r.qo), a.ob = r.os[0], a.ot = r.os[1], a.oh = r.os[2];
+    a.lengths = lengths, a.count = r.count, a.n_max = n_max, a.t_max = r.t_max, a.batch = batch, a.h_kv = r.h_kv;
+    a.G = r.h_q / r.h_kv, a.tokens = CX_M / a.G;
     a.bt = c->block_table, a.pshift = c->block_table ? log2_exact(c->page_rows) : 0, a.pps = c->pages_per_seq;
     a.n_pages = c->n_pages;
     a.scale2 = (float)(1.4426950408889634 / sqrt((double)MOG_D));
     const bool paged = c->block_table != nullptr;
     // a stride of 0 (one memory for all): a dim of one entry
     const int64_t h = !paged && c->stride_h == 0 ? 1 : r.h_kv, b = paged ? c->n_pages : c->stride_b == 0 ? 1 : batch;
-    a.hmul = h > 1, a.bmul = b > 1;
-    CUtensorMap km, vm;
-    const int box = paged ? std::min(CX_KEYS, c->page_rows) : CX_KEYS;
-    const int64_t n = paged ? c->page_rows : c->n_cap;
-    if (!row_map(&km, c->k, n, h, b, c->stride_n, c->stride_h, c->stride_b, box) ||
-        !row_map(&vm, c->v, n, h, b, c->stride_n, c->stride_h, c->stride_b, box))
+    const int64_t qb = r.qs[0] == 0 ? 1 : batch;
+    a.hmul = h > 1, a.bmul = b > 1, a.qmul = qb > 1;
+    CUtensorMap qm, km, vm;
+    const int64_t dims[4] = {MOG_D, paged ? c->page_rows : c->n_cap, h, b}, st[4] = {1, c->stride_n, c->stride_h, c->stride_b};
+    const int box[4] = {64, paged ? std::min(CX_KEYS, c->page_rows) : CX_KEYS, 1, 1};
+    const int64_t qdims[5] = {MOG_D, a.G, r.t_max, r.h_kv, qb}, qst[5] = {1, r.qs[2], r.qs[1], a.G * r.qs[2], r.qs[0]};
+    const int qbox[5] = {64, a.G, a.tokens, 1, 1};
+    if (!row_map(&km, c->k, 4, dims, st, box) || !row_map(&vm, c->v, 4, dims, st, box) || !row_map(&qm, r.q, 5, qdims, qst, qbox))
         return cudaErrorInvalidValue;
-    const int64_t rows = (int64_t)r.t_max * a.G, qt = ceil_div64(rows, 2 * CX_M), units = (int64_t)batch * r.h_kv;
-    a.splits = cross_splits(units * qt, ceil_div64(n_max, CX_KEYS));
-    a.rows_pad = (int)rows, a.part = scratch;
+    int64_t ctas;
+    cross_grid(batch, r.h_kv, a.G, r.t_max, n_max, ctas, a.whole);
+    a.part = scratch, a.part_rows = cross_part_rows(a.G, r.t_max);
     const auto fn = paged ? k_cross<true> : k_cross<false>;
-    const cudaError_t e = ensure_smem((const void *)fn, CX_SMEM);
+    cudaError_t e = ensure_smem((const void *)fn, CX_SMEM);
     if (e != cudaSuccess) return e;
-    fn<<<dim3((unsigned)qt, (unsigned)units, a.splits), CX_THREADS, CX_SMEM, s>>>(a, km, vm);
-    if (a.splits > 1) k_cross_merge<<<(unsigned)ceil_div64(units * rows, 8), 256, 0, s>>>(a, (int)units);
-    return cudaGetLastError();
+    fn<<<(unsigned)ctas, CX_THREADS, CX_SMEM, s>>>(a, qm, km, vm);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.whole || ctas == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas - 1, 4);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_cross_merge, a, (int)ctas);
 }
 
 }  // namespace mog

@@ -94,6 +94,7 @@ CASES = [  # lens, T, H, G, page
     ((500, 33), 40, 2, 8, 32), ((1111, 2000), 1, 2, 4, 64), ((777,), 200, 2, 2, 128), ((900, 300), 70, 1, 7, 256),
     ((20000,), 3, 2, 5, 64), ((20000, 9000), 1, 4, 4, 0), ((6000,), 300, 1, 1, 16),
     ((20000, 19000, 20000, 17000), 16, 16, 5, 64), ((15000, 16384), 80, 20, 4, 0),  # long streams, one query tile and two
+    ((5000,) * 8, 256, 32, 1, 0), ((5000, 4999, 5120, 5000, 4993, 5001, 5000, 5000), 300, 24, 1, 64),  # sequences alike: whole rounds first
 ]
 
 
@@ -117,10 +118,32 @@ def test_counts_strides_and_slack(page):
     m.check(q, out, G, count, fill=5.0)
     # lengths are clamped
     again = mog.cross_attend(*m.cache, m.lengths - torch.tensor([0, 1000, 0, 0], dtype=torch.int32, device=DEV), m.n_max, q)
-    assert torch.equal(again[0], out[0])
+    m.check(q, again, G)  # (not its bits: how the work is shared depends on all lengths and counts)
     big = Made(22, (300,), 1)
     a = mog.cross_attend(*big.cache, ints(1 << 30), 300, q[:1, :, :2])
     assert torch.equal(a, mog.cross_attend(*big.cache, ints(300), 300, q[:1, :, :2]))
+
+
+@pytest.mark.parametrize("page", [0, 32])
+@pytest.mark.parametrize("T,H,G,longest", [(1, 8, 2, 700), (40, 4, 4, 700), (100, 3, 3, 500), (300, 4, 1, 130), (7, 2, 1, 6000)])
+def test_many_sequences(T, H, G, longest, page):
+    """Lists of many short items, one query tile and two, with sequences that have no rows and no tokens."""
+    g = torch.Generator().manual_seed(T)
+    B = 45
+    lens = torch.randint(0, longest, (B,), generator=g)
+    lens[torch.tensor([0, 7, 8, B - 1])] = torch.tensor([0, 0, 128, 0])
+    count = torch.randint(-2, T + 3, (B,), generator=g)
+    count[torch.tensor([3, 4, B - 2])] = 0
+    m = Made(T, tuple(lens.tolist()), H, page)
+    q = randn(9, B, T, H * G, D)
+    out = torch.full(q.shape, 2.0, dtype=torch.bfloat16, device=DEV)
+    cnt = count.to(torch.int32).to(DEV)
+    mog.cross_attend(*m.cache, m.lengths, m.n_max, q, count=cnt, out=out)
+    m.check(q, out, G, count.tolist(), fill=2.0)
+    again = mog.cross_attend(*m.cache, m.lengths, m.n_max, q, count=cnt, out=torch.full_like(out, 2.0))
+    assert torch.equal(again, out)
+    cnt.zero_()
+    assert (mog.cross_attend(*m.cache, m.lengths, m.n_max, q, count=cnt, out=torch.full_like(out, 2.0)) == 2).all()
 
 
 def test_pages_that_do_not_exist_are_left_out():
