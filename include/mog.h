@@ -582,7 +582,8 @@ int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_ma
  *                initial contents needed, not shared by calls that overlap on the GPU
  * Products of bf16 with fp32 sums; the weights are rounded to bf16 for the second one, an error of the
  * size of the output's own rounding.  d must be 128, h_q / h_kv <= 16, batch * h_kv <= 65535, t_max *
- * h_q <= 2^30, n_max <= 2^30.  Should a bounded wait inside the kernel run out, its rows are NaN.
+ * h_q <= 2^30, n_max <= 2^30, and the products of 256 query rows by 128 keys that make up the work at
+ * most 2^30.  Should a bounded wait inside the kernel run out, its rows are NaN.
  */
 int mog_cross_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max,
                             int32_t n_max, size_t *bytes);

@@ -1030,6 +1030,8 @@ extern "C" int mog_cross_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q,
     if (!bytes || batch <= 0 || h_kv <= 0 || h_q <= 0 || t_max <= 0 || n_max <= 0) return MOG_ERR_INVALID_ARG;
     if (d != MOG_D || h_q % h_kv != 0 || h_q / h_kv > MOG_MAX_G) return MOG_ERR_SHAPE;
     if (n_max > (1 << 30) || (int64_t)batch * h_kv > 65535 || (int64_t)t_max * h_q > (1 << 30)) return MOG_ERR_SHAPE;
+    const int64_t tiles = ceil_div64(t_max, 128 / (h_q / h_kv));  // of queries; work is counted in 32 bits
+    if ((int64_t)batch * h_kv * ceil_div64(tiles, 2) > (1 << 30) / ceil_div64(n_max, 128)) return MOG_ERR_SHAPE;
     *bytes = cross_scratch(batch, h_kv, h_q / h_kv, t_max, n_max);
     return MOG_OK;
 }

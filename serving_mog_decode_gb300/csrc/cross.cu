@@ -53,6 +53,7 @@ struct CrossArgs {
     int n_max, t_max, batch, h_kv, G;
     int tokens;      // of a query tile
     int qmul;        // 0 where the queries of all sequences are one in memory
+    int out32;       // rows of the output begin at multiples of 32 bytes
     const int *bt;
     int pshift, pps, n_pages;
     int bmul, hmul;  // contiguous: 0 where all sequences (heads) are one in memory
@@ -67,8 +68,10 @@ struct CrossArgs {
 struct CrossSeq {
     int count, len, nt, pairs, units, half;
     __device__ __forceinline__ void load(const CrossArgs &a, int b) {
-        count = a.count ? min(max(a.count[b], 0), a.t_max) : a.t_max;
-        len = min(max(a.lengths[b], 0), a.n_max);
+        set(a, a.count ? min(max(a.count[b], 0), a.t_max) : a.t_max, min(max(a.lengths[b], 0), a.n_max));
+    }
+    __device__ __forceinline__ void set(const CrossArgs &a, int count_, int len_) {
+        count = count_, len = len_;
         nt = (int)(((unsigned)len + CX_KEYS - 1) / CX_KEYS);
         const int tiles = (count + a.tokens - 1) / a.tokens;
         pairs = tiles >> 1;
@@ -76,7 +79,7 @@ struct CrossSeq {
         half = tiles & 1 ? max((nt + 1) >> 1, 1) : 0;
     }
     __device__ __forceinline__ int items() const { return pairs + (half > 0); }  // of a KV head
-    __device__ __forceinline__ int64_t cost() const { return (int64_t)pairs * units + half; }
+    __device__ __forceinline__ int cost() const { return pairs * units + half; }
 };
 
 // Whole items: sequences by their number of key tiles, the longest first, and where each one's items end in that
@@ -84,17 +87,18 @@ struct CrossSeq {
 struct CrossOrder {
     int n, items;
     uint8_t seq[CX_SORT];
-    int end[CX_SORT];
+    int end[CX_SORT], count[CX_SORT], len[CX_SORT];  // (count, len: by sequence)
     // (by the whole CTA; followed by a barrier)
     __device__ __forceinline__ void make(const CrossArgs &a, int (&need)[CX_SORT], int (&key)[CX_SORT]) {
         const int tid = threadIdx.x, per = ((a.t_max + a.tokens - 1) / a.tokens + 1) / 2;
-        const bool sort = a.batch <= CX_SORT && (int64_t)a.batch * a.h_kv * per > gridDim.x;
+        const bool sort = a.batch <= CX_SORT && a.batch * a.h_kv * per > (int)gridDim.x;
         if (tid == 0) n = sort ? a.batch : 0, items = per;
         if (!sort) return;
         if (tid < a.batch) {
             CrossSeq c;
             c.load(a, tid);
             need[tid] = c.items() * a.h_kv, key[tid] = c.nt;
+            count[tid] = c.count, len[tid] = c.len;
         }
         __syncthreads();
         if (tid < a.batch) {
@@ -107,25 +111,25 @@ struct CrossOrder {
     }
 };
 
-// What a CTA works on next: `n` key tiles from `first` on of an item.
+// What a CTA works on next: `nt` key tiles from `first` on of an item.  The units of all items stay below 2^30.
 struct Segment {
     CrossSeq q;
     int b, h, x;      // sequence, KV head, item
     int at;           // its unit in the item
-    int64_t left;     // units of the CTA from here on;  whole items: how many it has had
+    int left;         // units of the CTA from here on;  whole items: how many it has had
     bool pair, begins, ends;
     int first, nt;
     // Equal shares: the list's units, a share.  Sequences alike: CTAs first take `rounds` whole items each (`skipped`
     // in all), in step with one another, so that those of a KV head read its tiles from L2 at the same time; the
     // list is of the other items, pairs and then halves.
-    int64_t total, chunk, skipped, index;
+    int total, chunk, skipped, index;
     int rounds;
     bool even;
 
     __device__ __forceinline__ int units() const { return x < q.pairs ? q.units : q.half; }
-    __device__ __forceinline__ void set(int64_t most) {
+    __device__ __forceinline__ void set(int most) {
         pair = x < q.pairs;
-        const int n = (int)min((int64_t)(units() - at), most);
+        const int n = min(units() - at, most);
         begins = at == 0, ends = at + n == units();
         first = pair ? at : 2 * at;
         nt = min(pair ? n : 2 * n, q.nt - first);
@@ -144,32 +148,32 @@ struct Segment {
         rounds = 0;
         if (even) {
             q.load(a, 0);
-            const int64_t units = (int64_t)a.batch * a.h_kv, p = units * q.pairs;
-            rounds = (int)(p / ctas);
-            skipped = (int64_t)rounds * ctas;
+            const int units = a.batch * a.h_kv, p = units * q.pairs;
+            rounds = p / ctas;
+            skipped = rounds * ctas;
             total = (p - skipped) * q.units + units * q.half;
         }
-        chunk = max((total + ctas - 1) / ctas, (int64_t)CX_LEAST);
+        chunk = max((total + ctas - 1) / ctas, CX_LEAST);
     }
     static constexpr int CX_LEAST = 3;  // units of a share: fewer are not worth a CTA's start
     // sequences alike: the next whole item
     __device__ __forceinline__ bool round(const CrossArgs &a) {
         item(a, left++ * gridDim.x + blockIdx.x);
         q.load(a, b);
-        set(INT64_MAX);
+        set(INT32_MAX);
         return true;
     }
     // sequences alike: pair item i, or half item i - all pairs
-    __device__ __forceinline__ void item(const CrossArgs &a, int64_t i) {
-        const int64_t p = (int64_t)a.batch * a.h_kv * q.pairs, u = i < p ? i / q.pairs : i - p;
-        x = i < p ? (int)(i - u * q.pairs) : q.pairs;
-        b = (int)(u / a.h_kv), h = (int)(u - (int64_t)b * a.h_kv);
+    __device__ __forceinline__ void item(const CrossArgs &a, int i) {
+        const int p = a.batch * a.h_kv * q.pairs, u = i < p ? i / q.pairs : i - p;
+        x = i < p ? i - u * q.pairs : q.pairs;
+        b = u / a.h_kv, h = u - b * a.h_kv;
         index = i, at = 0;
     }
     // the CTA's share of the list (called by full warps unless the sequences are alike)
     __device__ __forceinline__ bool share(const CrossArgs &a) {
         rounds = 0;
-        const int64_t p = (int64_t)blockIdx.x * chunk;
+        const int p = blockIdx.x * chunk;  // (below total + 2^30)
         if (p >= total) return false;
         left = min(chunk, total - p);
         seek(a, p);
@@ -179,12 +183,12 @@ struct Segment {
     // whole items: the next one of the snake
     __device__ __forceinline__ bool take(const CrossArgs &a, const CrossOrder &o) {
         while (true) {
-            const int64_t i = left * gridDim.x + (left & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            const int i = left * gridDim.x + (left & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             ++left;
             if (o.n == 0) {  // one item each, or too many sequences to sort: the sequences as they are
-                const int64_t unit = i / o.items;
-                if (unit >= (int64_t)a.batch * a.h_kv) return false;
-                b = (int)(unit / a.h_kv), h = (int)(unit - (int64_t)b * a.h_kv), x = (int)(i - unit * o.items);
+                const int unit = i / o.items;
+                if (unit >= a.batch * a.h_kv) return false;
+                b = unit / a.h_kv, h = unit - b * a.h_kv, x = i - unit * o.items;
                 q.load(a, b);
                 if (x < q.items()) break;
             } else {
@@ -192,14 +196,14 @@ struct Segment {
                 while (k < o.n && o.end[k] <= i) ++k;
                 if (k == o.n) return false;
                 b = o.seq[k];
-                q.load(a, b);
-                const int r = (int)(i - (k ? o.end[k - 1] : 0)), n = max(q.items(), 1);
+                q.set(a, o.count[b], o.len[b]);
+                const int r = i - (k ? o.end[k - 1] : 0), n = max(q.items(), 1);
                 h = min(r / n, a.h_kv - 1), x = r - r / n * n;
                 break;
             }
         }
         at = 0;
-        set(INT64_MAX);
+        set(INT32_MAX);
         return true;
     }
     // units of all sequences, and whether these are alike
@@ -207,7 +211,7 @@ struct Segment {
         const int lane = threadIdx.x & 31;
         CrossSeq f;
         f.load(a, 0);
-        int64_t s = 0;
+        int s = 0;
         bool same = true;
         for (int i = lane; i < a.batch; i += 32) {
             CrossSeq c;
@@ -221,26 +225,26 @@ struct Segment {
         even = __all_sync(0xffffffffu, same) && s > 0;
     }
     // The item that holds unit p of the list (p < total; called by full warps unless the sequences are alike).
-    __device__ __forceinline__ void seek(const CrossArgs &a, int64_t p) {
+    __device__ __forceinline__ void seek(const CrossArgs &a, int p) {
         if (even) {
-            const int64_t pairs = (int64_t)a.batch * a.h_kv * q.pairs, first = (pairs - skipped) * q.units;
-            const int64_t i = p < first ? p / q.units : (p - first) / q.half, n = p < first ? i * q.units : first + i * q.half;
+            const int pairs = a.batch * a.h_kv * q.pairs, first = (pairs - skipped) * q.units;
+            const int i = p < first ? p / q.units : (p - first) / q.half, n = p < first ? i * q.units : first + i * q.half;
             item(a, (p < first ? skipped : pairs) + i);
-            at = (int)(p - n);
+            at = p - n;
             q.load(a, b);
             return;
         }
         const int lane = threadIdx.x & 31;
-        int64_t base = 0;
+        int base = 0;
         b = a.batch - 1;
         for (int b0 = 0; b0 < a.batch; b0 += 32) {
             CrossSeq c;
-            int64_t mine = 0;
+            int mine = 0;
             if (b0 + lane < a.batch) c.load(a, b0 + lane), mine = c.cost() * a.h_kv;
-            int64_t end = mine;
+            int end = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, end, o);
+                const int v = __shfl_up_sync(0xffffffffu, end, o);
                 if (lane >= o) end += v;
             }
             const unsigned in = __ballot_sync(0xffffffffu, base + end > p);
@@ -253,16 +257,16 @@ struct Segment {
             base += __shfl_sync(0xffffffffu, end, 31);
         }
         q.load(a, b);
-        const int64_t c = max(q.cost(), (int64_t)1), r = p - base;
-        h = min((int)(r / c), a.h_kv - 1);
-        const int64_t o = r - h * c;
-        x = min((int)(o / q.units), q.pairs);
-        at = (int)(o - (int64_t)x * q.units);
+        const int c = max(q.cost(), 1), r = p - base;
+        h = min(r / c, a.h_kv - 1);
+        const int o = r - h * c;
+        x = min(o / q.units, q.pairs);
+        at = o - x * q.units;
     }
     __device__ __forceinline__ bool next(const CrossArgs &a, const CrossOrder &o) {
         if (a.whole) return take(a, o);
         if (rounds) return left < rounds ? round(a) : share(a);
-        left -= min((int64_t)(units() - at), left);
+        left -= min(units() - at, left);
         if (left <= 0) return false;
         if (even) {
             item(a, index + 1);
@@ -363,6 +367,10 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 x;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
     return x;
+}
+__device__ __forceinline__ void stg32(void *p, const uint32_t (&x)[8]) {  // 32-byte aligned
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -663,7 +671,11 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         bool ok = true;
         do {
             const int n = g.n_of(s), n1 = g.n_of(1), len = g.q.len;
-            const bool pair = g.pair;
+            const bool pair = g.pair, whole = g.begins && g.ends;
+            auto q_done = [&]() {  // the thread's part in freeing the query tiles
+                fence_proxy_async();
+                mbar_arrive(bar(bars.q_free));
+            };
             const int tile0 = g.tile_of(s, 0), tiles = pair ? 1 : 2;  // the stream's tiles: tile0, tile0 + tiles, ...
             const int *bt = PAGED ? a.bt + (int64_t)g.b * a.pps : nullptr;
             float m = -INFINITY, l = 0.f;
@@ -685,6 +697,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.s_full[s]), sp));
                 sp ^= 1;
                 if (!ok) break;
+                if (j + 1 == n && pair && whole) q_done();  // (all of the stream's logits have been computed)
                 tc_fence_after();
                 uint32_t x[4][32];
                 float(&v)[128] = reinterpret_cast<float(&)[128]>(x);
@@ -780,6 +793,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 }
                 ok = __all_sync(0xffffffffu, ok);
             }
+            if (!ok && pair && whole && some) q_done();
             if (reads && ok) {
                 if (join || s == 0) ok = mbar_wait(bar(bars.o_full[0]), op0);
                 if (join ? n1 > 0 : s == 1) ok = ok && mbar_wait(bar(bars.o_full[1]), op1);
@@ -794,30 +808,26 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 if (join) {
                     const float2 ml = s_ml[r];
                     mbar_arrive(bar(bars.j_free));
+                    if (whole) q_done(), q_done();  // (for stream 1 too, which may be an item ahead)
                     const float mn = fmaxf(m, ml.x), sh = mn == -INFINITY ? 0.f : mn;
                     mine = ex2(m - sh), his = n1 > 0 ? ex2(ml.x - sh) : 0.f;
                     m = mn;
                     l = l * mine + (n1 > 0 ? ml.y * his : 0.f);
                 }
-                const bool failed = !ok || *(volatile int *)&s_fail != 0, whole = g.begins && g.ends;
+                const bool failed = !ok || *(volatile int *)&s_fail != 0;
                 if (whole) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;  // (nothing seen: zeros; a sum that is NaN stays)
                     mine *= inv, his *= inv;
                 }
                 if (failed) mine = __int_as_float(0x7fffffff);  // a wait gave up: NaN, not a wrong number
-                // A warp's 32 rows pass through its part of the query tile, to leave in whole rows: 16-byte chunk ch
-                // of a row at chunk ch ^ (row & 7), without bank conflicts for a row a lane and for 16 lanes a row.
                 const int t0 = (2 * g.x + (pair ? s : 0)) * a.tokens;           // the tile's first token
                 const int live = min(a.tokens, g.q.count - t0) * a.G;          // its rows
                 const int w0 = (warp & 3) * 32, k0 = lane >> 4, ch = lane & 15;  // the warp's first row; what a lane copies
                 const uint32_t stage = sQ + (pair ? s : 0) * CX_TILE + w0 * 256;
-                const int G = a.G, dt = 2 / G, dg = 2 - dt * G;
-                int t = (w0 + k0) / G, hd = w0 + k0 - t * G;
-                uint16_t *dst = a.out + g.b * a.ob + t0 * a.ot + (int64_t)(g.h * G) * a.oh + 8 * ch;
                 float *part = a.part + ((2 * (int64_t)blockIdx.x + (g.begins ? 1 : 0)) * a.part_rows + (pair ? s * CX_M : 0)) * CX_PART;
                 if (!whole && r < live) *reinterpret_cast<float2 *>(part + (int64_t)r * CX_PART) = make_float2(failed ? mine : m, l);
                 auto get = [&](int c, float(&o)[32]) {  // 32 dimensions of the thread's row
-                    if (ok) {
+                    if (some && ok) {
                         tmem_ld32(tO(s) + lanes + 32 * c, o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] *= mine;
@@ -837,40 +847,39 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                     mbar_arrive(bar(bars.o_free[s]));
                     if (join) mbar_arrive(bar(bars.o_free[1]));
                 };
-                auto staged = [&]() {  // the outputs have left the query tile
-                    __syncwarp();
-                    fence_proxy_async();
-                    mbar_arrive(bar(bars.q_free));
-                    if (join) mbar_arrive(bar(bars.q_free));  // (in place of stream 1, which may be an item ahead)
-                };
-                auto put = [&](int k, uint4 x) {  // 16 lanes' row k of the warp's; every second one in turn
-                    if (w0 + k < live) *reinterpret_cast<uint4 *>(dst + t * a.ot + hd * a.oh) = x;
-                    t += dt, hd += dg;
-                    if (hd >= G) hd -= G, ++t;
-                };
-                if (!some) {  // no keys: zeros (the query tile may be the next item's already)
-                    for (int k = k0; k < 32; k += 2) put(k, make_uint4(0, 0, 0, 0));
-                } else if (whole) {
-#pragma unroll
+                if (whole) {  // a row a thread
+                    if (!some) mine = his = 0.f;  // no keys: zeros
+                    const int t = r / a.G, hd = r - t * a.G;
+                    uint16_t *dst = a.out + g.b * a.ob + (t0 + t) * a.ot + (int64_t)(g.h * a.G + hd) * a.oh;
+                    // (loops that are not unrolled: code that runs once an item waits for its instructions more than for
+                    // anything else)
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
                         get(c, o);
+                        if (r < live) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sts16(stage + lane * 256 + (((4 * c + i) ^ (lane & 7)) << 4), cvt_bf2(o[8 * i], o[8 * i + 1]),
-                                  cvt_bf2(o[8 * i + 2], o[8 * i + 3]), cvt_bf2(o[8 * i + 4], o[8 * i + 5]), cvt_bf2(o[8 * i + 6], o[8 * i + 7]));
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t x[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) x[k] = cvt_bf2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+                                uint16_t *to = dst + 32 * c + 16 * i;
+                                if (a.out32) {
+                                    stg32(to, x);
+                                } else {
+                                    *reinterpret_cast<uint4 *>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+                                    *reinterpret_cast<uint4 *>(to + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                                }
+                            }
+                        }
+                        __syncwarp();
                     }
-                    o_read();
-                    __syncwarp();
-                    uint4 y[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = lds16(stage + (k0 + 2 * i) * 256 + ((ch ^ ((k0 + 2 * i) & 7)) << 4));
-                    staged();  // (before the stores leave)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) put(k0 + 2 * i, y[i]);
+                    if (some) o_read();
                 } else {
-                    // a partial, fp32, 64 dimensions at a time
-#pragma unroll
+                    // A partial, fp32, 64 dimensions at a time: a warp's 32 rows pass through its part of the query tile, to
+                    // leave in whole pieces of 256 bytes: 16-byte chunk ch of a row at chunk ch ^ (row & 7), without bank
+                    // conflicts for a row a lane and for 16 lanes a row.
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
                         get(c, o);
@@ -889,7 +898,8 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                         }
                     }
                     o_read();
-                    staged();
+                    q_done();
+                    if (join) q_done();
                 }
                 __syncwarp();
             }
@@ -910,13 +920,13 @@ __global__ void __launch_bounds__(256) k_cross_merge(CrossArgs a, int ctas) {
     const int lane = threadIdx.x & 31;
     Segment g;
     g.plan(a, ctas);
-    const int64_t chunk = g.chunk, p = (blockIdx.x + 1) * chunk;
+    const int chunk = g.chunk, p = (blockIdx.x + 1) * chunk;
     if (p < g.total) g.seek(a, p);
     pdl_wait();  // (by every block: nothing behind this kernel starts before k_cross has ended)
     if (p >= g.total) return;
-    const int64_t begin = p - g.at, end = begin + g.units();
-    if (g.at == 0 || begin < (int64_t)blockIdx.x * chunk) return;
-    const int parts = (int)((end - 1) / chunk) - blockIdx.x + 1;  // of CTAs blockIdx.x ..
+    const int begin = p - g.at, end = begin + g.units();
+    if (g.at == 0 || begin < (int)blockIdx.x * chunk) return;
+    const int parts = (end - 1) / chunk - (int)blockIdx.x + 1;  // of CTAs blockIdx.x ..
     for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < a.part_rows; row += gridDim.y * 8) {
         const int r = row & (CX_M - 1), tile = 2 * g.x + (row >= CX_M);
         const int t = tile * a.tokens + r / a.G, hd = r % a.G;
@@ -1013,6 +1023,7 @@ cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, 
         return cudaErrorInvalidValue;
     int64_t ctas;
     cross_grid(batch, r.h_kv, a.G, r.t_max, n_max, ctas, a.whole);
+    a.out32 = ((uintptr_t)r.qo | (uintptr_t)(2 * a.ob) | (uintptr_t)(2 * a.ot) | (uintptr_t)(2 * a.oh)) % 32 == 0;
     a.part = scratch, a.part_rows = cross_part_rows(a.G, r.t_max);
     const auto fn = paged ? k_cross<true> : k_cross<false>;
     cudaError_t e = ensure_smem((const void *)fn, CX_SMEM);
