@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(HEADS == 1 ? 512 : 256) k_cache_merge(CacheArg
             f[k].add(ml, v);
         }
     }
-    finish<DIFF, BF16OUT>(f, weight, d, out, row);
+    if (a.count && a.count[b] <= 0) return;
+    finish<DIFF, BF16OUT>(f, weight, d, out, b * a.ob + (h * a.G + head) * a.oh);
 }
 
 int cache_splits(int units, int n_max) {
@@ -121,14 +122,16 @@ static cudaError_t launch_merge(cudaStream_t s, bool diff, bool bf_out, const Ca
 
 cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
                                 const void *q, const mog_diff_params *diff, int out_type, void *out, float *scratch,
-                                cudaStream_t s) {
+                                cudaStream_t s, const RowsIn *rows_in) {
     const bool i8 = c->type == MOG_CACHE_I8, row8 = i8 || c->type == MOG_CACHE_E4M3, bf_out = out_type == MOG_OUT_BF16;
     const int es = row8 ? 1 : 2;
     CacheArgs a{static_cast<const uint8_t *>(c->k), static_cast<const uint8_t *>(c->v), c->k_scale, c->v_scale,
                 c->stride_b * es, c->stride_h * es, c->stride_n * es, c->scale_b, c->scale_h, c->scale_n,
                 i8 ? log2_exact(c->block_rows) : 0, c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
-                lengths, n_max, batch, h_kv, G, static_cast<const uint16_t *>(q), scratch,
+                lengths, n_max, batch, h_kv, G, static_cast<const uint16_t *>(q), (int64_t)h_kv * G * MOG_D, MOG_D,
+                (int64_t)h_kv * G * MOG_D, MOG_D, nullptr, scratch,
                 (float)(LOG2E / sqrt(diff ? MOG_D / 2.0 : (double)MOG_D)), cache_cluster(batch * h_kv, n_max)};
+    if (rows_in) a.qb = rows_in->qs[0], a.qh = rows_in->qs[2], a.ob = rows_in->os[0], a.oh = rows_in->os[2], a.count = rows_in->count;
     DiffArgs d{};
     if (diff) d = DiffArgs{diff->lam, diff->lam_heads > 1 ? 4 * (MOG_D / 2) : 0, diff->gamma, diff->lambda_init, diff->eps};
     const bool wide = (diff ? 2 : 1) * G > 8;
@@ -138,6 +141,7 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
     while (a.cs > 1 && a.cs / 2 >= ceil_div64(n_max, rows)) a.cs /= 2;  // as many CTAs as tiles do
     const cudaError_t e = i8 ? launch_spliti8(a, d, out, diff != nullptr, bf_out, wide, splits, s)
                           : row8 ? launch_split8(a, d, out, diff != nullptr, bf_out, wide, splits, s)
+                          : !diff ? launch_split16(a, d, out, wide, splits, s)
                           : bf_out ? pick_split<false, true, true>(a, d, out, wide, splits, s)
                                    : pick_split<false, true, false>(a, d, out, wide, splits, s);
     if (e != cudaSuccess || a.cs) return e;

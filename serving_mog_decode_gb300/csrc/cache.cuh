@@ -1,10 +1,11 @@
 // cache.cuh -- decode attentions over a mog_cache (bf16, e4m3 or int8 rows, contiguous or paged):
-// the kernel that reads the cache.  Its instances are compiled in cache.cu (bf16 rows), cache8.cu
-// (e4m3 rows) and cachei8.cu (int8 rows).
+// the kernel that reads the cache.  Its instances are compiled in cache.cu (bf16 rows, differential), cache16.cu
+// (bf16 rows, one map), cache8.cu (e4m3 rows) and cachei8.cu (int8 rows).
 //
 // dense_decode8: softmax(tau q.K^T) V of an 8-bit cache whose row i stands for
 // k_scale[i]*code_i and v_scale[i]*code_i.  mog_diff_decode: the difference of two softmax
-// maps over one set of values, normalised.  Both are a split kernel and a fold of its partials,
+// maps over one set of values, normalised.  mog_cross_attend with one token: as dense_decode8, over bf16 rows.
+// Each is a split kernel and a fold of its partials,
 // or, for short caches, one kernel whose clusters take a unit each and fold it themselves.
 //
 // Split (k_cache_split): the tiles (128 8-bit rows, 64 of bf16) of all (sequence, KV head) units form one list;
@@ -101,6 +102,8 @@ struct CacheArgs {
     const int *lengths;
     int n_max, batch, h_kv, G;
     const uint16_t *q;
+    int64_t qb, qh, ob, oh;  // elements between sequences and heads of the queries, of the output
+    const int *count;        // null, or per sequence: at most 0: its output stays as it is
     float *part;
     float scale2;
     int cs;  // CTAs of a cluster that works on one unit; 0: the tile list is split
@@ -305,7 +308,8 @@ __device__ __forceinline__ float load_column(uint32_t (&w)[8][2], const CacheArg
     column<DIFF, WIDE>(c, map, head);
     const bool have = head < a.G;
     unit = min(unit, a.batch * a.h_kv - 1);  // (lengths that change under a call must not lead out of q)
-    const uint16_t *row = a.q + ((int64_t)unit * a.G + (have ? head : 0)) * MOG_D;
+    const int b = unit / a.h_kv;
+    const uint16_t *row = a.q + b * a.qb + ((unit - b * a.h_kv) * a.G + (have ? head : 0)) * a.qh;
     if (!ROW8) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
@@ -913,10 +917,10 @@ struct Fold {
 };
 
 // A head's output from the folds of its map (both maps: their difference, the root-mean-square
-// norm and its weights), four dimensions a lane of a full warp, as row `row` of out.
+// norm and its weights), four dimensions a lane of a full warp, from element `at` of out on.
 template <bool DIFF, bool BF16OUT>
 __device__ __forceinline__ void finish(const Fold (&f)[DIFF ? 2 : 1], float weight, const DiffArgs &d, void *out,
-                                       int64_t row) {
+                                       int64_t at) {
     const int lane = threadIdx.x & 31;
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -931,7 +935,7 @@ __device__ __forceinline__ void finish(const Fold (&f)[DIFF ? 2 : 1], float weig
         const float4 gm = d.gamma ? reinterpret_cast<const float4 *>(d.gamma)[lane] : make_float4(1.f, 1.f, 1.f, 1.f);
         r.x *= x * gm.x, r.y *= x * gm.y, r.z *= x * gm.z, r.w *= x * gm.w;
     }
-    const int64_t o = row * MOG_D + 4 * lane;
+    const int64_t o = at + 4 * lane;
     if (BF16OUT) {
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + o) = make_uint2(cvt_bf2(r.x, r.y), cvt_bf2(r.z, r.w));
     } else {
@@ -968,7 +972,9 @@ __device__ __forceinline__ void cluster_end(const CacheArgs &a, const DiffArgs &
                 f[k].add(ml, v);
             }
         }
-        finish<DIFF, BF16OUT>(f, map_weight<DIFF>(d, h * a.G + head), d, out, (int64_t)unit * a.G + head);
+        const int b = unit / a.h_kv;
+        if (a.count && a.count[b] <= 0) continue;
+        finish<DIFF, BF16OUT>(f, map_weight<DIFF>(d, h * a.G + head), d, out, b * a.ob + (h * a.G + head) * a.oh);
     }
     // nobody leaves while its partial is read
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1059,7 +1065,7 @@ __global__ void __launch_bounds__(CT_THREADS, Tile<ROW8, WIDE, CLUSTER, I8>::PER
 
 template <bool ROW8, bool WIDE, bool PAGED, bool DIFF, bool BF16OUT, bool I8>
 static cudaError_t launch_split(const CacheArgs &a, const DiffArgs &d, void *out, int splits, cudaStream_t s) {
-    const int smem = a.cs ? Tile<ROW8, WIDE, true>::SMEM : Tile<ROW8, WIDE>::SMEM;
+    const int smem = a.cs ? Tile<ROW8, WIDE, true, I8>::SMEM : Tile<ROW8, WIDE, false, I8>::SMEM;
     const auto fn = a.cs ? k_cache_split<ROW8, WIDE, PAGED, DIFF, BF16OUT, true, I8>
                          : k_cache_split<ROW8, WIDE, PAGED, DIFF, BF16OUT, false, I8>;
     const cudaError_t e = ensure_smem((const void *)fn, smem);
@@ -1090,6 +1096,7 @@ static cudaError_t pick_split(const CacheArgs &a, const DiffArgs &d, void *out, 
 
 cudaError_t launch_split8(const CacheArgs &a, const DiffArgs &d, void *out, bool diff, bool bf_out, bool wide, int splits,
                           cudaStream_t s);
+cudaError_t launch_split16(const CacheArgs &a, const DiffArgs &d, void *out, bool wide, int splits, cudaStream_t s);
 cudaError_t launch_spliti8(const CacheArgs &a, const DiffArgs &d, void *out, bool diff, bool bf_out, bool wide, int splits,
                            cudaStream_t s);
 

@@ -147,9 +147,6 @@ cudaError_t launch_dense(const mog_kv *kv, const int32_t *lengths, int n_max, in
 constexpr int MOG_MAX_POOLS = 64;  // page pools of one copy launch (further pools: further launches)
 int cache_splits(int units, int n_max);
 int cache_cluster(int units, int n_max);  // > 0: one launch that needs no scratch
-cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
-                                const void *q, const mog_diff_params *diff, int out_type, void *out, float *scratch,
-                                cudaStream_t s);
 cudaError_t launch_kv_store(const mog_cache *c, int batch, int h_kv, int t_max, const int32_t *pos,
                             const int32_t *count, const void *kn, const void *vn, int64_t nb, int64_t nt,
                             int64_t nh, cudaStream_t s);
@@ -164,6 +161,9 @@ struct RowsIn {
     int each, inverse;
     const mog_rope *rope;
 };
+cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int n_max, int batch, int h_kv, int G,
+                                const void *q, const mog_diff_params *diff, int out_type, void *out, float *scratch,
+                                cudaStream_t s, const RowsIn *rows_in = nullptr);  // rows_in: strides and counts of one token's rows
 cudaError_t launch_rope(const mog_cache *c, int batch, const RowsIn &r, cudaStream_t s);     // not int8 caches
 cudaError_t launch_rows_i8(const mog_cache *c, int batch, const RowsIn &r, cudaStream_t s);  // with or without rope
 cudaError_t launch_kv_load(const mog_cache *c, int batch, const RowsIn &r, void *ko, void *vo, cudaStream_t s);
