@@ -919,18 +919,19 @@ def kv_store(K, V, pos, count, k_new, v_new, stream=None):
 
 def _row_strides(t, shape, dev, name, write=False):
     """Element strides between sequences, tokens and heads of bf16 rows [B, T, H, 128]."""
-    torch = _torch()
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev:
+    if t.dtype is not _torch().bfloat16 or t.shape != shape or t.device != dev:
         raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on {dev}")
-    st = t.stride()
-    if st[3] != 1:
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
-    if write and any(s == 0 and n > 1 for s, n in zip(st, shape)):
+    B, T, H, _ = shape
+    if write and ((sb == 0 and B > 1) or (st == 0 and T > 1) or (sh == 0 and H > 1)):
         raise ValueError(f"{name} is written: its rows must not share memory")
-    return tuple(s if n > 1 else 0 for s, n in zip(st[:3], shape))
+    return sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0
 
 
-def _strides3(s):
+@functools.lru_cache(maxsize=1024)
+def _strides3(s):  # (making the array costs more than finding it)
     return (C.c_int64 * 3)(*s)
 
 

@@ -150,6 +150,12 @@ __device__ __forceinline__ uint4 ldg_nc16(const void *p) {
     return r;
 }
 
+// 32 bytes to a 32-byte aligned place
+__device__ __forceinline__ void stg32(void *p, const uint4 &x, const uint4 &y) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x),
+                 "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+}
+
 // --------------------------------------------------------------------- tensor-core mma
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2,

@@ -368,10 +368,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
     return x;
 }
-__device__ __forceinline__ void stg32(void *p, const uint32_t (&x)[8]) {  // 32-byte aligned
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
-}
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -864,11 +860,12 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) x[k] = cvt_bf2(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
                                 uint16_t *to = dst + 32 * c + 16 * i;
+                                const uint4 y = make_uint4(x[0], x[1], x[2], x[3]), z = make_uint4(x[4], x[5], x[6], x[7]);
                                 if (a.out32) {
-                                    stg32(to, x);
+                                    stg32(to, y, z);
                                 } else {
-                                    *reinterpret_cast<uint4 *>(to) = make_uint4(x[0], x[1], x[2], x[3]);
-                                    *reinterpret_cast<uint4 *>(to + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                                    *reinterpret_cast<uint4 *>(to) = y;
+                                    *reinterpret_cast<uint4 *>(to + 8) = z;
                                 }
                             }
                         }

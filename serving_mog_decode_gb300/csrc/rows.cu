@@ -19,6 +19,15 @@
 
 namespace mog {
 
+// Four int8 codes -> floats: u = code + 128 is the low byte of the number 2^23 + u.
+__device__ __forceinline__ float4 i8x4_to_float4(uint32_t w) {
+    w ^= 0x80808080u;
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | i)) - 8388736.f;
+    return make_float4(f[0], f[1], f[2], f[3]);
+}
+
 enum { TO_NONE, TO_BF16, TO_E4M3, TO_I8 };
 constexpr int RW_THREADS = 256, RW_GROUPS = RW_THREADS / 8;
 constexpr int RW_TOKENS = 16;  // tokens of a CTA's tile of whole rows
@@ -359,54 +368,63 @@ __global__ void __launch_bounds__(RW_THREADS) k_rows_i8(RowsArgs a) {
 }
 
 // ------------------------------------------------------------------------------------
-// mog_kv_load: rows of a cache as bf16, eight lanes a row; bound by HBM.
+// mog_kv_load: rows of a cache as bf16, eight lanes a row; bound by HBM, and close to it by the
+// instructions of the addresses, so that a group of lanes keeps to one head's keys or values: of its
+// addresses only the page and the row change (24K tokens of 8 heads from 64-row pages, 50 MB read, 100 MB
+// written, 22 us of HBM time: 29 us, and 39 with heads fastest in one list).
 // ------------------------------------------------------------------------------------
 template <int FROM>
-__global__ void __launch_bounds__(RW_THREADS) k_kv_load(RowsArgs a, uint16_t *ko, uint16_t *vo) {
-    const int b = blockIdx.y, l = threadIdx.x & 7, per = 2 * a.h_kv;
-    const int rows = seq_count(a, b) * per;  // (below 2^30)
-    const int step = gridDim.x * RW_GROUPS, dt = step / per, dr = step - dt * per;
-    int i = blockIdx.x * RW_GROUPS + threadIdx.x / 8, t = i / per, r = i - t * per;
-    const int start = a.pos[b];
-    while (i < rows) {
-        uint4 x[RW_DEPTH], y[RW_DEPTH];
-        float s[RW_DEPTH];
-        uint16_t *dst[RW_DEPTH];
+__global__ void __launch_bounds__(RW_THREADS) k_kv_load(RowsArgs a, uint16_t *ko, uint16_t *vo, int out32) {
+    const int b = blockIdx.y, l = threadIdx.x & 7, per = 2 * a.h_kv, grp = threadIdx.x / 8;
+    const int n = seq_count(a, b), start = a.pos[b];
+    // groups side by side: per <= 32: whole tokens (the groups left over have nothing); else the heads in turns
+    const int tokens = per <= RW_GROUPS ? RW_GROUPS / per : 1, wide = min(per, RW_GROUPS);
+    const int tl = grp / wide;
+    if (tl >= tokens) return;
+    const int step = tokens * gridDim.x;
+    for (int r = grp - tl * wide; r < per; r += wide) {
+        const bool val = r >= a.h_kv;
+        const int h = val ? r - a.h_kv : r;
+        uint16_t *out = (val ? vo : ko) + b * a.kb + h * a.kh + 16 * l;
+        const uint8_t *in = (val ? a.V : a.K) + h * a.sh + (FROM == TO_BF16 ? 32 : 16) * l;
+        const float *scale = (val ? a.vs : a.ks) + h * a.ssh;
+        for (int t = blockIdx.x * tokens + tl; t < n; t += step * RW_DEPTH) {
+            uint4 x[RW_DEPTH], y[RW_DEPTH];
+            float s[RW_DEPTH];
+            bool have[RW_DEPTH];
 #pragma unroll
-        for (int u = 0; u < RW_DEPTH; ++u, i += step) {
-            const bool val = r >= a.h_kv;
-            const int h = val ? r - a.h_kv : r, tok = t;
-            t += dt, r += dr;
-            if (r >= per) r -= per, ++t;
-            dst[u] = nullptr;
-            int slab, row;
-            if (i >= rows || !find_row(a, b, (int)((unsigned)start + (unsigned)tok), slab, row)) continue;
-            dst[u] = (val ? vo : ko) + b * a.kb + tok * a.kt + h * a.kh + 16 * l;
-            const uint8_t *src = (val ? a.V : a.K) + slab * a.sb + h * a.sh + row * a.sn;
-            if (FROM == TO_BF16) {
-                x[u] = ldg_nc16(src + 32 * l), y[u] = ldg_nc16(src + 32 * l + 16);
-            } else {
-                x[u] = ldg_nc16(src + 16 * l);
-                s[u] = __ldg((val ? a.vs : a.ks) + slab * a.ssb + h * a.ssh + (row >> a.bshift) * a.ssn);
+            for (int u = 0; u < RW_DEPTH; ++u) {
+                int slab, row;
+                have[u] = t + u * step < n && find_row(a, b, (int)((unsigned)start + (unsigned)(t + u * step)), slab, row);
+                if (!have[u]) continue;
+                const uint8_t *src = in + slab * a.sb + row * a.sn;
+                x[u] = ldg_nc16(src);
+                if (FROM == TO_BF16) y[u] = ldg_nc16(src + 16);
+                else s[u] = __ldg(scale + slab * a.ssb + (row >> a.bshift) * a.ssn);
             }
-        }
 #pragma unroll
-        for (int u = 0; u < RW_DEPTH; ++u) {
-            if (!dst[u]) continue;
-            if (FROM != TO_BF16) {
-                const uint32_t c[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                uint32_t o[8];
+            for (int u = 0; u < RW_DEPTH; ++u) {
+                if (!have[u]) continue;
+                if (FROM != TO_BF16) {
+                    const uint32_t c[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                    uint32_t o[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float4 f;
-                    if (FROM == TO_E4M3) f = e4m3x4_to_float4(c[k]);
-                    else f = make_float4((float)((int)(c[k] << 24) >> 24), (float)((int)(c[k] << 16) >> 24), (float)((int)(c[k] << 8) >> 24), (float)((int)c[k] >> 24));
-                    o[2 * k] = cvt_bf2(f.x * s[u], f.y * s[u]), o[2 * k + 1] = cvt_bf2(f.z * s[u], f.w * s[u]);
+                    for (int k = 0; k < 4; ++k) {
+                        float4 f;
+                        if (FROM == TO_E4M3) f = e4m3x4_to_float4(c[k]);
+                        else f = i8x4_to_float4(c[k]);
+                        o[2 * k] = cvt_bf2(f.x * s[u], f.y * s[u]), o[2 * k + 1] = cvt_bf2(f.z * s[u], f.w * s[u]);
+                    }
+                    x[u] = make_uint4(o[0], o[1], o[2], o[3]), y[u] = make_uint4(o[4], o[5], o[6], o[7]);
                 }
-                x[u] = make_uint4(o[0], o[1], o[2], o[3]), y[u] = make_uint4(o[4], o[5], o[6], o[7]);
+                uint16_t *dst = out + (int64_t)(t + u * step) * a.kt;
+                if (out32) {
+                    stg32(dst, x[u], y[u]);
+                } else {
+                    *reinterpret_cast<uint4 *>(dst) = x[u];
+                    *reinterpret_cast<uint4 *>(dst + 8) = y[u];
+                }
             }
-            *reinterpret_cast<uint4 *>(dst[u]) = x[u];
-            *reinterpret_cast<uint4 *>(dst[u] + 8) = y[u];
         }
     }
 }
@@ -491,12 +509,13 @@ cudaError_t launch_kv_load(const mog_cache *c, int batch, const RowsIn &r, void 
     set_cache(a, c);
     set_rows(a, r);
     const int64_t most = ceil_div64(16LL * num_sms(), batch);
-    const int64_t want = ceil_div64((int64_t)r.t_max * 2 * r.h_kv, RW_GROUPS * RW_DEPTH);
+    const int64_t want = ceil_div64(r.t_max, std::max(RW_GROUPS / (2 * r.h_kv), 1) * RW_DEPTH);
     const dim3 grid((unsigned)std::min(want, most), batch);
     uint16_t *k = static_cast<uint16_t *>(ko), *v = static_cast<uint16_t *>(vo);
-    if (c->type == MOG_CACHE_BF16) k_kv_load<TO_BF16><<<grid, RW_THREADS, 0, s>>>(a, k, v);
-    else if (c->type == MOG_CACHE_E4M3) k_kv_load<TO_E4M3><<<grid, RW_THREADS, 0, s>>>(a, k, v);
-    else k_kv_load<TO_I8><<<grid, RW_THREADS, 0, s>>>(a, k, v);
+    const int out32 = ((uintptr_t)ko | (uintptr_t)vo | (uintptr_t)(2 * a.kb) | (uintptr_t)(2 * a.kt) | (uintptr_t)(2 * a.kh)) % 32 == 0;
+    if (c->type == MOG_CACHE_BF16) k_kv_load<TO_BF16><<<grid, RW_THREADS, 0, s>>>(a, k, v, out32);
+    else if (c->type == MOG_CACHE_E4M3) k_kv_load<TO_E4M3><<<grid, RW_THREADS, 0, s>>>(a, k, v, out32);
+    else k_kv_load<TO_I8><<<grid, RW_THREADS, 0, s>>>(a, k, v, out32);
     return cudaGetLastError();
 }
 
