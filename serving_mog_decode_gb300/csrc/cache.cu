@@ -74,8 +74,12 @@ __global__ void __launch_bounds__(HEADS == 1 ? 512 : 256) k_cache_merge(CacheArg
             f[k].add(ml, v);
         }
     }
-    if (a.count && a.count[b] <= 0) return;
-    finish<DIFF, BF16OUT>(f, weight, d, out, b * a.ob + (h * a.G + head) * a.oh);
+    int64_t at = (int64_t)row * MOG_D;
+    if (own_rows(ROWS != 64, DIFF)) {  // (tiles of 64 rows: bf16)
+        if (a.count && a.count[b] <= 0) return;
+        at = b * a.ob + (h * a.G + head) * a.oh;
+    }
+    finish<DIFF, BF16OUT>(f, weight, d, out, at);
 }
 
 int cache_splits(int units, int n_max) {
@@ -128,8 +132,7 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
     CacheArgs a{static_cast<const uint8_t *>(c->k), static_cast<const uint8_t *>(c->v), c->k_scale, c->v_scale,
                 c->stride_b * es, c->stride_h * es, c->stride_n * es, c->scale_b, c->scale_h, c->scale_n,
                 i8 ? log2_exact(c->block_rows) : 0, c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
-                lengths, n_max, batch, h_kv, G, static_cast<const uint16_t *>(q), (int64_t)h_kv * G * MOG_D, MOG_D,
-                (int64_t)h_kv * G * MOG_D, MOG_D, nullptr, scratch,
+                lengths, n_max, batch, h_kv, G, static_cast<const uint16_t *>(q), 0, 0, 0, 0, nullptr, scratch,
                 (float)(LOG2E / sqrt(diff ? MOG_D / 2.0 : (double)MOG_D)), cache_cluster(batch * h_kv, n_max)};
     if (rows_in) a.qb = rows_in->qs[0], a.qh = rows_in->qs[2], a.ob = rows_in->os[0], a.oh = rows_in->os[2], a.count = rows_in->count;
     DiffArgs d{};

@@ -102,12 +102,16 @@ struct CacheArgs {
     const int *lengths;
     int n_max, batch, h_kv, G;
     const uint16_t *q;
-    int64_t qb, qh, ob, oh;  // elements between sequences and heads of the queries, of the output
-    const int *count;        // null, or per sequence: at most 0: its output stays as it is
+    int64_t qb, qh, ob, oh;  // own_rows: elements between sequences and heads of the queries, of the output
+    const int *count;        // own_rows: null, or per sequence: at most 0: its output stays as it is
     float *part;
     float scale2;
     int cs;  // CTAs of a cluster that works on one unit; 0: the tile list is split
 };
+
+// Queries and outputs with strides and counts of their own (qb .. count): cross attention, the reader of bf16 rows
+// with one map.  The others' are contiguous, [batch][h_kv * G][128].
+constexpr bool own_rows(bool row8, bool diff) { return !row8 && !diff; }
 
 struct DiffArgs {
     const float *lam;  // [heads][4][64]
@@ -308,8 +312,11 @@ __device__ __forceinline__ float load_column(uint32_t (&w)[8][2], const CacheArg
     column<DIFF, WIDE>(c, map, head);
     const bool have = head < a.G;
     unit = min(unit, a.batch * a.h_kv - 1);  // (lengths that change under a call must not lead out of q)
-    const int b = unit / a.h_kv;
-    const uint16_t *row = a.q + b * a.qb + ((unit - b * a.h_kv) * a.G + (have ? head : 0)) * a.qh;
+    const uint16_t *row = a.q + ((int64_t)unit * a.G + (have ? head : 0)) * MOG_D;
+    if (own_rows(ROW8, DIFF)) {
+        const int b = unit / a.h_kv;
+        row = a.q + b * a.qb + ((unit - b * a.h_kv) * a.G + (have ? head : 0)) * a.qh;
+    }
     if (!ROW8) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
@@ -972,9 +979,13 @@ __device__ __forceinline__ void cluster_end(const CacheArgs &a, const DiffArgs &
                 f[k].add(ml, v);
             }
         }
-        const int b = unit / a.h_kv;
-        if (a.count && a.count[b] <= 0) continue;
-        finish<DIFF, BF16OUT>(f, map_weight<DIFF>(d, h * a.G + head), d, out, b * a.ob + (h * a.G + head) * a.oh);
+        int64_t at = ((int64_t)unit * a.G + head) * MOG_D;
+        if (own_rows(T::ROW8, DIFF)) {
+            const int b = unit / a.h_kv;
+            if (a.count && a.count[b] <= 0) continue;
+            at = b * a.ob + (h * a.G + head) * a.oh;
+        }
+        finish<DIFF, BF16OUT>(f, map_weight<DIFF>(d, h * a.G + head), d, out, at);
     }
     // nobody leaves while its partial is read
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");

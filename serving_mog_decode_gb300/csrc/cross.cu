@@ -477,7 +477,12 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
             // bits by slot: the next phase of full; its occupant is the first of a group of two; the next phase of free
             uint32_t fullp = 0, two = 0, freep = 0;
             bool ok = true;
-            auto load = [&](const CUtensorMap *map, int tile, bool value, bool first_of_two) {
+            // paged: the pages of a tile (lane g: of its g-th copy), asked for a tile ahead
+            auto pages_of = [&](int tile) {
+                const int key = tile * CX_KEYS + lane * gr;
+                return PAGED && lane < ng && key < len ? __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift)) : -1;
+            };
+            auto load = [&](const CUtensorMap *map, int tile, int page, bool value, bool first_of_two) {
                 if (issued >= CX_RING) {  // the slot's last occupant has been used
                     const int w = two >> slot & 1 ? (slot + 1 == CX_RING ? 0 : slot + 1) : slot;
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.free[w]), (freep >> w & 1) ^ 1));
@@ -485,13 +490,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 if (!ok) return;
                 const uint32_t dst = sR + slot * CX_TILE;
                 const int key = tile * CX_KEYS + lane * gr;  // lane g: the tile's g-th copy
-                int page = 0;
-                const bool seen = lane < ng && key < len;
-                bool there = seen;
-                if (PAGED && seen) {
-                    page = __ldg(a.bt + (int64_t)b * a.pps + (key >> a.pshift));
-                    there = (unsigned)page < (unsigned)a.n_pages;
-                }
+                const bool seen = lane < ng && key < len, there = seen && (!PAGED || (unsigned)page < (unsigned)a.n_pages);
                 const unsigned have = __ballot_sync(0xffffffffu, there);
                 if (PAGED && value) {  // a page that is none: its weights are zero, and so must its values be finite
                     const unsigned none = __ballot_sync(0xffffffffu, seen && !there);
@@ -519,11 +518,22 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 // in the order of their use
                 const int ways = g.pair ? 1 : 2, nt = g.nt, first = g.first;
                 b = g.b, h = g.h, len = g.q.len;
-                for (int t = 0; t < min(nt, ways) && ok; ++t) load(&kmap, first + t, false, t + 1 < min(nt, ways));
+                int ahead = pages_of(first), now[2] = {0, 0};  // of the next K; of the V to come
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= min(nt, ways) || !ok) continue;
+                    now[t] = ahead;
+                    ahead = t + 1 < nt ? pages_of(first + t + 1) : -1;
+                    load(&kmap, first + t, now[t], false, t + 1 < min(nt, ways));
+                }
                 for (int t = 0; t < nt && ok; ++t) {
                     const bool more = t + ways < nt;
-                    load(&vmap, first + t, true, more);
-                    if (more && ok) load(&kmap, first + t + ways, false, false);
+                    load(&vmap, first + t, now[0], true, more);
+                    if (ways == 2) now[0] = now[1];
+                    if (!more || !ok) continue;
+                    (ways == 2 ? now[1] : now[0]) = ahead;
+                    ahead = t + ways + 1 < nt ? pages_of(first + t + ways + 1) : -1;
+                    load(&kmap, first + t + ways, ways == 2 ? now[1] : now[0], false, false);
                 }
                 if (nt > 0 && g.tail() > 0 && ok) {
                     // rows behind the sequence's end: their weights are zero, and so must their values be finite
