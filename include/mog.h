@@ -570,8 +570,8 @@ int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_ma
  * Cross attention: t_max query tokens of each sequence, or one, to the rows [0, N_b) of a bf16
  * cache, all of which every one of them sees: out = softmax(tau q.K^T) V per token and head, tau =
  * 1/sqrt(d).  A sequence without rows, and a query whose logits are all -infinity, give zeros.
- *  c           : MOG_CACHE_BF16, strides below 2^39 elements; stride_b = 0: the same rows for every
- *                sequence
+ *  c           : MOG_CACHE_BF16, strides below 2^39 elements; contiguous: stride_b = 0: the same rows
+ *                for every sequence, stride_h = 0: for every head
  *  lengths_dev : int32[batch] on the device, clamped to [0, n_max]; n_max <= the cache's positions
  *  count_dev   : int32[batch] query tokens, clamped to [0, t_max], or NULL: t_max each.  Rows of
  *                out behind them are left as they are

@@ -1050,6 +1050,7 @@ extern "C" int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, 
     if ((st = check_cache(c, n_max)) != MOG_OK) return st;
     for (int64_t x : {c->stride_b, c->stride_h, c->stride_n})
         if (x >= (int64_t)1 << 39) return MOG_ERR_SHAPE;  // (a tensor map's strides are below 2^40 bytes)
+    if (c->block_table && ((c->stride_b == 0 && c->n_pages > 1) || (c->stride_h == 0 && h_kv > 1))) return MOG_ERR_SHAPE;
     if (!lengths_dev || !q_strides || !out_strides || (need && !scratch_dev)) return MOG_ERR_INVALID_ARG;
     if ((st = check_rows(q_dev, q_strides)) != MOG_OK || (st = check_rows(out_dev, out_strides)) != MOG_OK) return st;
     if (!aligned16(scratch_dev)) return MOG_ERR_INVALID_ARG;

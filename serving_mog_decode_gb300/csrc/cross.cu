@@ -58,7 +58,10 @@ struct CrossArgs {
     int pshift, pps, n_pages;
     int bmul, hmul;  // contiguous: 0 where all sequences (heads) are one in memory
     float scale2;    // tau * log2(e)
-    float *part;     // [2 * CTAs][part_rows][CX_PART]: of CTA c, slot 2c: the item that it does not begin, 2c + 1: that it does not end
+    // equal shares: [CTAs] what to fold at the beginning of a CTA's share and the partials
+    // [2 * CTAs][part_rows][CX_PART]: of CTA c, slot 2c: the item that it does not begin, 2c + 1: that it does not end
+    int4 *fold;
+    float *part;
     int part_rows;
     int whole;       // whole items
 };
@@ -155,7 +158,7 @@ struct Segment {
         }
         chunk = max((total + ctas - 1) / ctas, CX_LEAST);
     }
-    static constexpr int CX_LEAST = 3;  // units of a share: fewer are not worth a CTA's start
+    static constexpr int CX_LEAST = 4;  // units of a share: fewer are not worth a CTA's start and its partials
     // sequences alike: the next whole item
     __device__ __forceinline__ bool round(const CrossArgs &a) {
         item(a, left++ * gridDim.x + blockIdx.x);
@@ -287,6 +290,18 @@ struct Segment {
         }
         set(left);
         return true;
+    }
+    // What k_cross_merge has to do for the item in which the share of CTA c > 0 begins, if that is the first share to
+    // begin inside it (by a full warp): (how many CTAs from c - 1 on have parts, 0 for none; sequence; KV head; item,
+    // from 2^30 on: a pair).
+    __device__ __forceinline__ int4 fold(const CrossArgs &a) {
+        plan(a, gridDim.x);
+        const int c = blockIdx.x, p = c * chunk;
+        if (c == 0 || p >= total) return make_int4(0, 0, 0, 0);
+        seek(a, p);
+        const int begin = p - at, end = begin + units();
+        if (at == 0 || begin < p - chunk) return make_int4(0, 0, 0, 0);
+        return make_int4((end - 1) / chunk - c + 2, b, h, x + (x < q.pairs ? 1 << 30 : 0));
     }
     // tiles of stream s, its j-th; rows of the last tile behind the sequence's end
     __device__ __forceinline__ int n_of(int s) const { return pair ? nt : (nt - s + 1) >> 1; }
@@ -426,7 +441,10 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     Segment &g = s_seg[warp];
     {
         Segment first;
-        if (!first.start(a, s_order)) return;
+        if (!first.start(a, s_order)) {
+            if (!a.whole && tid == 0) a.fold[blockIdx.x] = make_int4(0, 0, 0, 0);
+            return;
+        }
         if (lane == 0) g = first;
         __syncwarp();
     }
@@ -666,6 +684,10 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 if (seg > 0) mbar_wait(bar(bars.q_full), (seg - 1) & 1);  // no copy outlives the CTA
             }
             __syncwarp();
+        } else if (!a.whole) {
+            Segment f;
+            const int4 x = f.fold(a);
+            if (lane == 0) a.fold[blockIdx.x] = x;
         }
     } else {
         // ----------------------------------------------------------------- softmax
@@ -921,50 +943,49 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     }
 }
 
-// Folds the partials of an item that several CTAs share: boundary blockIdx.x + 1 of the chunks lies inside it,
-// and is the first one that does; a warp per query row, four dimensions a lane.
-__global__ void __launch_bounds__(256) k_cross_merge(CrossArgs a, int ctas) {
-    const int lane = threadIdx.x & 31;
-    Segment g;
-    g.plan(a, ctas);
-    const int chunk = g.chunk, p = (blockIdx.x + 1) * chunk;
-    if (p < g.total) g.seek(a, p);
+// Folds the partials of the items that several CTAs share: blocks (c - 1, *) that of a.fold[c], a warp per query row,
+// four dimensions a lane.
+__global__ void __launch_bounds__(256) k_cross_merge(CrossArgs a) {
+    constexpr int U = 8;  // partials in flight
+    const int lane = threadIdx.x & 31, c0 = blockIdx.x;
     pdl_wait();  // (by every block: nothing behind this kernel starts before k_cross has ended)
-    if (p >= g.total) return;
-    const int begin = p - g.at, end = begin + g.units();
-    if (g.at == 0 || begin < (int)blockIdx.x * chunk) return;
-    const int parts = (end - 1) / chunk - (int)blockIdx.x + 1;  // of CTAs blockIdx.x ..
-    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < a.part_rows; row += gridDim.y * 8) {
-        const int r = row & (CX_M - 1), tile = 2 * g.x + (row >= CX_M);
+    const int4 f = __ldcg(a.fold + c0 + 1);
+    if (f.x == 0) return;
+    const int b = f.y, h = f.z, x = f.w & ((1 << 30) - 1), rows = f.w >> 30 ? 2 * CX_M : CX_M;
+    const int count = a.count ? min(max(a.count[b], 0), a.t_max) : a.t_max;
+    for (int row = blockIdx.y * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.y * 8) {
+        const int r = row & (CX_M - 1), tile = 2 * x + (row >= CX_M);
         const int t = tile * a.tokens + r / a.G, hd = r % a.G;
-        if (r >= a.tokens * a.G || t >= g.q.count || (g.x >= g.q.pairs && row >= CX_M)) continue;
+        if (r >= a.tokens * a.G || t >= count) continue;
         float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         bool nan = false;
-        for (int k = 0; k < parts; k += 4) {
-            float2 ml[4];
-            float4 v[4];
+        for (int k = 0; k < f.x; k += U) {
+            float2 ml[U];
+            float4 v[U];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const bool ok = k + x < parts;
-                const int64_t slot = 2 * ((int64_t)blockIdx.x + k + x) + (k + x == 0 ? 1 : 0);
+            for (int i = 0; i < U; ++i) {
+                const bool ok = k + i < f.x;
+                const int64_t slot = 2 * ((int64_t)c0 + k + i) + (k + i == 0 ? 1 : 0);
                 const float *from = a.part + (slot * a.part_rows + row) * CX_PART;
-                ml[x] = ok ? __ldcg(reinterpret_cast<const float2 *>(from)) : make_float2(-INFINITY, 0.f);
-                v[x] = ok ? __ldcg(reinterpret_cast<const float4 *>(from + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+                ml[i] = ok ? __ldcg(reinterpret_cast<const float2 *>(from)) : make_float2(-INFINITY, 0.f);
+                v[i] = ok ? __ldcg(reinterpret_cast<const float4 *>(from + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
+            float mn = m;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                nan |= ml[x].x != ml[x].x;
-                const float mn = fmaxf(m, ml[x].x), sh = mn == -INFINITY ? 0.f : mn;
-                const float f = ex2(m - sh), e = ex2(ml[x].x - sh);
-                m = mn;
-                l = l * f + ml[x].y * e;
-                acc.x = acc.x * f + v[x].x * e, acc.y = acc.y * f + v[x].y * e;
-                acc.z = acc.z * f + v[x].z * e, acc.w = acc.w * f + v[x].w * e;
+            for (int i = 0; i < U; ++i) mn = fmaxf(mn, ml[i].x), nan |= ml[i].x != ml[i].x;
+            const float sh = mn == -INFINITY ? 0.f : mn, d = ex2(m - sh);
+            m = mn;
+            l *= d, acc.x *= d, acc.y *= d, acc.z *= d, acc.w *= d;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const float e = ex2(ml[i].x - sh);
+                l += ml[i].y * e;
+                acc.x += v[i].x * e, acc.y += v[i].y * e, acc.z += v[i].z * e, acc.w += v[i].w * e;
             }
         }
         const float inv = nan ? __int_as_float(0x7fffffff) : l == 0.f ? 0.f : 1.f / l;
-        uint16_t *dst = a.out + g.b * a.ob + t * a.ot + (int64_t)(g.h * a.G + hd) * a.oh + 4 * lane;
+        uint16_t *dst = a.out + b * a.ob + t * a.ot + (int64_t)(h * a.G + hd) * a.oh + 4 * lane;
         *reinterpret_cast<uint2 *>(dst) = make_uint2(cvt_bf2(acc.x * inv, acc.y * inv), cvt_bf2(acc.z * inv, acc.w * inv));
     }
 }
@@ -1004,7 +1025,7 @@ size_t cross_scratch(int batch, int h_kv, int G, int t_max, int n_max) {
     int64_t ctas;
     int whole;
     cross_grid(batch, h_kv, G, t_max, n_max, ctas, whole);
-    return whole ? 0 : (size_t)2 * ctas * cross_part_rows(G, t_max) * CX_PART * sizeof(float);
+    return whole ? 0 : ctas * (sizeof(int4) + (size_t)2 * cross_part_rows(G, t_max) * CX_PART * sizeof(float));
 }
 
 cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, int batch, const RowsIn &r, float *scratch,
@@ -1031,14 +1052,14 @@ cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, 
     int64_t ctas;
     cross_grid(batch, r.h_kv, a.G, r.t_max, n_max, ctas, a.whole);
     a.out32 = ((uintptr_t)r.qo | (uintptr_t)(2 * a.ob) | (uintptr_t)(2 * a.ot) | (uintptr_t)(2 * a.oh)) % 32 == 0;
-    a.part = scratch, a.part_rows = cross_part_rows(a.G, r.t_max);
+    a.fold = reinterpret_cast<int4 *>(scratch), a.part = scratch + 4 * ctas, a.part_rows = cross_part_rows(a.G, r.t_max);
     const auto fn = paged ? k_cross<true> : k_cross<false>;
     cudaError_t e = ensure_smem((const void *)fn, CX_SMEM);
     if (e != cudaSuccess) return e;
     fn<<<(unsigned)ctas, CX_THREADS, CX_SMEM, s>>>(a, qm, km, vm);
     if ((e = cudaGetLastError()) != cudaSuccess || a.whole || ctas == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas - 1, 4);
+    cfg.gridDim = dim3((unsigned)ctas - 1, (unsigned)a.part_rows / 16);  // two rows a warp
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1046,7 +1067,7 @@ cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_cross_merge, a, (int)ctas);
+    return cudaLaunchKernelEx(&cfg, k_cross_merge, a);
 }
 
 }  // namespace mog

@@ -238,6 +238,28 @@ def test_one_token_is_the_decode_step():
     assert ((out[:, 0].double() - want.double()).norm() / want.double().norm()) < 2 * BF / math.sqrt(3)
 
 
+@pytest.mark.parametrize("G", [1, 5, 16])
+@pytest.mark.parametrize("page", [0, 32])
+def test_one_token_with_strides_and_counts(G, page):
+    lens, H = (700, 0, 5000, 33, 64), 3
+    m = Made(100 + G, lens, H, page)
+    qkv = randn(101, 5, 1, (G + 2) * H, D)
+    q = qkv[:, :, H:(G + 1) * H]
+    out = torch.full((5, 1, 2 * G * H, D), 4.0, dtype=torch.bfloat16, device=DEV)
+    part = out[:, :, G * H:]
+    count = (1, 1, 0, 7, -2)
+    mog.cross_attend(*m.cache, m.lengths, m.n_max, q, count=ints(*count), out=part)
+    m.check(q, part, G, count, fill=4.0)
+    assert (out[:, :, : G * H] == 4).all()
+    long = Made(102, (60000,), 2, page)  # the split form
+    q = randn(103, 1, 1, 2 * G, D)
+    got = mog.cross_attend(*long.cache, long.lengths, long.n_max, q)
+    long.check(q, got, G)
+    keep = torch.full_like(got, 9.0)
+    mog.cross_attend(*long.cache, long.lengths, long.n_max, q, count=ints(0), out=keep)
+    assert (keep == 9).all()
+
+
 def test_read_back_from_8_bits_then_attended():
     """An int8 cache's rows read back are what several query tokens attend to."""
     g = gen(65)

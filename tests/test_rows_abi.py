@@ -176,6 +176,8 @@ def test_cross_refusals(lib):
     assert cross(cache()) == ARG and cross(cache(type=0)) == ARG
     for kw, why in [(dict(k=None), ARG), (dict(v=ODD.value), ARG), (dict(stride_n=64), SHAPE), (dict(n_cap=100), SHAPE),
                     (dict(stride_b=1 << 39), SHAPE), (dict(stride_h=1 << 39), SHAPE), (dict(stride_n=1 << 39), SHAPE),
+                    (dict(block_table=P.value, page_rows=64, pages_per_seq=1 << 18, n_pages=4, stride_h=0), SHAPE),
+                    (dict(block_table=P.value, page_rows=64, pages_per_seq=1 << 18, n_pages=4, stride_b=0), SHAPE),
                     (dict(block_table=P.value, page_rows=24, pages_per_seq=1 << 18, n_pages=4), SHAPE)]:
         assert cross(cache(**dict(dict(type=0, k_scale=None, v_scale=None), **kw))) == why, kw
     for kw, why in [(dict(lengths=None), ARG), (dict(n_max=0), ARG), (dict(n_max=(1 << 20) + 1), SHAPE),
@@ -183,6 +185,9 @@ def test_cross_refusals(lib):
                     (dict(h_q=33), SHAPE), (dict(h_kv=1, h_q=17), SHAPE), (dict(batch=8192), SHAPE), (dict(d=64), SHAPE),
                     (dict(t=0), ARG), (dict(t=1 << 26), SHAPE), (dict(q=None), ARG), (dict(q=ODD), ARG), (dict(out=ODD), ARG),
                     (dict(qs=S_ODD), SHAPE), (dict(os_=S_ODD), SHAPE), (dict(qs=None), ARG), (dict(scratch=None), ARG),
+                    (dict(qs=(C.c_int64 * 3)(1024, 0, 128)), SHAPE), (dict(qs=(C.c_int64 * 3)(1024, 1024, 0)), SHAPE),
+                    (dict(qs=(C.c_int64 * 3)(-1024, 1024, 128)), SHAPE), (dict(qs=(C.c_int64 * 3)(1 << 35, 1024, 128)), SHAPE),
+                    (dict(batch=4096, n_max=1 << 19, t=1 << 13, h_q=8), SHAPE),
                     (dict(scratch=ODD), ARG), (dict(nbytes=16), SMALL)]:
         assert cross(**kw) == why, kw
     assert mog.cross_scratch_bytes(1, 2, 8, 20, 200) == 0 and mog.cross_scratch_bytes(1, 1, 1, 20, 1 << 20) > 0
