@@ -13,6 +13,7 @@
 //   warp 8          issues the MMAs: S = Q K^T (128 x 128 x 128) and O += P V, P from tensor memory
 //   warp 9          TMA copies of K and V tiles through a ring of 32 KB slots, in the order of their use
 //   warp 10         TMA copies of the query tiles
+//   warp 11         finds the items, a few ahead
 //
 // Work: an item is a pair of query tiles of a (sequence, KV head).  Lengths and counts are read on the device (a
 // captured graph replays with others).  Either a CTA, one per SM, takes whole items, the longest sequences' first
@@ -37,7 +38,8 @@ constexpr int CX_M = 128, CX_KEYS = 128;         // query rows and keys of a til
 constexpr int CX_TILE = CX_KEYS * MOG_D * 2;     // bytes of a tile (K, V or Q): two halves of 64 dimensions
 constexpr int CX_HALF = CX_TILE / 2;
 constexpr int CX_RING = 5;                       // slots of K and V tiles
-constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 9, CX_Q = 10;  // (warp 11 fills the third warpgroup)
+constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 9, CX_Q = 10;
+constexpr int CX_ITEMS = 4;                      // items found ahead
 constexpr int CX_SORT = 64;                      // sequences that whole items are sorted over
 // Registers: 168 a thread at launch; the softmax warps take 208, the others leave theirs at 80
 // (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
@@ -303,6 +305,7 @@ struct Segment {
         if (at == 0 || begin < p - chunk) return make_int4(0, 0, 0, 0);
         return make_int4((end - 1) / chunk - c + 2, b, h, x + (x < q.pairs ? 1 << 30 : 0));
     }
+    bool end;  // (no item any more)
     // tiles of stream s, its j-th; rows of the last tile behind the sequence's end
     __device__ __forceinline__ int n_of(int s) const { return pair ? nt : (nt - s + 1) >> 1; }
     __device__ __forceinline__ int tile_of(int s, int j) const { return first + (pair ? j : 2 * j + s); }
@@ -418,6 +421,7 @@ struct CrossBars {
     uint64_t p_full[2][2];    // its weights, of each half of the keys
     uint64_t o_full[2], o_free[2];  // its sums are through; have been read
     uint64_t j_full, j_free;  // one query tile: stream 1's maxima and sums are there; have been read
+    uint64_t i_full[CX_ITEMS], i_free[CX_ITEMS];  // the items
     uint64_t v_tail[4];       // an item's last V: its rows behind the sequence's end are zero (the ring holds 2 such at most)
 };
 
@@ -431,31 +435,12 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     __shared__ int s_fail;
     pdl_trigger();  // (k_cross_merge waits for the whole grid)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // A warp's place in the list, in shared memory: it is looked at between items only.
-    __shared__ Segment s_seg[CX_THREADS / 32];
+    __shared__ Segment s_items[CX_ITEMS];  // what warp 11 has found for the others to do
     __shared__ CrossOrder s_order;
     if (a.whole) {
         s_order.make(a, *reinterpret_cast<int(*)[CX_SORT]>(cx_raw), *reinterpret_cast<int(*)[CX_SORT]>(cx_raw + 4 * CX_SORT));
         __syncthreads();
     }
-    Segment &g = s_seg[warp];
-    {
-        Segment first;
-        if (!first.start(a, s_order)) {
-            if (!a.whole && tid == 0) a.fold[blockIdx.x] = make_int4(0, 0, 0, 0);
-            return;
-        }
-        if (lane == 0) g = first;
-        __syncwarp();
-    }
-    auto next_item = [&]() {  // (by a whole warp)
-        __syncwarp();
-        int more = 0;
-        if (lane == 0) more = g.next(a, s_order);
-        more = __shfl_sync(0xffffffffu, more, 0);
-        __syncwarp();
-        return more != 0;
-    };
     const uint32_t sQ = (smem_u32(cx_raw) + 1023u) & ~1023u, sR = sQ + 2 * CX_TILE;
     auto bar = [&](const uint64_t &x) { return smem_u32(&x); };
     float2 *s_ml = reinterpret_cast<float2 *>(cx_raw + (sQ + CX_TILE - smem_u32(cx_raw)));  // (one query tile: the other's place)
@@ -472,6 +457,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         mbar_init(bar(bars.j_full), CX_M);
         mbar_init(bar(bars.j_free), CX_M);
         for (int i = 0; i < 4; ++i) mbar_init(bar(bars.v_tail[i]), 1);
+        for (int i = 0; i < CX_ITEMS; ++i) mbar_init(bar(bars.i_full[i]), 1), mbar_init(bar(bars.i_free[i]), 11);  // (warps 0 .. 10)
         fence_barrier_init();
         s_fail = 0;
     }
@@ -483,6 +469,21 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    // The CTA's it-th item (by a whole warp, or by one thread for its own); false behind the last one.  Every role
+    // goes through all of them, also after a wait that has given up.
+    auto item_at = [&](uint32_t it) {
+        if (!mbar_wait(bar(bars.i_full[it % CX_ITEMS]), (it / CX_ITEMS) & 1)) {
+            atomicExch(&s_fail, 1);
+            return false;
+        }
+        return !s_items[it % CX_ITEMS].end;
+    };
+    auto warp_item_at = [&](uint32_t it) { return __all_sync(0xffffffffu, item_at(it)) != 0; };
+    auto item_done = [&](uint32_t it) { mbar_arrive(bar(bars.i_free[it % CX_ITEMS])); };
+    auto warp_item_done = [&](uint32_t it) {
+        __syncwarp();
+        if (lane == 0) item_done(it);
+    };
     auto tS = [&](int s) { return tmem + (uint32_t)(s * 128); };
     auto tO = [&](int s) { return tmem + (uint32_t)(256 + s * 128); };
 
@@ -532,7 +533,9 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 ++issued;
                 slot = slot + 1 == CX_RING ? 0 : slot + 1;
             };
-            do {
+            for (uint32_t it = 0; warp_item_at(it); warp_item_done(it++)) {
+                const Segment &g = s_items[it % CX_ITEMS];
+                if (!ok) continue;
                 // in the order of their use
                 const int ways = g.pair ? 1 : 2, nt = g.nt, first = g.first;
                 b = g.b, h = g.h, len = g.q.len;
@@ -562,8 +565,8 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(bars.v_tail[tails++ & 3]));
                 }
-            } while (ok && next_item());
-            if (!ok) atomicExch(&s_fail, 1);
+                if (!ok) atomicExch(&s_fail, 1);
+            }
             // no copy outlives the CTA
             for (int i = 0; i < min(issued, CX_RING); ++i) mbar_wait(bar(bars.full[i]), (fullp >> i & 1) ^ 1);
         } else if (warp == CX_MMA) {
@@ -608,16 +611,16 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                     if (more) mma_s(s, k);
                     else tc_commit(bar(bars.o_full[s]));
                 };
-                do {
+                auto run = [&](const Segment &g) {
                     const int nt = g.nt, tail = g.tail();
                     pair = g.pair;
-                    if (nt == 0) continue;
-                    ok = ok && mbar_wait(bar(bars.q_full), seg & 1);
-                    if (!ok) break;
+                    if (nt == 0) return;
+                    ok = mbar_wait(bar(bars.q_full), seg & 1);
+                    if (!ok) return;
                     tc_fence_after();
                     if (pair) {
                         const int k0 = next_copy();
-                        if (!ok) break;
+                        if (!ok) return;
                         mma_s(0, k0), mma_s(1, k0);
                         tc_commit(bar(bars.free[k0]));
                         for (int s = 0; s < 2 && seg > 0; ++s) ok = ok && mbar_wait(bar(bars.o_free[s]), (seg - 1) & 1);
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                             k0 = next_copy();
                             if (ok) mma_s(1, k0);
                         }
-                        if (!ok) break;
+                        if (!ok) return;
                         tc_commit(bar(bars.free[k0]));
                         for (int s = 0; s < 2 && seg > 0; ++s) ok = ok && mbar_wait(bar(bars.o_free[s]), (seg - 1) & 1);
                         for (int t = 0; t < nt && ok; t += 2) {
@@ -658,8 +661,11 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                     }
                     ++seg;
                     tails += tail > 0;
-                } while (ok && g.next(a, s_order));
-                if (!ok) atomicExch(&s_fail, 1);
+                };
+                for (uint32_t it = 0; item_at(it); item_done(it++)) {
+                    if (ok) run(s_items[it % CX_ITEMS]);
+                    if (!ok) atomicExch(&s_fail, 1);
+                }
             }
             __syncwarp();
         } else if (warp == CX_Q) {
@@ -668,10 +674,14 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 const uint32_t bytes = (uint32_t)(a.tokens * a.G) * 256;  // of a tile; tokens from t_max on are zeros
                 uint32_t seg = 0;
                 bool ok = true;
-                do {
-                    if (g.nt == 0) continue;
+                for (uint32_t it = 0; item_at(it); item_done(it++)) {
+                    const Segment &g = s_items[it % CX_ITEMS];
+                    if (!ok || g.nt == 0) continue;
                     if (seg > 0) ok = mbar_wait(bar(bars.q_free), (seg - 1) & 1);
-                    if (!ok) break;
+                    if (!ok) {
+                        atomicExch(&s_fail, 1);
+                        continue;
+                    }
                     const int n = g.pair ? 2 : 1;
                     mbar_expect_tx(bar(bars.q_full), n * bytes);
                     for (int i = 0; i < n; ++i)
@@ -679,15 +689,29 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                             tma_load_5d(sQ + i * CX_TILE + d * CX_HALF, &qmap, 64 * d, 0, (2 * g.x + i) * a.tokens, g.h, g.b * a.qmul,
                                         bar(bars.q_full));
                     ++seg;
-                } while (g.next(a, s_order));
-                if (!ok) atomicExch(&s_fail, 1);
+                }
                 if (seg > 0) mbar_wait(bar(bars.q_full), (seg - 1) & 1);  // no copy outlives the CTA
             }
             __syncwarp();
-        } else if (!a.whole) {
-            Segment f;
-            const int4 x = f.fold(a);
-            if (lane == 0) a.fold[blockIdx.x] = x;
+        } else {
+            // ---------------------------------------------------------------- items
+            Segment w;
+            bool more = w.start(a, s_order), ok = true;
+            for (uint32_t it = 0; ok; ++it) {
+                if (it >= CX_ITEMS) ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.i_free[it % CX_ITEMS]), (it / CX_ITEMS - 1) & 1));
+                w.end = !more;
+                if (lane == 0 && ok) {
+                    s_items[it % CX_ITEMS] = w;
+                    mbar_arrive(bar(bars.i_full[it % CX_ITEMS]));
+                }
+                if (!more) break;
+                more = w.next(a, s_order);
+            }
+            if (!ok) atomicExch(&s_fail, 1);
+            if (!a.whole) {
+                const int4 f = w.fold(a);
+                if (lane == 0) a.fold[blockIdx.x] = f;
+            }
         }
     } else {
         // ----------------------------------------------------------------- softmax
@@ -697,7 +721,8 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         uint32_t sp = 0, op0 = 0, op1 = 0, joins = 0;       // the next phases of s_full and both o_full
         const bool row = r < a.tokens * a.G;  // (the rows behind the tile's tokens hold anything)
         bool ok = true;
-        do {
+        for (uint32_t it = 0; warp_item_at(it); warp_item_done(it++)) {
+            const Segment &g = s_items[it % CX_ITEMS];
             const int n = g.n_of(s), n1 = g.n_of(1), len = g.q.len;
             const bool pair = g.pair, whole = g.begins && g.ends;
             auto q_done = [&]() {  // the thread's part in freeing the query tiles
@@ -933,7 +958,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 __syncwarp();
             }
             joins += join;
-        } while (next_item());
+        }
     }
     tc_fence_before();
     __syncthreads();
