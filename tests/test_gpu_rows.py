@@ -493,6 +493,48 @@ def test_dense_over_int8_blocks(G, lens, page, block, bf16_out):
             assert ((got - want).abs() <= rel * size + (BF * want.abs() if bf16_out else 0)).all(), (b, h)
 
 
+@pytest.mark.parametrize("G", [2, 12])
+@pytest.mark.parametrize("spread", [0, 12, 40])
+def test_dense_over_int8_blocks_of_very_different_scales(G, spread):
+    """Value scales up to 2^spread apart, blocks of zeros as a store leaves them (the least scale), and a scale of 0."""
+    g = gen(90 + spread)
+    n, block = 2000, 32
+    blocks = -(-n // block)
+    codes = [torch.randint(-127, 128, (1, 2, n, D), generator=g, device=DEV, dtype=torch.int8) for _ in range(2)]
+    ks = torch.full((1, 2, blocks), 1 / 64, device=DEV)
+    vs = torch.exp2(torch.randint(-spread, spread + 1, (1, 2, blocks), generator=g, device=DEV).float())
+    for i in range(0, blocks, 3):
+        codes[1][:, :, i * block:(i + 1) * block] = 0
+        vs[:, :, i] = LEAST
+    vs[0, 1, 4], ks[0, 1, 7] = 0.0, 0.0
+    q = rows(91, 1, 2 * G, D, spread=0.0)
+    out = mog.dense_decode(mog.KVI8(*codes, ks, vs, block), None, ints(n), n, q)
+    for h in range(2):
+        K, V = (x[0, h].double() * s[0, h].double().repeat_interleave(block)[:n, None] for x, s in zip(codes, (ks, vs)))
+        want, size = attended(q[0, h * G:(h + 1) * G], K, V)
+        # as above; and a weight * scale is held to 2^-24 of the largest one of a row that is not zero
+        p = torch.softmax(q[0, h * G:(h + 1) * G].double() @ K.T / math.sqrt(D), -1)
+        top = (p * vs[0, h].double().repeat_interleave(block)[:n]).amax(-1, keepdim=True) * 127 * n * 2.0 ** -24
+        assert ((out[0, h * G:(h + 1) * G].double() - want).abs() <= 2.0 ** -14 * size + top).all(), h
+
+
+def test_dense_over_stored_zeros_and_nan():
+    """Zeros stored as keys and values weigh in; a NaN row shows in its head alone."""
+    c = Cache8(95, 1, 3, 128, 32)
+    k, v = rows(96, 1, 100, 3, D, spread=0.0), rows(97, 1, 100, 3, D, spread=0.0)
+    k[:, 32:64], v[:, 32:64] = 0, 0
+    v[0, 99, 2, 5] = float("nan")
+    mog.kv_store(c.cache, None, ints(0), None, k, v)
+    q = rows(98, 1, 3, D, spread=0.0)
+    out = mog.dense_decode(c.cache, None, ints(100), 100, q)
+    for h in range(2):
+        K, V = (x[0, h, :100].double() * s[0, h].double().repeat_interleave(32)[:100, None] for x, s in ((c.K, c.ks), (c.V, c.vs)))
+        assert (K[32:64] == 0).all() and (V[32:64] == 0).all()
+        want, size = attended(q[0, h:h + 1], K, V)
+        assert ((out[0, h].double() - want[0]).abs() <= 2.0 ** -14 * size[0]).all()
+    assert torch.isnan(out[0, 2]).all()
+
+
 def test_diff_over_int8_blocks():
     """The same rows in 16-bit products: the differential step over int8 blocks and over their bf16 values.
     int8 codes with power-of-two scales are bf16 values, so both steps read the same rows."""
