@@ -106,6 +106,7 @@ struct CacheArgs {
     const int *count;        // own_rows: null, or per sequence: at most 0: its output stays as it is
     float *part;
     float scale2;
+    int small;  // the strides fit 32 bits
     int cs;  // CTAs of a cluster that works on one unit; 0: the tile list is split
 };
 
@@ -234,6 +235,25 @@ __device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<T::ROWS> 
     const int first = c.t * T::ROWS, left = c.n - first;  // rows of the sequence from here on
     const int pmask = (1 << a.pshift) - 1;
     const int64_t head = c.h * a.sh + r0 * a.sn + ch * 16 + (PAGED ? 0 : c.b * a.sb);
+    // int8, contiguous: a tile all of whose rows are there, with strides of 32 bits, without the checks of its rows.
+    // The kernel is bound by its instructions there (1M tokens, 8 KV heads, G = 4: 405 us against 429); in pages the
+    // same made it slower (8 x 16-64K tokens, 32 KV heads: 502 us against 496).
+    if (T::I8 && !PAGED && a.small && left >= T::ROWS) {
+        const uint8_t *k = a.K + head + (int64_t)first * (int)a.sn;
+        const int64_t v = a.V - a.K;
+#pragma unroll
+        for (int i = 0; i < T::ROWS / RP; ++i) {
+            const uint8_t *src = k + (int64_t)(RP * i) * (int)a.sn;
+            cp_async16(stage + swz_k<ROW8>(r0 + RP * i, ch), src);
+            cp_async16(stage + T::KV + swz_v<ROW8>(r0 + RP * i, ch), src + v);
+        }
+        if (tid >= T::ROWS) return;
+        const int64_t so = c.b * a.ssb + c.h * a.ssh + (int64_t)((first + tid) >> a.sshift) * (int)a.ssn;
+        cp_async4(stage + T::AUX + 4 * tid, a.ks + so, 4);
+        cp_async4(stage + T::AUX + 4 * (T::ROWS + tid), a.vs + so, 4);
+        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + T::MASK + 4 * (tid >> 5)), "r"(0xffffffffu) : "memory");
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < T::ROWS / RP; ++i) {
         const int r = r0 + RP * i;
