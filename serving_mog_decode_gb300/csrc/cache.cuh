@@ -203,14 +203,22 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int src
 
 // Shared-memory position of a 16-byte chunk of a row, conflict-free for the readers.  e4m3
 // (128-byte rows): K is read at rows r, r+1 and chunks t (t < 4), V at rows 0, 2, 4, 6 (+1,
-// +8) and two neighbouring chunks.  bf16 (256-byte rows): ldmatrix.
+// +8) and two neighbouring chunks; int8's V by ldmatrix, 8 rows at a chunk.  bf16 (256-byte rows): ldmatrix.
 template <bool ROW8>
 __device__ __forceinline__ uint32_t swz_k(int row, int ch) {
     return ROW8 ? (uint32_t)(row * MOG_D + ((ch ^ ((row & 1) << 2)) << 4)) : swz(row, ch);
 }
-template <bool ROW8>
+template <bool ROW8, bool I8>
 __device__ __forceinline__ uint32_t swz_v(int row, int ch) {
-    return ROW8 ? (uint32_t)(row * MOG_D + ((ch ^ (row & 6)) << 4)) : swz(row, ch);
+    return ROW8 ? (uint32_t)(row * MOG_D + ((ch ^ (row & (I8 ? 7 : 6))) << 4)) : swz(row, ch);
+}
+// int8: the row of a block of 16 that the products take as their r-th.  ldmatrix hands out V with four
+// neighbouring rows of a dimension in a word, rows 4t .. 4t+3 to lane t; the second product has them at 2t, 2t+1,
+// 2t+8 and 2t+9.
+template <bool I8>
+__device__ __forceinline__ int block_row(int r) {
+    const int r8 = r & 7;
+    return I8 ? 2 * r8 - (r8 & 1) + 2 * (r >> 3) : r;
 }
 
 // Page of the tile's 16-row group `lane`, loaded one tile ahead of its use (unchecked: a
@@ -245,7 +253,7 @@ __device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<T::ROWS> 
         for (int i = 0; i < T::ROWS / RP; ++i) {
             const uint8_t *src = k + (int64_t)(RP * i) * (int)a.sn;
             cp_async16(stage + swz_k<ROW8>(r0 + RP * i, ch), src);
-            cp_async16(stage + T::KV + swz_v<ROW8>(r0 + RP * i, ch), src + v);
+            cp_async16(stage + T::KV + swz_v<ROW8, T::I8>(r0 + RP * i, ch), src + v);
         }
         if (tid >= T::ROWS) return;
         const int64_t so = c.b * a.ssb + c.h * a.ssh + (int64_t)((first + tid) >> a.sshift) * (int)a.ssn;
@@ -264,7 +272,7 @@ __device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<T::ROWS> 
         off = ok ? off : 0;
         const int bytes = ok ? 16 : 0;
         cp_async16(stage + swz_k<ROW8>(r, ch), a.K + off, bytes);
-        cp_async16(stage + T::KV + swz_v<ROW8>(r, ch), a.V + off, bytes);
+        cp_async16(stage + T::KV + swz_v<ROW8, T::I8>(r, ch), a.V + off, bytes);
     }
     // thread r: row r's scales and whether it is there
     if (tid >= T::ROWS) return;
@@ -430,6 +438,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
     return r;
 }
+// Two blocks of 16 rows by 16 bytes, transposed: r[2k], r[2k + 1]: of block k, bytes g and g + 8 of rows 4t .. 4t+3.
+// Lane l: the address of row l % 16 of block l / 16.
+__device__ __forceinline__ void ldsm_b8_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // The largest part of (x, y) that 16 bits hold, and what is left.
@@ -458,6 +472,14 @@ __device__ __forceinline__ float2 lds8(uint32_t addr) {
     return r;
 }
 
+// Wide: the scales of a block's rows 2t, 2t+1, 2t+8, 2t+9 of the products.
+template <bool I8>
+__device__ __forceinline__ void row_scales(float (&k)[4], uint32_t at) {
+    const int t = threadIdx.x & 3;
+    const float2 x = lds8(at + (I8 ? 16 : 8) * t), y = lds8(at + (I8 ? 16 * t + 8 : 8 * t + 32));
+    k[0] = x.x, k[1] = x.y, k[2] = y.x, k[3] = y.y;
+}
+
 // 16 rows by 16 dimensions of K: {rows g | rows g+8} x {dimension pairs 0 | 1} of step ks, as
 // the operand with rows in M; its halves (0, 2) and (1, 3) are the two with 8 rows in N.
 template <bool ROW8, bool I8>
@@ -479,10 +501,10 @@ __device__ __forceinline__ float column_max(float x) {
     return x;
 }
 // Row (of a block of 16) and column (of the lane's two) of logit i.
-template <bool WIDE>
+template <bool WIDE, bool I8>
 __device__ __forceinline__ int logit_row(int i) {
     const int lane = threadIdx.x & 31;
-    return WIDE ? 2 * (lane & 3) + (i & 1) + 8 * (i >> 2) : (lane >> 2) + 8 * (i >> 1);
+    return block_row<I8>(WIDE ? 2 * (lane & 3) + (i & 1) + 8 * (i >> 2) : (lane >> 2) + 8 * (i >> 1));
 }
 template <bool WIDE>
 __device__ __forceinline__ constexpr int logit_col(int i) { return WIDE ? (i >> 1) & 1 : i & 1; }
@@ -547,7 +569,7 @@ __device__ __forceinline__ void new_unit(State<T::WIDE> &st, const float (&s)[T:
     for (int blk = 0; blk < T::BLK; ++blk)
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const int v = __float_as_int(lds4(vsc + 4 * (16 * blk + logit_row<WIDE>(i)))) & 0x7fffffff;
+            const int v = __float_as_int(lds4(vsc + 4 * (16 * blk + logit_row<WIDE, T::I8>(i)))) & 0x7fffffff;
             // (rounded up: a weight must not pass the unit)
             const float x = v > 0 && v < F32_INF ? __fadd_ru(s[blk][i], (float)((v >> 23) - 126 - ve)) : -INFINITY;
             far[logit_col<WIDE>(i)] = fmaxf(far[logit_col<WIDE>(i)], x);
@@ -628,8 +650,8 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
             if (ROW8) {
 #pragma unroll
                 for (int blk = 0; blk < BLK; ++blk) {
-                    wa[blk] = lds16(sk + swz_k<ROW8>(16 * blk + g, t + 4 * j));
-                    wb[blk] = lds16(sk + swz_k<ROW8>(16 * blk + g + 8, t + 4 * j));
+                    wa[blk] = lds16(sk + swz_k<ROW8>(16 * blk + block_row<T::I8>(g), t + 4 * j));
+                    wb[blk] = lds16(sk + swz_k<ROW8>(16 * blk + block_row<T::I8>(g + 8), t + 4 * j));
                 }
             }
 #pragma unroll
@@ -662,17 +684,13 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
     // log2-domain logits; row of s[blk][i]: rowof(i).  They are rounded before the maximum is taken
     // from them (no fused multiply-add in the exponent): the largest weight has to be 1 however
     // large the logits.
-    auto rowof = [](int i) { return logit_row<WIDE>(i); };
+    auto rowof = [](int i) { return logit_row<WIDE, T::I8>(i); };
     auto colof = [](int i) { return logit_col<WIDE>(i); };
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
         float k[4];  // scales of this lane's rows of the block (narrow: two of them)
-        if (ROW8 && WIDE) {
-            const float2 x = lds8(sc + 4 * (16 * blk + 2 * t)), y = lds8(sc + 4 * (16 * blk + 2 * t + 8));
-            k[0] = x.x, k[1] = x.y, k[2] = y.x, k[3] = y.y;
-        } else if (ROW8) {
-            k[0] = lds4(sc + 4 * (16 * blk + g)), k[1] = lds4(sc + 4 * (16 * blk + g + 8));
-        }
+        if (ROW8 && WIDE) row_scales<T::I8>(k, sc + 64 * blk);
+        else if (ROW8) k[0] = lds4(sc + 4 * (16 * blk + rowof(0))), k[1] = lds4(sc + 4 * (16 * blk + rowof(2)));
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const float kk = ROW8 ? k[WIDE ? (i & 1) + 2 * (i >> 2) : i >> 1] : 1.f;
@@ -722,11 +740,12 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
     for (int blk = 0; blk < BLK; ++blk) {
         float v[4];
+        const uint32_t vsc = sc + 4 * (T::ROWS + 16 * blk);
         if (ROW8 && WIDE) {
-            const float2 x = lds8(sc + 4 * (T::ROWS + 16 * blk + 2 * t)), y = lds8(sc + 4 * (T::ROWS + 16 * blk + 2 * t + 8));
-            v[0] = x.x * inv, v[1] = x.y * inv, v[2] = y.x * inv, v[3] = y.y * inv;
+            row_scales<T::I8>(v, vsc);
+            v[0] *= inv, v[1] *= inv, v[2] *= inv, v[3] *= inv;
         } else if (ROW8) {
-            v[0] = lds4(sc + 4 * (T::ROWS + 16 * blk + g)) * inv, v[1] = lds4(sc + 4 * (T::ROWS + 16 * blk + g + 8)) * inv;
+            v[0] = lds4(vsc + 4 * rowof(0)) * inv, v[1] = lds4(vsc + 4 * rowof(2)) * inv;
         }
 #pragma unroll
         for (int i = 0; i < NS; i += 2) {
@@ -769,7 +788,26 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
                 o = fmaf(o, al[State<WIDE>::col(e)], d[k][e]);
             }
     };
-    if (ROW8) {
+    if (T::I8) {
+        // words of dimensions g and g + 8 of a block's 16, rows 4t .. 4t+3
+#pragma unroll
+        for (int mt = 0; mt < 8; mt += 2) {
+            uint32_t x[BLK][4];
+#pragma unroll
+            for (int blk = 0; blk < BLK; ++blk)
+                ldsm_b8_t(sv + swz_v<ROW8, T::I8>(16 * blk + (lane & 15), mt + (lane >> 4)), x[blk]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t a[BLK][4];
+#pragma unroll
+                for (int blk = 0; blk < BLK; ++blk) {
+                    widen<T::I8>(x[blk][2 * k], a[blk][0], a[blk][2]);
+                    widen<T::I8>(x[blk][2 * k + 1], a[blk][1], a[blk][3]);
+                }
+                add(mt + k, a);
+            }
+        }
+    } else if (ROW8) {
         // rows 2t, 2t+1, 2t+8, 2t+9 of a block, dimensions 16g .. 16g+15: word w holds
         // dimensions 16g + 4w .. +3, the sets 0 and 1 of mt = 2w, then of 2w + 1
         uint4 x[BLK][4];
@@ -777,7 +815,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
         for (int blk = 0; blk < BLK; ++blk)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[blk][i] = lds16(sv + swz_v<ROW8>(16 * blk + 2 * t + (i & 1) + 8 * (i >> 1), g));
+                x[blk][i] = lds16(sv + swz_v<ROW8, T::I8>(16 * blk + 2 * t + (i & 1) + 8 * (i >> 1), g));
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
@@ -793,7 +831,7 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
             uint32_t a[BLK][4];
-            ldsm_x4_t(sv + swz_v<ROW8>((mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0][0], a[0][1], a[0][2], a[0][3]);
+            ldsm_x4_t(sv + swz_v<ROW8, T::I8>((mat >> 1) * 8 + r8, 2 * mt + (mat & 1)), a[0][0], a[0][1], a[0][2], a[0][3]);
             add(mt, a);
         }
     }
@@ -845,7 +883,7 @@ __device__ __forceinline__ void state_fold(State<WIDE> &st, const float *x, cons
 
 template <class T, bool DIFF>
 __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex, const CacheArgs &a, float *dst) {
-    constexpr bool ROW8 = T::ROW8, WIDE = T::WIDE;
+    constexpr bool ROW8 = T::ROW8, WIDE = T::WIDE, E4M3 = T::ROW8 && !T::I8;  // (int8's dimensions are in the order of bf16's)
     using S = State<WIDE>;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     constexpr int SW = S::NT * 4 * 32;  // words of a warp's accumulators
@@ -883,8 +921,8 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
         if (WIDE) {
             // o[2 mt + k][2c + e]: e4m3: dimension 16(2t + e) + 2 mt + k; bf16: 16 mt + 8 k + 2t + e
 #pragma unroll
-            for (int i = 0; i < S::NT; i += ROW8 ? 4 : 1) {
-                if (ROW8) {
+            for (int i = 0; i < S::NT; i += E4M3 ? 4 : 1) {
+                if (E4M3) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         *reinterpret_cast<float4 *>(r + 16 * (2 * t + e) + i) =
@@ -898,7 +936,7 @@ __device__ __forceinline__ void flush(State<T::WIDE> &st, float *x, Exchange &ex
             // o[mt][c + 2 k]: e4m3: dimension 16 g + 2 mt + k; bf16: 16 mt + 8 k + g
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (ROW8) {
+                if (E4M3) {
                     *reinterpret_cast<float2 *>(r + 16 * g + 2 * i) = make_float2(st.o[i][c], st.o[i][c + 2]);
                 } else {
                     r[16 * i + g] = st.o[i][c];
