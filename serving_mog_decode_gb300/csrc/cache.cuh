@@ -23,8 +23,10 @@
 // one in the layout that the second takes) and a maximum over 4 lanes instead of 8.
 //
 // 8-bit rows are read by 16-byte loads in the order the fragments want (dimensions are
-// permuted alike in K and q, and back in the output), then widened in registers to fp16,
-// which holds every e4m3 and int8 value exactly.  The scale of an int8 block is copied to each of its rows
+// permuted alike in K and q, and, for e4m3, back in the output), then widened in registers to fp16,
+// which holds every e4m3 and int8 value exactly.  An int8 tile's V is read by the transposing ldmatrix for bytes, and the rows
+// of a block of 16 are taken in the order in which that hands them out (block_row): no shuffle of bytes is left before
+// widening, which for int8 takes five instructions for four codes instead of e4m3's two.  The scale of an int8 block is copied to each of its rows
 // in the stage, so that all 8-bit rows are alike from there on.  q enters as fp16 scaled by a power of two of its
 // own, so that its elements down to 2^-29 of the largest are exact.  Weights p * v_scale enter
 // the P.V product as fp16, 2^14 times their share of a running unit: high + low parts (2^-22
@@ -35,7 +37,9 @@
 // Bound by: HBM in the narrow form (whole steps: 1M e4m3 tokens, 8 KV heads, G = 4: 315 us,
 // 7.0 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 310 us, 6.9 TB/s; over e4m3 rows
 // 171 us, 6.5 TB/s); the wide form too over bf16 rows (G = 5: 315 us), but over e4m3 rows by the latencies of its
-// chains (G = 5, 4 x 128K: 220 us, 5.0 TB/s; 43% of issue slots, 37% of the tensor pipe).
+// chains (G = 5, 4 x 128K: 220 us, 5.0 TB/s; 43% of issue slots, 37% of the tensor pipe).  int8 rows: 1M tokens, 8 KV heads,
+// G = 4: 395 us, 5.4 TB/s; not HBM (75%) but the waits between a warp's products and its widening, at 52% of the
+// issue slots (three CTAs of four warps, which the registers allow).
 #pragma once
 
 #include <cuda_bf16.h>

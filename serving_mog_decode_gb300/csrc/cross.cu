@@ -21,6 +21,12 @@
 // tile products, of which each CTA takes an equal share (sequences alike: of what whole rounds leave).  The parts of an item that several CTAs have are partials (at most
 // two a CTA), which k_cross_merge folds.  cross_grid has the rule.  The copies of a CTA's next item run ahead.
 //
+// Bound by: the tensor cores, whose products the softmax does not hide completely.  4096 tokens of 32 heads over 32K rows
+// of 8 KV heads: 1.35 ms, 1.63 PFLOP/s, 0.86 of a library's matrix product in a burst, 0.96 of a sustained one; a unit (two tile products)
+// takes about 2.9K cycles, 2048 of them the MMA pipe's, and the GPU runs at its power limit (1.97 GHz).  The chain of a
+// softmax tile is about 1300 cycles; an item's start and end (O read, normalised, stored) about 10K.  Few query rows (16
+// tokens of 40 heads to 128K rows of 8 heads, 4 sequences, in pages): HBM, 335 us, 6.4 TB/s.
+//
 // Tensor memory holds S (then P) and O of both streams, 512 columns.  O is rescaled only when a row's
 // maximum has risen by more than 2^8 since the last time: weights are then at most 2^8, and O and
 // their sum (fp32) lose nothing.  Weights are rounded to bf16 (2^-9 of each; the product's other operand is bf16),
@@ -41,6 +47,7 @@ constexpr int CX_RING = 5;                       // slots of K and V tiles
 constexpr int CX_THREADS = 384, CX_MMA = 8, CX_LOAD = 9, CX_Q = 10;
 constexpr int CX_ITEMS = 4;                      // items found ahead
 constexpr int CX_SORT = 64;                      // sequences that whole items are sorted over
+constexpr int CX_ROUNDS = 64;                    // whole items of a CTA that are added up beforehand
 // Registers: 168 a thread at launch; the softmax warps take 208, the others leave theirs at 80
 // (256 * 208 + 128 * 80 = 63488 of 384 * 168 = 64512).
 constexpr int CX_REGS_MORE = 208, CX_REGS_LESS = 80;
@@ -91,16 +98,22 @@ struct CrossSeq {
 // order.  n = 0: not sorted; `items` of every (sequence, KV head), real or not.
 struct CrossOrder {
     int n, items;
+    int whole;                 // whole items: by cross_grid, or as `fits` finds
+    int total, longest, most;  // units: of all items, of the longest one, of the CTA with the most
+    int differ;                // sequences that are not like the first
     uint8_t seq[CX_SORT];
     int end[CX_SORT], count[CX_SORT], len[CX_SORT];  // (count, len: by sequence)
     // (by the whole CTA; followed by a barrier)
     __device__ __forceinline__ void make(const CrossArgs &a, int (&need)[CX_SORT], int (&key)[CX_SORT]) {
         const int tid = threadIdx.x, per = ((a.t_max + a.tokens - 1) / a.tokens + 1) / 2;
-        const bool sort = a.batch <= CX_SORT && a.batch * a.h_kv * per > (int)gridDim.x;
-        if (tid == 0) n = sort ? a.batch : 0, items = per;
+        const bool sort = a.batch <= CX_SORT && (a.whole ? a.batch * a.h_kv * per > (int)gridDim.x : a.batch > 1);
+        if (tid == 0) {
+            n = sort ? a.batch : 0, items = per, whole = a.whole;
+            total = longest = most = differ = 0;
+        }
         if (!sort) return;
+        CrossSeq c;
         if (tid < a.batch) {
-            CrossSeq c;
             c.load(a, tid);
             need[tid] = c.items() * a.h_kv, key[tid] = c.nt;
             count[tid] = c.count, len[tid] = c.len;
@@ -112,7 +125,43 @@ struct CrossOrder {
             for (int i = 0; i < a.batch; ++i)
                 if (key[i] > key[tid] || (key[i] == key[tid] && i < tid)) ++rank, e += need[i];
             seq[rank] = (uint8_t)tid, end[rank] = e;
+            if (!a.whole) {
+                CrossSeq f;
+                f.set(a, count[0], len[0]);
+                atomicAdd(&total, c.cost() * a.h_kv);
+                atomicMax(&longest, c.pairs ? c.units : c.half);
+                atomicOr(&differ, c.nt != f.nt || c.pairs != f.pairs || c.half != f.half);
+            }
         }
+        if (!a.whole) fits(a);
+    }
+    // Sequences that differ, in a call whose largest lengths ask for equal shares: whole items if these leave the CTA with
+    // the most to do little above the mean.  Equal shares of such sequences are more than their partials: CTAs are no longer in
+    // step at the same key tiles, and L2 serves each on its own.  24 ragged batches, both ways: whole items are the faster
+    // of the two up to 4/3 of the mean and 12 units (16 sequences, 16 heads, G = 8, 407 tokens to 1000 .. 4000 rows,
+    // 515 units at most, 509 in the mean: 869 us against 1109; 4 sequences, 4 heads, 146 tokens, 30 and 12.5: 53.5
+    // against 54.8; 4 sequences, 8 heads, G = 8, 69 tokens to 2000 .. 8000 rows, 59 and 17.9: 107 against 86).
+    // (A function of its own: inlined, it moves the code of the main loops, which then take 2% longer.)
+    __device__ __noinline__ void fits(const CrossArgs &a) {
+        __syncthreads();
+        const int ctas = gridDim.x, all = end[n - 1], limit = total / ctas + total / ctas / 3 + 12;
+        if (!differ || longest > limit || all > CX_ROUNDS * ctas) return;
+        const int c = threadIdx.x;
+        if (c < ctas) {
+            int sum = 0, k = 0;
+            CrossSeq q;
+            q.set(a, count[seq[0]], len[seq[0]]);
+            for (int r = 0;; ++r) {
+                const int i = r * ctas + (r & 1 ? ctas - 1 - c : c);
+                if (i >= all) break;  // (those of later rounds are greater)
+                while (end[k] <= i) ++k, q.set(a, count[seq[k]], len[seq[k]]);
+                const int j = (i - (k ? end[k - 1] : 0)) % q.items();
+                sum += j < q.pairs ? q.units : q.half;
+            }
+            atomicMax(&most, sum);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) whole = most <= limit;
     }
 };
 
@@ -142,7 +191,7 @@ struct Segment {
     // The CTA's first segment; false if it has none (called by full warps).
     __device__ __forceinline__ bool start(const CrossArgs &a, const CrossOrder &o) {
         left = 0;
-        if (a.whole) return take(a, o);
+        if (o.whole) return take(a, o);
         plan(a, gridDim.x);
         if (rounds) return round(a);
         return share(a);
@@ -269,7 +318,7 @@ struct Segment {
         at = o - x * q.units;
     }
     __device__ __forceinline__ bool next(const CrossArgs &a, const CrossOrder &o) {
-        if (a.whole) return take(a, o);
+        if (o.whole) return take(a, o);
         if (rounds) return left < rounds ? round(a) : share(a);
         left -= min(units() - at, left);
         if (left <= 0) return false;
@@ -437,10 +486,8 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     __shared__ Segment s_items[CX_ITEMS];  // what warp 11 has found for the others to do
     __shared__ CrossOrder s_order;
-    if (a.whole) {
-        s_order.make(a, *reinterpret_cast<int(*)[CX_SORT]>(cx_raw), *reinterpret_cast<int(*)[CX_SORT]>(cx_raw + 4 * CX_SORT));
-        __syncthreads();
-    }
+    s_order.make(a, *reinterpret_cast<int(*)[CX_SORT]>(cx_raw), *reinterpret_cast<int(*)[CX_SORT]>(cx_raw + 4 * CX_SORT));
+    __syncthreads();
     const uint32_t sQ = (smem_u32(cx_raw) + 1023u) & ~1023u, sR = sQ + 2 * CX_TILE;
     auto bar = [&](const uint64_t &x) { return smem_u32(&x); };
     float2 *s_ml = reinterpret_cast<float2 *>(cx_raw + (sQ + CX_TILE - smem_u32(cx_raw)));  // (one query tile: the other's place)
@@ -709,7 +756,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
             }
             if (!ok) atomicExch(&s_fail, 1);
             if (!a.whole) {
-                const int4 f = w.fold(a);
+                const int4 f = s_order.whole ? make_int4(0, 0, 0, 0) : w.fold(a);
                 if (lane == 0) a.fold[blockIdx.x] = f;
             }
         }
@@ -1017,7 +1064,9 @@ __global__ void __launch_bounds__(256) k_cross_merge(CrossArgs a) {
 
 // The grid and its work, by what the largest lengths and counts make of it.  Equal shares cost partials (up to 256 KB
 // written and read by each CTA) and their fold, as much as about 8 units of work; whole items leave the SMs
-// with unequal ones (8 sequences, 16 heads, 500 tokens to 375 .. 1500 rows: whole items 36 us, equal shares 105).
+// with unequal ones (8 sequences, 16 heads, 500 tokens to 375 .. 1500 rows: whole items 46 us, equal shares 84; 1 sequence,
+// 8 heads, G = 4, 64 tokens to 4000 rows: 57 against 28).  A call laid out for equal shares whose sequences differ may still
+// take whole items (CrossOrder::fits).
 static void cross_grid(int batch, int h_kv, int G, int t_max, int n_max, int64_t &ctas, int &whole) {
     const int64_t tiles = ceil_div64(t_max, CX_M / G), nt = ceil_div64(n_max, CX_KEYS), per = ceil_div64(tiles, 2);
     const int64_t units = (int64_t)batch * h_kv, all = units * (tiles / 2 * nt + tiles % 2 * ceil_div64(nt, 2));
