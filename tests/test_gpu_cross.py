@@ -304,6 +304,32 @@ def test_deterministic_captured_and_on_another_stream():
             assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("page", [0, 64])
+def test_how_the_work_is_shared_follows_the_lengths(page):
+    """One captured call, whose largest lengths ask for equal shares: sequences that balance as whole items, that do
+    not, that are alike, that are empty, and counts of their own."""
+    m = Made(85, (4000, 3100, 2000, 1100), 4, page)
+    q = randn(87, 4, 700, 16, D)
+    count, out = ints(700, 700, 700, 700), torch.empty_like(q)
+    rows = m.lens
+    for _ in range(2):
+        mog.cross_attend(*m.cache, m.lengths, m.n_max, q, count=count, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mog.cross_attend(*m.cache, m.lengths, m.n_max, q, count=count, out=out)
+    for lens, cnt in (((4000, 3100, 2000, 1100), (700,) * 4), ((4000, 700, 600, 500), (700,) * 4), ((1100,) * 4, (700,) * 4),
+                      ((0, 0, 2000, 1), (700, 0, 333, 32)), ((4000, 3100, 2000, 1100), (33, 700, 1, 640)), ((0,) * 4, (700, 1, 0, 65))):
+        lens = tuple(min(n, r) for n, r in zip(lens, rows))
+        m.lengths.copy_(torch.tensor(lens, dtype=torch.int32))
+        count.copy_(torch.tensor(cnt, dtype=torch.int32))
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        m.lens = lens
+        m.check(q, out, 4, cnt, fill=3.0)
+
+
 def test_past_32_bit_offsets():
     """Rows of one head spread over more than 4 GiB by their stride, and queries as far apart."""
     n, stride = 40000, 64 * 1024
