@@ -79,6 +79,20 @@ def test_rope(rot, pairs, T, H, B):
         check_turned(back[b], want, bound)
 
 
+@pytest.mark.parametrize("rot,pairs,inverse", [(128, False, False), (96, True, True), (16, False, True)])
+def test_rope_rounds_once(rot, pairs, inverse):
+    """Before the rounding to bf16, an element is off by no more than 3 * 2^-24 of its pair: the angle is within an eighth
+    of a turn of whole quarters and rounded there (pi 2^-27, times a slope of at most 0.71: 0.28 * 2^-24) and cut to 2^-32
+    turns (0.03), sincospi to one unit (1), the factor's product (0.5), and the two roundings of x c - y s (1.0)."""
+    r = mog.Rope(rot, base=500000.0, interleaved=pairs, factor=1.25)
+    x = rows(3, 1, 4000, 4, D)
+    for start in (0, 1 << 20):
+        out = mog.rope(x, ints(start), r, inverse=inverse)
+        want, bound = turned(x[0], start + torch.arange(4000, device=DEV), mog.rope_frequencies(rot, 500000.0)[0], 1.25, rot, pairs, inverse)
+        half = torch.exp2(torch.frexp(want).exponent.double() - 9)  # half a step of bf16
+        assert ((out[0].double() - want).abs() <= half + 3 * 2.0 ** -24 * (bound / 2.0 ** -20)).all()
+
+
 @pytest.mark.parametrize("start", [(1 << 31) - 9, -(1 << 31), -5, 16777217])
 def test_rope_far_positions(start):
     """Any int32: angles of 2^31 radians and more (64-bit reference: 2^-53 of 2^32 radians is 2^-21)."""
