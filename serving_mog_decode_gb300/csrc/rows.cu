@@ -6,9 +6,10 @@
 // pos * f_i.  A frequency is held as turns per position in 64-bit fixed point, so that the angle is
 // one integer product whose overflow drops the whole turns: exact to 2^-32 of a turn at any
 // position (in fp32, position 1M would leave a tenth of a radian).  A CTA computes the
-// cosines and sines of its tokens once, into shared memory, for all their heads.  A prompt's chunk is bound by HBM and by
-// the three CTAs an SM that the rows in flight leave room for: 4096 tokens of 40 + 8 + 8 heads into bf16 pages, 117 MB, 22.5 us,
-// 5.2 TB/s (issue 56%); a step's tokens by latency: 8 sequences, 4.7 us.
+// cosines and sines of its tokens once, into shared memory, for all their heads.  A prompt is bound by HBM: 24K tokens of
+// 32 + 8 + 8 heads into bf16 pages, 590 MB, 90 us, 6.5 TB/s; a chunk's start and end show (4096 tokens of 40 + 8 + 8 heads,
+// 117 MB: 22 us, 5.3 TB/s); a step's tokens are latency: 8 sequences, 4.7 us.  Four CTAs an SM (64 registers) against the
+// three of 80: 94.2 us against 95.7, launch included.
 //
 // A row (256 bytes) is the work of eight lanes, two 16-byte chunks each.  Lane l's chunks hold whole
 // pairs in either layout, of the frequencies 8l .. 8l+7: chunks 2l, 2l+1 of neighbouring pairs, chunks
@@ -204,7 +205,7 @@ __device__ __forceinline__ void whole_rows(const RowsArgs &a, const float4 *cs, 
 }
 
 template <int TO>
-__global__ void __launch_bounds__(RW_THREADS) k_rope_rows(RowsArgs a) {
+__global__ void __launch_bounds__(RW_THREADS, 4) k_rope_rows(RowsArgs a) {
     extern __shared__ float4 cs[];
     const int b = blockIdx.y, tile = blockIdx.x / a.slices, slice = blockIdx.x - tile * a.slices;
     const int t0 = tile * a.tile, n = min(a.tile, seq_count(a, b) - t0);
@@ -227,7 +228,9 @@ __global__ void __launch_bounds__(RW_THREADS) k_rope_rows(RowsArgs a) {
 // maxima in shared memory.  A CTA's tile is `slabs` times 16 positions, and 8 / slabs heads at a time.
 //
 // Bound by HBM together with the waits between a tile's loads and its maxima: 4 prompts, 24K tokens of 8 heads into 64-row
-// pages, 100 MB read and 50 MB written: 27 us, 5.6 TB/s (issue 51%); with 32 query heads turned too, 22.5 KB a token: 94 us.
+// pages, 100 MB read and 50 MB written: 27 us, 5.6 TB/s (issue 51%); with 32 query heads turned too, 22.5 KB a token: 85 us, 5.9 TB/s.
+// With turns, registers for three CTAs an SM: 92 us for pairs in half the row and 102 for halves of all of it, launch included
+// (100 and 106 as the compiler chooses them; 92 and 107 for four, where they spill); without turns, for four: as fast as three.
 // ------------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t u16x2_max(uint32_t a, uint32_t b) {
@@ -266,7 +269,7 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio) {
 constexpr uint32_t I8_NAN = 0xffffu;  // a maximum: there is a NaN
 
 template <bool TURN>
-__global__ void __launch_bounds__(RW_THREADS) k_rows_i8(RowsArgs a) {
+__global__ void __launch_bounds__(RW_THREADS, TURN ? 3 : 4) k_rows_i8(RowsArgs a) {
     extern __shared__ float4 cs[];
     __shared__ uint32_t s_amax[2][RW_THREADS / 32];
     const int b = blockIdx.y, count = seq_count(a, b);
