@@ -38,7 +38,7 @@
 // 7.0 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 310 us, 6.9 TB/s; over e4m3 rows
 // 171 us, 6.5 TB/s); the wide form too over bf16 rows (G = 5: 315 us), but over e4m3 rows by the latencies of its
 // chains (G = 5, 4 x 128K: 220 us, 5.0 TB/s; 43% of issue slots, 37% of the tensor pipe).  int8 rows: 1M tokens, 8 KV heads,
-// G = 4: 395 us, 5.4 TB/s; not HBM (75%) but the waits between a warp's products and its widening, at 52% of the
+// G = 4: 380 us, 5.65 TB/s; not HBM (79%) but the waits between a warp's products and its widening, at 52% of the
 // issue slots (three CTAs of four warps, which the registers allow).
 #pragma once
 
@@ -793,20 +793,23 @@ __device__ __forceinline__ void compute(State<T::WIDE> &st, const QF &qf, const 
             }
     };
     if (T::I8) {
-        // words of dimensions g and g + 8 of a block's 16, rows 4t .. 4t+3
+        // words of dimensions g and g + 8 of a block's 16, rows 4t .. 4t+3; all of them asked for at once (two
+        // sets at a time: 395 us for 380 at 1M tokens; before the maxima: 391)
+        uint32_t x[4][BLK][4];
 #pragma unroll
-        for (int mt = 0; mt < 8; mt += 2) {
-            uint32_t x[BLK][4];
+        for (int mt = 0; mt < 8; mt += 2)
 #pragma unroll
             for (int blk = 0; blk < BLK; ++blk)
-                ldsm_b8_t(sv + swz_v<ROW8, T::I8>(16 * blk + (lane & 15), mt + (lane >> 4)), x[blk]);
+                ldsm_b8_t(sv + swz_v<ROW8, T::I8>(16 * blk + (lane & 15), mt + (lane >> 4)), x[mt / 2][blk]);
+#pragma unroll
+        for (int mt = 0; mt < 8; mt += 2) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint32_t a[BLK][4];
 #pragma unroll
                 for (int blk = 0; blk < BLK; ++blk) {
-                    widen<T::I8>(x[blk][2 * k], a[blk][0], a[blk][2]);
-                    widen<T::I8>(x[blk][2 * k + 1], a[blk][1], a[blk][3]);
+                    widen<T::I8>(x[mt / 2][blk][2 * k], a[blk][0], a[blk][2]);
+                    widen<T::I8>(x[mt / 2][blk][2 * k + 1], a[blk][1], a[blk][3]);
                 }
                 add(mt + k, a);
             }
