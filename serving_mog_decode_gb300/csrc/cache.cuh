@@ -38,7 +38,7 @@
 // 7.0 TB/s; differential, 4 x 128K bf16 tokens in 64-row pages, G = 4: 310 us, 6.9 TB/s; over e4m3 rows
 // 171 us, 6.5 TB/s); the wide form too over bf16 rows (G = 5: 315 us), but over e4m3 rows by the latencies of its
 // chains (G = 5, 4 x 128K: 220 us, 5.0 TB/s; 43% of issue slots, 37% of the tensor pipe).  int8 rows: 1M tokens, 8 KV heads,
-// G = 4: 380 us, 5.65 TB/s; not HBM (79%) but the waits between a warp's products and its widening, at 52% of the
+// G = 4: 380 us, 5.65 TB/s; not HBM (78%) but the waits between a warp's products and its widening, at 54% of the
 // issue slots (three CTAs of four warps, which the registers allow).
 #pragma once
 
