@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(CX_REGS_MORE));
         const int s = warp >> 2, r = tid & 127, gshift = PAGED ? min(a.pshift, 7) : 7;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-        uint32_t sp = 0, op0 = 0, op1 = 0, joins = 0;       // the next phases of s_full and both o_full
+        uint32_t sp = 0, op0 = 0, op1 = 0, joins = 0;       // the next phases of s_full and both o_full (op0: of q_full, too)
         const bool row = r < a.tokens * a.G;  // (the rows behind the tile's tokens hold anything)
         bool ok = true;
         for (uint32_t it = 0; warp_item_at(it); warp_item_done(it++)) {
@@ -886,7 +886,11 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
             if (join) {  // stream 1's maxima and sums to stream 0, which reads both O
                 if (s == 1) {
                     if (joins > 0) ok = ok && mbar_wait(bar(bars.j_free), (joins - 1) & 1);
-                    s_ml[r] = make_float2(m, l);
+                    // With one key tile the stream has waited for nothing of this item, and another warp's partial of the last one
+                    // may still be passing through this place: it is free when the item's queries are there, which q_free has let in.
+                    if (n == 0) ok = ok && mbar_wait(bar(bars.q_full), op0);
+                    if (ok) s_ml[r] = make_float2(m, l);
+                    else atomicExch(&s_fail, 1);  // (before stream 0 reads it)
                     mbar_arrive(bar(bars.j_full));
                 } else {
                     ok = ok && mbar_wait(bar(bars.j_full), joins & 1);
