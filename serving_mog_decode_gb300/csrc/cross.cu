@@ -487,6 +487,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     __shared__ Segment s_items[CX_ITEMS];  // what warp 11 has found for the others to do
     __shared__ CrossOrder s_order;
     s_order.make(a, *reinterpret_cast<int(*)[CX_SORT]>(cx_raw), *reinterpret_cast<int(*)[CX_SORT]>(cx_raw + 4 * CX_SORT));
+    fence_proxy_async();  // (the queries may be copied to where that worked)
     __syncthreads();
     const uint32_t sQ = (smem_u32(cx_raw) + 1023u) & ~1023u, sR = sQ + 2 * CX_TILE;
     auto bar = [&](const uint64_t &x) { return smem_u32(&x); };
