@@ -583,7 +583,8 @@ int mog_diff_decode(const mog_cache *c, const int32_t *lengths_dev, int32_t n_ma
  * Products of bf16 with fp32 sums; the weights are rounded to bf16 for the second one, an error of the
  * size of the output's own rounding.  d must be 128, h_q / h_kv <= 16, batch * h_kv <= 65535, t_max *
  * h_q <= 2^30, n_max <= 2^30, and the products of 256 query rows by 128 keys that make up the work at
- * most 2^30.  Should a bounded wait inside the kernel run out, its rows are NaN.
+ * most 2^30.  Should a bounded wait inside the kernel run out (after seconds, and later where what it waits for
+ * takes longer the more keys there are), its rows are NaN.
  */
 int mog_cross_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max,
                             int32_t n_max, size_t *bytes);
@@ -591,6 +592,16 @@ int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, int32_t n_m
                      int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev,
                      const void *q_dev, const int64_t *q_strides, void *out_dev,
                      const int64_t *out_strides, void *scratch_dev, size_t scratch_bytes, void *stream);
+
+/*
+ * Self-check of the last sentence: mog_cross_attend with t_max > 1 whose waits for a CTA's next piece of work, and for
+ * the place of its queries, give up after `polls` >= 0 polls (0: at once).  Each row is what mog_cross_attend makes it, or NaN.
+ */
+int mog_check_cross_wait(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                         int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev,
+                         const void *q_dev, const int64_t *q_strides, void *out_dev,
+                         const int64_t *out_strides, void *scratch_dev, size_t scratch_bytes, int32_t polls,
+                         void *stream);
 
 /*
  * Write new keys and values into a cache: token t < count[b] of sequence b goes to position

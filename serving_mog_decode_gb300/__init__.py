@@ -356,6 +356,7 @@ _SIGS = {
     "mog_kv_store": (C.c_int, [_P] + [C.c_int32] * 4 + [_P] * 4 + [C.c_int64] * 3 + [_P]),
     "mog_cross_scratch_bytes": (C.c_int, [C.c_int32] * 6 + [_P]),
     "mog_cross_attend": (C.c_int, [_P, _P] + [C.c_int32] * 6 + [_P] * 6 + [C.c_size_t, _P]),
+    "mog_check_cross_wait": (C.c_int, [_P, _P] + [C.c_int32] * 6 + [_P] * 6 + [C.c_size_t, C.c_int32, _P]),
     "mog_kv_load": (C.c_int, [_P] + [C.c_int32] * 4 + [_P] * 4 + [C.c_int64] * 3 + [_P]),
     "mog_rope_apply": (C.c_int, [_P] + [C.c_int32] * 4 + [_P, C.c_int32, _P, C.c_int32] + [_P] * 5),
     "mog_rope_store": (C.c_int, [_P, _P] + [C.c_int32] * 5 + [_P] * 10),
@@ -831,6 +832,16 @@ def cross_attend(K, V, lengths_dev, n_max, q, count=None, out=None, scratch=None
     count: int32 [B] query tokens of each sequence, or None for T; rows of out behind them are not
     written.  out: bf16 like q, a new tensor by default.  8-bit caches: dense_decode for one token,
     kv_load for more.  -> out."""
+    return _cross(K, V, lengths_dev, n_max, q, count, out, scratch, stream)
+
+
+def check_cross_wait(K, V, lengths_dev, n_max, q, polls, count=None, out=None, stream=None):
+    """cross_attend of more than one token whose long waits give up after `polls` polls (mog_check_cross_wait): rows
+    are what cross_attend makes them, or NaN.  -> out."""
+    return _cross(K, V, lengths_dev, n_max, q, count, out, None, stream, polls)
+
+
+def _cross(K, V, lengths_dev, n_max, q, count, out, scratch, stream, polls=None):
     torch = _torch()
     if isinstance(K, _ROWS8):
         raise ValueError("cross_attend reads bf16 caches: dense_decode takes 8-bit ones for one token, kv_load reads them back")
@@ -838,7 +849,7 @@ def cross_attend(K, V, lengths_dev, n_max, q, count=None, out=None, scratch=None
     s = _here(dev, stream)
     if s is None:
         with _there(dev, stream):
-            return cross_attend(K, V, lengths_dev, n_max, q, count, out, scratch)
+            return _cross(K, V, lengths_dev, n_max, q, count, out, scratch, None, polls)
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != 128:
         raise ValueError(f"q must be a bf16 tensor [{B}, T, H_q, 128] on the cache's device")
     shape = q.shape
@@ -866,9 +877,10 @@ def cross_attend(K, V, lengths_dev, n_max, q, count=None, out=None, scratch=None
         nbytes = scratch.numel() * scratch.element_size()
         at = scratch.data_ptr()
     try:
-        rc = lib().mog_cross_attend(C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, T,
-                                    None if count is None else count.data_ptr(), q.data_ptr(), _strides3(qs),
-                                    out.data_ptr(), _strides3(os_), at, nbytes, s)
+        args = (C.byref(c), lengths_dev.data_ptr(), n_max, B, H_kv, H_q, 128, T,
+                None if count is None else count.data_ptr(), q.data_ptr(), _strides3(qs), out.data_ptr(), _strides3(os_), at,
+                nbytes)
+        rc = lib().mog_cross_attend(*args, s) if polls is None else lib().mog_check_cross_wait(*args, polls, s)
     finally:
         if own is not None:
             torch._C._cuda_cudaCachingAllocator_raw_delete(own)

@@ -1039,10 +1039,11 @@ extern "C" int mog_cross_scratch_bytes(int32_t batch, int32_t h_kv, int32_t h_q,
 
 static int check_rows(const void *p, const int64_t *strides);
 
-extern "C" int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
-                                int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev,
-                                const void *q_dev, const int64_t *q_strides, void *out_dev,
-                                const int64_t *out_strides, void *scratch_dev, size_t scratch_bytes, void *stream) {
+// polls >= 0: the limit of the long waits of k_cross
+static int cross_attend(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch, int32_t h_kv,
+                        int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev, const void *q_dev,
+                        const int64_t *q_strides, void *out_dev, const int64_t *out_strides, void *scratch_dev,
+                        size_t scratch_bytes, void *stream, int polls) {
     size_t need = 0;
     int st = mog_cross_scratch_bytes(batch, h_kv, h_q, d, t_max, n_max, &need);
     if (st != MOG_OK) return st;
@@ -1068,8 +1069,26 @@ extern "C" int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, 
     // heads, G = 4: 11.5 us against 22)
     const cudaError_t e = t_max == 1 ? launch_cache_decode(c, lengths_dev, n_max, batch, h_kv, h_q / h_kv, q_dev, nullptr,
                                                            MOG_OUT_BF16, out_dev, scratch, s, &r)
-                                     : launch_cross(c, lengths_dev, n_max, batch, r, scratch, s);
+                                     : launch_cross(c, lengths_dev, n_max, batch, r, scratch, s, polls);
     return e == cudaSuccess ? MOG_OK : cuda_fail(e, "mog_cross_attend launch");
+}
+
+extern "C" int mog_cross_attend(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                                int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev,
+                                const void *q_dev, const int64_t *q_strides, void *out_dev,
+                                const int64_t *out_strides, void *scratch_dev, size_t scratch_bytes, void *stream) {
+    return cross_attend(c, lengths_dev, n_max, batch, h_kv, h_q, d, t_max, count_dev, q_dev, q_strides, out_dev,
+                        out_strides, scratch_dev, scratch_bytes, stream, -1);
+}
+
+extern "C" int mog_check_cross_wait(const mog_cache *c, const int32_t *lengths_dev, int32_t n_max, int32_t batch,
+                                    int32_t h_kv, int32_t h_q, int32_t d, int32_t t_max, const int32_t *count_dev,
+                                    const void *q_dev, const int64_t *q_strides, void *out_dev,
+                                    const int64_t *out_strides, void *scratch_dev, size_t scratch_bytes, int32_t polls,
+                                    void *stream) {
+    if (polls < 0 || t_max <= 1) return MOG_ERR_INVALID_ARG;
+    return cross_attend(c, lengths_dev, n_max, batch, h_kv, h_q, d, t_max, count_dev, q_dev, q_strides, out_dev,
+                        out_strides, scratch_dev, scratch_bytes, stream, polls);
 }
 
 // ------------------------------------------------------------------------ rotary positions

@@ -73,6 +73,7 @@ struct CrossArgs {
     float *part;
     int part_rows;
     int whole;       // whole items
+    int polls;       // limit of the waits that last as long as an item: for the next one, for the queries' place
 };
 
 // A sequence as items of each of its KV heads: `pairs` of two query tiles, `units` units each, and one of a
@@ -472,7 +473,29 @@ struct CrossBars {
     uint64_t j_full, j_free;  // one query tile: stream 1's maxima and sums are there; have been read
     uint64_t i_full[CX_ITEMS], i_free[CX_ITEMS];  // the items
     uint64_t v_tail[4];       // an item's last V: its rows behind the sequence's end are zero (the ring holds 2 such at most)
+    uint64_t drained;         // no MMA runs any more
 };
+
+// The rows that the softmax thread r of stream s would have written of the CTA's items from the skip-th on are NaN, the
+// partials' by their maxima: a wait has given up, and the items did not come.  (by full warps; a function of its own, as `fits`)
+__device__ __noinline__ void lost_items(const CrossArgs &a, const CrossOrder &o, uint32_t skip, int s, int r) {
+    Segment g;
+    for (bool more = g.start(a, o); more; more = g.next(a, o)) {
+        const int t0 = (2 * g.x + (g.pair ? s : 0)) * a.tokens;
+        if (skip > 0) {
+            --skip;
+        } else if ((g.pair || s == 0) && r < min(a.tokens, g.q.count - t0) * a.G) {
+            if (g.begins && g.ends) {
+                const int t = r / a.G, hd = r - t * a.G;
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + g.b * a.ob + (t0 + t) * a.ot + (int64_t)(g.h * a.G + hd) * a.oh);
+                for (int i = 0; i < MOG_D / 8; ++i) dst[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            } else {
+                a.part[((2 * (int64_t)blockIdx.x + (g.begins ? 1 : 0)) * a.part_rows + (g.pair ? s * CX_M : 0) + r) * CX_PART] = __int_as_float(0x7fffffff);
+            }
+        }
+        __syncwarp();
+    }
+}
 
 template <bool PAGED>
 __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __grid_constant__ CUtensorMap qmap,
@@ -505,6 +528,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         mbar_init(bar(bars.j_full), CX_M);
         mbar_init(bar(bars.j_free), CX_M);
         for (int i = 0; i < 4; ++i) mbar_init(bar(bars.v_tail[i]), 1);
+        mbar_init(bar(bars.drained), 1);
         for (int i = 0; i < CX_ITEMS; ++i) mbar_init(bar(bars.i_full[i]), 1), mbar_init(bar(bars.i_free[i]), 11);  // (warps 0 .. 10)
         fence_barrier_init();
         s_fail = 0;
@@ -517,10 +541,10 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    // The CTA's it-th item (by a whole warp, or by one thread for its own); false behind the last one.  Every role
-    // goes through all of them, also after a wait that has given up.
+    // The CTA's it-th item (by a whole warp, or by one thread for its own); false behind the last one, and if it does not
+    // come.  Every role goes through all that come, also after another wait that has given up.
     auto item_at = [&](uint32_t it) {
-        if (!mbar_wait(bar(bars.i_full[it % CX_ITEMS]), (it / CX_ITEMS) & 1)) {
+        if (!mbar_wait(bar(bars.i_full[it % CX_ITEMS]), (it / CX_ITEMS) & 1, a.polls)) {
             atomicExch(&s_fail, 1);
             return false;
         }
@@ -714,6 +738,8 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                     if (ok) run(s_items[it % CX_ITEMS]);
                     if (!ok) atomicExch(&s_fail, 1);
                 }
+                tc_commit(bar(bars.drained));  // no MMA outlives the CTA
+                mbar_wait(bar(bars.drained), 0);
             }
             __syncwarp();
         } else if (warp == CX_Q) {
@@ -725,7 +751,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
                 for (uint32_t it = 0; item_at(it); item_done(it++)) {
                     const Segment &g = s_items[it % CX_ITEMS];
                     if (!ok || g.nt == 0) continue;
-                    if (seg > 0) ok = mbar_wait(bar(bars.q_free), (seg - 1) & 1);
+                    if (seg > 0) ok = mbar_wait(bar(bars.q_free), (seg - 1) & 1, a.polls);
                     if (!ok) {
                         atomicExch(&s_fail, 1);
                         continue;
@@ -746,7 +772,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
             Segment w;
             bool more = w.start(a, s_order), ok = true;
             for (uint32_t it = 0; ok; ++it) {
-                if (it >= CX_ITEMS) ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.i_free[it % CX_ITEMS]), (it / CX_ITEMS - 1) & 1));
+                if (it >= CX_ITEMS) ok = __all_sync(0xffffffffu, mbar_wait(bar(bars.i_free[it % CX_ITEMS]), (it / CX_ITEMS - 1) & 1, a.polls));
                 w.end = !more;
                 if (lane == 0 && ok) {
                     s_items[it % CX_ITEMS] = w;
@@ -769,7 +795,8 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
         uint32_t sp = 0, op0 = 0, op1 = 0, joins = 0;       // the next phases of s_full and both o_full (op0: of q_full, too)
         const bool row = r < a.tokens * a.G;  // (the rows behind the tile's tokens hold anything)
         bool ok = true;
-        for (uint32_t it = 0; warp_item_at(it); warp_item_done(it++)) {
+        uint32_t it = 0;
+        for (; warp_item_at(it); warp_item_done(it++)) {
             const Segment &g = s_items[it % CX_ITEMS];
             const int n = g.n_of(s), n1 = g.n_of(1), len = g.q.len;
             const bool pair = g.pair, whole = g.begins && g.ends;
@@ -1011,6 +1038,7 @@ __global__ void __launch_bounds__(CX_THREADS, 1) k_cross(CrossArgs a, const __gr
             }
             joins += join;
         }
+        if (__any_sync(0xffffffffu, *(volatile int *)&s_fail != 0)) lost_items(a, s_order, it, s, r);
     }
     tc_fence_before();
     __syncthreads();
@@ -1108,7 +1136,7 @@ size_t cross_scratch(int batch, int h_kv, int G, int t_max, int n_max) {
 }
 
 cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, int batch, const RowsIn &r, float *scratch,
-                         cudaStream_t s) {
+                         cudaStream_t s, int polls) {
     CrossArgs a{};
     a.out = static_cast<uint16_t *>(r.qo), a.ob = r.os[0], a.ot = r.os[1], a.oh = r.os[2];
     a.lengths = lengths, a.count = r.count, a.n_max = n_max, a.t_max = r.t_max, a.batch = batch, a.h_kv = r.h_kv;
@@ -1116,6 +1144,8 @@ cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, 
     a.bt = c->block_table, a.pshift = c->block_table ? log2_exact(c->page_rows) : 0, a.pps = c->pages_per_seq;
     a.n_pages = c->n_pages;
     a.scale2 = (float)(1.4426950408889634 / sqrt((double)MOG_D));
+    // as many polls as the other waits (some seconds), and 16 for the 1.5 us of each key tile that an item may have
+    a.polls = polls >= 0 ? polls : (1 << 20) + 16 * (int)ceil_div64(n_max, CX_KEYS);
     const bool paged = c->block_table != nullptr;
     // a stride of 0 (one memory for all): a dim of one entry
     const int64_t h = !paged && c->stride_h == 0 ? 1 : r.h_kv, b = paged ? c->n_pages : c->stride_b == 0 ? 1 : batch;

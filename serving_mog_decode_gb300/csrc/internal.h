@@ -169,7 +169,7 @@ cudaError_t launch_rows_i8(const mog_cache *c, int batch, const RowsIn &r, cudaS
 cudaError_t launch_kv_load(const mog_cache *c, int batch, const RowsIn &r, void *ko, void *vo, cudaStream_t s);
 size_t cross_scratch(int batch, int h_kv, int G, int t_max, int n_max);
 cudaError_t launch_cross(const mog_cache *c, const int32_t *lengths, int n_max, int batch, const RowsIn &r, float *scratch,
-                         cudaStream_t s);
+                         cudaStream_t s, int polls = -1);  // polls >= 0: the limit of its long waits
 enum { PAGES_FULL = 1, PAGES_BAD_INDEX = 2 };  // status bits of a pages work buffer
 size_t pages_work_ints(int n_pages, int batch);
 cudaError_t launch_pages_assign(const mog_pages *p, const int32_t *src, cudaStream_t s);
