@@ -134,7 +134,7 @@ cudaError_t launch_cache_decode(const mog_cache *c, const int32_t *lengths, int 
                 i8 ? log2_exact(c->block_rows) : 0, c->block_table, c->block_table ? log2_exact(c->page_rows) : 0, c->pages_per_seq, c->n_pages,
                 lengths, n_max, batch, h_kv, G, static_cast<const uint16_t *>(q), 0, 0, 0, 0, nullptr, scratch,
                 (float)(LOG2E / sqrt(diff ? MOG_D / 2.0 : (double)MOG_D)), 1, cache_cluster(batch * h_kv, n_max)};
-    for (int64_t x : {a.sb, a.sh, a.sn, a.ssb, a.ssh, a.ssn}) a.small = a.small && x >= INT32_MIN && x <= INT32_MAX;
+    for (int64_t x : {a.sn, a.ssn}) a.small = a.small && x >= INT32_MIN && x <= INT32_MAX;
     if (rows_in) a.qb = rows_in->qs[0], a.qh = rows_in->qs[2], a.ob = rows_in->os[0], a.oh = rows_in->os[2], a.count = rows_in->count;
     DiffArgs d{};
     if (diff) d = DiffArgs{diff->lam, diff->lam_heads > 1 ? 4 * (MOG_D / 2) : 0, diff->gamma, diff->lambda_init, diff->eps};

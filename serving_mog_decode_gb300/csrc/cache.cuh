@@ -110,7 +110,7 @@ struct CacheArgs {
     const int *count;        // own_rows: null, or per sequence: at most 0: its output stays as it is
     float *part;
     float scale2;
-    int small;  // the strides fit 32 bits
+    int small;  // the strides between rows, and between their scales, fit 32 bits
     int cs;  // CTAs of a cluster that works on one unit; 0: the tile list is split
 };
 
@@ -247,7 +247,7 @@ __device__ __forceinline__ void issue(const CacheArgs &a, const Cursor<T::ROWS> 
     const int first = c.t * T::ROWS, left = c.n - first;  // rows of the sequence from here on
     const int pmask = (1 << a.pshift) - 1;
     const int64_t head = c.h * a.sh + r0 * a.sn + ch * 16 + (PAGED ? 0 : c.b * a.sb);
-    // int8, contiguous: a tile all of whose rows are there, with strides of 32 bits, without the checks of its rows.
+    // int8, contiguous: a tile all of whose rows are there, with strides of 32 bits between them, without the checks of its rows.
     // The kernel is bound by its instructions there (1M tokens, 8 KV heads, G = 4: 405 us against 429); in pages the
     // same made it slower (8 x 16-64K tokens, 32 KV heads: 502 us against 496).
     if (T::I8 && !PAGED && a.small && left >= T::ROWS) {
