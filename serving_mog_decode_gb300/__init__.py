@@ -988,11 +988,13 @@ def rope_frequencies(rot_dim=128, base=10000.0, scaling=None):
     def plain(b):
         return [b ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
 
+    if not 0 < base < math.inf:
+        raise ValueError("base must be positive and finite")
     if scaling is None:
         return plain(base), 1.0
     kind, x = scaling["type"], float(scaling["factor"])
-    if not x > 0:
-        raise ValueError("a scaling's factor must be positive")
+    if not 0 < x < math.inf:
+        raise ValueError("a scaling's factor must be positive and finite")
     if kind == "linear":
         return [f / x for f in plain(base)], 1.0
     if kind == "ntk":
@@ -1002,8 +1004,13 @@ def rope_frequencies(rot_dim=128, base=10000.0, scaling=None):
     if kind not in ("yarn", "bands"):
         raise ValueError(f"unknown scaling type {kind!r}")
     n = float(scaling["original_len"])
+    if not 0 < n < math.inf:
+        raise ValueError("original_len must be positive and finite")
     f = plain(base)
     if kind == "yarn":
+        if not base > 1:
+            raise ValueError("yarn scaling needs a base above 1")
+
         def pair(turns):  # the pair that makes so many turns over the original length
             return rot_dim * math.log(n / (2 * math.pi * turns)) / (2 * math.log(base))
 
@@ -1043,6 +1050,8 @@ class Rope(_Fixed):
         f = torch.as_tensor(inv_freq, dtype=torch.float64)
         if f.shape != (rot_dim // 2,):
             raise ValueError(f"inv_freq must have {rot_dim // 2} entries")
+        if not torch.isfinite(f).all():
+            raise ValueError("frequencies must be finite")
         self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
         self.factor = float(of_scaling if factor is None else factor)
         if not math.isfinite(self.factor):
