@@ -1029,6 +1029,17 @@ def rope_frequencies(rot_dim=128, base=10000.0, scaling=None):
     return [g / x * (1 - k) + g * k for g, k in zip(f, keep)], float(scale)
 
 
+_TWO_PI = 6283185307179586476925286766559005768394338798750211641949889  # * 10^-60
+
+
+def _turns(f) -> int:
+    """f / 2 pi * 2^64, rounded to nearest, as a signed 64-bit fraction of a turn.  (In whole numbers: a quotient in fp64
+    would be off by 2^-25 of a turn at position 2^31.)"""
+    n, d = f.as_integer_ratio()
+    n, d = n * 10 ** 60 << 64, d * _TWO_PI
+    return ((2 * n + d) // (2 * d) + (1 << 63)) % (1 << 64) - (1 << 63)
+
+
 class Rope(_Fixed):
     """Rotary positions of the first rot_dim dimensions of a head (a multiple of 16 up to 128), for rope and
     rope_store; made once and kept.  interleaved: pairs of neighbouring dimensions 2i, 2i + 1;
@@ -1056,16 +1067,9 @@ class Rope(_Fixed):
         self.factor = float(of_scaling if factor is None else factor)
         if not math.isfinite(self.factor):
             raise ValueError("factor must be finite")
-        # turns per position as a 64-bit fraction: two exact steps of 32 bits
-        x = f / (2 * math.pi)
-        x = (x - torch.trunc(x)) * 2.0 ** 32
-        high = torch.floor(x)
-        low = torch.floor((x - high) * 2.0 ** 32)
-        high = high - 2.0 ** 32 * torch.floor((high + 2.0 ** 31) / 2.0 ** 32)
-        turns = high.long() * (1 << 32) + low.long()
         if device is None:
             device = f.device if f.is_cuda else torch.device("cuda", torch.cuda.current_device())
-        self.turns = turns.to(device)
+        self.turns = torch.tensor([_turns(x) for x in f.tolist()], dtype=torch.int64).to(device)
         self.device = self.turns.device
         self._s = RopeParams(self.turns.data_ptr(), rot_dim, 1 if interleaved else 0, self.factor)
         self._made = True
