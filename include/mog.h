@@ -620,8 +620,11 @@ int mog_check_cross_wait(const mog_cache *c, const int32_t *lengths_dev, int32_t
  * pos[b], which earlier stores wrote; else 0: a block whose first row is written starts afresh,
  * and what lies behind the new rows counts for nothing).  The new rows' codes are x * (1/s) rounded to
  * nearest even, infinities +-127; if s > held, the codes that the block holds become code * (held/s)
- * rounded to nearest even.  A NaN among the new rows makes the scale NaN, and so every row of
- * the block, whose codes stay as they are.  Products and quotients are rounded to fp32.
+ * rounded to nearest even.  So a row is off by half a step (s / 2) of the scale that it was stored with, and by half a
+ * step of each scale that the block has risen to since: these add up, the more often later rows of the block are larger
+ * than all before them.  A NaN among the new rows makes the scale NaN, and so every row of
+ * the block, whose codes stay as they are; it stays NaN, also after a step back to a position before that row, until the
+ * block's first row is written anew.  Products and quotients are rounded to fp32.
  */
 int mog_kv_store(const mog_cache *c, int32_t batch, int32_t h_kv, int32_t d, int32_t t_max,
                  const int32_t *pos_dev, const int32_t *count_dev, const void *k_new_dev,
