@@ -645,8 +645,8 @@ int mog_kv_load(const mog_cache *c, int32_t batch, int32_t h_kv, int32_t d, int3
  * position p becomes factor * (a cos x - b sin x, b cos x + a sin x), x = p * f_i; the other
  * dimensions stay.
  *  turns   : device int64 [rot_dim/2]: f_i / 2 pi as a 64-bit binary fraction of a turn
- *            (round(f_i / 2 pi * 2^64) mod 2^64), so that the angle of any position is exact
- *            to 2^-32 of a turn; 8-byte aligned
+ *            (round(f_i / 2 pi * 2^64) mod 2^64), so that the angle of any position is off
+ *            by less than 2^-31 of a turn; 8-byte aligned
  *  rot_dim : a multiple of 16, at most d
  *  layout  : MOG_ROPE_HALVES: pair i is dimensions i, i + rot_dim/2; MOG_ROPE_PAIRS: 2i, 2i + 1
  *  factor  : multiplies the turned dimensions (the attention factor of scaled contexts; else 1)

@@ -830,7 +830,7 @@ def cross_attend(K, V, lengths_dev, n_max, q, count=None, out=None, scratch=None
     strides of whole 16-byte chunks, last dim contiguous), to the rows [0, lengths_dev[b]) of a bf16
     cache, K, V [B, H_kv, n_cap, 128] (expanded over the batch, too) or K a PagedKV; every token sees every row.
     count: int32 [B] query tokens of each sequence, or None for T; rows of out behind them are not
-    written.  out: bf16 like q, a new tensor by default.  8-bit caches: dense_decode for one token,
+    written.  out: bf16 like q, a new tensor by default; it must not overlap q.  8-bit caches: dense_decode for one token,
     kv_load for more.  -> out."""
     return _cross(K, V, lengths_dev, n_max, q, count, out, scratch, stream)
 

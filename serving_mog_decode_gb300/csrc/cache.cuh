@@ -39,7 +39,8 @@
 // 171 us, 6.5 TB/s); the wide form too over bf16 rows (G = 5: 315 us), but over e4m3 rows by the latencies of its
 // chains (G = 5, 4 x 128K: 220 us, 5.0 TB/s; 43% of issue slots, 37% of the tensor pipe).  int8 rows: 1M tokens, 8 KV heads,
 // G = 4: 380 us, 5.65 TB/s; not HBM (78%) but the waits between a warp's products and its widening, at 54% of the
-// issue slots (three CTAs of four warps, which the registers allow).
+// issue slots (three CTAs of four warps, which the registers allow).  Wide int8 (G = 12, 256K tokens, 8 heads: 126 us, 4.3 TB/s; e4m3
+// 114) runs in the two CTAs and 32 rows a warp that were chosen by measurements of e4m3 rows (below); other splits were not measured for it.
 #pragma once
 
 #include <cuda_bf16.h>

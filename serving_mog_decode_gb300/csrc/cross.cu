@@ -22,8 +22,9 @@
 // two a CTA), which k_cross_merge folds.  cross_grid has the rule.  The copies of a CTA's next item run ahead.
 //
 // Bound by: the tensor cores, whose products the softmax does not hide completely.  4096 tokens of 32 heads over 32K rows
-// of 8 KV heads: 1.35 ms, 1.63 PFLOP/s, 0.86 of a library's matrix product in a burst, 0.96 of a sustained one; a unit (two tile products)
-// takes about 2.9K cycles, 2048 of them the MMA pipe's, and the GPU runs at its power limit (1.97 GHz).  The chain of a
+// of 8 KV heads: 1.33 to 1.46 ms, 1.50 to 1.65 PFLOP/s, the longer the GPU is at its power limit (1.40 ms in a graph of 20 calls: 1.57
+// PFLOP/s, 0.83 of a library's matrix product in a burst, 0.93 of a sustained one); a unit (two tile products)
+// takes about 2.9K cycles, 2048 of them the MMA pipe's, at 1.97 GHz.  The chain of a
 // softmax tile is about 1300 cycles; an item's start and end (O read, normalised, stored) about 10K.  Few query rows (16
 // tokens of 40 heads to 128K rows of 8 heads, 4 sequences, in pages): HBM, 335 us, 6.4 TB/s.
 //

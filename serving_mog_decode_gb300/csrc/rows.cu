@@ -4,7 +4,7 @@
 //
 // Rotary positions.  Pair i of a row's first rot_dim dimensions is turned by the angle
 // pos * f_i.  A frequency is held as turns per position in 64-bit fixed point, so that the angle is
-// one integer product whose overflow drops the whole turns: exact to 2^-32 of a turn at any
+// one integer product whose overflow drops the whole turns: off by less than 2^-31 of a turn at any
 // position (in fp32, position 1M would leave a tenth of a radian).  A CTA computes the
 // cosines and sines of its tokens once, into shared memory, for all their heads.  A prompt is bound by HBM: 24K tokens of
 // 32 + 8 + 8 heads into bf16 pages, 590 MB, 90 us, 6.5 TB/s; a chunk's start and end show (4096 tokens of 40 + 8 + 8 heads,

@@ -36,7 +36,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
                  : "memory");
 }
 // Wait for the phase with the given parity to complete; false after `limit` polls without
-// it (the default, 2^20 polls with 128 ns sleeps, is about a second).
+// it (the default, 2^20 polls with 128 ns sleeps, takes some four seconds).
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int limit = 1 << 20) {
     for (int i = 0; i < limit; ++i) {
         uint32_t done;
