@@ -1042,7 +1042,7 @@ def _turns(f) -> int:
 
 class Rope(_Fixed):
     """Rotary positions of the first rot_dim dimensions of a head (a multiple of 16 up to 128), for rope and
-    rope_store; made once and kept.  interleaved: pairs of neighbouring dimensions 2i, 2i + 1;
+    rope_store; made once, on the host and outside of graph captures, and kept.  interleaved: pairs of neighbouring dimensions 2i, 2i + 1;
     otherwise i, i + rot_dim/2.  Frequencies: rope_frequencies(rot_dim, base, scaling), or
     inv_freq (radians per position, rot_dim/2 of them, a sequence or a float64 tensor).  factor: the
     attention factor of the turned dimensions (default: the scaling's, or 1).  device: default
@@ -1061,7 +1061,8 @@ class Rope(_Fixed):
         f = torch.as_tensor(inv_freq, dtype=torch.float64)
         if f.shape != (rot_dim // 2,):
             raise ValueError(f"inv_freq must have {rot_dim // 2} entries")
-        if not torch.isfinite(f).all():
+        radians = f.tolist()
+        if not all(map(math.isfinite, radians)):
             raise ValueError("frequencies must be finite")
         self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
         self.factor = float(of_scaling if factor is None else factor)
@@ -1069,7 +1070,7 @@ class Rope(_Fixed):
             raise ValueError("factor must be finite")
         if device is None:
             device = f.device if f.is_cuda else torch.device("cuda", torch.cuda.current_device())
-        self.turns = torch.tensor([_turns(x) for x in f.tolist()], dtype=torch.int64).to(device)
+        self.turns = torch.tensor([_turns(x) for x in radians], dtype=torch.int64).to(device)
         self.device = self.turns.device
         self._s = RopeParams(self.turns.data_ptr(), rot_dim, 1 if interleaved else 0, self.factor)
         self._made = True
